@@ -31,21 +31,21 @@ CHUNK = 64
 # --------------------------------------------------------------------------
 def listed():
     return [
-        # One user's next token on one layer of the Mamba-2 block's head shape (24 heads, state
-        # 128 x 64): the smallest serving call, latency alone.
-        dict(name="attn step, 1 row", op="step", n=1, slots=8, H=24, G=24, Dk=128, Dv=64, dtype=BF16),
+        # One user's next token on one layer of the Mamba-3 MIMO block's head shape (16 heads,
+        # state 128 x 64): the smallest serving call, latency alone.
+        dict(name="attn step, 1 row", op="step", n=1, slots=8, H=16, G=16, Dk=128, Dv=64, dtype=BF16),
         # The decode batch of the repository's step workloads, 256 sequences whose states lie
         # scattered in a pool of 320 (sequences that paused keep theirs).
-        dict(name="attn step, 256 rows", op="step", n=256, slots=320, H=24, G=24, Dk=128, Dv=64, dtype=BF16),
+        dict(name="attn step, 256 rows", op="step", n=256, slots=320, H=16, G=16, Dk=128, Dv=64, dtype=BF16),
         # A few short prompts of odd lengths arriving together, states into pool slots; keys and
         # values shared by pairs of heads.
         dict(name="attn prompt, short", op="prompt", n=7, T=1021, H=8, G=4, Dk=64, Dv=64, dtype=BF16, packed=True),
         # A prefill batch as a server packs it: 16 thousand tokens of nine prompts.
-        dict(name="attn prompt, packed", op="prompt", n=9, T=16384, H=24, G=24, Dk=128, Dv=64, dtype=BF16, packed=True),
+        dict(name="attn prompt, packed", op="prompt", n=9, T=16384, H=16, G=16, Dk=128, Dv=64, dtype=BF16, packed=True),
         # fp32 evaluation of equal-length sequences, length not a multiple of any tile.
         dict(name="attn prompt, fp32", op="prompt", n=2, T=8190, H=16, G=16, Dk=64, Dv=64, dtype=F32, packed=False),
-        # The gradient of one training layer at the Mamba-2 block shape: batch 4, L 4096.
-        dict(name="attn backward, training", op="bwd", n=4, T=16384, H=24, G=24, Dk=128, Dv=64, dtype=BF16, packed=False),
+        # The gradient of one training layer: batch 4, L 4096 on the same heads.
+        dict(name="attn backward, training", op="bwd", n=4, T=16384, H=16, G=16, Dk=128, Dv=64, dtype=BF16, packed=False),
         # The norm in front of a block for a handful of decoding users, fp32 residual stream.
         dict(name="norm, 4 rows", op="norm", rows=4, D=768, dtype=BF16, res=F32, stride=768),
         # An odd width, rows cut out of a wider buffer so that no row is 16-byte aligned.
@@ -113,7 +113,7 @@ def _slopes(H, dev):
 def _clip_shapes(case):
     """Parameter shapes of a stack of scan blocks: projections, conv, per-channel vectors, embedding."""
     d, e = case["d"], 2 * case["d"]
-    layer = [(d,), (2 * e, d), (e, 4), (e,), (d // 16 + 32, e), (e, d // 16 or 1), (e,), (e, 16), (e,), (d, e)]
+    layer = [(d,), (e, d), (e, d), (e, 4), (e,), (d // 16 + 32, e), (e, d // 16 or 1), (e,), (e, 16), (e,), (d, e)]
     return [(case["vocab"], d)] + layer * case["layers"] + [(d,)]
 
 
