@@ -67,7 +67,11 @@ typedef enum {
     MB_OP_TRAP_SSD_BWD = 7,
     MB_OP_MIMO_SSD_BWD = 8,
     MB_OP_SSD_BLOCK = 9,        /* mb_ssd_block with MB_F32 */
-    MB_OP_SSD_BLOCK_BF16 = 10   /* mb_ssd_block with MB_BF16 */
+    MB_OP_SSD_BLOCK_BF16 = 10,  /* mb_ssd_block with MB_BF16 */
+    MB_OP_LINEAR_ATTN = 11,     /* sizes (n_seq, T, H, Dv, G, Dk) in (batch, L, H, P, G, N) */
+    MB_OP_LINEAR_ATTN_BWD = 12, /* likewise */
+    MB_OP_RMS_NORM_BWD = 13,    /* sizes (rows, D) in (batch, H) */
+    MB_OP_GRAD_NORM_CLIP = 14   /* the number of tensors in batch */
 } mb_op;
 
 /*
@@ -567,6 +571,152 @@ mb_status mb_ssd_chunked_bwd(const float* X, const float* logdecay, const float*
                              float* dC, float* dh0, int64_t batch, int64_t L, int64_t H,
                              int64_t P, int64_t G, int64_t N, mb_dtype dtype, void* ws,
                              size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Linear attention with one fixed decay per head, chunkwise (the SSD recurrence of
+ * mb_ssd_chunked with a constant decay, keys and values shared within a group, packed
+ * sequences and states in pool slots).  Per sequence and head h, with lambda =
+ * exp(log_decay[h]) and the group g = h / (H/G) of its keys and values:
+ *     S_t = lambda S_{t-1} + k_t[g] (outer) v_t[g]     (Dk x Dv)
+ *     o_t = scale S_t^T q_t[h]
+ *   q, o        : (T, H, Dk), (T, H, Dv)  dtype   the tokens of all sequences, one after another
+ *   k, v        : (T, G, Dk), (T, G, Dv)  dtype
+ *   q_stride, k_stride, v_stride : elements between tokens, at least H*Dk, G*Dk, G*Dv:
+ *                 q, k and v may be columns of one projection's output.  o is contiguous.
+ *   log_decay   : (H) fp32, <= 0 in use (-inf: no memory)
+ *   cu_seqlens  : (n_seq + 1) int32, nondecreasing: sequence s holds tokens cu_seqlens[s] to
+ *                 cu_seqlens[s+1] - 1, any length from zero; rows of o outside all sequences are
+ *                 left as they were.  NULL: n_seq sequences of T / n_seq tokens each.  The values
+ *                 are not read on the host: offsets outside [0, T] are taken as the nearest bound,
+ *                 and decreasing ones give unspecified results, but no access outside the tensors.
+ *   h0, h_out   : (n_seq, H, Dk, Dv) fp32, or (n_slots, H, Dk, Dv) with slots.  h0 NULL = zeros;
+ *                 h_out NULL = not written; h_out may equal h0.  A sequence of no tokens leaves
+ *                 its h0 (or zeros) in h_out.
+ *   has_h0      : (n_seq) bytes; a zero: the sequence starts from zeros, not from h0.  NULL: all have it
+ *   slots       : (n_seq) int32, the row of h0 and h_out of each sequence, or NULL (row s; n_slots is
+ *                 then 0).  A slot outside [0, n_slots) starts from zeros and its end state is not
+ *                 stored.  Slots inside must differ: what a repeated one holds afterwards, and the
+ *                 outputs of its sequences, are unspecified.
+ * Supported: 1 <= Dk, Dv <= 128, H <= 4096, T < 2^31, n_seq <= 2^20.  Any alignment of the
+ * element type's; 16-byte aligned pointers with Dk, Dv and strides multiples of 8
+ * (bf16; 4 for fp32) take the fast path.  fp32 arithmetic runs on fp32 matrix products; with MB_BF16 the
+ * products take bf16 operands with fp32 accumulation: the masked scores and a copy of the
+ * state are rounded, the carried state is not (its update splits the weighted values into
+ * three bf16 pieces).  NaN and infinities in v reach all outputs of their 64-token chunk.
+ * ws: at least mb_workspace_size(MB_OP_LINEAR_ATTN, n_seq, T, H, Dv, G, Dk, 1, 0) bytes, 256-byte
+ * aligned (may be 0: one segment per sequence).
+ */
+mb_status mb_linear_attn(const void* q, const void* k, const void* v, const float* log_decay,
+                         const int32_t* cu_seqlens, const float* h0, const uint8_t* has_h0,
+                         const int32_t* slots, void* o, float* h_out, int64_t n_seq, int64_t T,
+                         int64_t H, int64_t G, int64_t Dk, int64_t Dv, int64_t n_slots,
+                         int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                         mb_dtype dtype, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * One token of mb_linear_attn for n independent sequences (decode):
+ *     h[s] <- lambda h[s] + k (outer) v,   o = scale h[s]^T q
+ *   q (n, H, Dk), k (n, G, Dk), v (n, G, Dv), o (n, H, Dv) dtype; strides as above
+ *   h_in, h_out : (n, H, Dk, Dv) fp32, or (n_slots, H, Dk, Dv) with slots; h_in NULL = zeros;
+ *                 h_out == h_in (in place) is allowed; rows of h_out that no slot names are left alone
+ *   slots       : as above (outside [0, n_slots): starts from zeros, nothing stored)
+ * No workspace.
+ */
+mb_status mb_linear_attn_step(const void* q, const void* k, const void* v, const float* log_decay,
+                              const int32_t* slots, const float* h_in, float* h_out, void* o,
+                              int64_t n, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
+                              int64_t n_slots, int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, float scale, mb_dtype dtype, hipStream_t stream);
+
+/*
+ * Backward of mb_linear_attn: given d_o (gradient of the loss with respect to o) and
+ * dh_out (with respect to h_out; NULL = zero), the gradients of sum d_o . o + sum dh_out .
+ * h_out with respect to q, k, v and h0 (log_decay is fixed and has none).  With S_t the
+ * forward state and R its adjoint (R = dh_out, then per token from the last):
+ *     R_t = R + scale q_t d_o_t^T;  dk_t = R_t v_t;  dv_t = R_t^T k_t;  R = lambda R_t
+ *     dq_t = scale S_t d_o_t;  dh0 = R at the end
+ * (dk and dv summed over the heads of the group).  Nothing of the forward call is needed.
+ *   d_o (T, H, Dv), dq (T, H, Dk), dk (T, G, Dk), dv (T, G, Dv) dtype, contiguous
+ *   h0, dh_out, dh0 : (n_seq, H, Dk, Dv) fp32; h0, dh_out NULL = zeros; dh0 NULL = not wanted
+ * Rows of dq, dk, dv of tokens outside all sequences are zero.  Other arguments, limits
+ * and roundings as mb_linear_attn.  No output may overlap an input, another output or the
+ * workspace (MB_ERR_ALIAS).  Deterministic.
+ * ws: at least mb_workspace_size(MB_OP_LINEAR_ATTN_BWD, n_seq, T, H, Dv, G, Dk, 1, 0) bytes.
+ */
+mb_status mb_linear_attn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
+                             const int32_t* cu_seqlens, const float* h0, const void* d_o,
+                             const float* dh_out, void* dq, void* dk, void* dv, float* dh0,
+                             int64_t n_seq, int64_t T, int64_t H, int64_t G, int64_t Dk, int64_t Dv,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride, float scale,
+                             mb_dtype dtype, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, in front of a block:
+ *     r = x + residual,   rstd = 1 / sqrt(mean_d r_d^2 + eps),   y_d = r_d rstd weight_d
+ *   x            : (rows, D) dtype, x_stride >= D elements between rows
+ *   residual     : (rows, D) residual_dtype, or NULL (r = x)
+ *   weight       : (D) fp32 or NULL (ones)
+ *   y            : (rows, D) dtype
+ *   residual_out : (rows, D) residual_dtype: r; NULL = not written; may equal residual
+ *   rstd         : (rows) fp32, for the backward; NULL = not written
+ * residual_dtype is MB_F32 or dtype (MB_ERR_DTYPE otherwise).  The norm is taken of r before
+ * it is rounded to residual_dtype.  Supported: 1 <= D <= 16384, rows <= 2^30.  Any alignment of
+ * the element types'; 16-byte aligned pointers with D and x_stride multiples of 8 (bf16;
+ * 4 for fp32) take 16-byte accesses.
+ */
+mb_status mb_rms_norm(const void* x, const void* residual, const float* weight, void* y,
+                      void* residual_out, float* rstd, int64_t rows, int64_t D, int64_t x_stride,
+                      float eps, mb_dtype dtype, mb_dtype residual_dtype, hipStream_t stream);
+
+/*
+ * mb_rms_norm with y in 8 bits (e4m3, largest value 448) for an 8-bit projection: per row, or per
+ * `group` neighbouring columns of a row (the last group may be short),
+ *     scale = max(max |y|, 2^-96) / 448,   q = e4m3(y / scale)   (to nearest, ties to even)
+ *   y      : (rows, D) e4m3 bytes
+ *   scales : (rows, ceil(D / group)) fp32, (rows, 1) with group 0
+ *   group  : 0 (the whole row), 32, 64 or 128 (MB_ERR_SHAPE otherwise)
+ * A NaN in a row gives NaN scales and values.  Other arguments as mb_rms_norm.
+ */
+mb_status mb_rms_norm_fp8(const void* x, const void* residual, const float* weight, void* y,
+                          float* scales, void* residual_out, float* rstd, int64_t rows, int64_t D,
+                          int64_t x_stride, int64_t group, float eps, mb_dtype dtype,
+                          mb_dtype residual_dtype, hipStream_t stream);
+
+/*
+ * Backward of mb_rms_norm: given dy, r (its residual_out, or x when there was no
+ * residual) and rstd, with xh = r rstd and g = dy weight,
+ *     dr = dr_in + rstd (g - xh mean_d(g xh))    the gradient of x and of residual alike
+ *     dweight_d = sum_rows dy_d xh_d
+ *   dy, dx    : (rows, D) dtype            dx = dr in the type of x; NULL = not wanted
+ *   r, dr_in, dr : (rows, D) residual_dtype; dr_in (the gradient reaching residual_out) NULL = zeros;
+ *               dr NULL = not wanted; dr may equal dr_in
+ *   rstd (rows) fp32;  weight (D) fp32 or NULL;  dweight (D) fp32 or NULL = not wanted
+ * At least one of dx, dr, dweight.  Sums in a fixed order (deterministic).  Sizes as mb_rms_norm.
+ * ws: with dweight, at least mb_workspace_size(MB_OP_RMS_NORM_BWD, rows, 1, D, 1, 1, 1, 1, 0) bytes,
+ * 256-byte aligned (may be 0).
+ */
+mb_status mb_rms_norm_bwd(const void* dy, const void* r, const float* rstd, const float* weight,
+                          const void* dr_in, void* dx, void* dr, float* dweight, int64_t rows,
+                          int64_t D, mb_dtype dtype, mb_dtype residual_dtype, void* ws,
+                          size_t ws_bytes, hipStream_t stream);
+
+/*
+ * The global 2-norm of n gradient tensors, and their clipping to it:
+ *     norm = sqrt(sum of all squares),   out = g * min(1, max_norm / (norm + eps))
+ *   grads, outs, sizes : HOST arrays of n device pointers and element counts (>= 0; a pointer of
+ *               a tensor of no elements is not looked at), read during the call only.  outs NULL: in
+ *               place; an outs[i] may equal grads[i] and else must not overlap it.  Different
+ *               tensors must not overlap.
+ *   max_norm  : >= 0; INFINITY: the norm alone in place (nothing is written), a copy otherwise
+ *   norm      : (1) fp32 on the device
+ * Squares are summed in fp64 in a fixed order.  A NaN or infinite norm scales as the formula says
+ * (NaN; or zeros, and NaN where g is infinite).  Where in place and norm + eps <= max_norm, the
+ * gradients are not written.  n <= 65536.
+ * ws: at least mb_workspace_size(MB_OP_GRAD_NORM_CLIP, n, 1, 1, 1, 1, 1, 1, 0) bytes, 256-byte aligned.
+ */
+mb_status mb_grad_norm_clip(const void* const* grads, void* const* outs, const int64_t* sizes,
+                            int64_t n, float max_norm, float eps, float* norm, mb_dtype dtype,
+                            void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * Bytes of device workspace an entry point needs for the given sizes (0 if it

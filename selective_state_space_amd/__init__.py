@@ -20,6 +20,9 @@ __all__ = [
     "MB_OP_SELECTIVE_SCAN", "MB_OP_SSM_STEP", "MB_OP_SSD_CHUNKED", "MB_OP_TRAP_SSD",
     "MB_OP_MIMO_SSD", "MB_OP_SSD_CHUNKED_BWD", "MB_OP_SELECTIVE_SCAN_BWD", "MB_OP_TRAP_SSD_BWD",
     "MB_OP_MIMO_SSD_BWD", "MB_OP_SSD_BLOCK", "MB_OP_SSD_BLOCK_BF16", "mb_ssd_block",
+    "mb_linear_attn", "mb_linear_attn_step", "mb_linear_attn_bwd", "mb_rms_norm", "mb_rms_norm_fp8",
+    "mb_rms_norm_bwd", "mb_grad_norm_clip", "MB_OP_LINEAR_ATTN", "MB_OP_LINEAR_ATTN_BWD",
+    "MB_OP_RMS_NORM_BWD", "MB_OP_GRAD_NORM_CLIP",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -30,7 +33,8 @@ _lib = None
 MB_F32, MB_BF16 = 0, 1
 (MB_OP_SELECTIVE_SCAN, MB_OP_SSM_STEP, MB_OP_SSD_CHUNKED, MB_OP_TRAP_SSD,
  MB_OP_MIMO_SSD, MB_OP_SSD_CHUNKED_BWD, MB_OP_SELECTIVE_SCAN_BWD, MB_OP_TRAP_SSD_BWD,
- MB_OP_MIMO_SSD_BWD, MB_OP_SSD_BLOCK, MB_OP_SSD_BLOCK_BF16) = range(11)
+ MB_OP_MIMO_SSD_BWD, MB_OP_SSD_BLOCK, MB_OP_SSD_BLOCK_BF16, MB_OP_LINEAR_ATTN,
+ MB_OP_LINEAR_ATTN_BWD, MB_OP_RMS_NORM_BWD, MB_OP_GRAD_NORM_CLIP) = range(15)
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -111,6 +115,18 @@ def load_library():
         if hasattr(lib, "mb_ssd_step"):
             lib.mb_ssd_step.argtypes = [_vp] * 12 + [_i64] * 6 + [ctypes.c_int, _vp]
             lib.mb_ssd_step.restype = ctypes.c_int
+        if hasattr(lib, "mb_linear_attn"):
+            sz, fl, it = ctypes.c_size_t, ctypes.c_float, ctypes.c_int
+            lib.mb_linear_attn.argtypes = [_vp] * 10 + [_i64] * 10 + [fl, it, _vp, sz, _vp]
+            lib.mb_linear_attn_step.argtypes = [_vp] * 8 + [_i64] * 9 + [fl, it, _vp]
+            lib.mb_linear_attn_bwd.argtypes = [_vp] * 12 + [_i64] * 9 + [fl, it, _vp, sz, _vp]
+            lib.mb_rms_norm.argtypes = [_vp] * 6 + [_i64] * 3 + [fl, it, it, _vp]
+            lib.mb_rms_norm_fp8.argtypes = [_vp] * 7 + [_i64] * 4 + [fl, it, it, _vp]
+            lib.mb_rms_norm_bwd.argtypes = [_vp] * 8 + [_i64] * 2 + [it, it, _vp, sz, _vp]
+            lib.mb_grad_norm_clip.argtypes = [_vp] * 3 + [_i64, fl, fl, _vp, it, _vp, sz, _vp]
+            for f in ("mb_linear_attn", "mb_linear_attn_step", "mb_linear_attn_bwd", "mb_rms_norm", "mb_rms_norm_fp8",
+                      "mb_rms_norm_bwd", "mb_grad_norm_clip"):
+                getattr(lib, f).restype = ctypes.c_int
         lib.mb_status_str.argtypes = [ctypes.c_int]
         lib.mb_status_str.restype = ctypes.c_char_p
         lib.mb_last_hip_error.restype = ctypes.c_int
@@ -757,3 +773,281 @@ def mb_selective_scan_fused(x, conv_w, dt, A, B, C, D=None, h0=None, *, conv_b=N
           _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(h0), _ptr(y), _ptr(h_out), b, L, Dm, N, K, MB_F32,
           _stream(dev))
     return y, h_out
+
+
+# ----------------------------------------------------------------------------
+# linear attention with a decay per head
+# ----------------------------------------------------------------------------
+def _tokens(t, name, lead, heads, width, dtype, device):
+    """Check a (*lead, heads, width) tensor whose tokens lie at one stride (a view into a fused
+    projection's output may be passed as it is).  Returns that stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    shape = tuple(lead) + (heads, width)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    dense = heads * width
+    if t.numel() == 0 or t.is_contiguous():
+        return dense
+    st = t.stride()
+    if (width > 1 and st[-1] != 1) or (heads > 1 and st[-2] != width):
+        raise ValueError("%s: a token's heads must lie next to each other" % name)
+    if len(lead) == 1:
+        ts = st[0] if lead[0] > 1 else dense
+    else:
+        ts = st[1] if lead[1] > 1 else st[0] if lead[0] > 1 else dense
+        if lead[0] > 1 and lead[1] > 1 and st[0] != lead[1] * ts:
+            raise ValueError("%s: its tokens must lie at one stride" % name)
+    if ts < dense:
+        raise ValueError("%s: its tokens must not overlap" % name)
+    return ts
+
+
+def _attn_args(q, k, v, log_decay, cu_seqlens):
+    """Shapes, strides and device of a linear attention call: (device, dtype, code, lead, n_seq, T, H,
+    G, Dk, Dv, strides)."""
+    torch = _torch()
+    dev = _device_of(q)
+    code = _dtype_code(q, "q")
+    packed = cu_seqlens is not None
+    if q.dim() != (3 if packed else 4):
+        raise ValueError("q must be (T, H, Dk) with cu_seqlens, (batch, L, H, Dk) without")
+    lead, (H, Dk) = tuple(q.shape[:-2]), q.shape[-2:]
+    if k.dim() != q.dim() or v.dim() != q.dim():
+        raise ValueError("q, k and v must have the same number of axes")
+    G, Dv = k.shape[-2], v.shape[-1]
+    strides = (_tokens(q, "q", lead, H, Dk, q.dtype, dev), _tokens(k, "k", lead, G, Dk, q.dtype, dev),
+               _tokens(v, "v", lead, G, Dv, q.dtype, dev))
+    _check(log_decay, "log_decay", (H,), torch.float32, dev)
+    if packed:
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+            raise ValueError("cu_seqlens must hold n_seq + 1 offsets")
+        _check(cu_seqlens, "cu_seqlens", tuple(cu_seqlens.shape), torch.int32, dev)
+        n, T = cu_seqlens.shape[0] - 1, lead[0]
+    else:
+        n, T = lead[0], lead[0] * lead[1]
+    return dev, code, lead, n, T, H, G, Dk, Dv, strides
+
+
+def _pool_args(h0, h_out, slots, n, H, Dk, Dv, dev):
+    """Check the states; returns (n_slots, state shape)."""
+    torch = _torch()
+    if slots is None:
+        return 0, (n, H, Dk, Dv)
+    _check(slots, "slots", (n,), torch.int32, dev)
+    pool = h0 if h0 is not None else h_out
+    if pool is None or pool.dim() != 4 or pool.shape[0] < 1:
+        raise ValueError("slots need a pool of states (n_slots, H, Dk, Dv)")
+    return pool.shape[0], (pool.shape[0], H, Dk, Dv)
+
+
+def mb_linear_attn(q, k, v, log_decay, *, scale=None, cu_seqlens=None, h0=None, has_h0=None, slots=None, o=None,
+                   h_out=None, ws=None):
+    """Linear attention with one fixed decay per head.  q (batch, L, H, Dk), k (batch, L, G, Dk),
+    v (batch, L, G, Dv) in one dtype (float32 or bfloat16), views with one stride between tokens
+    allowed; log_decay (H,) float32.  With cu_seqlens (n_seq + 1,) int32 the tensors are (T, heads,
+    width), the sequences packed one after another.  h0 (n_seq, H, Dk, Dv) float32, or with slots
+    (n_seq,) int32 a pool (n_slots, H, Dk, Dv) that is updated in place unless h_out is given;
+    has_h0 (n_seq,) uint8 or bool marks the sequences that continue.  scale defaults to Dk ** -0.5.
+    Rows of o outside all sequences are not written (an o allocated here holds anything there).
+    Returns (o, h_out)."""
+    torch = _torch()
+    dev, code, lead, n, T, H, G, Dk, Dv, st = _attn_args(q, k, v, log_decay, cu_seqlens)
+    n_slots, hs = _pool_args(h0, h_out, slots, n, H, Dk, Dv, dev)
+    f32 = torch.float32
+    _check(h0, "h0", hs, f32, dev)
+    if has_h0 is not None:
+        _check(has_h0, "has_h0", (n,), torch.bool if has_h0.dtype == torch.bool else torch.uint8, dev)
+    o = torch.empty(lead + (H, Dv), dtype=q.dtype, device=dev) if o is None else _check(o, "o", lead + (H, Dv), q.dtype, dev)
+    if h_out is None:
+        h_out = h0 if slots is not None else torch.empty(hs, dtype=f32, device=dev)
+    _check(h_out, "h_out", hs, f32, dev)
+    ws, nws = _workspace(MB_OP_LINEAR_ATTN, dev, ws, (n, T, H, Dv, G, Dk, 1, 0))
+    with torch.cuda.device(dev):
+        _call("mb_linear_attn", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), _ptr(h0), _ptr(has_h0),
+              _ptr(slots), _ptr(o), _ptr(h_out), n, T, H, G, Dk, Dv, n_slots, *st, Dk ** -0.5 if scale is None else scale,
+              code, _ptr(ws), nws, _stream(dev))
+    return o, h_out
+
+
+def mb_linear_attn_step(q, k, v, log_decay, h, *, scale=None, slots=None, o=None, h_out=None):
+    """One token of mb_linear_attn per sequence.  q (n, H, Dk), k (n, G, Dk), v (n, G, Dv); h (n, H, Dk,
+    Dv) float32, or with slots (n,) int32 a pool (n_slots, H, Dk, Dv).  With h_out=None the states
+    are updated in place.  Returns (o, h_out)."""
+    torch = _torch()
+    dev = _device_of(q)
+    code = _dtype_code(q, "q")
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be (n, heads, width)")
+    n, H, Dk = q.shape
+    G, Dv = k.shape[1], v.shape[2]
+    st = (_tokens(q, "q", (n,), H, Dk, q.dtype, dev), _tokens(k, "k", (n,), G, Dk, q.dtype, dev),
+          _tokens(v, "v", (n,), G, Dv, q.dtype, dev))
+    _check(log_decay, "log_decay", (H,), torch.float32, dev)
+    n_slots, hs = _pool_args(h, h_out, slots, n, H, Dk, Dv, dev)
+    _check(h, "h", hs, torch.float32, dev)
+    h_out = h if h_out is None else _check(h_out, "h_out", hs, torch.float32, dev)
+    o = torch.empty((n, H, Dv), dtype=q.dtype, device=dev) if o is None else _check(o, "o", (n, H, Dv), q.dtype, dev)
+    with torch.cuda.device(dev):
+        _call("mb_linear_attn_step", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(slots), _ptr(h), _ptr(h_out), _ptr(o),
+              n, H, G, Dk, Dv, n_slots, *st, Dk ** -0.5 if scale is None else scale, code, _stream(dev))
+    return o, h_out
+
+
+def mb_linear_attn_bwd(q, k, v, log_decay, do, *, scale=None, cu_seqlens=None, h0=None, dh_out=None, dq=None, dk=None,
+                       dv=None, dh0=None, ws=None):
+    """Backward of mb_linear_attn: the gradients of sum do . o + sum dh_out . h_out with respect to q,
+    k, v and h0.  do like o; h0, dh_out (n_seq, H, Dk, Dv) float32 or None (zeros).  Rows of tokens
+    outside all sequences are zero.  Returns (dq, dk, dv, dh0)."""
+    torch = _torch()
+    dev, code, lead, n, T, H, G, Dk, Dv, st = _attn_args(q, k, v, log_decay, cu_seqlens)
+    f32, dt, hs = torch.float32, q.dtype, (n, H, Dk, Dv)
+    _check(do, "do", lead + (H, Dv), dt, dev)
+    _check(h0, "h0", hs, f32, dev)
+    _check(dh_out, "dh_out", hs, f32, dev)
+    out = []
+    for t, name, shp, d in ((dq, "dq", lead + (H, Dk), dt), (dk, "dk", lead + (G, Dk), dt), (dv, "dv", lead + (G, Dv), dt),
+                            (dh0, "dh0", hs, f32)):
+        out.append(torch.empty(shp, dtype=d, device=dev) if t is None else _check(t, name, shp, d, dev))
+    ws, nws = _workspace(MB_OP_LINEAR_ATTN_BWD, dev, ws, (n, T, H, Dv, G, Dk, 1, 0))
+    with torch.cuda.device(dev):
+        _call("mb_linear_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), _ptr(h0), _ptr(do),
+              _ptr(dh_out), *[_ptr(t) for t in out], n, T, H, G, Dk, Dv, *st, Dk ** -0.5 if scale is None else scale, code,
+              _ptr(ws), nws, _stream(dev))
+    return tuple(out)
+
+
+# ----------------------------------------------------------------------------
+# root-mean-square norm, gradient clipping
+# ----------------------------------------------------------------------------
+def _norm_args(x, weight, residual, residual_out, rstd):
+    """Check a norm's arguments; returns (device, code, residual code, rows, D, stride, residual dtype,
+    residual_out, rstd)."""
+    torch = _torch()
+    dev = _device_of(x)
+    code = _dtype_code(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must have at least one axis")
+    D = x.shape[-1]
+    rows = x.numel() // D if D else 0
+    if x.is_contiguous() or x.numel() == 0:
+        stride = D
+    elif x.dim() == 2 and (x.stride(1) == 1 or D == 1) and x.stride(0) >= D:
+        stride = x.stride(0) if rows > 1 else D
+    else:
+        raise ValueError("x must be contiguous, or (rows, D) with contiguous rows")
+    rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else x.dtype
+    if rdt not in (torch.float32, x.dtype):
+        raise TypeError("residual must be float32 or have the dtype of x, got %s" % rdt)
+    _check(weight, "weight", (D,), torch.float32, dev)
+    _check(residual, "residual", tuple(x.shape), rdt, dev)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=rdt, device=dev) if residual is not None else None
+    else:
+        _check(residual_out, "residual_out", tuple(x.shape), rdt, dev)
+    shp = tuple(x.shape[:-1])
+    rstd = torch.empty(shp, dtype=torch.float32, device=dev) if rstd is None else _check(rstd, "rstd", shp, torch.float32, dev)
+    return dev, code, MB_F32 if rdt == torch.float32 else MB_BF16, rows, D, stride, residual_out, rstd
+
+
+def mb_rms_norm(x, weight=None, residual=None, *, eps=1e-5, y=None, residual_out=None, rstd=None):
+    """Root-mean-square norm of r = x + residual over the last axis, times weight (D,) float32 or None.
+    x float32 or bfloat16; residual (like x, float32 or the dtype of x) or None.  residual_out may be
+    the residual itself.  Returns (y, r, rstd): r is x when there is no residual."""
+    torch = _torch()
+    dev, code, rcode, rows, D, stride, r, rstd = _norm_args(x, weight, residual, residual_out, rstd)
+    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else _check(y, "y", tuple(x.shape), x.dtype, dev)
+    with torch.cuda.device(dev):
+        _call("mb_rms_norm", _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(r), _ptr(rstd), rows, D, stride,
+              float(eps), code, rcode, _stream(dev))
+    return y, x if r is None else r, rstd
+
+
+def mb_rms_norm_fp8(x, weight=None, residual=None, *, group=0, eps=1e-5, y=None, scales=None, residual_out=None,
+                    rstd=None):
+    """mb_rms_norm with its output in 8 bits: y (torch.float8_e4m3fn, like x) and scales (rows...,
+    ceil(D / group)) float32, one per `group` columns (32, 64, 128) or per row (0).  y * scale is the
+    norm's value.  Returns (y, scales, r, rstd)."""
+    torch = _torch()
+    dev, code, rcode, rows, D, stride, r, rstd = _norm_args(x, weight, residual, residual_out, rstd)
+    f8 = torch.float8_e4m3fn
+    if group not in (0, 32, 64, 128):
+        raise ValueError("group must be 0, 32, 64 or 128, got %r" % (group,))
+    y = torch.empty(x.shape, dtype=f8, device=dev) if y is None else _check(y, "y", tuple(x.shape), f8, dev)
+    ss = tuple(x.shape[:-1]) + (-(-D // group) if group else 1,)
+    scales = torch.empty(ss, dtype=torch.float32, device=dev) if scales is None else \
+        _check(scales, "scales", ss, torch.float32, dev)
+    with torch.cuda.device(dev):
+        _call("mb_rms_norm_fp8", _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scales), _ptr(r), _ptr(rstd), rows,
+              D, stride, group, float(eps), code, rcode, _stream(dev))
+    return y, scales, x if r is None else r, rstd
+
+
+def mb_rms_norm_bwd(dy, r, rstd, weight=None, dr_in=None, *, dx=None, dr=None, dweight=None, ws=None):
+    """Backward of mb_rms_norm: dy (the gradient of y), r and rstd as the forward returned them, dr_in
+    (the gradient that reaches r from elsewhere, like r) or None.  Returns (dx, dr, dweight): dr is the
+    gradient of x and of residual in the dtype of r, dx the same in the dtype of dy (the very tensor
+    dr when the dtypes agree)."""
+    torch = _torch()
+    dev = _device_of(dy)
+    code, rcode = _dtype_code(dy, "dy"), _dtype_code(r, "r")
+    if rcode != code and rcode != MB_F32:
+        raise TypeError("r must be float32 or have the dtype of dy, got %s" % r.dtype)
+    if dy.dim() < 1:
+        raise ValueError("dy must have at least one axis")
+    shp, D = tuple(dy.shape), dy.shape[-1]
+    rows = dy.numel() // D if D else 0
+    _check(dy, "dy", shp, dy.dtype, dev)
+    _check(r, "r", shp, r.dtype, dev)
+    _check(rstd, "rstd", shp[:-1], torch.float32, dev)
+    _check(weight, "weight", (D,), torch.float32, dev)
+    _check(dr_in, "dr_in", shp, r.dtype, dev)
+    same = code == rcode
+    if same and dx is not None and dr is not None and dx is not dr:
+        raise ValueError("dx and dr are one tensor when dy and r have the same dtype")
+    dr = dx if same and dr is None else dr
+    dr = torch.empty(shp, dtype=r.dtype, device=dev) if dr is None else _check(dr, "dr", shp, r.dtype, dev)
+    if not same:
+        dx = torch.empty(shp, dtype=dy.dtype, device=dev) if dx is None else _check(dx, "dx", shp, dy.dtype, dev)
+    dweight = torch.empty((D,), dtype=torch.float32, device=dev) if dweight is None else \
+        _check(dweight, "dweight", (D,), torch.float32, dev)
+    ws, nws = _workspace(MB_OP_RMS_NORM_BWD, dev, ws, (rows, 1, D, 1, 1, 1, 1, 0))
+    with torch.cuda.device(dev):
+        _call("mb_rms_norm_bwd", _ptr(dy), _ptr(r), _ptr(rstd), _ptr(weight), _ptr(dr_in), None if same else _ptr(dx),
+              _ptr(dr), _ptr(dweight), rows, D, code, rcode, _ptr(ws), nws, _stream(dev))
+    return dr if same else dx, dr, dweight
+
+
+def mb_grad_norm_clip(grads, max_norm, *, eps=1e-6, out=None, norm=None, ws=None):
+    """The global 2-norm of a list of contiguous gradient tensors of one dtype (float32 or bfloat16), and
+    their scaling by min(1, max_norm / (norm + eps)), in place or into the tensors of `out`.  max_norm =
+    inf: the norm alone.  Returns (the scaled tensors, norm), norm a float32 tensor of no axes."""
+    torch = _torch()
+    grads = list(grads)
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    dev = _device_of(grads[0])
+    dt = grads[0].dtype
+    code = _dtype_code(grads[0], "grads[0]")
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError("out has %d tensors, grads %d" % (len(outs), len(grads)))
+    for i, (g, t) in enumerate(zip(grads, outs)):
+        _check(g, "grads[%d]" % i, tuple(g.shape), dt, dev)
+        if t is not g:
+            _check(t, "out[%d]" % i, tuple(g.shape), dt, dev)
+    norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else _check(norm, "norm", (), torch.float32, dev)
+    n = len(grads)
+    gp = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
+    op = gp if out is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
+    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    ws, nws = _workspace(MB_OP_GRAD_NORM_CLIP, dev, ws, (n, 1, 1, 1, 1, 1, 1, 0))
+    with torch.cuda.device(dev):
+        _call("mb_grad_norm_clip", ctypes.cast(gp, _vp), ctypes.cast(op, _vp), ctypes.cast(sizes, _vp), n, float(max_norm),
+              float(eps), _ptr(norm), code, _ptr(ws), nws, _stream(dev))
+    return outs, norm

@@ -1,0 +1,217 @@
+// gradclip.hip -- the global 2-norm of many gradient tensors, and their clipping.
+//
+//     norm = sqrt(sum over all tensors and elements of g^2)
+//     out  = g * min(1, max_norm / (norm + eps))
+//
+// Bound by HBM: the gradients are read once for the norm and once more, with a
+// write, for the scaling.  Each square is summed in fp64: no fp32 gradient's
+// square overflows or vanishes there, and the two extra fp64 operations an element
+// cost less than its load.  A workgroup's sum goes to its own place in the
+// workspace and every reader adds these in the same order: results do not depend on
+// the order in which workgroups run.
+//
+// The tensors' addresses travel as kernel arguments (kPer of them a launch, so a
+// captured graph holds them itself) into a table in the workspace that the two
+// passes read.
+#include "mb_internal.h"
+
+namespace mb {
+namespace {
+
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+constexpr int kPer = 120;             // tensors whose table entries fit one launch's arguments
+constexpr int kMaxTensors = 1 << 16;
+constexpr int64_t kPiece = 16384;     // elements a workgroup takes at a time
+constexpr int kGrid = 2048;           // partial sums at most
+
+struct Entry {
+    const void* g;
+    void* o;
+    int64_t n;
+    int64_t first;      // pieces of the tensors before this one
+};
+
+struct Batch {
+    Entry e[kPer];
+};
+
+__global__ void k_table(Batch b, Entry* table, int at, int n) {
+    // each entry is four words of eight bytes
+    const int64_t* src = (const int64_t*)b.e;
+    int64_t* dst = (int64_t*)(table + at);
+    for (int i = threadIdx.x; i < n * 4; i += blockDim.x) dst[i] = src[i];
+}
+
+// The tensor that piece p belongs to: the last whose first piece is not behind p.
+__device__ __forceinline__ int tensor_of(const Entry* t, int n, int64_t p) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t[mid].first <= p) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ double sum_block(double v, double* lds) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = lds[0] + lds[1] + lds[2] + lds[3];
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ double sum_piece(const T* g, int n) {
+    double s0 = 0.0, s1 = 0.0;
+    constexpr int V = 16 / sizeof(T);
+    int i = 0;
+    if (((uintptr_t)g & 15) == 0) {
+        const int nv = n / V;
+        for (int k = threadIdx.x; k < nv; k += 256) {
+            const u4 t = reinterpret_cast<const u4*>(g)[k];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 4) {
+                    const double a = (double)__uint_as_float(t[j]);
+                    (j & 1 ? s1 : s0) += a * a;
+                } else {
+                    // the square of a bf16 value is exact in fp32 but may leave its range
+                    const double a = (double)__uint_as_float(t[j] << 16), b = (double)__uint_as_float(t[j] & 0xffff0000u);
+                    s0 += a * a;
+                    s1 += b * b;
+                }
+            }
+        }
+        i = nv * V;
+    }
+    for (int k = i + threadIdx.x; k < n; k += 256) {
+        const double a = (double)to_f32(g[k]);
+        s0 += a * a;
+    }
+    return s0 + s1;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_norm_parts(const Entry* __restrict__ t, int n, int64_t pieces, double* __restrict__ part) {
+    __shared__ double lds[4];
+    double s = 0.0;
+    for (int64_t p = blockIdx.x; p < pieces; p += gridDim.x) {
+        const Entry e = t[tensor_of(t, n, p)];
+        const int64_t at = (p - e.first) * kPiece;
+        const int64_t left = e.n - at;
+        s += sum_piece((const T*)e.g + at, (int)(left < kPiece ? left : kPiece));
+    }
+    s = sum_block(s, lds);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+template <typename T>
+__device__ __forceinline__ void scale_piece(const T* g, T* o, int n, float f) {
+    constexpr int V = 16 / sizeof(T);
+    int i = 0;
+    if ((((uintptr_t)g | (uintptr_t)o) & 15) == 0) {
+        const int nv = n / V;
+        for (int k = threadIdx.x; k < nv; k += 256) {
+            u4 t = reinterpret_cast<const u4*>(g)[k];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(T) == 4) {
+                    t[j] = __float_as_uint(__uint_as_float(t[j]) * f);
+                } else {
+                    const float a = __uint_as_float(t[j] << 16) * f, b = __uint_as_float(t[j] & 0xffff0000u) * f;
+                    t[j] = (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
+                }
+            }
+            reinterpret_cast<u4*>(o)[k] = t;
+        }
+        i = nv * V;
+    }
+    for (int k = i + threadIdx.x; k < n; k += 256) store_out(o + k, to_f32(g[k]) * f);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_clip(const Entry* __restrict__ t, int n, int64_t pieces, const double* __restrict__ part,
+                                              int parts, float* __restrict__ norm_out, float max_norm, float eps) {
+    __shared__ double lds[4];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < parts; i += 256) s += part[i];
+    const float norm = (float)sqrt(sum_block(s, lds));
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
+    const float c = max_norm / (norm + eps);
+    const float f = c > 1.0f ? 1.0f : c;              // NaN stays
+    for (int64_t p = blockIdx.x; p < pieces; p += gridDim.x) {
+        const Entry e = t[tensor_of(t, n, p)];
+        if (f == 1.0f && e.g == e.o) continue;        // in place and nothing to scale
+        const int64_t at = (p - e.first) * kPiece;
+        const int64_t left = e.n - at;
+        scale_piece((const T*)e.g + at, (T*)e.o + at, (int)(left < kPiece ? left : kPiece), f);
+    }
+}
+
+size_t table_bytes(int64_t n) { return ((size_t)n * sizeof(Entry) + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t grad_clip_workspace(int64_t n) {
+    if (n < 1 || n > kMaxTensors) return 0;
+    return table_bytes(n) + kGrid * sizeof(double);
+}
+
+}  // namespace mb
+
+extern "C" mb_status mb_grad_norm_clip(const void* const* grads, void* const* outs, const int64_t* sizes, int64_t n,
+                                       float max_norm, float eps, float* norm, mb_dtype dtype, void* ws,
+                                       size_t ws_bytes, hipStream_t stream) {
+    using namespace mb;
+    if (!dtype_ok(dtype)) return MB_ERR_DTYPE;
+    if (n < 0 || n > kMaxTensors || !(max_norm >= 0.0f) || !(eps >= 0.0f) || eps > 3.0e38f) return MB_ERR_SHAPE;
+    if (!norm || (n > 0 && (!grads || !sizes))) return MB_ERR_NULL;
+    const size_t es = dtype_size(dtype);
+    if ((uintptr_t)norm & 3) return MB_ERR_ALIGN;
+    const size_t need = grad_clip_workspace(n);
+    if (n > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 255))) return MB_ERR_WORKSPACE;
+    int64_t total = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (sizes[i] < 0 || sizes[i] > ((int64_t)1 << 40)) return MB_ERR_SHAPE;
+        if (sizes[i] == 0) continue;
+        const void* o = outs ? outs[i] : grads[i];
+        if (!grads[i] || !o) return MB_ERR_NULL;
+        if ((uintptr_t)grads[i] % es || (uintptr_t)o % es) return MB_ERR_ALIGN;
+        const size_t b = (size_t)sizes[i] * es;
+        if ((o != grads[i] && overlaps(o, b, grads[i], b)) || overlaps(o, b, norm, 4) || overlaps(grads[i], b, norm, 4) ||
+            overlaps(ws, need, o, b) || overlaps(ws, need, grads[i], b))
+            return MB_ERR_ALIAS;
+        total += (sizes[i] + kPiece - 1) / kPiece;
+    }
+    if (n > 0 && overlaps(ws, need, norm, 4)) return MB_ERR_ALIAS;
+    if (total == 0) return copy_state(nullptr, norm, 1, stream);
+    Entry* table = (Entry*)ws;
+    double* part = (double*)((char*)ws + table_bytes(n));
+    int used = 0, at = 0;
+    int64_t pieces = 0;
+    Batch b;
+    for (int64_t i = 0; i < n; ++i) {
+        if (sizes[i]) {
+            b.e[used++] = Entry{grads[i], outs ? outs[i] : const_cast<void*>(grads[i]), sizes[i], pieces};
+            pieces += (sizes[i] + kPiece - 1) / kPiece;
+        }
+        if (used == kPer || (i == n - 1 && used)) {
+            hipLaunchKernelGGL(k_table, dim3(1), dim3(256), 0, stream, b, table, at, used);
+            mb_status st = check_launch();
+            if (st != MB_OK) return st;
+            at += used;
+            used = 0;
+        }
+    }
+    const int grid = (int)(pieces < kGrid ? pieces : kGrid);
+    if (dtype == MB_F32) {
+        hipLaunchKernelGGL(k_norm_parts<float>, dim3(grid), dim3(256), 0, stream, table, at, pieces, part);
+        hipLaunchKernelGGL(k_clip<float>, dim3(grid), dim3(256), 0, stream, table, at, pieces, part, grid, norm, max_norm, eps);
+    } else {
+        hipLaunchKernelGGL(k_norm_parts<bf16>, dim3(grid), dim3(256), 0, stream, table, at, pieces, part);
+        hipLaunchKernelGGL(k_clip<bf16>, dim3(grid), dim3(256), 0, stream, table, at, pieces, part, grid, norm, max_norm, eps);
+    }
+    return check_launch();
+}

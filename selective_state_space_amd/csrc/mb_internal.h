@@ -64,6 +64,14 @@ size_t trap_bwd_workspace(int64_t batch, int64_t L, int64_t H, int64_t P, int64_
 // Workspace bytes of the Mamba-2 SSD backward (0 for unsupported sizes).
 size_t ssd_bwd_workspace(int64_t batch, int64_t L, int64_t H, int64_t P, int64_t G, int64_t N);
 
+// Workspace bytes of linear attention, forward and backward (0 for unsupported sizes).
+size_t linear_attn_workspace(int64_t n_seq, int64_t T, int64_t H, int64_t G, int64_t Dk, int64_t Dv);
+size_t linear_attn_bwd_workspace(int64_t n_seq, int64_t T, int64_t H, int64_t G, int64_t Dk, int64_t Dv);
+
+// Workspace bytes of the norm's backward and of gradient clipping.
+size_t rms_norm_bwd_workspace(int64_t rows, int64_t D);
+size_t grad_clip_workspace(int64_t n);
+
 // Copy h0 (or zeros) into h_out; used for zero-length sequences.
 mb_status copy_state(const float* h0, float* h_out, int64_t n, hipStream_t stream);
 

@@ -1,0 +1,523 @@
+// rmsnorm.hip -- root-mean-square norm with the residual's addition, its 8-bit
+// output form, and its backward.
+//
+//     r = x + residual,  rstd = 1 / sqrt(mean_d r_d^2 + eps),  y_d = r_d rstd w_d
+//     8 bits: q_d = e4m3(y_d / s), s = max(amax over the group's |y|, 2^-96) / 448
+//     backward: g = dy w, xh = r rstd:
+//         dr = dr_in + rstd (g - xh mean_d(g xh)),  dw_d = sum_rows dy_d xh_d
+//
+// All three are bound by HBM: a row is read once, kept in registers between the
+// sum of squares and the scaling, and written once.  A row belongs to one wave
+// (D <= 2048), a workgroup of 256 (D <= 8192) or of 1024 threads (D <= 16384);
+// a thread holds E of its elements as E / VEC vectors, lanes side by side.
+#include "mb_internal.h"
+
+namespace mb {
+namespace {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kAmaxMin = 0x1p-96f;     // keeps 1 / scale and y / scale in range for a group of zeros
+constexpr int64_t kMaxD = 16384;
+
+template <int VEC>
+__device__ __forceinline__ void load_vec(const float* p, float* v) {
+    if constexpr (VEC == 1) {
+        v[0] = *p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            f4 t = reinterpret_cast<const f4*>(p)[i];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * i + k] = t[k];
+        }
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void load_vec(const bf16* p, float* v) {
+    if constexpr (VEC == 1) {
+        v[0] = to_f32(*p);
+    } else {
+        static_assert(VEC == 8, "bf16 vectors hold eight elements");
+        u4 t = *reinterpret_cast<const u4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(t[i] << 16);
+            v[2 * i + 1] = __uint_as_float(t[i] & 0xffff0000u);
+        }
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const float* v) {
+    if constexpr (VEC == 1) {
+        *p = v[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i)
+            reinterpret_cast<f4*>(p)[i] = f4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void store_vec(bf16* p, const float* v) {
+    if constexpr (VEC == 1) {
+        *p = f32_to_bf16(v[0]);
+    } else {
+        u4 t;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t[i] = (uint32_t)f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
+        *reinterpret_cast<u4*>(p) = t;
+    }
+}
+
+// Sum over the TPR threads of a row, the same value in all of them.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    if constexpr (TPR > 64) {
+        __syncthreads();                       // the previous use of lds is over
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) v += lds[i];
+    }
+    return v;
+}
+
+// Maximum over the row of absolute values given as bits: NaN's bits are the largest, so NaN wins.
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* lds) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+    if constexpr (TPR > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0;
+#pragma unroll
+        for (int i = 0; i < TPR / 64; ++i) v = max(v, lds[i]);
+    }
+    return v;
+}
+
+// Scale of a group from its amax bits (NaN stays NaN).
+__device__ __forceinline__ float group_scale(uint32_t amax) {
+    float a = __uint_as_float(amax);
+    a = a < kAmaxMin ? kAmaxMin : a;
+    return a / kE4m3Max;
+}
+
+// v / scale: the reciprocal's product with one residual correction is the
+// correctly rounded quotient but for rare cases, so values on a border of two
+// e4m3 steps fall as they do for the division.  An infinite scale (its group
+// then holds infinities) takes the product alone: the residual would be NaN.
+__device__ __forceinline__ float over(float v, float scale, float inv) {
+    float q = v * inv;
+    float c = fmaf(fmaf(-q, scale, v), inv, q);
+    return __builtin_isinf(scale) ? q : c;
+}
+
+struct NormArgs {
+    const void* x;
+    const void* res;
+    const float* w;
+    void* y;
+    float* scales;
+    void* r_out;
+    float* rstd;
+    int64_t rows, x_stride;
+    int D, group, ngroups;
+    float eps;
+};
+
+// MODE 0: y in the type of x.  MODE 1: e4m3 with scales.
+template <typename TX, typename TR, int VEC, int E, int TPR, int MODE>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) {
+    constexpr int NT = TPR < 256 ? 256 : TPR;
+    constexpr int ROWS = NT / TPR;
+    constexpr int NV = E / VEC;
+    __shared__ float red[16];
+    __shared__ uint32_t gmax[MODE == 1 && VEC == 1 ? 1024 : 1];
+    const int lane = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + slot;
+    const bool live = row < a.rows;
+    const TX* x = (const TX*)a.x + row * a.x_stride;
+    const TR* res = (const TR*)a.res + row * a.D;
+
+    float v[E];
+    float ss = 0.0f;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int d = (c * TPR + lane) * VEC;
+        if (live && d < a.D) {
+            load_vec<VEC>(x + d, v + c * VEC);
+            if (a.res) {
+                float t[VEC];
+                load_vec<VEC>(res + d, t);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) v[c * VEC + k] += t[k];
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[c * VEC + k] = 0.0f;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int d = (c * TPR + lane) * VEC;
+        if (a.r_out && live && d < a.D) store_vec<VEC>((TR*)a.r_out + row * a.D + d, v + c * VEC);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) ss = fmaf(v[c * VEC + k], v[c * VEC + k], ss);
+    }
+    ss = row_sum<TPR>(ss, red);
+    const float rstd = 1.0f / sqrtf(ss / (float)a.D + a.eps);
+    if (a.rstd && live && lane == 0) a.rstd[row] = rstd;
+
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int d = (c * TPR + lane) * VEC;
+        float w[VEC];
+        if (a.w && d < a.D) {
+            load_vec<VEC>(a.w + d, w);
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) w[k] = 1.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[c * VEC + k] = v[c * VEC + k] * rstd * w[k];
+        if constexpr (MODE == 0) {
+            if (live && d < a.D) store_vec<VEC>((TX*)a.y + row * a.D + d, v + c * VEC);
+        }
+    }
+    if constexpr (MODE == 1) {
+        float* scales = a.scales + row * a.ngroups;
+        uint8_t* q = (uint8_t*)a.y + row * a.D;
+        uint32_t m[NV];
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            m[c] = 0;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) m[c] = max(m[c], __float_as_uint(v[c * VEC + k]) & 0x7fffffffu);
+        }
+        if (a.group == 0) {
+            uint32_t t = 0;
+#pragma unroll
+            for (int c = 0; c < NV; ++c) t = max(t, m[c]);
+            t = row_max<TPR>(t, (uint32_t*)red);
+#pragma unroll
+            for (int c = 0; c < NV; ++c) m[c] = t;
+            if (live && lane == 0) scales[0] = group_scale(t);
+        } else if constexpr (VEC > 1) {
+            const int lanes = a.group / VEC;       // a power of two, at most 32
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                for (int o = 1; o < lanes; o <<= 1) m[c] = max(m[c], (uint32_t)__shfl_xor((int)m[c], o));
+                const int d = (c * TPR + lane) * VEC;
+                if (live && d < a.D && (lane & (lanes - 1)) == 0) scales[d / a.group] = group_scale(m[c]);
+            }
+        } else {
+            uint32_t* gm = gmax + slot * (1024 / ROWS);
+            for (int i = lane; i < a.ngroups; i += TPR) gm[i] = 0;
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                const int d = c * TPR + lane;
+                if (d < a.D) atomicMax(&gm[d / a.group], m[c]);    // a maximum: any order gives the same
+            }
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < NV; ++c) {
+                const int d = c * TPR + lane;
+                if (d < a.D) m[c] = gm[d / a.group];
+            }
+            if (live)
+                for (int i = lane; i < a.ngroups; i += TPR) scales[i] = group_scale(gm[i]);
+        }
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int d = (c * TPR + lane) * VEC;
+            const float s = group_scale(m[c]), inv = 1.0f / s;
+            if (live && d < a.D) {
+                float t[VEC];
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) t[k] = over(v[c * VEC + k], s, inv);
+                if constexpr (VEC == 1) {
+                    q[d] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[0], 0, false);
+                } else {
+                    uint32_t o[VEC / 4];
+#pragma unroll
+                    for (int k = 0; k < VEC / 4; ++k) {
+                        int p = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * k], t[4 * k + 1], 0, false);
+                        o[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * k + 2], t[4 * k + 3], p, true);
+                    }
+                    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q + d) = make_uint2(o[0], o[1]);
+                    else *reinterpret_cast<uint32_t*>(q + d) = o[0];
+                }
+            }
+        }
+    }
+}
+
+struct NormBwdArgs {
+    const void* dy;
+    const void* r;
+    const float* rstd;
+    const float* w;
+    const void* dr_in;
+    void* dx;
+    void* dr;
+    float* part;        // (gridDim.x, D) partial sums of dw, or dw itself when the grid is one workgroup
+    int64_t rows;
+    int D;
+};
+
+// A workgroup walks rows; every thread keeps its columns' share of dw in registers
+// and the rows' slots are added up in LDS at the end.
+template <typename TX, typename TR, int VEC, int E, int TPR>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm_bwd(NormBwdArgs a) {
+    constexpr int NT = TPR < 256 ? 256 : TPR;
+    constexpr int ROWS = NT / TPR;
+    constexpr int NV = E / VEC;
+    __shared__ float red[16];
+    __shared__ float dwl[ROWS > 1 ? (ROWS - 1) * TPR * E : 1];
+    const int lane = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    float dw[E], w[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) { dw[i] = 0.0f; w[i] = 1.0f; }
+    if (a.w) {
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int d = (c * TPR + lane) * VEC;
+            if (d < a.D) load_vec<VEC>(a.w + d, w + c * VEC);
+        }
+    }
+    const float inv_d = 1.0f / (float)a.D;
+    for (int64_t base = (int64_t)blockIdx.x * ROWS; base < a.rows; base += (int64_t)gridDim.x * ROWS) {
+        const int64_t row = base + slot;
+        const bool live = row < a.rows;
+        float dy[E], xh[E], in[E];
+        const float rstd = live ? a.rstd[row] : 0.0f;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int d = (c * TPR + lane) * VEC;
+            if (live && d < a.D) {
+                load_vec<VEC>((const TX*)a.dy + row * a.D + d, dy + c * VEC);
+                load_vec<VEC>((const TR*)a.r + row * a.D + d, xh + c * VEC);
+                if (a.dr_in) {
+                    load_vec<VEC>((const TR*)a.dr_in + row * a.D + d, in + c * VEC);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) in[c * VEC + k] = 0.0f;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) dy[c * VEC + k] = xh[c * VEC + k] = in[c * VEC + k] = 0.0f;
+            }
+        }
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            xh[i] *= rstd;
+            dw[i] = fmaf(dy[i], xh[i], dw[i]);
+            dy[i] *= w[i];
+            dot = fmaf(dy[i], xh[i], dot);
+        }
+        dot = row_sum<TPR>(dot, red) * inv_d;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            const int d = (c * TPR + lane) * VEC;
+            if (live && d < a.D) {
+                float o[VEC];
+#pragma unroll
+                for (int k = 0; k < VEC; ++k)
+                    o[k] = fmaf(rstd, fmaf(-xh[c * VEC + k], dot, dy[c * VEC + k]), in[c * VEC + k]);
+                if (a.dr) store_vec<VEC>((TR*)a.dr + row * a.D + d, o);
+                if (a.dx) store_vec<VEC>((TX*)a.dx + row * a.D + d, o);
+            }
+        }
+    }
+    if (!a.part) return;
+    if constexpr (ROWS > 1) {
+        if (slot > 0) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) dwl[((slot - 1) * E + i) * TPR + lane] = dw[i];
+        }
+        __syncthreads();
+        if (slot > 0) return;
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+#pragma unroll
+            for (int s = 0; s < ROWS - 1; ++s) dw[i] += dwl[(s * E + i) * TPR + lane];
+    }
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const int d = (c * TPR + lane) * VEC;
+        if (d < a.D) store_vec<VEC>(a.part + (int64_t)blockIdx.x * a.D + d, dw + c * VEC);
+    }
+}
+
+// dw = the sum of the workgroups' partial rows: 32 columns a workgroup, 8 rows at a time.
+__global__ void __launch_bounds__(256) k_dw_sum(const float* __restrict__ part, float* __restrict__ dw, int n, int D) {
+    __shared__ float red[8][33];
+    const int col = threadIdx.x & 31, sub = threadIdx.x >> 5;
+    const int d = blockIdx.x * 32 + col;
+    float s = 0.0f;
+    if (d < D)
+        for (int i = sub; i < n; i += 8) s += part[(int64_t)i * D + d];
+    red[sub][col] = s;
+    __syncthreads();
+    if (sub == 0 && d < D) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += red[i][col];
+        dw[d] = s;
+    }
+}
+
+inline bool vec_ok(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+template <typename TX, typename TR, int MODE, int VEC>
+void launch_norm(const NormArgs& a, hipStream_t s) {
+    const int per = a.D;
+    auto go = [&](auto kern, int nt, int rows) {
+        hipLaunchKernelGGL(kern, dim3((unsigned)((a.rows + rows - 1) / rows)), dim3(nt), 0, s, a);
+    };
+    if (per <= 64 * 8) go(k_rms_norm<TX, TR, VEC, 8, 64, MODE>, 256, 4);
+    else if (per <= 64 * 16) go(k_rms_norm<TX, TR, VEC, 16, 64, MODE>, 256, 4);
+    else if (per <= 64 * 32) go(k_rms_norm<TX, TR, VEC, 32, 64, MODE>, 256, 4);
+    else if (per <= 256 * 16) go(k_rms_norm<TX, TR, VEC, 16, 256, MODE>, 256, 1);
+    else if (per <= 256 * 32) go(k_rms_norm<TX, TR, VEC, 32, 256, MODE>, 256, 1);
+    else go(k_rms_norm<TX, TR, VEC, 16, 1024, MODE>, 1024, 1);
+}
+
+template <int MODE>
+mb_status norm(const void* x, const void* res, const float* w, void* y, float* scales, void* r_out, float* rstd,
+               int64_t rows, int64_t D, int64_t x_stride, int64_t group, float eps, mb_dtype dtype, mb_dtype rdtype,
+               hipStream_t stream) {
+    if (!dtype_ok(dtype) || !dtype_ok(rdtype) || (rdtype == MB_BF16 && dtype == MB_F32)) return MB_ERR_DTYPE;
+    if (rows < 0 || D < 1 || D > kMaxD || x_stride < D || !(eps >= 0.0f) || eps > 3.0e38f) return MB_ERR_SHAPE;
+    if (rows > (int64_t)1 << 30) return MB_ERR_SHAPE;
+    if (MODE == 1 && group != 0 && group != 32 && group != 64 && group != 128) return MB_ERR_SHAPE;
+    if (rows == 0) return MB_OK;
+    if (!x || !y || (MODE == 1 && !scales)) return MB_ERR_NULL;
+    const size_t ex = dtype_size(dtype), er = dtype_size(rdtype);
+    const int64_t ng = group ? (D + group - 1) / group : 1;
+    const size_t n = (size_t)rows * D;
+    const size_t nx = ((size_t)(rows - 1) * x_stride + D) * ex;
+    if (((uintptr_t)x % ex) || ((uintptr_t)res % er) || ((uintptr_t)r_out % er) || (MODE == 0 && (uintptr_t)y % ex) ||
+        ((uintptr_t)w & 3) || ((uintptr_t)scales & 3) || ((uintptr_t)rstd & 3))
+        return MB_ERR_ALIGN;
+    const Span ins[3] = {{x, nx}, {res, n * er}, {w, (size_t)D * 4}};
+    Span outs[4] = {{y, n * (MODE == 1 ? 1 : ex)}, {r_out, n * er}, {rstd, (size_t)rows * 4}, {scales, (size_t)rows * ng * 4}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 3; ++j) {
+            if (i == 1 && j == 1 && r_out == res) continue;      // the residual stream is updated in place
+            if (overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return MB_ERR_ALIAS;
+        }
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return MB_ERR_ALIAS;
+    }
+    NormArgs a{x, res, w, y, scales, r_out, rstd, rows, x_stride, (int)D, (int)group, (int)ng, eps};
+    const int V = dtype == MB_BF16 ? 8 : 4;
+    const bool vec = D % V == 0 && x_stride % V == 0 && vec_ok(x) && vec_ok(res) && vec_ok(w) && vec_ok(y) && vec_ok(r_out);
+    if (dtype == MB_F32)
+        vec ? launch_norm<float, float, MODE, 4>(a, stream) : launch_norm<float, float, MODE, 1>(a, stream);
+    else if (rdtype == MB_F32)
+        vec ? launch_norm<bf16, float, MODE, 8>(a, stream) : launch_norm<bf16, float, MODE, 1>(a, stream);
+    else
+        vec ? launch_norm<bf16, bf16, MODE, 8>(a, stream) : launch_norm<bf16, bf16, MODE, 1>(a, stream);
+    return check_launch();
+}
+
+// Workgroups of the backward: enough to fill the device twice, so that the partial
+// rows of dw stay few.
+int bwd_grid(int64_t rows, int64_t D) {
+    const int64_t per = D <= 2048 ? 4 : 1;
+    const int64_t want = (rows + per - 1) / per, cap = 2 * (int64_t)device_cu_count();
+    return (int)(want < cap ? want : cap);
+}
+
+template <typename TX, typename TR, int VEC>
+void launch_bwd(const NormBwdArgs& a, int grid, hipStream_t s) {
+    auto go = [&](auto kern, int nt) { hipLaunchKernelGGL(kern, dim3(grid), dim3(nt), 0, s, a); };
+    if (a.D <= 64 * 8) go(k_rms_norm_bwd<TX, TR, VEC, 8, 64>, 256);
+    else if (a.D <= 64 * 16) go(k_rms_norm_bwd<TX, TR, VEC, 16, 64>, 256);
+    else if (a.D <= 64 * 32) go(k_rms_norm_bwd<TX, TR, VEC, 32, 64>, 256);
+    else if (a.D <= 256 * 16) go(k_rms_norm_bwd<TX, TR, VEC, 16, 256>, 256);
+    else if (a.D <= 256 * 32) go(k_rms_norm_bwd<TX, TR, VEC, 32, 256>, 256);
+    else go(k_rms_norm_bwd<TX, TR, VEC, 16, 1024>, 1024);
+}
+
+}  // namespace
+
+size_t rms_norm_bwd_workspace(int64_t rows, int64_t D) {
+    if (rows < 1 || D < 1 || D > kMaxD || rows > (int64_t)1 << 30) return 0;
+    const int g = bwd_grid(rows, D);
+    return g == 1 ? 0 : ((size_t)g * D * 4 + 255) / 256 * 256;
+}
+
+}  // namespace mb
+
+extern "C" mb_status mb_rms_norm(const void* x, const void* residual, const float* weight, void* y, void* residual_out,
+                                 float* rstd, int64_t rows, int64_t D, int64_t x_stride, float eps, mb_dtype dtype,
+                                 mb_dtype residual_dtype, hipStream_t stream) {
+    return mb::norm<0>(x, residual, weight, y, nullptr, residual_out, rstd, rows, D, x_stride, 0, eps, dtype,
+                       residual_dtype, stream);
+}
+
+extern "C" mb_status mb_rms_norm_fp8(const void* x, const void* residual, const float* weight, void* y, float* scales,
+                                     void* residual_out, float* rstd, int64_t rows, int64_t D, int64_t x_stride,
+                                     int64_t group, float eps, mb_dtype dtype, mb_dtype residual_dtype,
+                                     hipStream_t stream) {
+    return mb::norm<1>(x, residual, weight, y, scales, residual_out, rstd, rows, D, x_stride, group, eps, dtype,
+                       residual_dtype, stream);
+}
+
+extern "C" mb_status mb_rms_norm_bwd(const void* dy, const void* r, const float* rstd, const float* weight,
+                                     const void* dr_in, void* dx, void* dr, float* dweight, int64_t rows, int64_t D,
+                                     mb_dtype dtype, mb_dtype residual_dtype, void* ws, size_t ws_bytes,
+                                     hipStream_t stream) {
+    using namespace mb;
+    if (!dtype_ok(dtype) || !dtype_ok(residual_dtype) || (residual_dtype == MB_BF16 && dtype == MB_F32)) return MB_ERR_DTYPE;
+    if (rows < 0 || D < 1 || D > kMaxD || rows > (int64_t)1 << 30) return MB_ERR_SHAPE;
+    if (rows == 0) return dweight ? copy_state(nullptr, dweight, D, stream) : MB_OK;
+    if (!dy || !r || !rstd || (!dx && !dr && !dweight)) return MB_ERR_NULL;
+    const size_t ex = dtype_size(dtype), er = dtype_size(residual_dtype), n = (size_t)rows * D;
+    if (((uintptr_t)dy % ex) || ((uintptr_t)dx % ex) || ((uintptr_t)r % er) || ((uintptr_t)dr_in % er) ||
+        ((uintptr_t)dr % er) || ((uintptr_t)rstd & 3) || ((uintptr_t)weight & 3) || ((uintptr_t)dweight & 3))
+        return MB_ERR_ALIGN;
+    const size_t need = dweight ? rms_norm_bwd_workspace(rows, D) : 0;
+    if (need && (!ws || ws_bytes < need || ((uintptr_t)ws & 255))) return MB_ERR_WORKSPACE;
+    const Span ins[5] = {{dy, n * ex}, {r, n * er}, {rstd, (size_t)rows * 4}, {weight, (size_t)D * 4}, {dr_in, n * er}};
+    const Span outs[4] = {{dx, n * ex}, {dr, n * er}, {dweight, (size_t)D * 4}, {need ? ws : nullptr, need}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 5; ++j) {
+            if (i == 1 && j == 4 && dr == dr_in) continue;      // the stream's gradient is updated in place
+            if (overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return MB_ERR_ALIAS;
+        }
+        for (int j = 0; j < i; ++j)
+            if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return MB_ERR_ALIAS;
+    }
+    const int grid = bwd_grid(rows, D);
+    float* part = !dweight ? nullptr : need ? (float*)ws : dweight;
+    NormBwdArgs a{dy, r, rstd, weight, dr_in, dx, dr, part, rows, (int)D};
+    const int V = dtype == MB_BF16 ? 8 : 4;
+    const bool vec = D % V == 0 && vec_ok(dy) && vec_ok(r) && vec_ok(weight) && vec_ok(dr_in) && vec_ok(dx) && vec_ok(dr) &&
+                     vec_ok(part);
+    if (dtype == MB_F32)
+        vec ? launch_bwd<float, float, 4>(a, grid, stream) : launch_bwd<float, float, 1>(a, grid, stream);
+    else if (residual_dtype == MB_F32)
+        vec ? launch_bwd<bf16, float, 8>(a, grid, stream) : launch_bwd<bf16, float, 1>(a, grid, stream);
+    else
+        vec ? launch_bwd<bf16, bf16, 8>(a, grid, stream) : launch_bwd<bf16, bf16, 1>(a, grid, stream);
+    mb_status st = check_launch();
+    if (st != MB_OK || !need) return st;
+    hipLaunchKernelGGL(k_dw_sum, dim3((unsigned)((D + 31) / 32)), dim3(256), 0, stream, (const float*)ws, dweight, grid, (int)D);
+    return check_launch();
+}

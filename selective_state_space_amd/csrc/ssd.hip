@@ -3268,6 +3268,12 @@ extern "C" size_t mb_workspace_size(mb_op op, int64_t batch, int64_t L, int64_t 
                                     int64_t G, int64_t N, int64_t R, int64_t chunk) {
     (void)chunk;
     if (op == MB_OP_SSM_STEP) return 0;
+    // norm backward: (rows, D) travel as (batch, H); clipping: the number of tensors as batch
+    if (op == MB_OP_RMS_NORM_BWD) return rms_norm_bwd_workspace(batch, H);
+    if (op == MB_OP_GRAD_NORM_CLIP) return grad_clip_workspace(batch);
+    // linear attention: (n_seq, T, H, Dv, G, Dk) travel as (batch, L, H, P, G, N)
+    if (op == MB_OP_LINEAR_ATTN) return linear_attn_workspace(batch, L, H, G, N, P);
+    if (op == MB_OP_LINEAR_ATTN_BWD) return linear_attn_bwd_workspace(batch, L, H, G, N, P);
     // Mamba-1 scan: the sizes (batch, L, D, N) travel as (batch, L, H, N)
     if (op == MB_OP_SELECTIVE_SCAN) return m1_scan_workspace(batch, L, H, N);
     if (op == MB_OP_SSD_CHUNKED_BWD) return ssd_bwd_workspace(batch, L, H, P, G, N);
