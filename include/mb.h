@@ -581,8 +581,8 @@ mb_status mb_ssd_chunked_bwd(const float* X, const float* logdecay, const float*
  *     o_t = scale S_t^T q_t[h]
  *   q, o        : (T, H, Dk), (T, H, Dv)  dtype   the tokens of all sequences, one after another
  *   k, v        : (T, G, Dk), (T, G, Dv)  dtype
- *   q_stride, k_stride, v_stride : elements between tokens, at least H*Dk, G*Dk, G*Dv:
- *                 q, k and v may be columns of one projection's output.  o is contiguous.
+ *   q_stride, k_stride, v_stride : elements between tokens, at least H*Dk, G*Dk, G*Dv and below
+ *                 2^22: q, k and v may be columns of one projection's output.  o is contiguous.
  *   log_decay   : (H) fp32, <= 0 in use (-inf: no memory)
  *   cu_seqlens  : (n_seq + 1) int32, nondecreasing: sequence s holds tokens cu_seqlens[s] to
  *                 cu_seqlens[s+1] - 1, any length from zero; rows of o outside all sequences are

@@ -10,6 +10,7 @@ If the library is missing the first call raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -142,15 +143,21 @@ def mb_status_str(status: int) -> str:
 
 
 def mb_workspace_size(op, batch, L, H, P, G, N, R=1, chunk=0) -> int:
-    return int(load_library().mb_workspace_size(int(op), batch, L, H, P, G, N, R, chunk))
+    return (_lib or load_library()).mb_workspace_size(op, batch, L, H, P, G, N, R, chunk)
 
 
 # ----------------------------------------------------------------------------
 # marshalling helpers
 # ----------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t, name):
@@ -170,9 +177,9 @@ def _check(t, name, shape, dtype, device):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -180,18 +187,27 @@ def _check(t, name, shape, dtype, device):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    torch = _torch()
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the handle alone: a torch.cuda.Stream object costs over a microsecond a call
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _call(fn, *args):
-    st = getattr(load_library(), fn)(*args)
+    st = getattr(_lib or load_library(), fn)(*args)
     if st != 0:
         raise MBError(fn, st)
+
+
+def _call_on(device, fn, *args):
+    """_call with `device` current, which the library launches on."""
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        return _call(fn, *args, _stream(device))
+    with torch.cuda.device(device):
+        return _call(fn, *args, _stream(device))
 
 
 def _device_of(t):
@@ -208,6 +224,14 @@ def _workspace(op, device, ws, dims):
     if ws.device != device or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % device)
     return ws, ws.numel() * ws.element_size()
+
+
+def _scratch(op, device, ws, dims):
+    """_workspace that allocates nothing where the call needs none."""
+    if ws is None:
+        need = mb_workspace_size(op, *dims)
+        return (_torch().empty(need, dtype=_torch().uint8, device=device), need) if need else (None, 0)
+    return _workspace(op, device, ws, dims)
 
 
 # ----------------------------------------------------------------------------
@@ -867,11 +891,10 @@ def mb_linear_attn(q, k, v, log_decay, *, scale=None, cu_seqlens=None, h0=None, 
     if h_out is None:
         h_out = h0 if slots is not None else torch.empty(hs, dtype=f32, device=dev)
     _check(h_out, "h_out", hs, f32, dev)
-    ws, nws = _workspace(MB_OP_LINEAR_ATTN, dev, ws, (n, T, H, Dv, G, Dk, 1, 0))
-    with torch.cuda.device(dev):
-        _call("mb_linear_attn", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), _ptr(h0), _ptr(has_h0),
-              _ptr(slots), _ptr(o), _ptr(h_out), n, T, H, G, Dk, Dv, n_slots, *st, Dk ** -0.5 if scale is None else scale,
-              code, _ptr(ws), nws, _stream(dev))
+    ws, nws = _scratch(MB_OP_LINEAR_ATTN, dev, ws, (n, T, H, Dv, G, Dk, 1, 0))
+    _call_on(dev, "mb_linear_attn", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), _ptr(h0), _ptr(has_h0),
+             _ptr(slots), _ptr(o), _ptr(h_out), n, T, H, G, Dk, Dv, n_slots, *st, Dk ** -0.5 if scale is None else scale,
+             code, _ptr(ws), nws)
     return o, h_out
 
 
@@ -893,9 +916,8 @@ def mb_linear_attn_step(q, k, v, log_decay, h, *, scale=None, slots=None, o=None
     _check(h, "h", hs, torch.float32, dev)
     h_out = h if h_out is None else _check(h_out, "h_out", hs, torch.float32, dev)
     o = torch.empty((n, H, Dv), dtype=q.dtype, device=dev) if o is None else _check(o, "o", (n, H, Dv), q.dtype, dev)
-    with torch.cuda.device(dev):
-        _call("mb_linear_attn_step", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(slots), _ptr(h), _ptr(h_out), _ptr(o),
-              n, H, G, Dk, Dv, n_slots, *st, Dk ** -0.5 if scale is None else scale, code, _stream(dev))
+    _call_on(dev, "mb_linear_attn_step", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(slots), _ptr(h), _ptr(h_out), _ptr(o),
+             n, H, G, Dk, Dv, n_slots, *st, Dk ** -0.5 if scale is None else scale, code)
     return o, h_out
 
 
@@ -914,11 +936,10 @@ def mb_linear_attn_bwd(q, k, v, log_decay, do, *, scale=None, cu_seqlens=None, h
     for t, name, shp, d in ((dq, "dq", lead + (H, Dk), dt), (dk, "dk", lead + (G, Dk), dt), (dv, "dv", lead + (G, Dv), dt),
                             (dh0, "dh0", hs, f32)):
         out.append(torch.empty(shp, dtype=d, device=dev) if t is None else _check(t, name, shp, d, dev))
-    ws, nws = _workspace(MB_OP_LINEAR_ATTN_BWD, dev, ws, (n, T, H, Dv, G, Dk, 1, 0))
-    with torch.cuda.device(dev):
-        _call("mb_linear_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), _ptr(h0), _ptr(do),
-              _ptr(dh_out), *[_ptr(t) for t in out], n, T, H, G, Dk, Dv, *st, Dk ** -0.5 if scale is None else scale, code,
-              _ptr(ws), nws, _stream(dev))
+    ws, nws = _scratch(MB_OP_LINEAR_ATTN_BWD, dev, ws, (n, T, H, Dv, G, Dk, 1, 0))
+    _call_on(dev, "mb_linear_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), _ptr(h0), _ptr(do),
+             _ptr(dh_out), *[_ptr(t) for t in out], n, T, H, G, Dk, Dv, *st, Dk ** -0.5 if scale is None else scale, code,
+             _ptr(ws), nws)
     return tuple(out)
 
 
@@ -962,9 +983,8 @@ def mb_rms_norm(x, weight=None, residual=None, *, eps=1e-5, y=None, residual_out
     torch = _torch()
     dev, code, rcode, rows, D, stride, r, rstd = _norm_args(x, weight, residual, residual_out, rstd)
     y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else _check(y, "y", tuple(x.shape), x.dtype, dev)
-    with torch.cuda.device(dev):
-        _call("mb_rms_norm", _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(r), _ptr(rstd), rows, D, stride,
-              float(eps), code, rcode, _stream(dev))
+    _call_on(dev, "mb_rms_norm", _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(r), _ptr(rstd), rows, D, stride,
+             float(eps), code, rcode)
     return y, x if r is None else r, rstd
 
 
@@ -982,9 +1002,8 @@ def mb_rms_norm_fp8(x, weight=None, residual=None, *, group=0, eps=1e-5, y=None,
     ss = tuple(x.shape[:-1]) + (-(-D // group) if group else 1,)
     scales = torch.empty(ss, dtype=torch.float32, device=dev) if scales is None else \
         _check(scales, "scales", ss, torch.float32, dev)
-    with torch.cuda.device(dev):
-        _call("mb_rms_norm_fp8", _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scales), _ptr(r), _ptr(rstd), rows,
-              D, stride, group, float(eps), code, rcode, _stream(dev))
+    _call_on(dev, "mb_rms_norm_fp8", _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scales), _ptr(r), _ptr(rstd), rows,
+             D, stride, group, float(eps), code, rcode)
     return y, scales, x if r is None else r, rstd
 
 
@@ -1016,10 +1035,9 @@ def mb_rms_norm_bwd(dy, r, rstd, weight=None, dr_in=None, *, dx=None, dr=None, d
         dx = torch.empty(shp, dtype=dy.dtype, device=dev) if dx is None else _check(dx, "dx", shp, dy.dtype, dev)
     dweight = torch.empty((D,), dtype=torch.float32, device=dev) if dweight is None else \
         _check(dweight, "dweight", (D,), torch.float32, dev)
-    ws, nws = _workspace(MB_OP_RMS_NORM_BWD, dev, ws, (rows, 1, D, 1, 1, 1, 1, 0))
-    with torch.cuda.device(dev):
-        _call("mb_rms_norm_bwd", _ptr(dy), _ptr(r), _ptr(rstd), _ptr(weight), _ptr(dr_in), None if same else _ptr(dx),
-              _ptr(dr), _ptr(dweight), rows, D, code, rcode, _ptr(ws), nws, _stream(dev))
+    ws, nws = _scratch(MB_OP_RMS_NORM_BWD, dev, ws, (rows, 1, D, 1, 1, 1, 1, 0))
+    _call_on(dev, "mb_rms_norm_bwd", _ptr(dy), _ptr(r), _ptr(rstd), _ptr(weight), _ptr(dr_in), None if same else _ptr(dx),
+             _ptr(dr), _ptr(dweight), rows, D, code, rcode, _ptr(ws), nws)
     return dr if same else dx, dr, dweight
 
 
@@ -1037,17 +1055,24 @@ def mb_grad_norm_clip(grads, max_norm, *, eps=1e-6, out=None, norm=None, ws=None
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
         raise ValueError("out has %d tensors, grads %d" % (len(outs), len(grads)))
-    for i, (g, t) in enumerate(zip(grads, outs)):
-        _check(g, "grads[%d]" % i, tuple(g.shape), dt, dev)
-        if t is not g:
-            _check(t, "out[%d]" % i, tuple(g.shape), dt, dev)
+    # one pass over the lists for each property: there may be hundreds of tensors
+    T = torch.Tensor
+    sizes = list(map(T.numel, grads))
+    for name, ts in (("grads", grads),) if out is None else (("grads", grads), ("out", outs)):
+        if set(map(T.get_device, ts)) != {dev.index}:
+            raise ValueError("%s must be on %s" % (name, dev))
+        if {t.dtype for t in ts} != {dt}:
+            raise TypeError("%s must have one dtype, %s" % (name, dt))
+        if not all(map(T.is_contiguous, ts)):
+            raise ValueError("%s must be contiguous" % name)
+    if out is not None and list(map(T.numel, outs)) != sizes:
+        raise ValueError("out must have the sizes of grads")
     norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else _check(norm, "norm", (), torch.float32, dev)
     n = len(grads)
-    gp = (ctypes.c_void_p * n)(*[g.data_ptr() for g in grads])
-    op = gp if out is None else (ctypes.c_void_p * n)(*[t.data_ptr() for t in outs])
-    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    ws, nws = _workspace(MB_OP_GRAD_NORM_CLIP, dev, ws, (n, 1, 1, 1, 1, 1, 1, 0))
-    with torch.cuda.device(dev):
-        _call("mb_grad_norm_clip", ctypes.cast(gp, _vp), ctypes.cast(op, _vp), ctypes.cast(sizes, _vp), n, float(max_norm),
-              float(eps), _ptr(norm), code, _ptr(ws), nws, _stream(dev))
+    gp = array.array("Q", map(T.data_ptr, grads))
+    op = gp if out is None else array.array("Q", map(T.data_ptr, outs))
+    sizes = array.array("q", sizes)
+    ws, nws = _scratch(MB_OP_GRAD_NORM_CLIP, dev, ws, (n, 1, 1, 1, 1, 1, 1, 0))
+    _call_on(dev, "mb_grad_norm_clip", gp.buffer_info()[0], op.buffer_info()[0], sizes.buffer_info()[0], n, float(max_norm),
+             float(eps), _ptr(norm), code, _ptr(ws), nws)
     return outs, norm

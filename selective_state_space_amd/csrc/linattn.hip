@@ -40,12 +40,19 @@ typedef float f2 __attribute__((ext_vector_type(2)));
 constexpr int kC = 64;          // tokens of a chunk
 constexpr int kV = 64;          // value columns of a workgroup
 constexpr int kMaxDim = 128;    // of keys and of values
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;     // k_la_state
+constexpr int kWalkThreads = 512; // k_la_out: four waves make outputs, four carry the state
 
-struct __attribute__((aligned(16))) PlanEntry {
-    int seq, first, len, idx;         // sequence (-1: none), its first token and length, the segment's place in it
-    int state, pad[3];                // where the segment's entering state lies
+// A segment of a sequence.  A sequence of L tokens is cut into ceil(L / target) segments (one if it
+// is empty) of equal length, rounded up to whole chunks.
+struct __attribute__((aligned(16))) Seg {
+    int seq;             // < 0: nothing to do
+    int first, len;      // the sequence's first token and length
+    int p0, n;           // the segment's first position in walking order, its tokens
+    int idx, count;      // its place among the sequence's segments
+    int state;           // where its entering state lies
 };
+__device__ __forceinline__ bool is_last(const Seg& g) { return g.idx + 1 == g.count; }
 
 struct LaArgs {
     const void* a;              // query role, key role, value role, output
@@ -55,16 +62,17 @@ struct LaArgs {
     int64_t a_ts, b_ts, c_ts, o_ts;   // elements between tokens
     int a_rep, b_rep, c_rep;          // heads that share one row of it
     int H, Da, Dv, nv;                // heads, width of a and b, width of c and o, column tiles of c
+    int share;                        // heads side by side that read the same rows of b or c
     const float* log_decay;
     float s_in, s_carry, s_up;        // factors: masked scores, carried state's product, state update
     int shift;                        // a token's own power of lambda on the carried state: 1, reversed 0
     int reversed;
     int n_seq;
-    int64_t T, L;                     // tokens in all; of a sequence when they are equal
-    int seg_len, nseg;                // segment length, segments launched
+    int T, L;                         // tokens in all; of a sequence when they are equal
+    int target, nseg;                 // longest segment, segments launched
     int per_seq;                      // segments of a sequence when lengths are equal, else 0
     const int32_t* cu;
-    const struct PlanEntry* plan;     // one for each segment; NULL: by arithmetic
+    const Seg* plan;                  // segments of many packed sequences; NULL: worked out by every workgroup
     const int2* seqs;                 // (first state, segments) of a sequence, with plan
     float* states;                    // per (state, head, column tile): a state in fragment order
     const float* h0;
@@ -75,44 +83,109 @@ struct LaArgs {
     float* h_out;
 };
 
-struct Seg {
-    int seq;             // < 0: nothing to do
-    int64_t first, len;  // the sequence's first token and length
-    int idx;             // the segment's place in it
-    int state;           // where its entering state lies
-    int64_t p0;          // its first position in walking order
-    int n;               // its tokens
-    bool last, only;
+__device__ __forceinline__ int segments_of(int len, int target) { return max((int)(((int64_t)len + target - 1) / target), 1); }
+
+// Fills in p0 and n from idx and count.
+__device__ __forceinline__ void place(Seg& g) {
+    const int even = (g.len + g.count - 1) / g.count, each = (even + kC - 1) / kC * kC;
+    g.p0 = g.idx * each;
+    g.n = max(min(each, g.len - g.p0), 0);
+}
+
+// 64 packed sequences, one a lane: their tokens, segments, and the sums of segments and states in
+// front of them.  Offsets that decrease or leave [0, T] are taken as empty sequences, so that
+// the sequences' lengths never add up to more than T, the segments to T / target + n_seq, and those of
+// sequences of several (each at most 2 len / target) to 2 T / target.
+struct Lane64 {
+    int first, len, count, at, state;
+    int reach, segs, states;       // running over the groups of 64: largest offset, segments, states
+
+    __device__ __forceinline__ void read(const LaArgs& A, int s0, int lane) {
+        const int s = s0 + lane;
+        const bool in = s < A.n_seq;
+        const int b = in ? min(max(A.cu[s], 0), A.T) : 0, e = in ? min(max(A.cu[s + 1], 0), A.T) : 0;
+        int top = max(reach, max(b, e));
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(top, o);
+            if (lane >= o) top = max(top, v);
+        }
+        const int before = __shfl_up(top, 1);
+        first = max(b, lane ? before : reach);
+        len = max(e - first, 0);
+        count = in ? segments_of(len, A.target) : 0;
+        const int own = count > 1 ? count : 0;
+        int x = count, y = own;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int u = __shfl_up(x, o), v = __shfl_up(y, o);
+            if (lane >= o) {
+                x += u;
+                y += v;
+            }
+        }
+        at = segs + x - count;
+        state = states + y - own;
+        reach = __builtin_amdgcn_readlane(top, 63);
+        segs += __builtin_amdgcn_readlane(x, 63);
+        states += __builtin_amdgcn_readlane(y, 63);
+    }
 };
 
+// Segment s of the launch, in every wave (uniform).
 __device__ __forceinline__ Seg segment(const LaArgs& A, int s) {
     Seg g;
-    if (A.plan) {
-        const PlanEntry e = A.plan[s];
-        g.seq = e.seq;
-        g.first = e.first;
-        g.len = e.len;
-        g.idx = e.idx;
-        g.state = e.state;
-    } else if (A.cu) {   // every sequence is one segment
-        const int64_t b = min((int64_t)max(A.cu[s], 0), A.T), e = min((int64_t)max(A.cu[s + 1], 0), A.T);
-        g.seq = s;
-        g.first = b;
-        g.len = max(e - b, (int64_t)0);
-        g.idx = 0;
-        g.state = 0;
+    if (A.plan) return A.plan[s];
+    g.seq = -1;
+    if (A.cu) {
+        const int lane = threadIdx.x & 63;
+        Lane64 l;
+        l.reach = l.segs = l.states = 0;
+        for (int s0 = 0; s0 < A.n_seq; s0 += 64) {
+            l.read(A, s0, lane);
+            if (s >= l.segs) continue;
+            const uint64_t hit = __ballot(l.count > 0 && l.at <= s && s < l.at + l.count);
+            const int k = __ffsll((unsigned long long)hit) - 1;
+            g.seq = s0 + k;
+            g.first = __builtin_amdgcn_readlane(l.first, k);
+            g.len = __builtin_amdgcn_readlane(l.len, k);
+            g.count = __builtin_amdgcn_readlane(l.count, k);
+            g.idx = s - __builtin_amdgcn_readlane(l.at, k);
+            g.state = __builtin_amdgcn_readlane(l.state, k) + g.idx;
+            break;
+        }
+        if (g.seq < 0) return g;
     } else {
         g.seq = s / A.per_seq;
         g.idx = s - g.seq * A.per_seq;
         g.first = g.seq * A.L;
         g.len = A.L;
+        g.count = A.per_seq;
         g.state = s;
     }
-    g.p0 = (int64_t)g.idx * A.seg_len;
-    g.n = (int)min((int64_t)A.seg_len, g.len - g.p0);
-    g.last = g.p0 + g.n >= g.len;
-    g.only = g.last && g.idx == 0;
+    place(g);
     return g;
+}
+
+// First state, segments and segment length of a sequence.
+__device__ __forceinline__ void sequence(const LaArgs& A, int seq, int& state, int& count, int& len) {
+    if (A.plan) {
+        state = A.seqs[seq].x;
+        count = A.seqs[seq].y;
+        len = min(max(A.cu[seq + 1], 0), A.T) - min(max(A.cu[seq], 0), A.T);
+    } else if (A.cu) {
+        const int lane = threadIdx.x & 63;
+        Lane64 l;
+        l.reach = l.segs = l.states = 0;
+        for (int s0 = 0; s0 <= seq; s0 += 64) l.read(A, s0, lane);
+        state = __builtin_amdgcn_readlane(l.state, seq & 63);
+        count = __builtin_amdgcn_readlane(l.count, seq & 63);
+        len = __builtin_amdgcn_readlane(l.len, seq & 63);
+    } else {
+        state = seq * A.per_seq;
+        count = A.per_seq;
+        len = A.L;
+    }
 }
 
 // Row of h0 / h_out of a sequence, or -1 where it has none.
@@ -163,50 +236,110 @@ __device__ __forceinline__ u2 tr4(const bf16* p) {
     return __builtin_bit_cast(u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p)));
 }
 
-// One row's vector of VE elements from global memory; elements at and behind `n` are zero.
+// A chunk's tokens of one tensor as a buffer: base at the lowest row, so that rows behind
+// the chunk's tokens (and, reversed, in front of them) lie outside its range and read zero.
+struct Window {
+    __amdgpu_buffer_rsrc_t r;
+    int row0, step;      // byte offsets: of the first row in walking order, and to the next one
+};
+
+// p: the chunk's first token in walking order; ts: elements between tokens; n: tokens; width: elements of a row in use.
+template <typename T>
+__device__ __forceinline__ Window window(const T* p, int64_t ts, bool reversed, int n, int width) {
+    const int b = (int)(ts * (int64_t)sizeof(T));
+    Window w;
+    w.row0 = reversed ? (n - 1) * b : 0;
+    w.step = reversed ? -b : b;
+    const char* base = (const char*)p - (reversed && n > 0 ? w.row0 : 0);
+    w.r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, n > 0 ? (n - 1) * b + width * (int)sizeof(T) : 0, 0x00027000);
+    return w;
+}
+
+// VE elements from column c of row r; columns at and behind `width` are zero.
 template <typename T, bool VEC>
-__device__ __forceinline__ u4 load_row(const T* p, int n) {
-    u4 v = {0, 0, 0, 0};
+__device__ __forceinline__ u4 load_row(const Window& w, int r, int c, int width) {
+    const uint32_t off = (uint32_t)(w.row0 + r * w.step + c * (int)sizeof(T));
+    u4 v;
     if constexpr (VEC) {
-        if (n > 0) v = *reinterpret_cast<const u4*>(p);
+        v = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(w.r, c < width ? off : 0x80000000u, 0, 0));
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < n) v[e] = __float_as_uint(p[e]);
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_raw_buffer_load_b32(w.r, c + e < width ? off + 4 * e : 0x80000000u, 0, 0);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < n) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, c + 2 * e < width ? off + 4 * e : 0x80000000u, 0, 0);
+            const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, c + 2 * e + 1 < width ? off + 4 * e + 2 : 0x80000000u, 0, 0);
+            v[e] = lo | hi << 16;
+        }
     }
     return v;
 }
 
+// Where (row, col) of an LDS tile lies, in elements.  bf16: 16-byte pieces of a row change places by
+// an exclusive-or with bits of the row, so that the 16 rows of a fragment read, the 8 rows of a
+// transposed read and the rows of a store each fall into different banks without padding (rows
+// of 128 bytes share the banks in pairs).  fp32: one piece of padding a row.
+//
+// Readers go from the place of their lane's first (row, col) to the others by `go`, a step whose
+// column bits and lane's column bits do not meet (so that adding them is an exclusive-or) and whose
+// rows change no bit of the row that the places depend on, but for row bit 2, given as `row4`.
+template <typename T, int W>
+struct Tiled {
+    static constexpr int ROW = sizeof(T) == 2 ? W : W + 4;
+    static_assert(W == 64 || W == 128, "tile widths");
+    // tokens by columns
+    static __device__ __forceinline__ int at(int r, int c) {
+        if constexpr (sizeof(T) == 4) return r * ROW + c;
+        const int b1 = (r >> 1) & 1, b2 = (r >> 2) & 1, b3 = (r >> 3) & 1;
+        const int f = W == 128 ? b2 | (r & 1) << 1 | b1 << 2 | (b2 ^ b3) << 3 : b2 | b1 << 1 | (b2 ^ b3) << 2;
+        return r * ROW + ((((c >> 3) ^ f) << 3) | (c & 7));
+    }
+    static __device__ __forceinline__ int go(int at, int rows, int cols, bool row4 = false) {
+        if constexpr (sizeof(T) == 4) return at + (rows + (row4 ? 4 : 0)) * ROW + cols;
+        return (at ^ (cols ^ (row4 ? (W == 128 ? 0x48 : 0x28) : 0))) + (rows + (row4 ? 4 : 0)) * ROW;
+    }
+    // the state's copy: value columns by state rows; the places depend on row bits 0 - 4
+    static __device__ __forceinline__ int at_state(int r, int c) {
+        if constexpr (sizeof(T) == 4) return r * ROW + c;
+        const int b1 = (r >> 1) & 1, b3 = (r >> 3) & 1, b24 = ((r >> 2) ^ (r >> 4)) & 1;
+        const int f = W == 128 ? (r & 3) | b3 << 2 | b24 << 3 : b1 | b3 << 1 | b24 << 2;
+        return r * ROW + ((((c >> 3) ^ f) << 3) | (c & 7));
+    }
+    // `flip`: the step changes one of row bits 2 and 4
+    static __device__ __forceinline__ int go_state(int at, int rows, int cols, bool flip) {
+        if constexpr (sizeof(T) == 4) return at + rows * ROW + cols;
+        return (at ^ (cols ^ (flip ? W / 2 : 0))) + rows * ROW;
+    }
+};
+
+// Hides how a lane's place came about, once a chunk: the places derived from it are then worked out
+// where they are used instead of being held in registers over the whole walk.
+__device__ __forceinline__ void forget(int& x) { asm volatile("" : "+v"(x)); }
+
 // A tile of kC tokens by W columns: its global reads into registers, and from there to LDS.
 template <typename T, int W, bool VEC>
 struct Tile {
+    static constexpr int NT = kThreads;
     static constexpr int VE = Frag<T>::VE;
     static constexpr int PER_ROW = W / VE;
-    static constexpr int N = kC * PER_ROW / kThreads;
-    static constexpr int STRIDE = W + 16 / (int)sizeof(T);   // 16 bytes of padding spread rows over the banks
-    static_assert(N * kThreads == kC * PER_ROW, "whole vectors for every thread");
+    static constexpr int N = kC * PER_ROW / NT;
+    static constexpr int SIZE = kC * Tiled<T, W>::ROW;
+    static_assert(N * NT == kC * PER_ROW, "whole vectors for every thread");
     u4 v[N];
 
-    // base: the tile's first token's row; step: signed elements to the next token's row.
-    __device__ __forceinline__ void load(const T* base, int64_t step, int tokens, int width) {
+    __device__ __forceinline__ void load(const Window& w, int width, int thread) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int k = i * kThreads + threadIdx.x;
-            const int r = k / PER_ROW, c = (k % PER_ROW) * VE;
-            v[i] = load_row<T, VEC>(base + r * step + c, r < tokens ? width - c : 0);
+            const int k = i * NT + thread;
+            v[i] = load_row<T, VEC>(w, k / PER_ROW, (k % PER_ROW) * VE, width);
         }
     }
-    __device__ __forceinline__ void store(T* lds) const {
+    __device__ __forceinline__ void store(T* lds, int thread) const {
+        static_assert(NT / PER_ROW % 16 == 0 || sizeof(T) == 4, "steps of 16 rows keep the places' pattern");
+        const int at = Tiled<T, W>::at(thread / PER_ROW, (thread % PER_ROW) * VE);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int k = i * kThreads + threadIdx.x;
-            const int r = k / PER_ROW, c = (k % PER_ROW) * VE;
-            *reinterpret_cast<u4*>(lds + r * STRIDE + c) = v[i];
-        }
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u4*>(lds + Tiled<T, W>::go(at, i * (NT / PER_ROW), 0)) = v[i];
     }
 };
 
@@ -220,34 +353,48 @@ struct Tile {
 // product), three products on the exact K.
 template <typename T, int DA>
 __device__ __forceinline__ void update_state(f4 (&S)[DA / 16], const T* kt, const T* vt, const float* wt, int wave, int lane) {
-    constexpr int KS = Tile<T, DA, true>::STRIDE, VS = Tile<T, kV, true>::STRIDE;
+    using KL = Tiled<T, DA>;
+    using VL = Tiled<T, kV>;
     const int m = lane & 15, g = lane >> 4;
     if constexpr (sizeof(T) == 2) {
+        int ka = KL::at(8 * g + (m >> 2), 4 * (m & 3)), va = VL::at(8 * g + (m >> 2), 16 * wave + 4 * (m & 3));
+        forget(ka);
+        forget(va);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const int t0 = 32 * s + 8 * g + (m >> 2);
-            const u2 v0 = tr4(vt + t0 * VS + 16 * wave + 4 * (m & 3)), v1 = tr4(vt + (t0 + 4) * VS + 16 * wave + 4 * (m & 3));
+            const u2 v0 = tr4(vt + VL::go(va, 32 * s, 0)), v1 = tr4(vt + VL::go(va, 32 * s, 0, true));
             const uint32_t raw[4] = {v0[0], v0[1], v1[0], v1[1]};
             const f4 w0 = *reinterpret_cast<const f4*>(wt + 32 * s + 8 * g), w1 = *reinterpret_cast<const f4*>(wt + 32 * s + 8 * g + 4);
+            const float w[8] = {w0[0], w0[1], w0[2], w0[3], w1[0], w1[1], w1[2], w1[3]};
             u4 p[3];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float x = __uint_as_float(raw[e] << 16) * (e < 2 ? w0[2 * e] : w1[2 * e - 4]);
-                float y = __uint_as_float(raw[e] & 0xffff0000u) * (e < 2 ? w0[2 * e + 1] : w1[2 * e - 3]);
+            for (int h = 0; h < DA / 64; ++h) {              // four accumulators' reads at a time
+                u4 a[4];
 #pragma unroll
-                for (int q = 0; q < 3; ++q) {
-                    const uint32_t hx = __float_as_uint(x) & 0xffff0000u, hy = __float_as_uint(y) & 0xffff0000u;
-                    p[q][e] = (hx >> 16) | hy;
-                    x -= __uint_as_float(hx);
-                    y -= __uint_as_float(hy);
+                for (int u = 0; u < 4; ++u) {
+                    const int c = 64 * h + 16 * u;
+                    const u2 a0 = tr4(kt + KL::go(ka, 32 * s, c)), a1 = tr4(kt + KL::go(ka, 32 * s, c, true));
+                    a[u] = u4{a0[0], a0[1], a1[0], a1[1]};
                 }
-            }
+                if (h == 0) {
 #pragma unroll
-            for (int u = 0; u < DA / 16; ++u) {
-                const u2 a0 = tr4(kt + t0 * KS + 16 * u + 4 * (m & 3)), a1 = tr4(kt + (t0 + 4) * KS + 16 * u + 4 * (m & 3));
-                const u4 a = {a0[0], a0[1], a1[0], a1[1]};
+                    for (int e = 0; e < 4; ++e) {
+                        float x = __uint_as_float(raw[e] << 16) * w[2 * e];
+                        float y = __uint_as_float(raw[e] & 0xffff0000u) * w[2 * e + 1];
 #pragma unroll
-                for (int q = 0; q < 3; ++q) S[u] = Frag<T>::mma(a, p[q], S[u]);
+                        for (int q = 0; q < 3; ++q) {
+                            const uint32_t hx = __float_as_uint(x) & 0xffff0000u, hy = __float_as_uint(y) & 0xffff0000u;
+                            p[q][e] = __builtin_amdgcn_perm(hy, hx, 0x07060302u);   // (hx >> 16) | hy
+                            x -= __uint_as_float(hx);
+                            y -= __uint_as_float(hy);
+                        }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);           // the reads are under way before the first product
+#pragma unroll
+                for (int q = 0; q < 3; ++q)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) S[4 * h + u] = Frag<T>::mma(a[u], p[q], S[4 * h + u]);
             }
         }
     } else {
@@ -257,27 +404,30 @@ __device__ __forceinline__ void update_state(f4 (&S)[DA / 16], const T* kt, cons
             const f4 w = *reinterpret_cast<const f4*>(wt + t0);
             u4 b;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(vt[(t0 + e) * VS + 16 * wave + m] * w[e]);
+            for (int e = 0; e < 4; ++e) b[e] = __float_as_uint(vt[VL::at(t0 + e, 16 * wave + m)] * w[e]);
 #pragma unroll
-            for (int u = 0; u < DA / 16; ++u) {
-                u4 a;
+            for (int h = 0; h < DA / 64; ++h) {
+                u4 a[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) a[e] = __float_as_uint(kt[(t0 + e) * KS + 16 * u + m]);
-                S[u] = Frag<T>::mma(a, b, S[u]);
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[u][e] = __float_as_uint(kt[KL::at(t0 + e, 64 * h + 16 * u + m)]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) S[4 * h + u] = Frag<T>::mma(a[u], b, S[4 * h + u]);
             }
         }
     }
 }
 
-// Weights of the state update of a chunk of n tokens: s_up lambda^{n - shift - j}; the rows
-// behind its tokens are zeros, and their weight too.
-__device__ __forceinline__ void fill_weights(float* wt, float l2, int n, int shift, float s_up) {
-    if (threadIdx.x < kC) wt[threadIdx.x] = (int)threadIdx.x < n ? s_up * power(l2, n - shift - (int)threadIdx.x) : 0.0f;
+// Weights of the state update of a chunk of n tokens, token by token in the 64 lanes of a wave:
+// s_up lambda^{n - shift - j}; the rows behind the tokens hold zeros, and so do their weights.
+__device__ __forceinline__ void fill_weights(float* wt, float l2, int n, int shift, float s_up, int lane) {
+    wt[lane] = lane < n ? s_up * power(l2, n - shift - lane) : 0.0f;
 }
 
 template <typename T>
 __device__ __forceinline__ const T* rows_of(const void* p, const LaArgs& A, const Seg& g, int64_t pos, int64_t ts, int head_off) {
-    const int64_t t = A.reversed ? g.first + g.len - 1 - pos : g.first + pos;
+    const int64_t t = A.reversed ? (int64_t)g.first + g.len - 1 - pos : (int64_t)g.first + pos;
     return (const T*)p + t * ts + head_off;
 }
 
@@ -285,68 +435,42 @@ __device__ __forceinline__ int64_t state_at(const LaArgs& A, int at, int h, int 
     return (((int64_t)at * A.H + h) * A.nv + tile) * (da * kV);
 }
 
+// What a workgroup does.  Those that read the same rows (column tiles, heads that share keys) have
+// numbers eight apart: workgroups go to the eight dies in turn, and such a group meets in one L2.
 struct Unit { int seg, h, tile; };
 __device__ __forceinline__ Unit unit_of(const LaArgs& A) {
-    int b = blockIdx.x;
+    const int inner = A.share * A.nv, b = blockIdx.x;
+    const int outer = b / (8 * inner) * 8 + b % 8, i = b / 8 % inner;
+    const int groups = A.H / A.share;
     Unit u;
-    u.tile = b % A.nv;
-    b /= A.nv;
-    u.h = b % A.H;
-    u.seg = b / A.H;
+    u.tile = i % A.nv;
+    u.h = outer % groups * A.share + i / A.nv;
+    u.seg = outer / groups;
     return u;
+}
+inline unsigned grid_of(const LaArgs& A) {
+    const int64_t outer = (int64_t)A.nseg * (A.H / A.share);
+    return (unsigned)((outer + 7) / 8 * 8 * A.share * A.nv);
 }
 
 // ------------------------------------------------------------------ plan ----
-// Inclusive running sum and maximum over the workgroup's 256 threads.
-__device__ __forceinline__ int running(int v, bool sum, int* lds) {
-    lds[threadIdx.x] = v;
-    __syncthreads();
-    for (int o = 1; o < 256; o <<= 1) {
-        const int u = (int)threadIdx.x >= o ? lds[threadIdx.x - o] : 0;
-        __syncthreads();
-        v = sum ? v + u : max(v, u);
-        lds[threadIdx.x] = v;
-        __syncthreads();
-    }
-    return v;
-}
-
-// Segments of packed sequences.  Offsets that decrease or leave [0, T] are taken as
-// empty sequences, so there are never more than T / seg_len + n_seq segments, nor more
-// than 2 T / seg_len in sequences of several (each such has at most 2 len / seg_len).
-__global__ void __launch_bounds__(256) k_la_plan(const int32_t* cu, int n_seq, int64_t T, int seg_len, int nseg, PlanEntry* plan,
-                                                 int2* seqs) {
-    __shared__ int lds[256], total[3];
-    int base = 0, sbase = 0, reach = 0;          // segments, states, largest offset so far
-    for (int s0 = 0; s0 < n_seq; s0 += 256) {
-        const int s = s0 + threadIdx.x;
-        const bool in = s < n_seq;
-        const int b0 = in ? (int)min((int64_t)max(cu[s], 0), T) : 0, e0 = in ? (int)min((int64_t)max(cu[s + 1], 0), T) : 0;
-        const int top = max(reach, running(max(b0, e0), false, lds));
-        const int before = threadIdx.x ? max(reach, lds[threadIdx.x - 1]) : reach;
-        const int b = max(b0, before), len = max(e0 - b, 0);
-        const int cnt = in ? max((int)(((int64_t)len + seg_len - 1) / seg_len), 1) : 0, st = cnt > 1 ? cnt : 0;
-        __syncthreads();
-        const int at = running(cnt, true, lds) - cnt;
-        __syncthreads();
-        const int sat = running(st, true, lds) - st;
-        if (in) {
-            seqs[s] = make_int2(sbase + sat, cnt);
-            for (int i = 0; i < cnt; ++i)
-                if (base + at + i < nseg) plan[base + at + i] = PlanEntry{s, b, len, i, sbase + sat + i, {0, 0, 0}};
+// The segments of more packed sequences than a workgroup should look through for itself.
+__global__ void __launch_bounds__(64) k_la_plan(LaArgs A, Seg* plan, int2* seqs) {
+    const int lane = threadIdx.x;
+    Lane64 l;
+    l.reach = l.segs = l.states = 0;
+    for (int s0 = 0; s0 < A.n_seq; s0 += 64) {
+        l.read(A, s0, lane);
+        const int s = s0 + lane;
+        if (s >= A.n_seq) continue;
+        seqs[s] = make_int2(l.state, l.count);
+        for (int i = 0; i < l.count; ++i) {
+            Seg g{s, l.first, l.len, 0, 0, i, l.count, l.state + i};
+            place(g);
+            if (l.at + i < A.nseg) plan[l.at + i] = g;
         }
-        if (threadIdx.x == 255) {
-            total[0] = at + cnt;
-            total[1] = sat + st;
-            total[2] = top;
-        }
-        __syncthreads();
-        base += total[0];
-        sbase += total[1];
-        reach = total[2];
-        __syncthreads();
     }
-    for (int i = base + threadIdx.x; i < nseg; i += 256) plan[i] = PlanEntry{-1, 0, 0, 0, 0, {0, 0, 0}};
+    for (int i = l.segs + lane; i < A.nseg; i += 64) plan[i].seq = -1;
 }
 
 // ---------------------------------------------------------- segment state ----
@@ -354,12 +478,13 @@ template <typename T, int DA, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_la_state(LaArgs A) {
     using KT = Tile<T, DA, VEC>;
     using VT = Tile<T, kV, VEC>;
-    __shared__ __attribute__((aligned(16))) T kt[kC * KT::STRIDE];
-    __shared__ __attribute__((aligned(16))) T vt[kC * VT::STRIDE];
+    __shared__ __attribute__((aligned(16))) T kt[KT::SIZE];
+    __shared__ __attribute__((aligned(16))) T vt[VT::SIZE];
     __shared__ __attribute__((aligned(16))) float wt[kC];
     const Unit u = unit_of(A);
+    if (u.seg >= A.nseg) return;
     const Seg g = segment(A, u.seg);
-    if (g.seq < 0 || g.last) return;             // a last segment's end state is the final state: the walk makes it
+    if (g.seq < 0 || is_last(g)) return;             // a last segment's end state is the final state: the walk makes it
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const float l2 = log2_decay(A, u.h);
     const int64_t bs = A.reversed ? -A.b_ts : A.b_ts, cs = A.reversed ? -A.c_ts : A.c_ts;
@@ -369,21 +494,22 @@ __global__ void __launch_bounds__(kThreads) k_la_state(LaArgs A) {
     f4 S[DA / 16];
 #pragma unroll
     for (int i = 0; i < DA / 16; ++i) S[i] = f4{0, 0, 0, 0};
-    fill_weights(wt, l2, kC, A.shift, A.s_up);
+    if (wave == 0) fill_weights(wt, l2, kC, A.shift, A.s_up, lane);
     const float carry = power(l2, kC);
     KT k;
     VT v;
-    k.load(kp, bs, min(kC, g.n), A.Da);
-    v.load(vp, cs, min(kC, g.n), vw);
+    auto load = [&](int c0) {
+        const int n = min(kC, g.n - c0);
+        k.load(window(kp + c0 * bs, A.b_ts, A.reversed, n, A.Da), A.Da, threadIdx.x);
+        v.load(window(vp + c0 * cs, A.c_ts, A.reversed, n, vw), vw, threadIdx.x);
+    };
+    load(0);
     for (int c0 = 0; c0 < g.n; c0 += kC) {       // whole chunks: only a last segment has a ragged one
         __syncthreads();
-        k.store(kt);
-        v.store(vt);
+        k.store(kt, threadIdx.x);
+        v.store(vt, threadIdx.x);
         __syncthreads();
-        if (c0 + kC < g.n) {
-            k.load(kp + (c0 + kC) * bs, bs, min(kC, g.n - c0 - kC), A.Da);
-            v.load(vp + (c0 + kC) * cs, cs, min(kC, g.n - c0 - kC), vw);
-        }
+        if (c0 + kC < g.n) load(c0 + kC);
 #pragma unroll
         for (int i = 0; i < DA / 16; ++i) S[i] *= carry;
         update_state<T, DA>(S, kt, vt, wt, wave, lane);
@@ -419,219 +545,411 @@ __global__ void __launch_bounds__(256) k_la_carry(LaArgs A) {
     const int tile = b % A.nv;
     b /= A.nv;
     const int h = b % A.H, seq = b / A.H;
-    int first, n;
-    if (A.plan) {
-        const int2 e = A.seqs[seq];
-        first = e.x;
-        n = e.y;
-    } else {
-        first = seq * A.per_seq;
-        n = A.per_seq;
-    }
+    int first, n, len;
+    sequence(A, seq, first, n, len);
     if (n <= 1) return;                          // the walk reads h0 itself
     const int frag = part * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     f4 run = load_h0(A, seq, h, tile, frag / (DA / 16), frag % (DA / 16), lane);
-    const float f = power(log2_decay(A, h), A.seg_len);
+    const float f = power(log2_decay(A, h), ((len + n - 1) / n + kC - 1) / kC * kC);
     float* p = A.states + state_at(A, first, h, tile, DA) + (frag * 64 + lane) * 4;
     const int64_t step = state_at(A, 1, 0, 0, DA);
-    for (int i = 0; i < n; ++i) {
-        f4* q = reinterpret_cast<f4*>(p + i * step);
-        f4 own = {0, 0, 0, 0};
-        if (i + 1 < n) own = *q;
-        *q = run;
-        run = run * f + own;
+    constexpr int B = 8;                         // states read ahead of the first one's use
+    for (int i = 0; i < n; i += B) {
+        f4 own[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            own[j] = i + j + 1 < n ? *reinterpret_cast<const f4*>(p + (i + j) * step) : f4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            if (i + j >= n) break;
+            *reinterpret_cast<f4*>(p + (i + j) * step) = run;
+            run = run * f + own[j];
+        }
     }
 }
 
 // ----------------------------------------------------------------- walk ----
-// TO: type of the output (fp32 where several heads' gradients are still to be added up).
-template <typename T, typename TO, int DA, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_la_out(LaArgs A) {
-    using KT = Tile<T, DA, VEC>;
-    using VT = Tile<T, kV, VEC>;
-    constexpr int SS = KT::STRIDE;               // state copy [value column][row]
-    constexpr int NK = DA / Frag<T>::K;
-    __shared__ __attribute__((aligned(16))) T kt[kC * KT::STRIDE];
-    __shared__ __attribute__((aligned(16))) T vt[kC * VT::STRIDE];
-    __shared__ __attribute__((aligned(16))) T st[kV * SS];
-    __shared__ __attribute__((aligned(16))) float wt[kC];
-    const Unit un = unit_of(A);
-    const Seg g = segment(A, un.seg);
-    if (g.seq < 0) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, gr = lane >> 4;
-    const float l2 = log2_decay(A, un.h);
-    const int64_t as = A.reversed ? -A.a_ts : A.a_ts, bs = A.reversed ? -A.b_ts : A.b_ts, cs = A.reversed ? -A.c_ts : A.c_ts;
-    const T* ap = rows_of<T>(A.a, A, g, g.p0, A.a_ts, (un.h / A.a_rep) * A.Da);
+// N rows of 16x16 products with the NK fragments of `q`: y = sum_s fetch(x, s) q[s], handed to use(x, y).
+// bf16 reads two operands ahead of the ones it multiplies; fp32 four at a time, whose 16
+// instructions cover the next read themselves.
+template <typename T, int N, int NK, typename Fetch, typename Use>
+__device__ __forceinline__ void products(const u4 (&q)[NK], Fetch fetch, Use use) {
+    constexpr int GS = sizeof(T) == 2 ? 2 : 4, NG = NK / GS, NB = sizeof(T) == 2 ? 2 : 1;
+    u4 fr[NB][GS];
+    auto read = [&](int z) {
+#pragma unroll
+        for (int s = 0; s < GS; ++s) fr[z % NB][s] = fetch(z / NG, z % NG * GS + s);
+    };
+    if (NB == 2) read(0);
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+        f4 y = {0, 0, 0, 0};
+#pragma unroll
+        for (int z = x * NG; z < (x + 1) * NG; ++z) {
+            if (NB == 1) read(z);
+            else if (z + 1 < N * NG) read(z + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < GS; ++s) y = Frag<T>::mma(fr[z % NB][s], q[z % NG * GS + s], y);
+        }
+        use(x, y);
+    }
+}
+
+// Value column of row 4 g of accumulator x: such that a lane's accumulators join to the 16 bytes it
+// stores at a time, and the four lanes of a token store 64 bytes side by side.
+template <typename TO>
+__device__ __forceinline__ constexpr int column(int x, int g) {
+    return sizeof(TO) == 2 ? 32 * (x >> 1) + 8 * g + 4 * (x & 1) : 16 * x + 4 * g;
+}
+
+// Masked, decayed scores P^T (rows j, column i = 16 wave + m): what a lane holds of them is the operand
+// of the product with the values as it stands, tokens in the same order on both sides.
+template <typename T>
+struct Scores {
+    static constexpr int N = sizeof(T) == 2 ? 2 : 4;
+    u4 p[N];
+};
+// s_in lambda^{i - j} with j = 16 t + 4 gr + r: on the diagonal block (t = wave) as it is, in front of it
+// through the power of the next block's distance, between 1 and 31, times lambda^{16 (wave - 1 - t)}.
+struct Decay {
+    float diag[4], near[4], far[4];          // far: uniform
+    __device__ __forceinline__ Decay(float l2, float s_in, int wave, int m, int gr) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int d = m - 4 * gr - r;
+            diag[r] = s_in * power(l2, max(d, 0));
+            near[r] = s_in * power(l2, d + 16);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) far[t] = power(l2, 16 * max(wave - 1 - t, 0));
+    }
+    template <typename T>
+    __device__ __forceinline__ void apply(Scores<T>& P, int t, f4 y, int wave, int m, int gr) const {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            y[r] = t > wave || (t == wave && 4 * gr + r > m) ? 0.0f : y[r] * (t == wave ? diag[r] : near[r] * far[t]);
+        if constexpr (sizeof(T) == 2) {
+            P.p[t >> 1][2 * (t & 1)] = pack_bf16(y[0], y[1]);
+            P.p[t >> 1][2 * (t & 1) + 1] = pack_bf16(y[2], y[3]);
+        } else {
+            P.p[t] = __builtin_bit_cast(u4, y);
+        }
+    }
+};
+
+// o[x] += V^T P^T for NT accumulators, V a tile of W columns.
+template <typename T, typename TO, int W, int NT>
+__device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, const T* vt, int m, int gr) {
+    using VL = Tiled<T, W>;
+    if constexpr (sizeof(T) == 2) {
+        int va = VL::at(4 * gr + (m >> 2), column<TO>(0, m & 3));
+        forget(va);
+#pragma unroll
+        for (int h = 0; h < NT; h += 4) {
+            u4 a[2][4];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const u2 v0 = tr4(vt + VL::go(va, 32 * s, column<TO>(h + x, 0)));
+                    const u2 v1 = tr4(vt + VL::go(va, 32 * s + 16, column<TO>(h + x, 0)));
+                    a[s][x] = u4{v0[0], v0[1], v1[0], v1[1]};
+                }
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[h + x] = Frag<T>::mma(a[s][x], P.p[s], o[h + x]);
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int h = 0; h < NT; h += 4) {
+                u4 a[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        a[x][e] = __float_as_uint(vt[VL::at(16 * t + 4 * gr + e, column<TO>(h + x, m >> 2) + (m & 3))]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) o[h + x] = Frag<T>::mma(a[x], P.p[t], o[h + x]);
+            }
+    }
+}
+
+// A token's row of `width` columns from its lanes' accumulators.
+template <typename TO, bool VEC, int NT>
+__device__ __forceinline__ void store_row(TO* row, const f4 (&o)[NT], int width, int gr) {
+    if constexpr (VEC && sizeof(TO) == 2) {
+#pragma unroll
+        for (int e = 0; e < NT / 2; ++e)
+            if (column<TO>(2 * e, gr) < width)
+                *reinterpret_cast<u4*>(row + column<TO>(2 * e, gr)) =
+                    u4{pack_bf16(o[2 * e][0], o[2 * e][1]), pack_bf16(o[2 * e][2], o[2 * e][3]),
+                       pack_bf16(o[2 * e + 1][0], o[2 * e + 1][1]), pack_bf16(o[2 * e + 1][2], o[2 * e + 1][3])};
+    } else if constexpr (VEC) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+            if (column<TO>(x, gr) < width) *reinterpret_cast<f4*>(row + column<TO>(x, gr)) = o[x];
+    } else {
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (column<TO>(x, gr) + r < width) store_out(row + column<TO>(x, gr) + r, o[x][r]);
+    }
+}
+
+// The state's waves of a walk: they hold the state, 16 value columns each, put its copy and the
+// chunks' K and V tiles to LDS, and bring it to the next chunk.
+template <typename T, int DA, bool VEC>
+__device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const Unit& un, float l2, T* kt, T* vt, T* st, float* wt,
+                                            int wave, int lane) {
+    using SL = Tiled<T, DA>;
+    const int m = lane & 15, gr = lane >> 4, thread = threadIdx.x & 255;
+    const int64_t bs = A.reversed ? -A.b_ts : A.b_ts, cs = A.reversed ? -A.c_ts : A.c_ts;
     const T* kp = rows_of<T>(A.b, A, g, g.p0, A.b_ts, (un.h / A.b_rep) * A.Da);
     const T* vp = rows_of<T>(A.c, A, g, g.p0, A.c_ts, (un.h / A.c_rep) * A.Dv + un.tile * kV);
-    const int64_t os = A.reversed ? -A.o_ts : A.o_ts;
-    TO* op = const_cast<TO*>(rows_of<TO>(A.o, A, g, g.p0, A.o_ts, un.h * A.Dv + un.tile * kV));
     const int vw = A.Dv - un.tile * kV;
-
+    const int64_t hrow = is_last(g) && A.h_out ? state_row(A, g.seq) : -1;
+    Tile<T, DA, VEC> k;
+    Tile<T, kV, VEC> v;
+    auto load = [&](int c0) {
+        const int n = min(kC, g.n - c0);
+        k.load(window(kp + c0 * bs, A.b_ts, A.reversed, n, A.Da), A.Da, thread);
+        v.load(window(vp + c0 * cs, A.c_ts, A.reversed, n, vw), vw, thread);
+    };
+    load(0);
     f4 S[DA / 16];
-    if (g.only) {
+    if (g.count == 1) {
 #pragma unroll
         for (int i = 0; i < DA / 16; ++i) S[i] = load_h0(A, g.seq, un.h, un.tile, wave, i, lane);
     } else {
         const float* in = A.states + state_at(A, g.state, un.h, un.tile, DA);
 #pragma unroll
-        for (int i = 0; i < DA / 16; ++i)
-            S[i] = *reinterpret_cast<const f4*>(in + ((wave * (DA / 16) + i) * 64 + lane) * 4);
+        for (int i = 0; i < DA / 16; ++i) S[i] = *reinterpret_cast<const f4*>(in + ((wave * (DA / 16) + i) * 64 + lane) * 4);
     }
-    const int64_t hrow = g.last && A.h_out ? state_row(A, g.seq) : -1;
-
-    const int qi = 16 * wave + m;                // this lane's query position in the chunk
-    const float carry = power(l2, kC), at_q = A.s_carry * power(l2, qi + A.shift);
-    float dec[4][4];                             // s_in lambda^{i - j}, j = 16 t + 4 gr + r
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int d = qi - (16 * t + 4 * gr + r);
-            dec[t][r] = d >= 0 ? A.s_in * power(l2, d) : 0.0f;
-        }
-    fill_weights(wt, l2, min(kC, g.n), A.shift, A.s_up);
-
-    KT k;
-    VT v;
-    u4 q[NK], qn[NK];
-    auto load_q = [&](int c0) {
-#pragma unroll
-        for (int s = 0; s < NK; ++s) {
-            const int c = Frag<T>::K * s + Frag<T>::VE * gr;
-            qn[s] = load_row<T, VEC>(ap + (c0 + qi) * as + c, c0 + qi < g.n ? A.Da - c : 0);
-        }
-    };
-    if (g.n > 0) {
-        k.load(kp, bs, min(kC, g.n), A.Da);
-        v.load(vp, cs, min(kC, g.n), vw);
-        load_q(0);
-    }
+    float f = power(l2, kC);
+    const int sw = SL::at_state(16 * wave + m, 4 * gr);
     for (int c0 = 0; c0 < g.n; c0 += kC) {
         const int n = min(kC, g.n - c0);
         const bool more = c0 + kC < g.n;
-        __syncthreads();                         // the last chunk's reads of the tiles are over
-        k.store(kt);
-        v.store(vt);
-        if (n < kC && c0 > 0) fill_weights(wt, l2, n, A.shift, A.s_up);
+        k.store(kt, thread);
+        v.store(vt, thread);
+        if (c0 == 0 || n < kC) {
+            if (wave == 0) fill_weights(wt, l2, n, A.shift, A.s_up, lane);
+            f = power(l2, n);
+        }
 #pragma unroll
-        for (int i = 0; i < DA / 16; ++i) {      // S^T for this chunk's product
-            T* p = st + (16 * wave + m) * SS + 16 * i + 4 * gr;
+        for (int i = 0; i < DA / 16; ++i) {      // the copy that this chunk's products read
+            T* p = st + SL::go_state(sw, 0, 16 * i, false);
             if constexpr (sizeof(T) == 2) {
                 *reinterpret_cast<u2*>(p) = u2{pack_bf16(S[i][0], S[i][1]), pack_bf16(S[i][2], S[i][3])};
             } else {
                 *reinterpret_cast<f4*>(p) = S[i];
             }
         }
-#pragma unroll
-        for (int s = 0; s < NK; ++s) q[s] = qn[s];
         __syncthreads();
-        if (more) {
-            k.load(kp + (c0 + kC) * bs, bs, min(kC, g.n - c0 - kC), A.Da);
-            v.load(vp + (c0 + kC) * cs, cs, min(kC, g.n - c0 - kC), vw);
-            load_q(c0 + kC);
-        }
-
-        // carried part: O^T = S^T Q^T, then lambda^{i + shift} for the lane's token.  Value
-        // columns are dealt to accumulators so that a lane ends with 16 neighbours: row
-        // 4 g' + r of accumulator tv is column 16 g' + 4 tv + r.
-        f4 o[4];
-#pragma unroll
-        for (int tv = 0; tv < 4; ++tv) {
-            o[tv] = f4{0, 0, 0, 0};
-            const T* sp = st + (16 * (m >> 2) + 4 * tv + (m & 3)) * SS + Frag<T>::VE * gr;
-#pragma unroll
-            for (int s = 0; s < NK; ++s)
-                o[tv] = Frag<T>::mma(*reinterpret_cast<const u4*>(sp + Frag<T>::K * s), q[s], o[tv]);
-            o[tv] *= at_q;
-        }
-        // masked scores P^T = K Q^T, rows j, column i: what a lane holds is the operand of
-        // the product with V as it stands, tokens in the same order on both sides.
-        u4 p[sizeof(T) == 2 ? 2 : 4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            f4 x = {0, 0, 0, 0};
-            if (t <= wave) {
-                const T* kr = kt + (16 * t + m) * KT::STRIDE + Frag<T>::VE * gr;
-#pragma unroll
-                for (int s = 0; s < NK; ++s) x = Frag<T>::mma(*reinterpret_cast<const u4*>(kr + Frag<T>::K * s), q[s], x);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = 16 * t + 4 * gr + r <= qi ? x[r] * dec[t][r] : 0.0f;
-            }
-            if constexpr (sizeof(T) == 2) {
-                p[t >> 1][2 * (t & 1)] = pack_bf16(x[0], x[1]);
-                p[t >> 1][2 * (t & 1) + 1] = pack_bf16(x[2], x[3]);
-            } else {
-                p[t] = __builtin_bit_cast(u4, x);
-            }
-        }
-        if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (2 * s > wave) continue;
-                const bf16* vr = vt + (32 * s + 4 * gr + (m >> 2)) * VT::STRIDE + 16 * (m & 3);
-#pragma unroll
-                for (int tv = 0; tv < 4; ++tv) {
-                    const u2 v0 = tr4(vr + 4 * tv), v1 = tr4(vr + 16 * VT::STRIDE + 4 * tv);
-                    o[tv] = Frag<T>::mma(u4{v0[0], v0[1], v1[0], v1[1]}, p[s], o[tv]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (t > wave) continue;
-                const float* vr = vt + (16 * t + 4 * gr) * VT::STRIDE + 16 * (m >> 2) + (m & 3);
-#pragma unroll
-                for (int tv = 0; tv < 4; ++tv) {
-                    u4 a;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) a[e] = __float_as_uint(vr[e * VT::STRIDE + 4 * tv]);
-                    o[tv] = Frag<T>::mma(a, p[t], o[tv]);
-                }
-            }
-        }
-        if (qi < n) {
-            TO* row = op + (c0 + qi) * os + 16 * gr;
-            if constexpr (VEC) {
-                if (16 * gr < vw) {
-                    if constexpr (sizeof(TO) == 2) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (16 * gr + 8 * e < vw)
-                                *reinterpret_cast<u4*>(row + 8 * e) =
-                                    u4{pack_bf16(o[2 * e][0], o[2 * e][1]), pack_bf16(o[2 * e][2], o[2 * e][3]),
-                                       pack_bf16(o[2 * e + 1][0], o[2 * e + 1][1]), pack_bf16(o[2 * e + 1][2], o[2 * e + 1][3])};
-                    } else {
-#pragma unroll
-                        for (int tv = 0; tv < 4; ++tv)
-                            if (16 * gr + 4 * tv < vw) *reinterpret_cast<f4*>(row + 4 * tv) = o[tv];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int tv = 0; tv < 4; ++tv)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * gr + 4 * tv + r < vw) store_out(row + 4 * tv + r, o[tv][r]);
-            }
-        }
+        if (more) load(c0 + kC);
         if (more || hrow >= 0) {
-            const float f = n == kC ? carry : power(l2, n);
 #pragma unroll
             for (int i = 0; i < DA / 16; ++i) S[i] *= f;
             update_state<T, DA>(S, kt, vt, wt, wave, lane);
         }
+        __syncthreads();
     }
     if (hrow >= 0) {
+        int late = lane;                         // keeps these addresses out of the walk's registers
+        forget(late);
         float* p = A.h_out + (hrow * A.H + un.h) * (int64_t)A.Da * A.Dv;
-        const int col = un.tile * kV + 16 * wave + m;
+        const int col = un.tile * kV + 16 * wave + (late & 15);
 #pragma unroll
         for (int i = 0; i < DA / 16; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = 16 * i + 4 * gr + r;
-                if (col < A.Dv && row < A.Da) p[(int64_t)row * A.Dv + col] = S[i][r];
+                const int row = 16 * i + 4 * (late >> 4) + r;
+                if (col < A.Dv && row < A.Da) p[A.transposed ? (int64_t)col * A.Da + row : (int64_t)row * A.Dv + col] = S[i][r];
             }
+    }
+}
+
+// Eight waves on one chunk: waves 0 - 3 make the outputs of 16 tokens each, waves 4 - 7
+// bring the state to the next chunk at the same time.  Both read the chunk's K and V tiles; the
+// state entering the chunk reaches the output waves as an LDS copy.  The state's waves load the
+// next chunk's tiles into registers while this one is computed (the output waves the next
+// queries, which only they read) and put them to LDS between two barriers.
+// TO: type of the output (fp32 where several heads' gradients are still to be added up).
+template <typename T, typename TO, int DA, bool VEC>
+__global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_la_out(LaArgs A) {
+    using KL = Tiled<T, DA>;
+    constexpr int NK = DA / Frag<T>::K;
+    __shared__ __attribute__((aligned(16))) T kt[Tile<T, DA, VEC>::SIZE];
+    __shared__ __attribute__((aligned(16))) T vt[Tile<T, kV, VEC>::SIZE];
+    __shared__ __attribute__((aligned(16))) T st[kV * KL::ROW];      // the state's copy [value column][row]
+    __shared__ __attribute__((aligned(16))) float wt[kC];
+    const Unit un = unit_of(A);
+    if (un.seg >= A.nseg) return;
+    const Seg g = segment(A, un.seg);
+    if (g.seq < 0) return;
+    const int lane = threadIdx.x & 63, m = lane & 15, gr = lane >> 4;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3;
+    const float l2 = log2_decay(A, un.h);
+    // Every wave meets the same barriers: two a chunk.
+    if (wave8 >= 4) {
+        carry_state<T, DA, VEC>(A, g, un, l2, kt, vt, st, wt, wave, lane);
+        return;
+    }
+    const int64_t as = A.reversed ? -A.a_ts : A.a_ts, os = A.reversed ? -A.o_ts : A.o_ts;
+    const T* ap = rows_of<T>(A.a, A, g, g.p0, A.a_ts, (un.h / A.a_rep) * A.Da);
+    TO* op = const_cast<TO*>(rows_of<TO>(A.o, A, g, g.p0, A.o_ts, un.h * A.Dv + un.tile * kV));
+    const int qi = 16 * wave + m;                // this lane's query position in the chunk
+    const float at_q = A.s_carry * power(l2, qi + A.shift);
+    const Decay dec(l2, A.s_in, wave, m, gr);
+    u4 q[NK], qn[NK];
+    auto load_q = [&](int c0) {
+        const Window w = window(ap + c0 * as, A.a_ts, A.reversed, min(kC, g.n - c0), A.Da);
+#pragma unroll
+        for (int s = 0; s < NK; ++s) qn[s] = load_row<T, VEC>(w, qi, Frag<T>::K * s + Frag<T>::VE * gr, A.Da);
+    };
+    load_q(0);
+    for (int c0 = 0; c0 < g.n; c0 += kC) {
+#pragma unroll
+        for (int s = 0; s < NK; ++s) q[s] = qn[s];
+        __syncthreads();
+        if (c0 + kC < g.n) load_q(c0 + kC);
+
+        // the carried part O^T = S^T Q^T (four accumulators of value columns), then the scores K Q^T
+        f4 o[4];
+        Scores<T> P;
+        int sa = KL::at_state(column<TO>(0, m >> 2) + (m & 3), Frag<T>::VE * gr), ka = KL::at(m, Frag<T>::VE * gr);
+        forget(sa);
+        forget(ka);
+        products<T, 8, NK>(
+            q,
+            [&](int x, int s) {
+                const int c = Frag<T>::K * s;
+                return *reinterpret_cast<const u4*>(x < 4 ? st + KL::go_state(sa, column<TO>(x, 0), c, x & 1) : kt + KL::go(ka, 16 * (x - 4), c));
+            },
+            [&](int x, f4 y) {
+                if (x < 4) o[x] = y * at_q;      // lambda^{i + shift} of the lane's token
+                else dec.apply(P, x - 4, y, wave, m, gr);
+            });
+        add_values<T, TO, kV>(o, P, vt, m, gr);
+        if (qi < g.n - c0) store_row<TO, VEC>(op + (c0 + qi) * os, o, A.Dv - un.tile * kV, gr);
+        __syncthreads();
+    }
+}
+
+// The gradients of keys and values in one reversed walk, for values of one column tile.  In the roles of
+// the walk: keys q, values do (A.b, A.c), queries k (A.a) give dv (A.o),
+//     dv_j = scale sum_{i>=j} lambda^{i-j} (k_j . q_i) do_i + lambda^{..} k_j^T R,
+// and on the same tiles and state, with queries v (X.v),
+//     dk_j = scale sum_{i>=j} lambda^{i-j} (v_j . do_i) q_i + lambda^{..} R v_j   (X.dk).
+// R's copy lies with its rows (key width) side by side: the first product reads it as it lies, the second
+// transposed.
+struct SecondArgs {
+    const void* v;
+    void* dk;
+    int64_t v_ts, dk_ts;
+    int v_rep;
+};
+template <typename T, typename TO, int DA, bool VEC>
+__global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkdv(LaArgs A, SecondArgs X) {
+    using KL = Tiled<T, DA>;
+    using VL = Tiled<T, kV>;
+    constexpr int NK = DA / Frag<T>::K, NV = kV / Frag<T>::K, NA = DA / 16;
+    __shared__ __attribute__((aligned(16))) T kt[Tile<T, DA, VEC>::SIZE];
+    __shared__ __attribute__((aligned(16))) T vt[Tile<T, kV, VEC>::SIZE];
+    __shared__ __attribute__((aligned(16))) T st[kV * KL::ROW];
+    __shared__ __attribute__((aligned(16))) float wt[kC];
+    const Unit un = unit_of(A);
+    if (un.seg >= A.nseg) return;
+    const Seg g = segment(A, un.seg);
+    if (g.seq < 0) return;
+    const int lane = threadIdx.x & 63, m = lane & 15, gr = lane >> 4;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3;
+    const float l2 = log2_decay(A, un.h);
+    if (wave8 >= 4) {
+        carry_state<T, DA, VEC>(A, g, un, l2, kt, vt, st, wt, wave, lane);
+        return;
+    }
+    const T* ap = rows_of<T>(A.a, A, g, g.p0, A.a_ts, (un.h / A.a_rep) * A.Da);
+    const T* vp = rows_of<T>(X.v, A, g, g.p0, X.v_ts, (un.h / X.v_rep) * A.Dv);
+    TO* dv = const_cast<TO*>(rows_of<TO>(A.o, A, g, g.p0, A.o_ts, un.h * A.Dv));
+    TO* dk = const_cast<TO*>(rows_of<TO>(X.dk, A, g, g.p0, X.dk_ts, un.h * A.Da));
+    const int qi = 16 * wave + m;
+    const float at_q = A.s_carry * power(l2, qi + A.shift);
+    const Decay dec(l2, A.s_in, wave, m, gr);
+    u4 q[NK], qn[NK], v[NV], vn[NV];
+    auto load = [&](int c0) {
+        const int n = min(kC, g.n - c0);
+        const Window wq = window(ap - c0 * A.a_ts, A.a_ts, true, n, A.Da), wv = window(vp - c0 * X.v_ts, X.v_ts, true, n, A.Dv);
+#pragma unroll
+        for (int s = 0; s < NK; ++s) qn[s] = load_row<T, VEC>(wq, qi, Frag<T>::K * s + Frag<T>::VE * gr, A.Da);
+#pragma unroll
+        for (int s = 0; s < NV; ++s) vn[s] = load_row<T, VEC>(wv, qi, Frag<T>::K * s + Frag<T>::VE * gr, A.Dv);
+    };
+    load(0);
+    for (int c0 = 0; c0 < g.n; c0 += kC) {
+#pragma unroll
+        for (int s = 0; s < NK; ++s) q[s] = qn[s];
+#pragma unroll
+        for (int s = 0; s < NV; ++s) v[s] = vn[s];
+        __syncthreads();
+        if (c0 + kC < g.n) load(c0 + kC);
+        const bool live = qi < g.n - c0;
+        {
+            f4 o[4];
+            Scores<T> P;
+            int sa = KL::at_state(column<TO>(0, m >> 2) + (m & 3), Frag<T>::VE * gr), ka = KL::at(m, Frag<T>::VE * gr);
+            forget(sa);
+            forget(ka);
+            products<T, 8, NK>(
+                q,
+                [&](int x, int s) {
+                    const int c = Frag<T>::K * s;
+                    return *reinterpret_cast<const u4*>(x < 4 ? st + KL::go_state(sa, column<TO>(x, 0), c, x & 1) : kt + KL::go(ka, 16 * (x - 4), c));
+                },
+                [&](int x, f4 y) {
+                    if (x < 4) o[x] = y * at_q;
+                    else dec.apply(P, x - 4, y, wave, m, gr);
+                });
+            add_values<T, TO, kV>(o, P, vt, m, gr);
+            if (live) store_row<TO, VEC>(dv - (c0 + qi) * A.o_ts, o, A.Dv, gr);
+        }
+        {
+            f4 o[NA];
+            Scores<T> P;
+            int va = VL::at(m, Frag<T>::VE * gr);
+            int sa = KL::at_state(8 * gr + (m >> 2), column<TO>(0, m & 3));
+            forget(va);
+            forget(sa);
+            products<T, NA + 4, NV>(
+                v,
+                [&](int x, int s) {
+                    if (x >= NA) return *reinterpret_cast<const u4*>(vt + VL::go(va, 16 * (x - NA), Frag<T>::K * s));
+                    if constexpr (sizeof(T) == 2) {      // rows of R: key columns of the copy, eight value columns a lane
+                        const u2 a0 = tr4(st + KL::go_state(sa, 32 * s, column<TO>(x, 0), false));
+                        const u2 a1 = tr4(st + KL::go_state(sa, 32 * s + 4, column<TO>(x, 0), true));
+                        return u4{a0[0], a0[1], a1[0], a1[1]};
+                    } else {
+                        u4 a;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            a[e] = __float_as_uint(st[KL::at_state(16 * s + 4 * gr + e, column<TO>(x, m >> 2) + (m & 3))]);
+                        return a;
+                    }
+                },
+                [&](int x, f4 y) {
+                    if (x < NA) o[x] = y * at_q;
+                    else dec.apply(P, x - NA, y, wave, m, gr);
+                });
+            add_values<T, TO, DA>(o, P, kt, m, gr);
+            if (live) store_row<TO, VEC>(dk - (c0 + qi) * X.dk_ts, o, A.Da, gr);
+        }
+        __syncthreads();
     }
 }
 
@@ -763,12 +1081,16 @@ __global__ void __launch_bounds__(256) k_la_step(StepArgs A) {
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 inline bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-// Segment length: as many segments as it takes to put about four workgroups on each
-// compute unit, no shorter than 256 tokens (a segment costs its state's trip through
-// memory).
-int plan_seg_len(int64_t n_seq, int64_t T, int64_t H, int64_t Dv) {
+constexpr int kLookThrough = 256;   // packed sequences that every workgroup looks through itself
+
+// Longest segment: as many segments as it takes to put about two workgroups on each compute unit (all
+// that fit at a time; packed sequences end in half a segment on average), no shorter than 256 tokens: a
+// segment's state makes four trips through memory.  Up to 1024 tokens in all, one segment a sequence.
+int plan_target(int64_t n_seq, int64_t T, int64_t H, int64_t Dv, bool packed) {
+    if (T <= 1024) return 1024;
     const int64_t units = H * ((Dv + kV - 1) / kV);
-    const int64_t want = (4 * (int64_t)device_cu_count() + units - 1) / units;
+    int64_t want = (2 * (int64_t)device_cu_count() + units - 1) / units;
+    if (packed) want = std::max(want - n_seq / 2, (want + 1) / 2);
     int64_t len = (T + want - 1) / want;
     len = (len + kC - 1) / kC * kC;
     if (len < 256) len = 256;
@@ -777,26 +1099,25 @@ int plan_seg_len(int64_t n_seq, int64_t T, int64_t H, int64_t Dv) {
 }
 
 struct Plan {
-    int seg_len, nseg, per_seq;
-    bool table;         // packed sequences of more than one segment
+    int target, nseg, per_seq;
+    bool table;         // more packed sequences than kLookThrough, some of several segments
     size_t states, seqs_at, table_bytes;
     int da;
 };
 
 Plan make_plan(int64_t n_seq, int64_t T, int64_t H, int64_t Da, int64_t Dv, bool packed) {
     Plan p;
-    p.seg_len = plan_seg_len(n_seq, T, H, Dv);
+    p.target = plan_target(n_seq, T, H, Dv, packed);
     p.da = Da <= 64 ? 64 : 128;
     const int64_t L = T / n_seq;
-    p.table = packed && T > p.seg_len;
-    p.per_seq = packed ? 0 : (int)((L + p.seg_len - 1) / p.seg_len);
-    if (!packed && p.per_seq < 1) p.per_seq = 1;
-    const int64_t nseg = packed ? (p.table ? T / p.seg_len + n_seq : n_seq) : n_seq * p.per_seq;
-    p.nseg = (int)nseg;
-    const bool states = packed ? p.table : p.per_seq > 1;
-    const int64_t nst = packed ? std::min(nseg, 2 * T / p.seg_len) : nseg;
-    p.states = states ? (size_t)nst * H * ((Dv + kV - 1) / kV) * p.da * kV * 4 : 0;
-    p.seqs_at = up256((size_t)nseg * sizeof(PlanEntry));
+    const bool several = packed ? T > p.target : L > p.target;
+    p.table = packed && several && n_seq > kLookThrough;
+    p.per_seq = packed ? 0 : several ? (int)((L + p.target - 1) / p.target) : 1;
+    const int64_t nseg = !packed ? n_seq * p.per_seq : several ? T / p.target + n_seq : n_seq;
+    p.nseg = (int)std::min<int64_t>(nseg, 0x7fffffff);
+    const int64_t nst = packed ? std::min(nseg, 2 * T / p.target) : nseg;
+    p.states = several ? (size_t)nst * H * ((Dv + kV - 1) / kV) * p.da * kV * 4 : 0;
+    p.seqs_at = up256((size_t)nseg * sizeof(Seg));
     p.table_bytes = p.table ? p.seqs_at + up256((size_t)n_seq * 8) : 0;
     return p;
 }
@@ -807,66 +1128,85 @@ bool sizes_ok(int64_t n_seq, int64_t T, int64_t H, int64_t G, int64_t Dk, int64_
     return true;
 }
 
+// A chunk's rows are addressed in 31 bits: 64 strides of four bytes.
+bool strides_ok(int64_t stride, int64_t row) { return stride >= row && stride < 1 << 22; }
+
 template <typename T, typename TO, int DA, bool VEC>
-mb_status run_passes(const LaArgs& A, const Plan& p, hipStream_t s) {
-    const int64_t units = (int64_t)p.nseg * A.H * A.nv;
+mb_status run_passes(const LaArgs& A, const SecondArgs* X, const Plan& p, hipStream_t s) {
+    const dim3 grid(grid_of(A)), wide(kWalkThreads);
     if (p.states) {
-        hipLaunchKernelGGL((k_la_state<T, DA, VEC>), dim3((unsigned)units), dim3(kThreads), 0, s, A);
+        hipLaunchKernelGGL((k_la_state<T, DA, VEC>), grid, dim3(kThreads), 0, s, A);
         mb_status st = check_launch();
         if (st != MB_OK) return st;
         hipLaunchKernelGGL(k_la_carry<DA>, dim3((unsigned)((int64_t)A.n_seq * A.H * A.nv * (DA * kV / 1024))), dim3(256), 0, s, A);
         st = check_launch();
         if (st != MB_OK) return st;
     }
-    hipLaunchKernelGGL((k_la_out<T, TO, DA, VEC>), dim3((unsigned)units), dim3(kThreads), 0, s, A);
+    if (X) hipLaunchKernelGGL((k_la_dkdv<T, TO, DA, VEC>), grid, wide, 0, s, A, *X);
+    else hipLaunchKernelGGL((k_la_out<T, TO, DA, VEC>), grid, wide, 0, s, A);
     return check_launch();
 }
 
 template <typename T, typename TO>
-mb_status run_typed(LaArgs A, const Plan& p, hipStream_t s) {
+mb_status run_typed(const LaArgs& A, const SecondArgs* X, const Plan& p, hipStream_t s) {
     constexpr int VE = Frag<T>::VE, VO = 16 / sizeof(TO);
-    const bool vec = A.Da % VE == 0 && A.Dv % VE == 0 && A.Dv % VO == 0 && A.a_ts % VE == 0 && A.b_ts % VE == 0 && A.c_ts % VE == 0 &&
-                     al16(A.a) && al16(A.b) && al16(A.c) && al16(A.o);
-    if (p.da == 64) return vec ? run_passes<T, TO, 64, true>(A, p, s) : run_passes<T, TO, 64, false>(A, p, s);
-    return vec ? run_passes<T, TO, 128, true>(A, p, s) : run_passes<T, TO, 128, false>(A, p, s);
+    bool vec = A.Da % VE == 0 && A.Dv % VE == 0 && A.Dv % VO == 0 && A.a_ts % VE == 0 && A.b_ts % VE == 0 && A.c_ts % VE == 0 &&
+               al16(A.a) && al16(A.b) && al16(A.c) && al16(A.o);
+    if (X) vec = vec && X->v_ts % VE == 0 && A.Da % VO == 0 && al16(X->v) && al16(X->dk);
+    if (p.da == 64) return vec ? run_passes<T, TO, 64, true>(A, X, p, s) : run_passes<T, TO, 64, false>(A, X, p, s);
+    return vec ? run_passes<T, TO, 128, true>(A, X, p, s) : run_passes<T, TO, 128, false>(A, X, p, s);
 }
 
-// One run of the chunked form; `out_f32` where heads' gradients are added up afterwards.
-mb_status run(LaArgs A, const Plan& p, mb_dtype dtype, bool out_f32, char* ws, hipStream_t s) {
+// Fills in what the plan says.
+void use_plan(LaArgs& A, const Plan& p, char* ws) {
     A.nv = (A.Dv + kV - 1) / kV;
-    A.seg_len = p.seg_len;
+    A.target = p.target;
     A.nseg = p.nseg;
     A.per_seq = p.per_seq;
-    A.plan = p.table ? (const PlanEntry*)ws : nullptr;
+    A.plan = p.table ? (const Seg*)ws : nullptr;
     A.seqs = p.table ? (const int2*)(ws + p.seqs_at) : nullptr;
     A.states = p.states ? (float*)(ws + p.table_bytes) : nullptr;
-    if (dtype == MB_F32) return run_typed<float, float>(A, p, s);
-    return out_f32 ? run_typed<bf16, float>(A, p, s) : run_typed<bf16, bf16>(A, p, s);
 }
 
-mb_status launch_plan(const LaArgs& A, const Plan& p, char* ws, hipStream_t s) {
+// One run of the chunked form (with X: of both gradients); `out_f32` where heads' gradients are added up afterwards.
+mb_status run(const LaArgs& A, const SecondArgs* X, const Plan& p, mb_dtype dtype, bool out_f32, hipStream_t s) {
+    if (dtype == MB_F32) return run_typed<float, float>(A, X, p, s);
+    return out_f32 ? run_typed<bf16, float>(A, X, p, s) : run_typed<bf16, bf16>(A, X, p, s);
+}
+
+mb_status launch_plan(LaArgs A, const Plan& p, char* ws, hipStream_t s) {
     if (!p.table) return MB_OK;
-    hipLaunchKernelGGL(k_la_plan, dim3(1), dim3(256), 0, s, A.cu, A.n_seq, A.T, p.seg_len, p.nseg, (PlanEntry*)ws,
-                       (int2*)(ws + p.seqs_at));
+    A.plan = nullptr;
+    hipLaunchKernelGGL(k_la_plan, dim3(1), dim3(64), 0, s, A, (Seg*)ws, (int2*)(ws + p.seqs_at));
     return check_launch();
 }
 
+// Workgroups a launch may have.
+bool grid_ok(const Plan& p, int64_t n_seq, int64_t H, int64_t Dv) {
+    const int64_t nv = (Dv + kV - 1) / kV;
+    return ((int64_t)p.nseg + 8) * H * nv <= 0x7fffffff && n_seq * H * nv * 8 <= 0x7fffffff;
+}
+
+// The backward: one run for dq, and for dk and dv one walk over both where one of them is at most a
+// column tile wide (that one takes the values' role), two runs otherwise.
 struct BwdPlan {
-    Plan q, k, v;          // the three runs
-    size_t states, fold;
-    size_t total;
+    Plan q, k, v;          // k, v: both runs, or v the common one
+    bool both, swapped;    // swapped: keys have the values' role
+    size_t states, fold[2], total;
 };
 
 BwdPlan bwd_plan(int64_t n_seq, int64_t T, int64_t H, int64_t G, int64_t Dk, int64_t Dv, bool packed) {
     BwdPlan b;
+    b.both = Dv <= kV || Dk <= kV;
+    b.swapped = b.both && Dv > kV;
     b.q = make_plan(n_seq, T, H, Dv, Dk, packed);
     b.k = b.q;
-    b.v = make_plan(n_seq, T, H, Dk, Dv, packed);
-    auto most = [](size_t x, size_t y) { return x > y ? x : y; };
-    b.states = most(b.q.table_bytes + b.q.states, b.v.table_bytes + b.v.states);
-    b.states = up256(b.states);
-    b.fold = G < H ? up256((size_t)T * H * most(Dk, Dv) * 4) : 0;
-    b.total = b.states + b.fold;
+    b.v = b.swapped ? b.q : make_plan(n_seq, T, H, Dk, Dv, packed);
+    b.states = up256(std::max(b.q.table_bytes + b.q.states, b.v.table_bytes + b.v.states));
+    const auto rows = [&](int64_t D) { return G < H ? up256((size_t)T * H * D * 4) : 0; };
+    b.fold[0] = b.both ? rows(Dk) : rows(std::max(Dk, Dv));       // dk, or both one after the other
+    b.fold[1] = b.both ? rows(Dv) : 0;
+    b.total = b.states + b.fold[0] + b.fold[1];
     return b;
 }
 
@@ -902,7 +1242,7 @@ extern "C" mb_status mb_linear_attn(const void* q, const void* k, const void* v,
     using namespace mb;
     if (!dtype_ok(dtype)) return MB_ERR_DTYPE;
     if (!sizes_ok(n_seq, T, H, G, Dk, Dv)) return MB_ERR_SHAPE;
-    if (q_stride < H * Dk || k_stride < G * Dk || v_stride < G * Dv) return MB_ERR_SHAPE;
+    if (!strides_ok(q_stride, H * Dk) || !strides_ok(k_stride, G * Dk) || !strides_ok(v_stride, G * Dv)) return MB_ERR_SHAPE;
     if (slots ? n_slots < 1 : n_slots != 0) return MB_ERR_SHAPE;
     if (n_seq == 0) return MB_OK;
     if (!cu_seqlens && T % n_seq) return MB_ERR_SHAPE;
@@ -913,7 +1253,7 @@ extern "C" mb_status mb_linear_attn(const void* q, const void* k, const void* v,
         return MB_ERR_ALIGN;
     const Plan p = make_plan(n_seq, T, H, Dk, Dv, cu_seqlens != nullptr);
     const size_t need = p.table_bytes + p.states;
-    if ((int64_t)p.nseg * H * ((Dv + kV - 1) / kV) > 0x7fffffff || n_seq * H * 16 > 0x7fffffff) return MB_ERR_SHAPE;
+    if (!grid_ok(p, n_seq, H, Dv)) return MB_ERR_SHAPE;
     if (need && (!ws || ws_bytes < need || ((uintptr_t)ws & 255))) return MB_ERR_WORKSPACE;
     const size_t nh = (size_t)(slots ? n_slots : n_seq) * H * Dk * Dv * 4;
     const Span ins[8] = {{q, span_of(T, q_stride, H * Dk, es)}, {k, span_of(T, k_stride, G * Dk, es)}, {v, span_of(T, v_stride, G * Dv, es)},
@@ -931,12 +1271,14 @@ extern "C" mb_status mb_linear_attn(const void* q, const void* k, const void* v,
     A.log_decay = log_decay;
     A.s_in = A.s_carry = scale; A.s_up = 1.0f;
     A.shift = 1; A.reversed = 0;
-    A.n_seq = (int)n_seq; A.T = T; A.L = T / n_seq;
+    A.n_seq = (int)n_seq; A.T = (int)T; A.L = (int)(T / n_seq);
+    A.share = rep;
     A.cu = cu_seqlens;
     A.h0 = h0; A.has_h0 = has_h0; A.slots = slots; A.n_slots = n_slots;
     A.h_out = h_out;
+    use_plan(A, p, (char*)ws);
     mb_status st = launch_plan(A, p, (char*)ws, stream);
-    return st != MB_OK ? st : run(A, p, dtype, false, (char*)ws, stream);
+    return st != MB_OK ? st : run(A, nullptr, p, dtype, false, stream);
 }
 
 extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void* v, const float* log_decay,
@@ -948,7 +1290,7 @@ extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void
     using namespace mb;
     if (!dtype_ok(dtype)) return MB_ERR_DTYPE;
     if (!sizes_ok(n_seq, T, H, G, Dk, Dv)) return MB_ERR_SHAPE;
-    if (q_stride < H * Dk || k_stride < G * Dk || v_stride < G * Dv) return MB_ERR_SHAPE;
+    if (!strides_ok(q_stride, H * Dk) || !strides_ok(k_stride, G * Dk) || !strides_ok(v_stride, G * Dv)) return MB_ERR_SHAPE;
     if (n_seq == 0) return MB_OK;
     if (!cu_seqlens && T % n_seq) return MB_ERR_SHAPE;
     if (!log_decay || (T > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv))) return MB_ERR_NULL;
@@ -958,8 +1300,7 @@ extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void
         ((uintptr_t)h0 & 3) || ((uintptr_t)dh_out & 3) || ((uintptr_t)dh0 & 3))
         return MB_ERR_ALIGN;
     const BwdPlan bp = bwd_plan(n_seq, T, H, G, Dk, Dv, cu_seqlens != nullptr);
-    const int64_t tiles = (std::max(Dk, Dv) + kV - 1) / kV;
-    if (std::max(bp.q.nseg, bp.v.nseg) * H * tiles > 0x7fffffff || n_seq * H * 16 > 0x7fffffff) return MB_ERR_SHAPE;
+    if (!grid_ok(bp.q, n_seq, H, Dk) || !grid_ok(bp.v, n_seq, H, Dv)) return MB_ERR_SHAPE;
     if (bp.total && (!ws || ws_bytes < bp.total || ((uintptr_t)ws & 255))) return MB_ERR_WORKSPACE;
     const size_t nh = (size_t)n_seq * H * Dk * Dv * 4;
     const Span ins[8] = {{q, span_of(T, q_stride, H * Dk, es)}, {k, span_of(T, k_stride, G * Dk, es)}, {v, span_of(T, v_stride, G * Dv, es)},
@@ -973,19 +1314,21 @@ extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void
     }
     const int rep = (int)(H / G);
     char* w = (char*)ws;
-    float* fold = (float*)(w + bp.states);
+    float* fold_k = (float*)(w + bp.states);
+    float* fold_v = bp.both ? (float*)(w + bp.states + bp.fold[0]) : fold_k;
     LaArgs A{};
     A.H = (int)H;
     A.log_decay = log_decay;
-    A.n_seq = (int)n_seq; A.T = T; A.L = T / n_seq;
+    A.n_seq = (int)n_seq; A.T = (int)T; A.L = (int)(T / n_seq);
+    A.share = rep;
     A.cu = cu_seqlens;
     mb_status st;
-    auto add_up = [&](void* out, int64_t D) -> mb_status {
+    auto add_up = [&](const float* in, void* out, int64_t D) -> mb_status {
         const int64_t n = T * G * D;
         if (rep == 1 || n == 0) return MB_OK;
         const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 8192);
-        if (dtype == MB_F32) hipLaunchKernelGGL(k_la_fold<float>, dim3(blocks), dim3(256), 0, stream, fold, (float*)out, n, (int)G, rep, (int)D);
-        else hipLaunchKernelGGL(k_la_fold<bf16>, dim3(blocks), dim3(256), 0, stream, fold, (bf16*)out, n, (int)G, rep, (int)D);
+        if (dtype == MB_F32) hipLaunchKernelGGL(k_la_fold<float>, dim3(blocks), dim3(256), 0, stream, in, (float*)out, n, (int)G, rep, (int)D);
+        else hipLaunchKernelGGL(k_la_fold<bf16>, dim3(blocks), dim3(256), 0, stream, in, (bf16*)out, n, (int)G, rep, (int)D);
         return check_launch();
     };
     // dq: queries do, keys v, values k, forward; the state is S^T.
@@ -997,27 +1340,41 @@ extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void
     Q.s_in = Q.s_carry = scale; Q.s_up = 1.0f;
     Q.shift = 1; Q.reversed = 0;
     Q.h0 = h0; Q.transposed = 1;
-    if ((st = launch_plan(Q, bp.q, w, stream)) != MB_OK || (st = run(Q, bp.q, dtype, false, w, stream)) != MB_OK) return st;
+    use_plan(Q, bp.q, w);
+    if ((st = launch_plan(Q, bp.q, w, stream)) != MB_OK || (st = run(Q, nullptr, bp.q, dtype, false, stream)) != MB_OK) return st;
     // dk: queries v, keys do, values q, reversed; the state is R^T and holds the scale.
     LaArgs K = A;
-    K.a = v; K.b = d_o; K.c = q; K.o = rep > 1 ? (void*)fold : dk;
+    K.a = v; K.b = d_o; K.c = q; K.o = rep > 1 ? (void*)fold_k : dk;
     K.a_ts = v_stride; K.b_ts = H * Dv; K.c_ts = q_stride; K.o_ts = H * Dk;
     K.a_rep = rep; K.b_rep = K.c_rep = 1;
     K.Da = (int)Dv; K.Dv = (int)Dk;
     K.s_in = K.s_up = scale; K.s_carry = 1.0f;
     K.shift = 0; K.reversed = 1;
     K.h0 = dh_out; K.transposed = 1;
-    if ((st = run(K, bp.k, dtype, rep > 1, w, stream)) != MB_OK || (st = add_up(dk, Dk)) != MB_OK) return st;
-    // dv: queries k, keys q, values do, reversed; the state is R, its end the gradient of h0.
+    // dv: queries k, keys q, values do, reversed; the state is R.  The end of the state is the gradient of h0.
     LaArgs V = K;
-    V.a = k; V.b = q; V.c = d_o; V.o = rep > 1 ? (void*)fold : dv;
+    V.a = k; V.b = q; V.c = d_o; V.o = rep > 1 ? (void*)fold_v : dv;
     V.a_ts = k_stride; V.b_ts = q_stride; V.c_ts = H * Dv; V.o_ts = H * Dv;
     V.Da = (int)Dk; V.Dv = (int)Dv;
     V.transposed = 0;
-    V.h_out = dh0;
-    if ((st = launch_plan(V, bp.v, w, stream)) != MB_OK || (st = run(V, bp.v, dtype, rep > 1, w, stream)) != MB_OK ||
-        (st = add_up(dv, Dv)) != MB_OK)
-        return st;
+    if (bp.both) {
+        LaArgs& B = bp.swapped ? K : V;
+        const LaArgs& o = bp.swapped ? V : K;
+        const SecondArgs X{o.a, o.o, o.a_ts, o.o_ts, o.a_rep};
+        B.h_out = dh0;
+        use_plan(B, bp.v, w);
+        if ((st = launch_plan(B, bp.v, w, stream)) != MB_OK || (st = run(B, &X, bp.v, dtype, rep > 1, stream)) != MB_OK ||
+            (st = add_up(fold_k, dk, Dk)) != MB_OK || (st = add_up(fold_v, dv, Dv)) != MB_OK)
+            return st;
+    } else {
+        use_plan(K, bp.k, w);
+        if ((st = run(K, nullptr, bp.k, dtype, rep > 1, stream)) != MB_OK || (st = add_up(fold_k, dk, Dk)) != MB_OK) return st;
+        V.h_out = dh0;
+        use_plan(V, bp.v, w);
+        if ((st = launch_plan(V, bp.v, w, stream)) != MB_OK || (st = run(V, nullptr, bp.v, dtype, rep > 1, stream)) != MB_OK ||
+            (st = add_up(fold_v, dv, Dv)) != MB_OK)
+            return st;
+    }
     if (cu_seqlens && T > 0) {
         if (dtype == MB_F32)
             hipLaunchKernelGGL(k_la_clear<float>, dim3(256), dim3(256), 0, stream, cu_seqlens, (int)n_seq, T, (float*)dq, H * Dk,
@@ -1038,7 +1395,7 @@ extern "C" mb_status mb_linear_attn_step(const void* q, const void* k, const voi
     using namespace mb;
     if (!dtype_ok(dtype)) return MB_ERR_DTYPE;
     if (!sizes_ok(n, 0, H, G, Dk, Dv)) return MB_ERR_SHAPE;
-    if (q_stride < H * Dk || k_stride < G * Dk || v_stride < G * Dv) return MB_ERR_SHAPE;
+    if (!strides_ok(q_stride, H * Dk) || !strides_ok(k_stride, G * Dk) || !strides_ok(v_stride, G * Dv)) return MB_ERR_SHAPE;
     if (slots ? n_slots < 1 : n_slots != 0) return MB_ERR_SHAPE;
     if (n == 0) return MB_OK;
     if (!q || !k || !v || !log_decay || !o || !h_out) return MB_ERR_NULL;

@@ -80,7 +80,8 @@ CASES = [  # lens (packed) or (n, L), H, G, Dk, Dv, decay
     ((1, 300), 2, 2, 24, 100, "strong"), ((1, 300), 2, 2, 17, 33, "forget"),
     ([5, 0, 1, 64, 0, 200, 63], 4, 2, 64, 64, "mixed"), ([0, 0], 2, 2, 16, 16, "mixed"),
     ([700, 3, 0, 600, 1], 2, 1, 128, 64, "mixed"), ([1] * 300, 1, 1, 16, 16, "none"),
-    ([0, 900, 0], 2, 2, 40, 24, "mixed"), ([256, 512, 257], 1, 1, 64, 20, "none")]
+    ([1100, 3, 0, 600, 1], 2, 1, 128, 64, "mixed"), ([2] * 300 + [900] + [1] * 40, 2, 2, 16, 32, "mixed"),
+    ((1, 1100), 2, 2, 128, 72, "mixed"), ((3, 520), 3, 3, 20, 40, "none"), ([0, 900, 0], 2, 2, 40, 24, "mixed"), ([256, 512, 257], 1, 1, 64, 20, "none")]
 
 
 def _id(c):
@@ -156,20 +157,21 @@ def test_forward_split_chains(dtype):
 
 def test_offsets_out_of_range_stay_inside():
     """Offsets that decrease or leave [0, T] are empty or cut sequences: nothing outside is touched."""
-    T, H, D = 700, 2, 16
+    T, H, D = 1100, 2, 16
     d = inputs(12, T, H, H, D, D, "f32", 4)
-    cu = torch.tensor([-5, 300, 200, 900, 1000], dtype=torch.int32).cuda()   # [0,300), empty, [300,700), empty
+    cu = torch.tensor([-5, 300, 200, 1500, 2000], dtype=torch.int32).cuda()   # [0,300), empty, [300,1100), empty
     q, k, v = (d[x].cuda() for x in "qkv")
     o, h = mb.mb_linear_attn(q, k, v, decays(H).cuda(), cu_seqlens=cu, h0=d["h0"].cuda())
     ref = {x: d[x] for x in "qkv"}
-    ro, rh, Mo, Mh = reference({**ref}, decays(H), D ** -0.5, [300, 0, 400, 0], d["h0"])
-    close(o, ro, bound("f32", D, [400], Mo, ro), "o")
-    close(h, rh, bound("f32", D, [400], Mh, rh), "h")
+    ro, rh, Mo, Mh = reference({**ref}, decays(H), D ** -0.5, [300, 0, 800, 0], d["h0"])
+    close(o, ro, bound("f32", D, [800], Mo, ro), "o")
+    close(h, rh, bound("f32", D, [800], Mh, rh), "h")
 
 
 BWD = [((1, 1), 1, 1, 16, 16, "mixed"), ((2, 65), 4, 2, 64, 20, "mixed"), ((1, 300), 2, 2, 128, 64, "mixed"),
        ((1, 130), 2, 1, 17, 33, "none"), ((1, 700), 3, 1, 40, 128, "mixed"), ((1, 200), 2, 2, 16, 16, "forget"),
-       ([5, 0, 1, 64, 200], 4, 2, 64, 64, "mixed"), ([700, 3, 0, 300], 2, 1, 128, 32, "mixed"), ([0, 0], 1, 1, 16, 16, "mixed")]
+       ([5, 0, 1, 64, 200], 4, 2, 64, 64, "mixed"), ([700, 3, 0, 300], 2, 1, 128, 32, "mixed"),
+       ((1, 1100), 2, 1, 72, 128, "mixed"), ([900, 0, 300, 1], 2, 2, 64, 100, "mixed"), ([1100, 130], 2, 1, 128, 64, "mixed"), ([0, 0], 1, 1, 16, 16, "mixed")]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -284,9 +286,9 @@ def _graph(fn):
 
 def test_captured_and_replayed():
     """Forward, step and backward in one graph, replayed on new inputs with eager work in between."""
-    lens, H, G, Dk, Dv = [300, 1, 400], 2, 1, 64, 64
+    lens, H, G, Dk, Dv = [600, 1, 700], 2, 1, 64, 64
     T, n = sum(lens), len(lens)
-    cu = torch.tensor([0, 300, 301, 701], dtype=torch.int32).cuda()
+    cu = torch.tensor([0, 600, 601, 1301], dtype=torch.int32).cuda()
     d = {x: t.cuda() for x, t in inputs(61, T, H, G, Dk, Dv, "bf16", n, with_do=True).items()}
     ld, one = decays(H).cuda(), [t[:n].clone() for t in (d["q"], d["k"], d["v"])]
 
@@ -300,7 +302,7 @@ def test_captured_and_replayed():
         new = inputs(70 + r, T, H, G, Dk, Dv, "bf16", n, with_do=True)
         for x in d:
             d[x].copy_(new[x])
-        cu.copy_(torch.tensor([[0, 300, 301, 701], [0, 0, 700, 701], [0, 1, 2, 701], [0, 350, 700, 701]][r], dtype=torch.int32))
+        cu.copy_(torch.tensor([[0, 600, 601, 1301], [0, 0, 1300, 1301], [0, 1, 2, 1301], [0, 650, 1300, 1301]][r], dtype=torch.int32))
         want = fn()
         g.replay()
         torch.cuda.synchronize()

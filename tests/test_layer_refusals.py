@@ -37,7 +37,7 @@ def test_linear_attn(lib):
         assert attn(lib, dt=dt) == E_DTYPE
     for kw in (dict(n=-1), dict(T=-1), dict(H=0), dict(G=0), dict(G=3), dict(Dk=0), dict(Dk=129), dict(Dv=0), dict(Dv=129), dict(T=201),
                dict(qs=255), dict(ks=127), dict(vs=1), dict(T=1 << 31), dict(n=(1 << 20) + 1), dict(H=4097, G=4097),
-               dict(ns=3), dict(slots=8 * M, ns=0), dict(slots=8 * M, ns=-1)):
+               dict(qs=1 << 22), dict(ns=3), dict(slots=8 * M, ns=0), dict(slots=8 * M, ns=-1)):
         assert attn(lib, **kw) == E_SHAPE, kw
     for kw in (dict(q=0), dict(k=0), dict(v=0), dict(o=0), dict(ld=0)):
         assert attn(lib, **kw) == E_NULL, kw
