@@ -887,9 +887,9 @@ def mb_linear_attn(q, k, v, log_decay, *, scale=None, cu_seqlens=None, h0=None, 
     _check(h0, "h0", hs, f32, dev)
     if has_h0 is not None:
         _check(has_h0, "has_h0", (n,), torch.bool if has_h0.dtype == torch.bool else torch.uint8, dev)
-    o = torch.empty(lead + (H, Dv), dtype=q.dtype, device=dev) if o is None else _check(o, "o", lead + (H, Dv), q.dtype, dev)
+    o = q.new_empty(lead + (H, Dv)) if o is None else _check(o, "o", lead + (H, Dv), q.dtype, dev)
     if h_out is None:
-        h_out = h0 if slots is not None else torch.empty(hs, dtype=f32, device=dev)
+        h_out = h0 if slots is not None else log_decay.new_empty(hs)
     _check(h_out, "h_out", hs, f32, dev)
     ws, nws = _scratch(MB_OP_LINEAR_ATTN, dev, ws, (n, T, H, Dv, G, Dk, 1, 0))
     _call_on(dev, "mb_linear_attn", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), _ptr(h0), _ptr(has_h0),
@@ -915,7 +915,7 @@ def mb_linear_attn_step(q, k, v, log_decay, h, *, scale=None, slots=None, o=None
     n_slots, hs = _pool_args(h, h_out, slots, n, H, Dk, Dv, dev)
     _check(h, "h", hs, torch.float32, dev)
     h_out = h if h_out is None else _check(h_out, "h_out", hs, torch.float32, dev)
-    o = torch.empty((n, H, Dv), dtype=q.dtype, device=dev) if o is None else _check(o, "o", (n, H, Dv), q.dtype, dev)
+    o = q.new_empty((n, H, Dv)) if o is None else _check(o, "o", (n, H, Dv), q.dtype, dev)
     _call_on(dev, "mb_linear_attn_step", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(slots), _ptr(h), _ptr(h_out), _ptr(o),
              n, H, G, Dk, Dv, n_slots, *st, Dk ** -0.5 if scale is None else scale, code)
     return o, h_out
@@ -935,7 +935,7 @@ def mb_linear_attn_bwd(q, k, v, log_decay, do, *, scale=None, cu_seqlens=None, h
     out = []
     for t, name, shp, d in ((dq, "dq", lead + (H, Dk), dt), (dk, "dk", lead + (G, Dk), dt), (dv, "dv", lead + (G, Dv), dt),
                             (dh0, "dh0", hs, f32)):
-        out.append(torch.empty(shp, dtype=d, device=dev) if t is None else _check(t, name, shp, d, dev))
+        out.append(q.new_empty(shp, dtype=d) if t is None else _check(t, name, shp, d, dev))
     ws, nws = _scratch(MB_OP_LINEAR_ATTN_BWD, dev, ws, (n, T, H, Dv, G, Dk, 1, 0))
     _call_on(dev, "mb_linear_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), _ptr(h0), _ptr(do),
              _ptr(dh_out), *[_ptr(t) for t in out], n, T, H, G, Dk, Dv, *st, Dk ** -0.5 if scale is None else scale, code,
@@ -968,11 +968,11 @@ def _norm_args(x, weight, residual, residual_out, rstd):
     _check(weight, "weight", (D,), torch.float32, dev)
     _check(residual, "residual", tuple(x.shape), rdt, dev)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=rdt, device=dev) if residual is not None else None
+        residual_out = torch.empty_like(residual) if residual is not None else None
     else:
         _check(residual_out, "residual_out", tuple(x.shape), rdt, dev)
     shp = tuple(x.shape[:-1])
-    rstd = torch.empty(shp, dtype=torch.float32, device=dev) if rstd is None else _check(rstd, "rstd", shp, torch.float32, dev)
+    rstd = x.new_empty(shp, dtype=torch.float32) if rstd is None else _check(rstd, "rstd", shp, torch.float32, dev)
     return dev, code, MB_F32 if rdt == torch.float32 else MB_BF16, rows, D, stride, residual_out, rstd
 
 
@@ -982,7 +982,7 @@ def mb_rms_norm(x, weight=None, residual=None, *, eps=1e-5, y=None, residual_out
     the residual itself.  Returns (y, r, rstd): r is x when there is no residual."""
     torch = _torch()
     dev, code, rcode, rows, D, stride, r, rstd = _norm_args(x, weight, residual, residual_out, rstd)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y is None else _check(y, "y", tuple(x.shape), x.dtype, dev)
+    y = x.new_empty(x.shape) if y is None else _check(y, "y", tuple(x.shape), x.dtype, dev)
     _call_on(dev, "mb_rms_norm", _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(r), _ptr(rstd), rows, D, stride,
              float(eps), code, rcode)
     return y, x if r is None else r, rstd
@@ -998,9 +998,9 @@ def mb_rms_norm_fp8(x, weight=None, residual=None, *, group=0, eps=1e-5, y=None,
     f8 = torch.float8_e4m3fn
     if group not in (0, 32, 64, 128):
         raise ValueError("group must be 0, 32, 64 or 128, got %r" % (group,))
-    y = torch.empty(x.shape, dtype=f8, device=dev) if y is None else _check(y, "y", tuple(x.shape), f8, dev)
+    y = x.new_empty(x.shape, dtype=f8) if y is None else _check(y, "y", tuple(x.shape), f8, dev)
     ss = tuple(x.shape[:-1]) + (-(-D // group) if group else 1,)
-    scales = torch.empty(ss, dtype=torch.float32, device=dev) if scales is None else \
+    scales = x.new_empty(ss, dtype=torch.float32) if scales is None else \
         _check(scales, "scales", ss, torch.float32, dev)
     _call_on(dev, "mb_rms_norm_fp8", _ptr(x), _ptr(residual), _ptr(weight), _ptr(y), _ptr(scales), _ptr(r), _ptr(rstd), rows,
              D, stride, group, float(eps), code, rcode)
@@ -1030,10 +1030,10 @@ def mb_rms_norm_bwd(dy, r, rstd, weight=None, dr_in=None, *, dx=None, dr=None, d
     if same and dx is not None and dr is not None and dx is not dr:
         raise ValueError("dx and dr are one tensor when dy and r have the same dtype")
     dr = dx if same and dr is None else dr
-    dr = torch.empty(shp, dtype=r.dtype, device=dev) if dr is None else _check(dr, "dr", shp, r.dtype, dev)
+    dr = torch.empty_like(r) if dr is None else _check(dr, "dr", shp, r.dtype, dev)
     if not same:
-        dx = torch.empty(shp, dtype=dy.dtype, device=dev) if dx is None else _check(dx, "dx", shp, dy.dtype, dev)
-    dweight = torch.empty((D,), dtype=torch.float32, device=dev) if dweight is None else \
+        dx = torch.empty_like(dy) if dx is None else _check(dx, "dx", shp, dy.dtype, dev)
+    dweight = rstd.new_empty((D,)) if dweight is None else \
         _check(dweight, "dweight", (D,), torch.float32, dev)
     ws, nws = _scratch(MB_OP_RMS_NORM_BWD, dev, ws, (rows, 1, D, 1, 1, 1, 1, 0))
     _call_on(dev, "mb_rms_norm_bwd", _ptr(dy), _ptr(r), _ptr(rstd), _ptr(weight), _ptr(dr_in), None if same else _ptr(dx),
@@ -1067,7 +1067,7 @@ def mb_grad_norm_clip(grads, max_norm, *, eps=1e-6, out=None, norm=None, ws=None
             raise ValueError("%s must be contiguous" % name)
     if out is not None and list(map(T.numel, outs)) != sizes:
         raise ValueError("out must have the sizes of grads")
-    norm = torch.empty((), dtype=torch.float32, device=dev) if norm is None else _check(norm, "norm", (), torch.float32, dev)
+    norm = grads[0].new_empty((), dtype=torch.float32) if norm is None else _check(norm, "norm", (), torch.float32, dev)
     n = len(grads)
     gp = array.array("Q", map(T.data_ptr, grads))
     op = gp if out is None else array.array("Q", map(T.data_ptr, outs))

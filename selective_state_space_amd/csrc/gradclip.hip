@@ -10,9 +10,9 @@
 // workspace and every reader adds these in the same order: results do not depend on
 // the order in which workgroups run.
 //
-// The tensors' addresses travel as kernel arguments (kPer of them a launch, so a
-// captured graph holds them itself) into a table in the workspace that the two
-// passes read.
+// The tensors' addresses travel as kernel arguments, so a captured graph holds them
+// itself: up to kPer of them with the two passes' own launches, more through a table in the
+// workspace that launches of kPer each write first.
 #include "mb_internal.h"
 
 namespace mb {
@@ -22,7 +22,7 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 
 constexpr int kPer = 120;             // tensors whose table entries fit one launch's arguments
 constexpr int kMaxTensors = 1 << 16;
-constexpr int64_t kPiece = 16384;     // elements a workgroup takes at a time
+constexpr int64_t kPiece = 16384;     // bytes a workgroup takes at a time: four 16-byte vectors a thread
 constexpr int kGrid = 2048;           // partial sums at most
 
 struct Entry {
@@ -35,6 +35,9 @@ struct Entry {
 struct Batch {
     Entry e[kPer];
 };
+struct InWorkspace {
+    const Entry* e;
+};
 
 __global__ void k_table(Batch b, Entry* table, int at, int n) {
     // each entry is four words of eight bytes
@@ -43,14 +46,44 @@ __global__ void k_table(Batch b, Entry* table, int at, int n) {
     for (int i = threadIdx.x; i < n * 4; i += blockDim.x) dst[i] = src[i];
 }
 
-// The tensor that piece p belongs to: the last whose first piece is not behind p.
-__device__ __forceinline__ int tensor_of(const Entry* t, int n, int64_t p) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (t[mid].first <= p) lo = mid; else hi = mid - 1;
+// A workgroup's run of pieces, and the tensor that its first belongs to: the last whose first
+// piece is not behind it, found by all lanes of a wave together, 64 tensors a step.
+struct Run {
+    int64_t p, end;
+    int at;
+};
+template <typename Table>
+__device__ __forceinline__ Run run_of(const Table& t, int n, int64_t pieces, int64_t block) {
+    Run r;
+    r.p = pieces * block / gridDim.x;
+    r.end = pieces * (block + 1) / gridDim.x;
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64, i = lo + lane * step;
+        const int c = __popcll(__ballot(i < hi && t.e[i].first <= r.p));
+        lo += (c - 1) * step;
+        hi = min(lo + step, hi);
     }
-    return lo;
+    r.at = lo;
+    return r;
+}
+
+// Calls f(entry, first element, elements) for each piece of a run.
+template <typename T, typename Table, typename F>
+__device__ __forceinline__ void for_pieces(const Table& t, int n, const Run& r, F f) {
+    int at = r.at;
+    Entry e = t.e[at];
+    int64_t next = at + 1 < n ? t.e[at + 1].first : INT64_MAX;
+    for (int64_t p = r.p; p < r.end; ++p) {
+        if (p >= next) {                  // a tensor has at least one piece
+            e = t.e[++at];
+            next = at + 1 < n ? t.e[at + 1].first : INT64_MAX;
+        }
+        constexpr int64_t M = kPiece / sizeof(T);
+        const int64_t first = (p - e.first) * M, left = e.n - first;
+        f(e, first, (int)(left < M ? left : M));
+    }
 }
 
 __device__ __forceinline__ double sum_block(double v, double* lds) {
@@ -69,8 +102,7 @@ __device__ __forceinline__ double sum_piece(const T* g, int n) {
     int i = 0;
     if (((uintptr_t)g & 15) == 0) {
         const int nv = n / V;
-        for (int k = threadIdx.x; k < nv; k += 256) {
-            const u4 t = reinterpret_cast<const u4*>(g)[k];
+        const auto add = [&](u4 t) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if constexpr (sizeof(T) == 4) {
@@ -83,7 +115,17 @@ __device__ __forceinline__ double sum_piece(const T* g, int n) {
                     s1 += b * b;
                 }
             }
+        };
+        constexpr int B = 4;              // reads under way
+        int k = threadIdx.x;
+        for (; k + (B - 1) * 256 < nv; k += B * 256) {
+            u4 t[B];
+#pragma unroll
+            for (int j = 0; j < B; ++j) t[j] = reinterpret_cast<const u4*>(g)[k + j * 256];
+#pragma unroll
+            for (int j = 0; j < B; ++j) add(t[j]);
         }
+        for (; k < nv; k += 256) add(reinterpret_cast<const u4*>(g)[k]);
         i = nv * V;
     }
     for (int k = i + threadIdx.x; k < n; k += 256) {
@@ -93,28 +135,22 @@ __device__ __forceinline__ double sum_piece(const T* g, int n) {
     return s0 + s1;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_norm_parts(const Entry* __restrict__ t, int n, int64_t pieces, double* __restrict__ part) {
+template <typename T, typename Table>
+__global__ void __launch_bounds__(256, 8) k_norm_parts(Table t, int n, int64_t pieces, double* __restrict__ part) {
     __shared__ double lds[4];
     double s = 0.0;
-    for (int64_t p = blockIdx.x; p < pieces; p += gridDim.x) {
-        const Entry e = t[tensor_of(t, n, p)];
-        const int64_t at = (p - e.first) * kPiece;
-        const int64_t left = e.n - at;
-        s += sum_piece((const T*)e.g + at, (int)(left < kPiece ? left : kPiece));
-    }
+    for_pieces<T>(t, n, run_of(t, n, pieces, blockIdx.x), [&](const Entry& e, int64_t at, int m) { s += sum_piece((const T*)e.g + at, m); });
     s = sum_block(s, lds);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
 template <typename T>
-__device__ __forceinline__ void scale_piece(const T* g, T* o, int n, float f) {
+__device__ __forceinline__ void scale_piece(const T* g, T* o, int n, float f, bool stream) {
     constexpr int V = 16 / sizeof(T);
     int i = 0;
     if ((((uintptr_t)g | (uintptr_t)o) & 15) == 0) {
         const int nv = n / V;
-        for (int k = threadIdx.x; k < nv; k += 256) {
-            u4 t = reinterpret_cast<const u4*>(g)[k];
+        const auto scaled = [&](u4 t) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if constexpr (sizeof(T) == 4) {
@@ -124,30 +160,50 @@ __device__ __forceinline__ void scale_piece(const T* g, T* o, int n, float f) {
                     t[j] = (uint32_t)f32_to_bf16(a) | ((uint32_t)f32_to_bf16(b) << 16);
                 }
             }
-            reinterpret_cast<u4*>(o)[k] = t;
+            return t;
+        };
+        constexpr int B = 4;              // reads under way
+        int k = threadIdx.x;
+        for (; k + (B - 1) * 256 < nv; k += B * 256) {
+            u4 t[B];
+#pragma unroll
+            for (int j = 0; j < B; ++j) t[j] = reinterpret_cast<const u4*>(g)[k + j * 256];
+#pragma unroll
+            for (int j = 0; j < B; ++j) put(reinterpret_cast<u4*>(o) + k + j * 256, scaled(t[j]), stream);
         }
+        for (; k < nv; k += 256) reinterpret_cast<u4*>(o)[k] = scaled(reinterpret_cast<const u4*>(g)[k]);
         i = nv * V;
     }
     for (int k = i + threadIdx.x; k < n; k += 256) store_out(o + k, to_f32(g[k]) * f);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_clip(const Entry* __restrict__ t, int n, int64_t pieces, const double* __restrict__ part,
-                                              int parts, float* __restrict__ norm_out, float max_norm, float eps) {
+// The pieces in the opposite order: what the first pass read last may still lie in the last-level cache.
+template <typename T, typename Table>
+__global__ void __launch_bounds__(256) k_clip(Table t, int n, int64_t pieces, const double* __restrict__ part, int parts,
+                                              float* __restrict__ norm_out, float max_norm, float eps, bool stream) {
     __shared__ double lds[4];
     double s = 0.0;
     for (int i = threadIdx.x; i < parts; i += 256) s += part[i];
+    const Run r = run_of(t, n, pieces, gridDim.x - 1 - blockIdx.x);
     const float norm = (float)sqrt(sum_block(s, lds));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
     const float c = max_norm / (norm + eps);
     const float f = c > 1.0f ? 1.0f : c;              // NaN stays
-    for (int64_t p = blockIdx.x; p < pieces; p += gridDim.x) {
-        const Entry e = t[tensor_of(t, n, p)];
-        if (f == 1.0f && e.g == e.o) continue;        // in place and nothing to scale
-        const int64_t at = (p - e.first) * kPiece;
-        const int64_t left = e.n - at;
-        scale_piece((const T*)e.g + at, (T*)e.o + at, (int)(left < kPiece ? left : kPiece), f);
-    }
+    for_pieces<T>(t, n, r, [&](const Entry& e, int64_t at, int m) {
+        if (f == 1.0f && e.g == e.o) return;          // in place and nothing to scale
+        scale_piece((const T*)e.g + at, (T*)e.o + at, m, f, stream);
+    });
+}
+
+template <typename T, typename Table>
+mb_status passes(const Table& t, int n, int64_t pieces, double* part, float* norm, float max_norm, float eps, hipStream_t s) {
+    const bool stream = pieces * 2 * kPiece > (int64_t)kStreamBytes;
+    const int grid = (int)(pieces < kGrid ? pieces : kGrid);
+    hipLaunchKernelGGL((k_norm_parts<T, Table>), dim3(grid), dim3(256), 0, s, t, n, pieces, part);
+    mb_status st = check_launch();
+    if (st != MB_OK) return st;
+    hipLaunchKernelGGL((k_clip<T, Table>), dim3(grid), dim3(256), 0, s, t, n, pieces, part, grid, norm, max_norm, eps, stream);
+    return check_launch();
 }
 
 size_t table_bytes(int64_t n) { return ((size_t)n * sizeof(Entry) + 255) / 256 * 256; }
@@ -169,6 +225,7 @@ extern "C" mb_status mb_grad_norm_clip(const void* const* grads, void* const* ou
     if (n < 0 || n > kMaxTensors || !(max_norm >= 0.0f) || !(eps >= 0.0f) || eps > 3.0e38f) return MB_ERR_SHAPE;
     if (!norm || (n > 0 && (!grads || !sizes))) return MB_ERR_NULL;
     const size_t es = dtype_size(dtype);
+    const int64_t piece = kPiece / (int64_t)es;
     if ((uintptr_t)norm & 3) return MB_ERR_ALIGN;
     const size_t need = grad_clip_workspace(n);
     if (n > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 255))) return MB_ERR_WORKSPACE;
@@ -183,21 +240,22 @@ extern "C" mb_status mb_grad_norm_clip(const void* const* grads, void* const* ou
         if ((o != grads[i] && overlaps(o, b, grads[i], b)) || overlaps(o, b, norm, 4) || overlaps(grads[i], b, norm, 4) ||
             overlaps(ws, need, o, b) || overlaps(ws, need, grads[i], b))
             return MB_ERR_ALIAS;
-        total += (sizes[i] + kPiece - 1) / kPiece;
+        total += (sizes[i] + piece - 1) / piece;
     }
     if (n > 0 && overlaps(ws, need, norm, 4)) return MB_ERR_ALIAS;
     if (total == 0) return copy_state(nullptr, norm, 1, stream);
     Entry* table = (Entry*)ws;
     double* part = (double*)((char*)ws + table_bytes(n));
+    int64_t filled = 0;
+    for (int64_t i = 0; i < n; ++i) filled += sizes[i] != 0;
     int used = 0, at = 0;
     int64_t pieces = 0;
     Batch b;
     for (int64_t i = 0; i < n; ++i) {
-        if (sizes[i]) {
-            b.e[used++] = Entry{grads[i], outs ? outs[i] : const_cast<void*>(grads[i]), sizes[i], pieces};
-            pieces += (sizes[i] + kPiece - 1) / kPiece;
-        }
-        if (used == kPer || (i == n - 1 && used)) {
+        if (sizes[i] == 0) continue;
+        b.e[used++] = Entry{grads[i], outs ? outs[i] : const_cast<void*>(grads[i]), sizes[i], pieces};
+        pieces += (sizes[i] + piece - 1) / piece;
+        if (filled > kPer && (used == kPer || at + used == filled)) {
             hipLaunchKernelGGL(k_table, dim3(1), dim3(256), 0, stream, b, table, at, used);
             mb_status st = check_launch();
             if (st != MB_OK) return st;
@@ -205,13 +263,11 @@ extern "C" mb_status mb_grad_norm_clip(const void* const* grads, void* const* ou
             used = 0;
         }
     }
-    const int grid = (int)(pieces < kGrid ? pieces : kGrid);
-    if (dtype == MB_F32) {
-        hipLaunchKernelGGL(k_norm_parts<float>, dim3(grid), dim3(256), 0, stream, table, at, pieces, part);
-        hipLaunchKernelGGL(k_clip<float>, dim3(grid), dim3(256), 0, stream, table, at, pieces, part, grid, norm, max_norm, eps);
-    } else {
-        hipLaunchKernelGGL(k_norm_parts<bf16>, dim3(grid), dim3(256), 0, stream, table, at, pieces, part);
-        hipLaunchKernelGGL(k_clip<bf16>, dim3(grid), dim3(256), 0, stream, table, at, pieces, part, grid, norm, max_norm, eps);
+    if (filled > kPer) {
+        const InWorkspace t{table};
+        return dtype == MB_F32 ? passes<float>(t, at, pieces, part, norm, max_norm, eps, stream)
+                               : passes<bf16>(t, at, pieces, part, norm, max_norm, eps, stream);
     }
-    return check_launch();
+    return dtype == MB_F32 ? passes<float>(b, used, pieces, part, norm, max_norm, eps, stream)
+                           : passes<bf16>(b, used, pieces, part, norm, max_norm, eps, stream);
 }

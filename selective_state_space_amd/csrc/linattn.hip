@@ -20,8 +20,12 @@
 // i + 1 and C - j instead of C - 1 - j.
 //
 // A sequence is cut into segments so that the device is full: k_la_state computes
-// each segment's own end state, k_la_carry composes them into the states that enter
-// the segments, k_la_out walks the chunks of every segment from there.
+// each segment's own end state (the first one's from h0), and k_la_out walks the chunks of
+// every segment from the state that enters it, composed from the end states in front of it: by
+// the walk itself where a sequence has few segments, by k_la_carry beforehand where it has many.
+// A sequence of n segments has n places for states: end states 0 to n - 2, and in the last, which has
+// no end state to hand on, a copy of h0 (h_out may be h0, and the last segment may write it
+// before the first one reads it).
 #include <algorithm>
 
 #include "mb_internal.h"
@@ -41,6 +45,7 @@ constexpr int kC = 64;          // tokens of a chunk
 constexpr int kV = 64;          // value columns of a workgroup
 constexpr int kMaxDim = 128;    // of keys and of values
 constexpr int kThreads = 256;     // k_la_state
+constexpr int kFewSegments = 8; // up to these the walk composes its entering state itself
 constexpr int kWalkThreads = 512; // k_la_out: four waves make outputs, four carry the state
 
 // A segment of a sequence.  A sequence of L tokens is cut into ceil(L / target) segments (one if it
@@ -473,6 +478,25 @@ __global__ void __launch_bounds__(64) k_la_plan(LaArgs A, Seg* plan, int2* seqs)
     for (int i = l.segs + lane; i < A.nseg; i += 64) plan[i].seq = -1;
 }
 
+// The four state values of accumulator i of a wave's lane: rows 16 i + 4 g + r, one column.
+__device__ __forceinline__ f4 load_h0(const LaArgs& A, int seq, int h, int tile, int wave, int i, int lane) {
+    f4 v = {0, 0, 0, 0};
+    const int64_t row = state_row(A, seq);
+    if (!A.h0 || row < 0 || (A.has_h0 && !A.has_h0[seq])) return v;
+    const float* p = A.h0 + (row * A.H + h) * (int64_t)A.Da * A.Dv;
+    const int col = tile * kV + 16 * wave + (lane & 15), r0 = 16 * i + 4 * (lane >> 4);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (col < A.Dv && r0 + r < A.Da) v[r] = A.transposed ? p[(int64_t)col * A.Da + r0 + r] : p[(int64_t)(r0 + r) * A.Dv + col];
+    return v;
+}
+
+// Accumulator i of a wave's lane in a state's place in the workspace.
+template <int DA>
+__device__ __forceinline__ f4* state_piece(const LaArgs& A, int at, int h, int tile, int wave, int i, int lane) {
+    return reinterpret_cast<f4*>(A.states + state_at(A, at, h, tile, DA)) + (wave * (DA / 16) + i) * 64 + lane;
+}
+
 // ---------------------------------------------------------- segment state ----
 template <typename T, int DA, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_la_state(LaArgs A) {
@@ -504,6 +528,13 @@ __global__ void __launch_bounds__(kThreads) k_la_state(LaArgs A) {
         v.load(window(vp + c0 * cs, A.c_ts, A.reversed, n, vw), vw, threadIdx.x);
     };
     load(0);
+    if (g.idx == 0) {
+#pragma unroll
+        for (int i = 0; i < DA / 16; ++i) {
+            S[i] = load_h0(A, g.seq, u.h, u.tile, wave, i, lane);
+            *state_piece<DA>(A, g.state + g.count - 1, u.h, u.tile, wave, i, lane) = S[i];
+        }
+    }
     for (int c0 = 0; c0 < g.n; c0 += kC) {       // whole chunks: only a last segment has a ragged one
         __syncthreads();
         k.store(kt, threadIdx.x);
@@ -514,27 +545,12 @@ __global__ void __launch_bounds__(kThreads) k_la_state(LaArgs A) {
         for (int i = 0; i < DA / 16; ++i) S[i] *= carry;
         update_state<T, DA>(S, kt, vt, wt, wave, lane);
     }
-    float* out = A.states + state_at(A, g.state, u.h, u.tile, DA);
 #pragma unroll
-    for (int i = 0; i < DA / 16; ++i)
-        *reinterpret_cast<f4*>(out + ((wave * (DA / 16) + i) * 64 + lane) * 4) = S[i];
-}
-
-// The four state values of accumulator i of a wave's lane: rows 16 i + 4 g + r, one column.
-__device__ __forceinline__ f4 load_h0(const LaArgs& A, int seq, int h, int tile, int wave, int i, int lane) {
-    f4 v = {0, 0, 0, 0};
-    const int64_t row = state_row(A, seq);
-    if (!A.h0 || row < 0 || (A.has_h0 && !A.has_h0[seq])) return v;
-    const float* p = A.h0 + (row * A.H + h) * (int64_t)A.Da * A.Dv;
-    const int col = tile * kV + 16 * wave + (lane & 15), r0 = 16 * i + 4 * (lane >> 4);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        if (col < A.Dv && r0 + r < A.Da) v[r] = A.transposed ? p[(int64_t)col * A.Da + r0 + r] : p[(int64_t)(r0 + r) * A.Dv + col];
-    return v;
+    for (int i = 0; i < DA / 16; ++i) *state_piece<DA>(A, g.state, u.h, u.tile, wave, i, lane) = S[i];
 }
 
 // ---------------------------------------------------------------- carry ----
-// In place over a sequence's segments: the state that enters each of them.  A workgroup
+// In place over a sequence's places: the state that enters each of its segments.  A workgroup
 // takes 1024 values (256 lanes of four) of one (sequence, head, tile).
 template <int DA>
 __global__ void __launch_bounds__(256) k_la_carry(LaArgs A) {
@@ -547,22 +563,21 @@ __global__ void __launch_bounds__(256) k_la_carry(LaArgs A) {
     const int h = b % A.H, seq = b / A.H;
     int first, n, len;
     sequence(A, seq, first, n, len);
-    if (n <= 1) return;                          // the walk reads h0 itself
-    const int frag = part * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    f4 run = load_h0(A, seq, h, tile, frag / (DA / 16), frag % (DA / 16), lane);
+    if (n <= kFewSegments) return;
     const float f = power(log2_decay(A, h), ((len + n - 1) / n + kC - 1) / kC * kC);
-    float* p = A.states + state_at(A, first, h, tile, DA) + (frag * 64 + lane) * 4;
-    const int64_t step = state_at(A, 1, 0, 0, DA);
+    f4* p = reinterpret_cast<f4*>(A.states + state_at(A, first, h, tile, DA)) + part * 256 + threadIdx.x;
+    const int64_t step = state_at(A, 1, 0, 0, DA) / 4;
+    f4 run = p[0];
+    p[0] = p[(n - 1) * step];                    // h0
     constexpr int B = 8;                         // states read ahead of the first one's use
-    for (int i = 0; i < n; i += B) {
+    for (int i = 1; i < n; i += B) {
         f4 own[B];
 #pragma unroll
-        for (int j = 0; j < B; ++j)
-            own[j] = i + j + 1 < n ? *reinterpret_cast<const f4*>(p + (i + j) * step) : f4{0, 0, 0, 0};
+        for (int j = 0; j < B; ++j) own[j] = i + j + 1 < n ? p[(i + j) * step] : f4{0, 0, 0, 0};
 #pragma unroll
         for (int j = 0; j < B; ++j) {
             if (i + j >= n) break;
-            *reinterpret_cast<f4*>(p + (i + j) * step) = run;
+            p[(i + j) * step] = run;
             run = run * f + own[j];
         }
     }
@@ -727,9 +742,16 @@ __device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const
 #pragma unroll
         for (int i = 0; i < DA / 16; ++i) S[i] = load_h0(A, g.seq, un.h, un.tile, wave, i, lane);
     } else {
-        const float* in = A.states + state_at(A, g.state, un.h, un.tile, DA);
+        const int base = g.state - g.idx;
+        const bool few = g.count <= kFewSegments;
+        const int from = !few ? g.state : g.idx ? base : base + g.count - 1;
 #pragma unroll
-        for (int i = 0; i < DA / 16; ++i) S[i] = *reinterpret_cast<const f4*>(in + ((wave * (DA / 16) + i) * 64 + lane) * 4);
+        for (int i = 0; i < DA / 16; ++i) S[i] = *state_piece<DA>(A, from, un.h, un.tile, wave, i, lane);
+        const float each = power(l2, g.p0 / max(g.idx, 1));
+        for (int j = 1; few && j < g.idx; ++j) {
+#pragma unroll
+            for (int i = 0; i < DA / 16; ++i) S[i] = S[i] * each + *state_piece<DA>(A, base + j, un.h, un.tile, wave, i, lane);
+        }
     }
     float f = power(l2, kC);
     const int sw = SL::at_state(16 * wave + m, 4 * gr);
@@ -993,6 +1015,7 @@ struct StepArgs {
     int64_t n, n_slots, q_ts, k_ts, v_ts;
     int H, rep, Dk, Dv, cols, tiles;     // value columns of a workgroup, workgroups of a row's head
     float scale;
+    bool stream;                         // states past the caches
 };
 
 // A workgroup owns CW = 4 LN value columns of one (row, head): LN lanes side by side hold
@@ -1061,7 +1084,7 @@ __global__ void __launch_bounds__(256) k_la_step(StepArgs A) {
             }
             if (A.h_out && slot >= 0 && in) {
                 float* p = A.h_out + at + (int64_t)r * A.Dv;
-                if constexpr (VEC) *reinterpret_cast<f4*>(p) = f4{s[i][0], s[i][1], s[i][2], s[i][3]};
+                if constexpr (VEC) put(reinterpret_cast<f4*>(p), f4{s[i][0], s[i][1], s[i][2], s[i][3]}, A.stream);
                 else *p = s[i][0];
             }
         }
@@ -1138,9 +1161,11 @@ mb_status run_passes(const LaArgs& A, const SecondArgs* X, const Plan& p, hipStr
         hipLaunchKernelGGL((k_la_state<T, DA, VEC>), grid, dim3(kThreads), 0, s, A);
         mb_status st = check_launch();
         if (st != MB_OK) return st;
-        hipLaunchKernelGGL(k_la_carry<DA>, dim3((unsigned)((int64_t)A.n_seq * A.H * A.nv * (DA * kV / 1024))), dim3(256), 0, s, A);
-        st = check_launch();
-        if (st != MB_OK) return st;
+        // some sequence may have many segments
+        if ((A.per_seq ? A.per_seq : (A.T + A.target - 1) / A.target) > kFewSegments) {
+            hipLaunchKernelGGL(k_la_carry<DA>, dim3((unsigned)((int64_t)A.n_seq * A.H * A.nv * (DA * kV / 1024))), dim3(256), 0, s, A);
+            if ((st = check_launch()) != MB_OK) return st;
+        }
     }
     if (X) hipLaunchKernelGGL((k_la_dkdv<T, TO, DA, VEC>), grid, wide, 0, s, A, *X);
     else hipLaunchKernelGGL((k_la_out<T, TO, DA, VEC>), grid, wide, 0, s, A);
@@ -1409,7 +1434,7 @@ extern "C" mb_status mb_linear_attn_step(const void* q, const void* k, const voi
     if (overlaps_any(o, no, ins, 6) || overlaps_any(h_out, nh, ins, h_out == h_in ? 5 : 6) || overlaps(o, no, h_out, nh)) return MB_ERR_ALIAS;
     const bool vec = Dv % 4 == 0 && al16(h_in) && al16(h_out);
     StepArgs A{q, k, v, log_decay, slots, h_in, h_out, o, n, n_slots, q_stride, k_stride, v_stride,
-               (int)H, (int)(H / G), (int)Dk, (int)Dv, 0, 0, scale};
+               (int)H, (int)(H / G), (int)Dk, (int)Dv, 0, 0, scale, (size_t)n * H * Dk * Dv * 8 > kStreamBytes};
     // Few rows: narrow column tiles, so that the one token's states are read by more compute
     // units; many rows: a tile as wide as a row of the state.
     const bool few = n * H < 2 * device_cu_count();

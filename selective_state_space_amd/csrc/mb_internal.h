@@ -91,6 +91,25 @@ __device__ __forceinline__ bf16 f32_to_bf16(float f) {
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(bf16* p, float v) { *p = f32_to_bf16(v); }
 
+// Calls of whole-line stores that move more than this, half of the 256 MB last-level cache, store
+// their outputs past the caches: what they write would be gone before anyone reads it, and its
+// lines, written back during the next call, take that call's bandwidth.  Measured: 235 MB of the norm to
+// 8 bits 57.4 -> 51.2 us, 517 MB of clipping 170 -> 147 us, 270 MB of decode states 60.4 -> 46.4 us;
+// the norm's backward (79.6 -> 82.2 us) and linear attention's 64-byte pieces of rows (packed prompt 86.6
+// -> 91.1 us) lose by it and keep ordinary stores.
+constexpr size_t kStreamBytes = (size_t)128 << 20;
+
+template <typename T>
+__device__ __forceinline__ void put(T* p, T v, bool stream) {
+    if (stream) {
+        asm volatile("");     // without these the two stores are merged into one of the ordinary kind
+        __builtin_nontemporal_store(v, p);
+        asm volatile("");
+    } else {
+        *p = v;
+    }
+}
+
 // exp(v) through the hardware base-2 exponential; callers pass v * log2(e).
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 

@@ -17,6 +17,7 @@ namespace {
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kAmaxMin = 0x1p-96f;     // keeps 1 / scale and y / scale in range for a group of zeros
@@ -52,18 +53,18 @@ __device__ __forceinline__ void load_vec(const bf16* p, float* v) {
 }
 
 template <int VEC>
-__device__ __forceinline__ void store_vec(float* p, const float* v) {
+__device__ __forceinline__ void store_vec(float* p, const float* v, bool stream) {
     if constexpr (VEC == 1) {
         *p = v[0];
     } else {
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i)
-            reinterpret_cast<f4*>(p)[i] = f4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+            put(reinterpret_cast<f4*>(p) + i, f4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, stream);
     }
 }
 
 template <int VEC>
-__device__ __forceinline__ void store_vec(bf16* p, const float* v) {
+__device__ __forceinline__ void store_vec(bf16* p, const float* v, bool stream) {
     if constexpr (VEC == 1) {
         *p = f32_to_bf16(v[0]);
     } else {
@@ -71,7 +72,7 @@ __device__ __forceinline__ void store_vec(bf16* p, const float* v) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             t[i] = (uint32_t)f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
-        *reinterpret_cast<u4*>(p) = t;
+        put(reinterpret_cast<u4*>(p), t, stream);
     }
 }
 
@@ -135,6 +136,7 @@ struct NormArgs {
     int64_t rows, x_stride;
     int D, group, ngroups;
     float eps;
+    bool stream;
 };
 
 // MODE 0: y in the type of x.  MODE 1: e4m3 with scales.
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         const int d = (c * TPR + lane) * VEC;
-        if (a.r_out && live && d < a.D) store_vec<VEC>((TR*)a.r_out + row * a.D + d, v + c * VEC);
+        if (a.r_out && live && d < a.D) store_vec<VEC>((TR*)a.r_out + row * a.D + d, v + c * VEC, a.stream);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) ss = fmaf(v[c * VEC + k], v[c * VEC + k], ss);
     }
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
 #pragma unroll
         for (int k = 0; k < VEC; ++k) v[c * VEC + k] = v[c * VEC + k] * rstd * w[k];
         if constexpr (MODE == 0) {
-            if (live && d < a.D) store_vec<VEC>((TX*)a.y + row * a.D + d, v + c * VEC);
+            if (live && d < a.D) store_vec<VEC>((TX*)a.y + row * a.D + d, v + c * VEC, a.stream);
         }
     }
     if constexpr (MODE == 1) {
@@ -257,8 +259,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
                         int p = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * k], t[4 * k + 1], 0, false);
                         o[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * k + 2], t[4 * k + 3], p, true);
                     }
-                    if constexpr (VEC == 8) *reinterpret_cast<uint2*>(q + d) = make_uint2(o[0], o[1]);
-                    else *reinterpret_cast<uint32_t*>(q + d) = o[0];
+                    if constexpr (VEC == 8) put(reinterpret_cast<u2*>(q + d), u2{o[0], o[1]}, a.stream);
+                    else put(reinterpret_cast<uint32_t*>(q + d), o[0], a.stream);
                 }
             }
         }
@@ -338,8 +340,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm_bwd(NormBwdA
 #pragma unroll
                 for (int k = 0; k < VEC; ++k)
                     o[k] = fmaf(rstd, fmaf(-xh[c * VEC + k], dot, dy[c * VEC + k]), in[c * VEC + k]);
-                if (a.dr) store_vec<VEC>((TR*)a.dr + row * a.D + d, o);
-                if (a.dx) store_vec<VEC>((TX*)a.dx + row * a.D + d, o);
+                if (a.dr) store_vec<VEC>((TR*)a.dr + row * a.D + d, o, false);
+                if (a.dx) store_vec<VEC>((TX*)a.dx + row * a.D + d, o, false);
             }
         }
     }
@@ -359,24 +361,46 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm_bwd(NormBwdA
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         const int d = (c * TPR + lane) * VEC;
-        if (d < a.D) store_vec<VEC>(a.part + (int64_t)blockIdx.x * a.D + d, dw + c * VEC);
+        if (d < a.D) store_vec<VEC>(a.part + (int64_t)blockIdx.x * a.D + d, dw + c * VEC, false);
     }
 }
 
-// dw = the sum of the workgroups' partial rows: 32 columns a workgroup, 8 rows at a time.
+// dw = the sum of the workgroups' partial rows: 32 columns a workgroup, the rows dealt to its
+// VEC * 8 groups of lanes, eight reads of each under way at a time.
+template <int VEC>
 __global__ void __launch_bounds__(256) k_dw_sum(const float* __restrict__ part, float* __restrict__ dw, int n, int D) {
-    __shared__ float red[8][33];
-    const int col = threadIdx.x & 31, sub = threadIdx.x >> 5;
-    const int d = blockIdx.x * 32 + col;
-    float s = 0.0f;
-    if (d < D)
-        for (int i = sub; i < n; i += 8) s += part[(int64_t)i * D + d];
-    red[sub][col] = s;
-    __syncthreads();
-    if (sub == 0 && d < D) {
+    constexpr int LN = 32 / VEC, SUB = 256 / LN;
+    __shared__ float red[SUB][33];
+    const int ln = threadIdx.x % LN, sub = threadIdx.x / LN;
+    const int d = blockIdx.x * 32 + ln * VEC;
+    float s[VEC];
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += red[i][col];
-        dw[d] = s;
+    for (int k = 0; k < VEC; ++k) s[k] = 0.0f;
+    if (d < D)
+        for (int i = sub; i < n; i += 8 * SUB) {
+            float t[8][VEC];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (i + j * SUB < n) {
+                    load_vec<VEC>(part + (int64_t)(i + j * SUB) * D + d, t[j]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k) t[j][k] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) s[k] += t[j][k];
+        }
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) red[sub][ln * VEC + k] = s[k];
+    __syncthreads();
+    if (threadIdx.x < 32 && blockIdx.x * 32 + (int)threadIdx.x < D) {
+        float x = 0.0f;
+#pragma unroll 8
+        for (int i = 0; i < SUB; ++i) x += red[i][threadIdx.x];
+        dw[blockIdx.x * 32 + threadIdx.x] = x;
     }
 }
 
@@ -423,7 +447,8 @@ mb_status norm(const void* x, const void* res, const float* w, void* y, float* s
         for (int j = 0; j < i; ++j)
             if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return MB_ERR_ALIAS;
     }
-    NormArgs a{x, res, w, y, scales, r_out, rstd, rows, x_stride, (int)D, (int)group, (int)ng, eps};
+    NormArgs a{x, res, w, y, scales, r_out, rstd, rows, x_stride, (int)D, (int)group, (int)ng, eps,
+               nx + outs[0].bytes + (res ? n * er : 0) + (r_out ? n * er : 0) > kStreamBytes};
     const int V = dtype == MB_BF16 ? 8 : 4;
     const bool vec = D % V == 0 && x_stride % V == 0 && vec_ok(x) && vec_ok(res) && vec_ok(w) && vec_ok(y) && vec_ok(r_out);
     if (dtype == MB_F32)
@@ -518,6 +543,8 @@ extern "C" mb_status mb_rms_norm_bwd(const void* dy, const void* r, const float*
         vec ? launch_bwd<bf16, bf16, 8>(a, grid, stream) : launch_bwd<bf16, bf16, 1>(a, grid, stream);
     mb_status st = check_launch();
     if (st != MB_OK || !need) return st;
-    hipLaunchKernelGGL(k_dw_sum, dim3((unsigned)((D + 31) / 32)), dim3(256), 0, stream, (const float*)ws, dweight, grid, (int)D);
+    const dim3 cols((unsigned)((D + 31) / 32));
+    if (D % 4 == 0) hipLaunchKernelGGL(k_dw_sum<4>, cols, dim3(256), 0, stream, (const float*)ws, dweight, grid, (int)D);
+    else hipLaunchKernelGGL(k_dw_sum<1>, cols, dim3(256), 0, stream, (const float*)ws, dweight, grid, (int)D);
     return check_launch();
 }
