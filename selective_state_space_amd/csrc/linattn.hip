@@ -44,9 +44,8 @@ typedef float f2 __attribute__((ext_vector_type(2)));
 constexpr int kC = 64;          // tokens of a chunk
 constexpr int kV = 64;          // value columns of a workgroup
 constexpr int kMaxDim = 128;    // of keys and of values
-constexpr int kThreads = 256;     // k_la_state
 constexpr int kFewSegments = 8; // up to these the walk composes its entering state itself
-constexpr int kWalkThreads = 512; // k_la_out: four waves make outputs, four carry the state
+constexpr int kWalkThreads = 512;
 
 // A segment of a sequence.  A sequence of L tokens is cut into ceil(L / target) segments (one if it
 // is empty) of equal length, rounded up to whole chunks.
@@ -207,6 +206,15 @@ __device__ __forceinline__ float log2_decay(const LaArgs& A, int h) {
 }
 __device__ __forceinline__ float power(float l2, int64_t n) { return exp2_fast(l2 * (float)n); }
 
+// A barrier for what waves share through LDS: it waits for this wave's LDS operations alone.  The
+// ordinary one would also wait for the loads of the next chunk and for the stores of this one's outputs.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);          // lgkmcnt(0), no other counter
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // ------------------------------------------------------------- fragments ----
 // A fragment is 16 bytes a lane: bf16 eight values of one 16x16x32 product, fp32
 // four values of four 16x16x4 products (lane group g then holds contraction indices
@@ -323,14 +331,12 @@ struct Tiled {
 __device__ __forceinline__ void forget(int& x) { asm volatile("" : "+v"(x)); }
 
 // A tile of kC tokens by W columns: its global reads into registers, and from there to LDS.
-template <typename T, int W, bool VEC>
+template <typename T, int W, bool VEC, int NT>
 struct Tile {
-    static constexpr int NT = kThreads;
     static constexpr int VE = Frag<T>::VE;
     static constexpr int PER_ROW = W / VE;
     static constexpr int N = kC * PER_ROW / NT;
-    static constexpr int SIZE = kC * Tiled<T, W>::ROW;
-    static_assert(N * NT == kC * PER_ROW, "whole vectors for every thread");
+    static_assert(N > 0 && N * NT == kC * PER_ROW, "whole vectors for every thread");
     u4 v[N];
 
     __device__ __forceinline__ void load(const Window& w, int width, int thread) {
@@ -356,17 +362,20 @@ struct Tile {
 // bf16: w V does not fit bf16, and one rounding of it would leave 2^-9 in a state that
 // is kept in fp32.  It is cut into three bf16 pieces (8 + 8 + 8 bits hold all 24 of the
 // product), three products on the exact K.
-template <typename T, int DA>
-__device__ __forceinline__ void update_state(f4 (&S)[DA / 16], const T* kt, const T* vt, const float* wt, int wave, int lane) {
+// PARTS = 2: one half of the chunk's tokens, `part`; another wave adds the other half.
+template <typename T, int DA, int PARTS = 1>
+__device__ __forceinline__ void update_state(f4 (&S)[DA / 16], const T* kt, const T* vt, const float* wt, int wave, int lane, int part = 0) {
     using KL = Tiled<T, DA>;
     using VL = Tiled<T, kV>;
     const int m = lane & 15, g = lane >> 4;
     if constexpr (sizeof(T) == 2) {
-        int ka = KL::at(8 * g + (m >> 2), 4 * (m & 3)), va = VL::at(8 * g + (m >> 2), 16 * wave + 4 * (m & 3));
+        int ka = KL::at(8 * g + (m >> 2), 4 * (m & 3)) + part * 32 * KL::ROW;
+        int va = VL::at(8 * g + (m >> 2), 16 * wave + 4 * (m & 3)) + part * 32 * VL::ROW;
+        wt += part * 32;
         forget(ka);
         forget(va);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 2 / PARTS; ++s) {
             const u2 v0 = tr4(vt + VL::go(va, 32 * s, 0)), v1 = tr4(vt + VL::go(va, 32 * s, 0, true));
             const uint32_t raw[4] = {v0[0], v0[1], v1[0], v1[1]};
             const f4 w0 = *reinterpret_cast<const f4*>(wt + 32 * s + 8 * g), w1 = *reinterpret_cast<const f4*>(wt + 32 * s + 8 * g + 4);
@@ -404,8 +413,8 @@ __device__ __forceinline__ void update_state(f4 (&S)[DA / 16], const T* kt, cons
         }
     } else {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int t0 = 16 * s + 4 * g;
+        for (int s = 0; s < 4 / PARTS; ++s) {
+            const int t0 = 32 * part + 16 * s + 4 * g;
             const f4 w = *reinterpret_cast<const f4*>(wt + t0);
             u4 b;
 #pragma unroll
@@ -498,55 +507,67 @@ __device__ __forceinline__ f4* state_piece(const LaArgs& A, int at, int h, int t
 }
 
 // ---------------------------------------------------------- segment state ----
+// Eight waves: a wave holds 16 value columns of the state and half of the tokens of each chunk, so
+// that the weighted values' splitting, which costs more than the products, is shared out; the two
+// halves are added up at the end.  Weights reach to the segment's end, so nothing is rescaled on the way.
 template <typename T, int DA, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_la_state(LaArgs A) {
-    using KT = Tile<T, DA, VEC>;
-    using VT = Tile<T, kV, VEC>;
-    __shared__ __attribute__((aligned(16))) T kt[KT::SIZE];
-    __shared__ __attribute__((aligned(16))) T vt[VT::SIZE];
-    __shared__ __attribute__((aligned(16))) float wt[kC];
+__global__ void __launch_bounds__(kWalkThreads) k_la_state(LaArgs A) {
+    constexpr int NA = DA / 16, TILES = kC * (Tiled<T, DA>::ROW + Tiled<T, kV>::ROW) * (int)sizeof(T), SUMS = NA * 4 * 64 * 16;
+    __shared__ __attribute__((aligned(16))) char mem[TILES > SUMS ? TILES : SUMS];
+    __shared__ __attribute__((aligned(16))) float wt[2][kC];
+    T* kt = reinterpret_cast<T*>(mem);
+    T* vt = kt + kC * Tiled<T, DA>::ROW;
     const Unit u = unit_of(A);
     if (u.seg >= A.nseg) return;
     const Seg g = segment(A, u.seg);
-    if (g.seq < 0 || is_last(g)) return;             // a last segment's end state is the final state: the walk makes it
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (g.seq < 0 || is_last(g)) return;         // a last segment's end state is the final state: the walk makes it
+    const int lane = threadIdx.x & 63, wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3, part = wave8 >> 2;
     const float l2 = log2_decay(A, u.h);
     const int64_t bs = A.reversed ? -A.b_ts : A.b_ts, cs = A.reversed ? -A.c_ts : A.c_ts;
     const T* kp = rows_of<T>(A.b, A, g, g.p0, A.b_ts, (u.h / A.b_rep) * A.Da);
     const T* vp = rows_of<T>(A.c, A, g, g.p0, A.c_ts, (u.h / A.c_rep) * A.Dv + u.tile * kV);
     const int vw = A.Dv - u.tile * kV;
-    f4 S[DA / 16];
-#pragma unroll
-    for (int i = 0; i < DA / 16; ++i) S[i] = f4{0, 0, 0, 0};
-    if (wave == 0) fill_weights(wt, l2, kC, A.shift, A.s_up, lane);
-    const float carry = power(l2, kC);
-    KT k;
-    VT v;
+    Tile<T, DA, VEC, kWalkThreads> k;
+    Tile<T, kV, VEC, kWalkThreads> v;
     auto load = [&](int c0) {
         const int n = min(kC, g.n - c0);
         k.load(window(kp + c0 * bs, A.b_ts, A.reversed, n, A.Da), A.Da, threadIdx.x);
         v.load(window(vp + c0 * cs, A.c_ts, A.reversed, n, vw), vw, threadIdx.x);
     };
     load(0);
-    if (g.idx == 0) {
+    f4 S[NA];
 #pragma unroll
-        for (int i = 0; i < DA / 16; ++i) {
-            S[i] = load_h0(A, g.seq, u.h, u.tile, wave, i, lane);
-            *state_piece<DA>(A, g.state + g.count - 1, u.h, u.tile, wave, i, lane) = S[i];
+    for (int i = 0; i < NA; ++i) S[i] = f4{0, 0, 0, 0};
+    if (g.idx == 0 && part == 0) {
+        const float f = power(l2, g.n);
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const f4 h = load_h0(A, g.seq, u.h, u.tile, wave, i, lane);
+            *state_piece<DA>(A, g.state + g.count - 1, u.h, u.tile, wave, i, lane) = h;
+            S[i] = h * f;
         }
     }
     for (int c0 = 0; c0 < g.n; c0 += kC) {       // whole chunks: only a last segment has a ragged one
-        __syncthreads();
+        float* w = wt[c0 / kC & 1];
+        if (wave8 == 4) fill_weights(w, l2, g.n - c0, A.shift, A.s_up, lane);
+        lds_barrier();
         k.store(kt, threadIdx.x);
         v.store(vt, threadIdx.x);
-        __syncthreads();
+        lds_barrier();
         if (c0 + kC < g.n) load(c0 + kC);
-#pragma unroll
-        for (int i = 0; i < DA / 16; ++i) S[i] *= carry;
-        update_state<T, DA>(S, kt, vt, wt, wave, lane);
+        update_state<T, DA, 2>(S, kt, vt, w, wave, lane, part);
     }
+    lds_barrier();
+    f4* sums = reinterpret_cast<f4*>(mem) + wave * NA * 64 + lane;
+    if (part) {
 #pragma unroll
-    for (int i = 0; i < DA / 16; ++i) *state_piece<DA>(A, g.state, u.h, u.tile, wave, i, lane) = S[i];
+        for (int i = 0; i < NA; ++i) sums[i * 64] = S[i];
+    }
+    lds_barrier();
+    if (!part) {
+#pragma unroll
+        for (int i = 0; i < NA; ++i) *state_piece<DA>(A, g.state, u.h, u.tile, wave, i, lane) = S[i] + sums[i * 64];
+    }
 }
 
 // ---------------------------------------------------------------- carry ----
@@ -561,6 +582,7 @@ __global__ void __launch_bounds__(256) k_la_carry(LaArgs A) {
     const int tile = b % A.nv;
     b /= A.nv;
     const int h = b % A.H, seq = b / A.H;
+    if (A.cu && (int64_t)A.cu[seq + 1] - A.cu[seq] <= (int64_t)kFewSegments * A.target) return;
     int first, n, len;
     sequence(A, seq, first, n, len);
     if (n <= kFewSegments) return;
@@ -587,8 +609,9 @@ __global__ void __launch_bounds__(256) k_la_carry(LaArgs A) {
 // N rows of 16x16 products with the NK fragments of `q`: y = sum_s fetch(x, s) q[s], handed to use(x, y).
 // bf16 reads two operands ahead of the ones it multiplies; fp32 four at a time, whose 16
 // instructions cover the next read themselves.
+// fp32, bound by its products, leaves out the rows from `end` on (scores of later tokens): use gets zeros.
 template <typename T, int N, int NK, typename Fetch, typename Use>
-__device__ __forceinline__ void products(const u4 (&q)[NK], Fetch fetch, Use use) {
+__device__ __forceinline__ void products(const u4 (&q)[NK], int end, Fetch fetch, Use use) {
     constexpr int GS = sizeof(T) == 2 ? 2 : 4, NG = NK / GS, NB = sizeof(T) == 2 ? 2 : 1;
     u4 fr[NB][GS];
     auto read = [&](int z) {
@@ -599,6 +622,10 @@ __device__ __forceinline__ void products(const u4 (&q)[NK], Fetch fetch, Use use
 #pragma unroll
     for (int x = 0; x < N; ++x) {
         f4 y = {0, 0, 0, 0};
+        if (NB == 1 && x >= end) {
+            use(x, y);
+            continue;
+        }
 #pragma unroll
         for (int z = x * NG; z < (x + 1) * NG; ++z) {
             if (NB == 1) read(z);
@@ -655,7 +682,7 @@ struct Decay {
 
 // o[x] += V^T P^T for NT accumulators, V a tile of W columns.
 template <typename T, typename TO, int W, int NT>
-__device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, const T* vt, int m, int gr) {
+__device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, const T* vt, int wave, int m, int gr) {
     using VL = Tiled<T, W>;
     if constexpr (sizeof(T) == 2) {
         int va = VL::at(4 * gr + (m >> 2), column<TO>(0, m & 3));
@@ -679,7 +706,8 @@ __device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, cons
         }
     } else {
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) {
+            if (t > wave) break;
 #pragma unroll
             for (int h = 0; h < NT; h += 4) {
                 u4 a[4];
@@ -691,29 +719,59 @@ __device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, cons
 #pragma unroll
                 for (int x = 0; x < 4; ++x) o[h + x] = Frag<T>::mma(a[x], P.p[t], o[h + x]);
             }
+        }
     }
 }
 
-// A token's row of `width` columns from its lanes' accumulators.
-template <typename TO, bool VEC, int NT>
-__device__ __forceinline__ void store_row(TO* row, const f4 (&o)[NT], int width, int gr) {
+// The tokens' rows of `width` columns from their lanes' accumulators: token i of n lies at base + i step.
+// LINES (16-bit rows): the lanes of two neighbouring tokens swap halves of 64 columns, so that eight
+// lanes store a whole 128-byte line; packed prompt 86.5 -> 84 us.  The walk for keys' and values' gradients,
+// short of registers, stores pieces of 64 bytes instead (80 us; with lines 90).
+template <typename TO, bool VEC, bool LINES, int NT>
+__device__ __forceinline__ void store_rows(TO* base, int64_t step, int i, int n, const f4 (&o)[NT], int width, int gr) {
     if constexpr (VEC && sizeof(TO) == 2) {
+        const bool odd = LINES && (i & 1);
 #pragma unroll
-        for (int e = 0; e < NT / 2; ++e)
-            if (column<TO>(2 * e, gr) < width)
-                *reinterpret_cast<u4*>(row + column<TO>(2 * e, gr)) =
-                    u4{pack_bf16(o[2 * e][0], o[2 * e][1]), pack_bf16(o[2 * e][2], o[2 * e][3]),
-                       pack_bf16(o[2 * e + 1][0], o[2 * e + 1][1]), pack_bf16(o[2 * e + 1][2], o[2 * e + 1][3])};
-    } else if constexpr (VEC) {
+        for (int e = 0; e < NT / 2; e += 2) {
+            u4 x[2];
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
-            if (column<TO>(x, gr) < width) *reinterpret_cast<f4*>(row + column<TO>(x, gr)) = o[x];
-    } else {
+            for (int k = 0; k < 2; ++k)
+                x[k] = u4{pack_bf16(o[2 * e + 2 * k][0], o[2 * e + 2 * k][1]), pack_bf16(o[2 * e + 2 * k][2], o[2 * e + 2 * k][3]),
+                          pack_bf16(o[2 * e + 2 * k + 1][0], o[2 * e + 2 * k + 1][1]),
+                          pack_bf16(o[2 * e + 2 * k + 1][2], o[2 * e + 2 * k + 1][3])};
+            if constexpr (LINES) {
+                u4 a, b;
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t send = odd ? x[0][k] : x[1][k];
+                    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)send, 0xb1, 0xf, 0xf, true);   // lane ^ 1
+                    a[k] = odd ? got : x[0][k];
+                    b[k] = odd ? x[1][k] : got;
+                }
+                const int col = column<TO>(2 * e + (odd ? 2 : 0), gr), t = i & ~1;
+                if (col < width) {
+                    if (t < n) *reinterpret_cast<u4*>(base + t * step + col) = a;
+                    if (t + 1 < n) *reinterpret_cast<u4*>(base + (t + 1) * step + col) = b;
+                }
+            } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (column<TO>(x, gr) + r < width) store_out(row + column<TO>(x, gr) + r, o[x][r]);
+                for (int k = 0; k < 2; ++k)
+                    if (i < n && column<TO>(2 * e + 2 * k, gr) < width)
+                        *reinterpret_cast<u4*>(base + i * step + column<TO>(2 * e + 2 * k, gr)) = x[k];
+            }
+        }
+    } else if (i < n) {
+        TO* row = base + i * step;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            if constexpr (VEC) {
+                if (column<TO>(x, gr) < width) *reinterpret_cast<f4*>(row + column<TO>(x, gr)) = o[x];
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (column<TO>(x, gr) + r < width) store_out(row + column<TO>(x, gr) + r, o[x][r]);
+            }
+        }
     }
 }
 
@@ -729,8 +787,8 @@ __device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const
     const T* vp = rows_of<T>(A.c, A, g, g.p0, A.c_ts, (un.h / A.c_rep) * A.Dv + un.tile * kV);
     const int vw = A.Dv - un.tile * kV;
     const int64_t hrow = is_last(g) && A.h_out ? state_row(A, g.seq) : -1;
-    Tile<T, DA, VEC> k;
-    Tile<T, kV, VEC> v;
+    Tile<T, DA, VEC, 256> k;
+    Tile<T, kV, VEC, 256> v;
     auto load = [&](int c0) {
         const int n = min(kC, g.n - c0);
         k.load(window(kp + c0 * bs, A.b_ts, A.reversed, n, A.Da), A.Da, thread);
@@ -773,14 +831,14 @@ __device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const
                 *reinterpret_cast<f4*>(p) = S[i];
             }
         }
-        __syncthreads();
+        lds_barrier();
         if (more) load(c0 + kC);
         if (more || hrow >= 0) {
 #pragma unroll
             for (int i = 0; i < DA / 16; ++i) S[i] *= f;
             update_state<T, DA>(S, kt, vt, wt, wave, lane);
         }
-        __syncthreads();
+        lds_barrier();
     }
     if (hrow >= 0) {
         int late = lane;                         // keeps these addresses out of the walk's registers
@@ -797,6 +855,15 @@ __device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const
     }
 }
 
+// Which 16 tokens of the chunk an output wave takes (or which 16 columns a state's wave holds).  In
+// fp32 later tokens cost more products, and a wave's SIMD goes by its number: every other round of
+// 256 workgroups counts backwards, so that two workgroups on a compute unit even out.
+template <typename T>
+__device__ __forceinline__ int block_of(int wave8) {
+    const bool back = sizeof(T) == 4 && wave8 < 4 && (blockIdx.x >> 8 & 1);
+    return back ? 3 - wave8 : wave8 & 3;
+}
+
 // Eight waves on one chunk: waves 0 - 3 make the outputs of 16 tokens each, waves 4 - 7
 // bring the state to the next chunk at the same time.  Both read the chunk's K and V tiles; the
 // state entering the chunk reaches the output waves as an LDS copy.  The state's waves load the
@@ -807,8 +874,8 @@ template <typename T, typename TO, int DA, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_la_out(LaArgs A) {
     using KL = Tiled<T, DA>;
     constexpr int NK = DA / Frag<T>::K;
-    __shared__ __attribute__((aligned(16))) T kt[Tile<T, DA, VEC>::SIZE];
-    __shared__ __attribute__((aligned(16))) T vt[Tile<T, kV, VEC>::SIZE];
+    __shared__ __attribute__((aligned(16))) T kt[kC * Tiled<T, DA>::ROW];
+    __shared__ __attribute__((aligned(16))) T vt[kC * Tiled<T, kV>::ROW];
     __shared__ __attribute__((aligned(16))) T st[kV * KL::ROW];      // the state's copy [value column][row]
     __shared__ __attribute__((aligned(16))) float wt[kC];
     const Unit un = unit_of(A);
@@ -816,7 +883,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
     const Seg g = segment(A, un.seg);
     if (g.seq < 0) return;
     const int lane = threadIdx.x & 63, m = lane & 15, gr = lane >> 4;
-    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = block_of<T>(wave8);
     const float l2 = log2_decay(A, un.h);
     // Every wave meets the same barriers: two a chunk.
     if (wave8 >= 4) {
@@ -839,7 +906,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
     for (int c0 = 0; c0 < g.n; c0 += kC) {
 #pragma unroll
         for (int s = 0; s < NK; ++s) q[s] = qn[s];
-        __syncthreads();
+        lds_barrier();
         if (c0 + kC < g.n) load_q(c0 + kC);
 
         // the carried part O^T = S^T Q^T (four accumulators of value columns), then the scores K Q^T
@@ -849,7 +916,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
         forget(sa);
         forget(ka);
         products<T, 8, NK>(
-            q,
+            q, 5 + wave,
             [&](int x, int s) {
                 const int c = Frag<T>::K * s;
                 return *reinterpret_cast<const u4*>(x < 4 ? st + KL::go_state(sa, column<TO>(x, 0), c, x & 1) : kt + KL::go(ka, 16 * (x - 4), c));
@@ -858,9 +925,9 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
                 if (x < 4) o[x] = y * at_q;      // lambda^{i + shift} of the lane's token
                 else dec.apply(P, x - 4, y, wave, m, gr);
             });
-        add_values<T, TO, kV>(o, P, vt, m, gr);
-        if (qi < g.n - c0) store_row<TO, VEC>(op + (c0 + qi) * os, o, A.Dv - un.tile * kV, gr);
-        __syncthreads();
+        add_values<T, TO, kV>(o, P, vt, wave, m, gr);
+        store_rows<TO, VEC, true>(op + c0 * os, os, qi, g.n - c0, o, A.Dv - un.tile * kV, gr);
+        lds_barrier();
     }
 }
 
@@ -882,8 +949,8 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
     using KL = Tiled<T, DA>;
     using VL = Tiled<T, kV>;
     constexpr int NK = DA / Frag<T>::K, NV = kV / Frag<T>::K, NA = DA / 16;
-    __shared__ __attribute__((aligned(16))) T kt[Tile<T, DA, VEC>::SIZE];
-    __shared__ __attribute__((aligned(16))) T vt[Tile<T, kV, VEC>::SIZE];
+    __shared__ __attribute__((aligned(16))) T kt[kC * Tiled<T, DA>::ROW];
+    __shared__ __attribute__((aligned(16))) T vt[kC * Tiled<T, kV>::ROW];
     __shared__ __attribute__((aligned(16))) T st[kV * KL::ROW];
     __shared__ __attribute__((aligned(16))) float wt[kC];
     const Unit un = unit_of(A);
@@ -891,7 +958,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
     const Seg g = segment(A, un.seg);
     if (g.seq < 0) return;
     const int lane = threadIdx.x & 63, m = lane & 15, gr = lane >> 4;
-    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 & 3;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = block_of<T>(wave8);
     const float l2 = log2_decay(A, un.h);
     if (wave8 >= 4) {
         carry_state<T, DA, VEC>(A, g, un, l2, kt, vt, st, wt, wave, lane);
@@ -919,9 +986,8 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
         for (int s = 0; s < NK; ++s) q[s] = qn[s];
 #pragma unroll
         for (int s = 0; s < NV; ++s) v[s] = vn[s];
-        __syncthreads();
+        lds_barrier();
         if (c0 + kC < g.n) load(c0 + kC);
-        const bool live = qi < g.n - c0;
         {
             f4 o[4];
             Scores<T> P;
@@ -929,7 +995,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
             forget(sa);
             forget(ka);
             products<T, 8, NK>(
-                q,
+                q, 5 + wave,
                 [&](int x, int s) {
                     const int c = Frag<T>::K * s;
                     return *reinterpret_cast<const u4*>(x < 4 ? st + KL::go_state(sa, column<TO>(x, 0), c, x & 1) : kt + KL::go(ka, 16 * (x - 4), c));
@@ -938,8 +1004,8 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
                     if (x < 4) o[x] = y * at_q;
                     else dec.apply(P, x - 4, y, wave, m, gr);
                 });
-            add_values<T, TO, kV>(o, P, vt, m, gr);
-            if (live) store_row<TO, VEC>(dv - (c0 + qi) * A.o_ts, o, A.Dv, gr);
+            add_values<T, TO, kV>(o, P, vt, wave, m, gr);
+            store_rows<TO, VEC, false>(dv - c0 * A.o_ts, -A.o_ts, qi, g.n - c0, o, A.Dv, gr);
         }
         {
             f4 o[NA];
@@ -949,7 +1015,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
             forget(va);
             forget(sa);
             products<T, NA + 4, NV>(
-                v,
+                v, NA + 1 + wave,
                 [&](int x, int s) {
                     if (x >= NA) return *reinterpret_cast<const u4*>(vt + VL::go(va, 16 * (x - NA), Frag<T>::K * s));
                     if constexpr (sizeof(T) == 2) {      // rows of R: key columns of the copy, eight value columns a lane
@@ -968,10 +1034,10 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
                     if (x < NA) o[x] = y * at_q;
                     else dec.apply(P, x - NA, y, wave, m, gr);
                 });
-            add_values<T, TO, DA>(o, P, kt, m, gr);
-            if (live) store_row<TO, VEC>(dk - (c0 + qi) * X.dk_ts, o, A.Da, gr);
+            add_values<T, TO, DA>(o, P, kt, wave, m, gr);
+            store_rows<TO, VEC, false>(dk - c0 * X.dk_ts, -X.dk_ts, qi, g.n - c0, o, A.Da, gr);
         }
-        __syncthreads();
+        lds_barrier();
     }
 }
 
@@ -1158,7 +1224,7 @@ template <typename T, typename TO, int DA, bool VEC>
 mb_status run_passes(const LaArgs& A, const SecondArgs* X, const Plan& p, hipStream_t s) {
     const dim3 grid(grid_of(A)), wide(kWalkThreads);
     if (p.states) {
-        hipLaunchKernelGGL((k_la_state<T, DA, VEC>), grid, dim3(kThreads), 0, s, A);
+        hipLaunchKernelGGL((k_la_state<T, DA, VEC>), grid, wide, 0, s, A);
         mb_status st = check_launch();
         if (st != MB_OK) return st;
         // some sequence may have many segments
