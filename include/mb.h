@@ -602,7 +602,8 @@ mb_status mb_ssd_chunked_bwd(const float* X, const float* logdecay, const float*
  * (bf16; 4 for fp32) take the fast path.  fp32 arithmetic runs on fp32 matrix products; with MB_BF16 the
  * products take bf16 operands with fp32 accumulation: the masked scores and a copy of the
  * state are rounded, the carried state is not (its update splits the weighted values into
- * three bf16 pieces).  NaN and infinities in v reach all outputs of their 64-token chunk.
+ * three bf16 pieces).  NaN and infinities reach the outputs and states from their token on, never
+ * earlier tokens or other sequences (in a state an infinity may become NaN).
  * ws: at least mb_workspace_size(MB_OP_LINEAR_ATTN, n_seq, T, H, Dv, G, Dk, 1, 0) bytes, 256-byte
  * aligned (may be 0: one segment per sequence).
  */
@@ -653,7 +654,7 @@ mb_status mb_linear_attn_bwd(const void* q, const void* k, const void* v, const 
 /*
  * Root-mean-square norm with the residual's addition, in front of a block:
  *     r = x + residual,   rstd = 1 / sqrt(mean_d r_d^2 + eps),   y_d = r_d rstd weight_d
- *   x            : (rows, D) dtype, x_stride >= D elements between rows
+ *   x            : (rows, D) dtype, x_stride (D to 2^31 - 1) elements between rows
  *   residual     : (rows, D) residual_dtype, or NULL (r = x)
  *   weight       : (D) fp32 or NULL (ones)
  *   y            : (rows, D) dtype

@@ -346,6 +346,21 @@ struct Tile {
             v[i] = load_row<T, VEC>(w, k / PER_ROW, (k % PER_ROW) * VE, width);
         }
     }
+    // Whether one of this thread's elements is infinite or NaN.
+    __device__ __forceinline__ bool odd_values() const {
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (sizeof(T) == 2) {  // an exponent of ones carries into the bit above it
+                    any |= ((v[i][e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                } else {
+                    any |= ((v[i][e] & 0x7f800000u) + 0x00800000u) & 0x80000000u;
+                }
+            }
+        return any != 0;
+    }
     __device__ __forceinline__ void store(T* lds, int thread) const {
         static_assert(NT / PER_ROW % 16 == 0 || sizeof(T) == 4, "steps of 16 rows keep the places' pattern");
         const int at = Tiled<T, W>::at(thread / PER_ROW, (thread % PER_ROW) * VE);
@@ -654,23 +669,27 @@ struct Scores {
 };
 // s_in lambda^{i - j} with j = 16 t + 4 gr + r: on the diagonal block (t = wave) as it is, in front of it
 // through the power of the next block's distance, between 1 and 31, times lambda^{16 (wave - 1 - t)}.
+// The powers are the same for all four waves and lie in LDS, two f4 a lane, diagonal and near: in eight
+// registers they cost the walk for keys' and values' gradients its last ones (80 us from LDS, 103 so).
 struct Decay {
-    float diag[4], near[4], far[4];          // far: uniform
-    __device__ __forceinline__ Decay(float l2, float s_in, int wave, int m, int gr) {
+    const f4* lds;
+    float far[4];                            // uniform
+    __device__ __forceinline__ Decay(f4* table, float l2, float s_in, int wave, int lane) : lds(table + lane) {
+        const int m = lane & 15, gr = lane >> 4;
+        f4 w;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int d = m - 4 * gr - r;
-            diag[r] = s_in * power(l2, max(d, 0));
-            near[r] = s_in * power(l2, d + 16);
-        }
+        for (int r = 0; r < 4; ++r) w[r] = s_in * power(l2, wave == 0 ? max(m - 4 * gr - r, 0) : m - 4 * gr - r + 16);
+        if (wave < 2) table[wave * 64 + lane] = w;       // read behind the first barrier
 #pragma unroll
         for (int t = 0; t < 4; ++t) far[t] = power(l2, 16 * max(wave - 1 - t, 0));
     }
+    __device__ __forceinline__ f4 weights(int t, int wave) const { return lds[t == wave ? 0 : 64]; }
     template <typename T>
     __device__ __forceinline__ void apply(Scores<T>& P, int t, f4 y, int wave, int m, int gr) const {
+        const f4 w = weights(t, wave);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            y[r] = t > wave || (t == wave && 4 * gr + r > m) ? 0.0f : y[r] * (t == wave ? diag[r] : near[r] * far[t]);
+            y[r] = t > wave || (t == wave && 4 * gr + r > m) ? 0.0f : y[r] * (t == wave ? w[r] : w[r] * far[t]);
         if constexpr (sizeof(T) == 2) {
             P.p[t >> 1][2 * (t & 1)] = pack_bf16(y[0], y[1]);
             P.p[t >> 1][2 * (t & 1) + 1] = pack_bf16(y[2], y[3]);
@@ -680,10 +699,56 @@ struct Decay {
     }
 };
 
-// o[x] += V^T P^T for NT accumulators, V a tile of W columns.
-template <typename T, typename TO, int W, int NT>
-__device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, const T* vt, int wave, int m, int gr) {
+// A fragment of the V tile, tokens from t on along the lane's elements, for accumulator x.
+template <typename T, typename TO, int W>
+__device__ __forceinline__ u4 value_fragment(const T* vt, int va, int x, int t, int m, int gr) {
     using VL = Tiled<T, W>;
+    if constexpr (sizeof(T) == 2) {
+        const u2 v0 = tr4(vt + VL::go(va, t, column<TO>(x, 0)));
+        const u2 v1 = tr4(vt + VL::go(va, t + 16, column<TO>(x, 0)));
+        return u4{v0[0], v0[1], v1[0], v1[1]};
+    } else {
+        u4 a;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[e] = __float_as_uint(vt[VL::at(t + 4 * gr + e, column<TO>(x, m >> 2) + (m & 3))]);
+        return a;
+    }
+}
+
+// o[x] += V^T P^T for NT accumulators, V a tile of W columns.  The matrix product multiplies the zero
+// scores of later tokens with whatever those hold: where the chunk has infinities or NaN among its values
+// (`odd`), it is made once for each of the 16 tokens, later ones cleared from the tile's fragments.
+template <typename T, typename TO, int W, int NT>
+__device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, const T* vt, bool odd, int wave, int m, int gr) {
+    using VL = Tiled<T, W>;
+    constexpr int STEP = sizeof(T) == 2 ? 32 : 16;       // tokens of a fragment
+    if (__builtin_expect(odd, false)) {
+        const int va = sizeof(T) == 2 ? VL::at(4 * gr + (m >> 2), column<TO>(0, m & 3)) : 0;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            f4 own = o[x];
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+                f4 y = o[x];
+#pragma unroll
+                for (int s = 0; s < Scores<T>::N; ++s) {
+                    u4 a = value_fragment<T, TO, W>(vt, va, x, STEP * s, m, gr);
+                    const int left = 16 * wave + i - STEP * s - 4 * gr;      // the fragment's tokens up to the i-th
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (sizeof(T) == 2)
+                            a[e] &= (left >= 16 * (e >> 1) + 2 * (e & 1) ? 0xffffu : 0u) | (left > 16 * (e >> 1) + 2 * (e & 1) ? 0xffff0000u : 0u);
+                        else
+                            a[e] = left >= e ? a[e] : 0u;
+                    }
+                    y = Frag<T>::mma(a, P.p[s], y);
+                }
+                if (m == i) own = y;
+            }
+            o[x] = own;
+        }
+        return;
+    }
     if constexpr (sizeof(T) == 2) {
         int va = VL::at(4 * gr + (m >> 2), column<TO>(0, m & 3));
         forget(va);
@@ -693,11 +758,7 @@ __device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, cons
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const u2 v0 = tr4(vt + VL::go(va, 32 * s, column<TO>(h + x, 0)));
-                    const u2 v1 = tr4(vt + VL::go(va, 32 * s + 16, column<TO>(h + x, 0)));
-                    a[s][x] = u4{v0[0], v0[1], v1[0], v1[1]};
-                }
+                for (int x = 0; x < 4; ++x) a[s][x] = value_fragment<T, TO, W>(vt, va, h + x, 32 * s, m, gr);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
@@ -712,10 +773,7 @@ __device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, cons
             for (int h = 0; h < NT; h += 4) {
                 u4 a[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        a[x][e] = __float_as_uint(vt[VL::at(16 * t + 4 * gr + e, column<TO>(h + x, m >> 2) + (m & 3))]);
+                for (int x = 0; x < 4; ++x) a[x] = value_fragment<T, TO, W>(vt, 0, h + x, 16 * t, m, gr);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) o[h + x] = Frag<T>::mma(a[x], P.p[t], o[h + x]);
             }
@@ -779,7 +837,7 @@ __device__ __forceinline__ void store_rows(TO* base, int64_t step, int i, int n,
 // chunks' K and V tiles to LDS, and bring it to the next chunk.
 template <typename T, int DA, bool VEC>
 __device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const Unit& un, float l2, T* kt, T* vt, T* st, float* wt,
-                                            int wave, int lane) {
+                                            int* odd, int wave, int lane) {
     using SL = Tiled<T, DA>;
     const int m = lane & 15, gr = lane >> 4, thread = threadIdx.x & 255;
     const int64_t bs = A.reversed ? -A.b_ts : A.b_ts, cs = A.reversed ? -A.c_ts : A.c_ts;
@@ -818,6 +876,8 @@ __device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const
         const bool more = c0 + kC < g.n;
         k.store(kt, thread);
         v.store(vt, thread);
+        const int have = (__ballot(v.odd_values()) ? 1 : 0) | (__ballot(k.odd_values()) ? 2 : 0);
+        if (lane == 0) odd[wave] = have;
         if (c0 == 0 || n < kC) {
             if (wave == 0) fill_weights(wt, l2, n, A.shift, A.s_up, lane);
             f = power(l2, n);
@@ -878,6 +938,8 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
     __shared__ __attribute__((aligned(16))) T vt[kC * Tiled<T, kV>::ROW];
     __shared__ __attribute__((aligned(16))) T st[kV * KL::ROW];      // the state's copy [value column][row]
     __shared__ __attribute__((aligned(16))) float wt[kC];
+    __shared__ __attribute__((aligned(16))) f4 powers[128];
+    __shared__ int odd[4];                       // infinities or NaN in the chunk: in the V tile 1, in the K tile 2
     const Unit un = unit_of(A);
     if (un.seg >= A.nseg) return;
     const Seg g = segment(A, un.seg);
@@ -887,7 +949,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
     const float l2 = log2_decay(A, un.h);
     // Every wave meets the same barriers: two a chunk.
     if (wave8 >= 4) {
-        carry_state<T, DA, VEC>(A, g, un, l2, kt, vt, st, wt, wave, lane);
+        carry_state<T, DA, VEC>(A, g, un, l2, kt, vt, st, wt, odd, wave, lane);
         return;
     }
     const int64_t as = A.reversed ? -A.a_ts : A.a_ts, os = A.reversed ? -A.o_ts : A.o_ts;
@@ -895,7 +957,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
     TO* op = const_cast<TO*>(rows_of<TO>(A.o, A, g, g.p0, A.o_ts, un.h * A.Dv + un.tile * kV));
     const int qi = 16 * wave + m;                // this lane's query position in the chunk
     const float at_q = A.s_carry * power(l2, qi + A.shift);
-    const Decay dec(l2, A.s_in, wave, m, gr);
+    const Decay dec(powers, l2, A.s_in, wave, lane);
     u4 q[NK], qn[NK];
     auto load_q = [&](int c0) {
         const Window w = window(ap + c0 * as, A.a_ts, A.reversed, min(kC, g.n - c0), A.Da);
@@ -925,7 +987,8 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
                 if (x < 4) o[x] = y * at_q;      // lambda^{i + shift} of the lane's token
                 else dec.apply(P, x - 4, y, wave, m, gr);
             });
-        add_values<T, TO, kV>(o, P, vt, wave, m, gr);
+        const int has = odd[0] | odd[1] | odd[2] | odd[3];
+        add_values<T, TO, kV>(o, P, vt, has & 1, wave, m, gr);
         store_rows<TO, VEC, true>(op + c0 * os, os, qi, g.n - c0, o, A.Dv - un.tile * kV, gr);
         lds_barrier();
     }
@@ -953,6 +1016,8 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
     __shared__ __attribute__((aligned(16))) T vt[kC * Tiled<T, kV>::ROW];
     __shared__ __attribute__((aligned(16))) T st[kV * KL::ROW];
     __shared__ __attribute__((aligned(16))) float wt[kC];
+    __shared__ __attribute__((aligned(16))) f4 powers[128];
+    __shared__ int odd[4];                       // infinities or NaN in the chunk: in the V tile 1, in the K tile 2
     const Unit un = unit_of(A);
     if (un.seg >= A.nseg) return;
     const Seg g = segment(A, un.seg);
@@ -961,7 +1026,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
     const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = block_of<T>(wave8);
     const float l2 = log2_decay(A, un.h);
     if (wave8 >= 4) {
-        carry_state<T, DA, VEC>(A, g, un, l2, kt, vt, st, wt, wave, lane);
+        carry_state<T, DA, VEC>(A, g, un, l2, kt, vt, st, wt, odd, wave, lane);
         return;
     }
     const T* ap = rows_of<T>(A.a, A, g, g.p0, A.a_ts, (un.h / A.a_rep) * A.Da);
@@ -970,7 +1035,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
     TO* dk = const_cast<TO*>(rows_of<TO>(X.dk, A, g, g.p0, X.dk_ts, un.h * A.Da));
     const int qi = 16 * wave + m;
     const float at_q = A.s_carry * power(l2, qi + A.shift);
-    const Decay dec(l2, A.s_in, wave, m, gr);
+    const Decay dec(powers, l2, A.s_in, wave, lane);
     u4 q[NK], qn[NK], v[NV], vn[NV];
     auto load = [&](int c0) {
         const int n = min(kC, g.n - c0);
@@ -988,6 +1053,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
         for (int s = 0; s < NV; ++s) v[s] = vn[s];
         lds_barrier();
         if (c0 + kC < g.n) load(c0 + kC);
+        const int has = odd[0] | odd[1] | odd[2] | odd[3];
         {
             f4 o[4];
             Scores<T> P;
@@ -1004,7 +1070,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
                     if (x < 4) o[x] = y * at_q;
                     else dec.apply(P, x - 4, y, wave, m, gr);
                 });
-            add_values<T, TO, kV>(o, P, vt, wave, m, gr);
+            add_values<T, TO, kV>(o, P, vt, has & 1, wave, m, gr);
             store_rows<TO, VEC, false>(dv - c0 * A.o_ts, -A.o_ts, qi, g.n - c0, o, A.Dv, gr);
         }
         {
@@ -1034,7 +1100,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
                     if (x < NA) o[x] = y * at_q;
                     else dec.apply(P, x - NA, y, wave, m, gr);
                 });
-            add_values<T, TO, DA>(o, P, kt, wave, m, gr);
+            add_values<T, TO, DA>(o, P, kt, has & 2, wave, m, gr);
             store_rows<TO, VEC, false>(dk - c0 * X.dk_ts, -X.dk_ts, qi, g.n - c0, o, A.Da, gr);
         }
         lds_barrier();
@@ -1333,6 +1399,7 @@ extern "C" mb_status mb_linear_attn(const void* q, const void* k, const void* v,
     using namespace mb;
     if (!dtype_ok(dtype)) return MB_ERR_DTYPE;
     if (!sizes_ok(n_seq, T, H, G, Dk, Dv)) return MB_ERR_SHAPE;
+    if (n_slots > 0x7fffffff) return MB_ERR_SHAPE;
     if (!strides_ok(q_stride, H * Dk) || !strides_ok(k_stride, G * Dk) || !strides_ok(v_stride, G * Dv)) return MB_ERR_SHAPE;
     if (slots ? n_slots < 1 : n_slots != 0) return MB_ERR_SHAPE;
     if (n_seq == 0) return MB_OK;
@@ -1382,16 +1449,16 @@ extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void
     if (!dtype_ok(dtype)) return MB_ERR_DTYPE;
     if (!sizes_ok(n_seq, T, H, G, Dk, Dv)) return MB_ERR_SHAPE;
     if (!strides_ok(q_stride, H * Dk) || !strides_ok(k_stride, G * Dk) || !strides_ok(v_stride, G * Dv)) return MB_ERR_SHAPE;
-    if (n_seq == 0) return MB_OK;
-    if (!cu_seqlens && T % n_seq) return MB_ERR_SHAPE;
+    if (!cu_seqlens && (n_seq ? T % n_seq : T) != 0) return MB_ERR_SHAPE;
+    if (T == 0 && n_seq == 0) return MB_OK;
     if (!log_decay || (T > 0 && (!q || !k || !v || !d_o || !dq || !dk || !dv))) return MB_ERR_NULL;
     const size_t es = dtype_size(dtype);
     if ((uintptr_t)q % es || (uintptr_t)k % es || (uintptr_t)v % es || (uintptr_t)d_o % es || (uintptr_t)dq % es ||
         (uintptr_t)dk % es || (uintptr_t)dv % es || ((uintptr_t)log_decay & 3) || ((uintptr_t)cu_seqlens & 3) ||
         ((uintptr_t)h0 & 3) || ((uintptr_t)dh_out & 3) || ((uintptr_t)dh0 & 3))
         return MB_ERR_ALIGN;
-    const BwdPlan bp = bwd_plan(n_seq, T, H, G, Dk, Dv, cu_seqlens != nullptr);
-    if (!grid_ok(bp.q, n_seq, H, Dk) || !grid_ok(bp.v, n_seq, H, Dv)) return MB_ERR_SHAPE;
+    const BwdPlan bp = n_seq ? bwd_plan(n_seq, T, H, G, Dk, Dv, cu_seqlens != nullptr) : BwdPlan{};
+    if (n_seq && (!grid_ok(bp.q, n_seq, H, Dk) || !grid_ok(bp.v, n_seq, H, Dv))) return MB_ERR_SHAPE;
     if (bp.total && (!ws || ws_bytes < bp.total || ((uintptr_t)ws & 255))) return MB_ERR_WORKSPACE;
     const size_t nh = (size_t)n_seq * H * Dk * Dv * 4;
     const Span ins[8] = {{q, span_of(T, q_stride, H * Dk, es)}, {k, span_of(T, k_stride, G * Dk, es)}, {v, span_of(T, v_stride, G * Dv, es)},
@@ -1410,7 +1477,7 @@ extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void
     LaArgs A{};
     A.H = (int)H;
     A.log_decay = log_decay;
-    A.n_seq = (int)n_seq; A.T = (int)T; A.L = (int)(T / n_seq);
+    A.n_seq = (int)n_seq; A.T = (int)T; A.L = n_seq ? (int)(T / n_seq) : 0;
     A.share = rep;
     A.cu = cu_seqlens;
     mb_status st;
@@ -1431,8 +1498,8 @@ extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void
     Q.s_in = Q.s_carry = scale; Q.s_up = 1.0f;
     Q.shift = 1; Q.reversed = 0;
     Q.h0 = h0; Q.transposed = 1;
-    use_plan(Q, bp.q, w);
-    if ((st = launch_plan(Q, bp.q, w, stream)) != MB_OK || (st = run(Q, nullptr, bp.q, dtype, false, stream)) != MB_OK) return st;
+    if (n_seq) use_plan(Q, bp.q, w);
+    if (n_seq && ((st = launch_plan(Q, bp.q, w, stream)) != MB_OK || (st = run(Q, nullptr, bp.q, dtype, false, stream)) != MB_OK)) return st;
     // dk: queries v, keys do, values q, reversed; the state is R^T and holds the scale.
     LaArgs K = A;
     K.a = v; K.b = d_o; K.c = q; K.o = rep > 1 ? (void*)fold_k : dk;
@@ -1448,7 +1515,9 @@ extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void
     V.a_ts = k_stride; V.b_ts = q_stride; V.c_ts = H * Dv; V.o_ts = H * Dv;
     V.Da = (int)Dk; V.Dv = (int)Dv;
     V.transposed = 0;
-    if (bp.both) {
+    if (!n_seq) {
+        // no sequence: the gradients of all tokens are zero, below
+    } else if (bp.both) {
         LaArgs& B = bp.swapped ? K : V;
         const LaArgs& o = bp.swapped ? V : K;
         const SecondArgs X{o.a, o.o, o.a_ts, o.o_ts, o.a_rep};

@@ -426,7 +426,7 @@ mb_status norm(const void* x, const void* res, const float* w, void* y, float* s
                hipStream_t stream) {
     if (!dtype_ok(dtype) || !dtype_ok(rdtype) || (rdtype == MB_BF16 && dtype == MB_F32)) return MB_ERR_DTYPE;
     if (rows < 0 || D < 1 || D > kMaxD || x_stride < D || !(eps >= 0.0f) || eps > 3.0e38f) return MB_ERR_SHAPE;
-    if (rows > (int64_t)1 << 30) return MB_ERR_SHAPE;
+    if (rows > (int64_t)1 << 30 || x_stride > 0x7fffffff) return MB_ERR_SHAPE;
     if (MODE == 1 && group != 0 && group != 32 && group != 64 && group != 128) return MB_ERR_SHAPE;
     if (rows == 0) return MB_OK;
     if (!x || !y || (MODE == 1 && !scales)) return MB_ERR_NULL;

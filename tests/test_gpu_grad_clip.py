@@ -84,6 +84,17 @@ def test_clip_far_magnitudes():
         check(out, norm, gs, sd, "f32", eps=0.0)
 
 
+def test_clip_tensor_of_more_than_two_to_the_31_elements():
+    big = torch.zeros(2 ** 31 + 12_345, dtype=torch.bfloat16, device="cuda")
+    big[-1], big[5] = 3.0, 4.0
+    small = torch.zeros(7, dtype=torch.bfloat16, device="cuda")
+    out, norm = mb.mb_grad_norm_clip([small, big], 1.0, eps=0.0)
+    assert float(norm) == 5.0
+    # 3 / 5 and 4 / 5 to half a bf16 step
+    assert abs(float(out[1][-1]) - 0.6) <= 0.6 * HB and abs(float(out[1][5]) - 0.8) <= 0.8 * HB
+    assert float(out[1].float().abs().max()) <= 0.8 * (1 + HB)
+
+
 def test_clip_zeros_infinities_and_nan():
     z = [torch.zeros(100).cuda()]
     out, norm = mb.mb_grad_norm_clip(z, 1.0)

@@ -258,18 +258,92 @@ def test_step_continues_the_chunked_form():
     check_forward(torch.cat(rows, 1), h, d, decays(H), Dk ** -0.5, [L], "f32", None)
 
 
-def test_future_tokens_do_not_reach_back_across_chunks_or_sequences():
-    """NaN keys and infinite values in one sequence leave the others alone, and the chunks before theirs."""
-    lens, H, D = [100, 200], 2, 64
-    d = inputs(51, 300, H, H, D, D, "bf16", 2)
-    clean, _ = mb.mb_linear_attn(*(d[x].cuda() for x in "qkv"), decays(H).cuda(),
-                                 cu_seqlens=torch.tensor([0, 100, 300], dtype=torch.int32).cuda())
-    d["k"][100 + 150] = float("nan")
-    d["v"][100 + 140] = float("inf")
-    o, h = mb.mb_linear_attn(*(d[x].cuda() for x in "qkv"), decays(H).cuda(),
-                             cu_seqlens=torch.tensor([0, 100, 300], dtype=torch.int32).cuda())
-    assert torch.equal(o[:100 + 128], clean[:100 + 128])
-    assert bool(torch.isfinite(h[0]).all()) and not bool(torch.isfinite(h[1]).all())
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_later_tokens_and_other_sequences_do_not_reach_back(dtype):
+    """Infinite values and NaN keys, in the middle of a chunk: earlier tokens and the other sequences as without."""
+    lens, H, D = [100, 200, 30], 2, 64
+    T, bad = sum(lens), 100 + 140
+    cu = torch.tensor([0, 100, 300, 330], dtype=torch.int32).cuda()
+    d = inputs(51, T, H, H, D, D, dtype, 3)
+    ld = decays(H)
+    ro, rh, Mo, Mh = reference(d, ld, D ** -0.5, lens, None)
+    tol = bound(dtype, D, lens, Mo, ro)
+    for what, value in (("v", float("inf")), ("v", float("nan")), ("k", float("nan")), ("q", float("nan"))):
+        c = {x: d[x].clone() for x in "qkv"}
+        c[what][bad, :, 5] = value
+        o, h = mb.mb_linear_attn(*(c[x].cuda() for x in "qkv"), ld.cuda(), cu_seqlens=cu)
+        keep = [i for i in range(T) if i < bad or i >= 300 or (what == "q" and i != bad)]
+        close(o[keep], ro[keep], tol[keep], "o beside %s = %s" % (what, value))
+        close(h[[0, 2]], rh[[0, 2]], bound("f32", D, lens, Mh, rh)[[0, 2]], "h")
+        if what == "q":
+            assert bool(torch.isnan(o[bad]).all())
+        else:
+            hit = o[bad:300, :, 5] if what == "v" else o[bad:300]
+            assert not bool(torch.isfinite(hit[0]).any()) and not bool(torch.isfinite(h[1]).all())
+            if what == "v":
+                rest = [i for i in range(D) if i != 5]
+                close(o[:, :, rest], ro[:, :, rest], tol[:, :, rest], "other columns")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_backward_of_later_tokens_alone(dtype):
+    """A NaN in do reaches dq of its own token and dk, dv up to it, nothing behind it and no other sequence."""
+    lens, H, D = [40, 200, 30], 2, 64
+    T, bad = sum(lens), 40 + 100
+    cu = torch.tensor([0, 40, 240, 270], dtype=torch.int32).cuda()
+    d = inputs(52, T, H, H, D, D, dtype, 3, with_do=True)
+    ld = decays(H)
+    D64 = {x: t.double() for x, t in d.items()}
+    A = {x: t.abs() for x, t in D64.items()}
+    ref = lf.attn_bwd(D64["q"], D64["k"], D64["v"], ld, 0.3, lens, D64["do"])
+    mag = lf.attn_bwd(A["q"], A["k"], A["v"], ld, 0.3, lens, A["do"])
+    d["do"][bad, :, 3] = float("nan")
+    out = mb.mb_linear_attn_bwd(*(d[x].cuda() for x in "qkv"), ld.cuda(), d["do"].cuda(), scale=0.3, cu_seqlens=cu)
+    keep_q = [i for i in range(T) if i != bad]
+    keep_kv = [i for i in range(T) if i < 40 or i > bad]
+    for name, got, r, M, keep in (("dq", out[0], ref[0], mag[0], keep_q), ("dk", out[1], ref[1], mag[1], keep_kv), ("dv", out[2], ref[2], mag[2], keep_kv)):
+        close(got[keep], r[keep], bound(dtype, D + 4, lens, M, r)[keep], name)
+    assert bool(torch.isnan(out[0][bad]).all()) and bool(torch.isnan(out[1][40:bad + 1]).all())
+
+
+def test_no_sequences_and_no_tokens():
+    q = torch.randn(5, 2, 16).cuda()
+    ld, cu = decays(2).cuda(), torch.tensor([3], dtype=torch.int32).cuda()
+    o = torch.full_like(q, 7.0)
+    o2, h = mb.mb_linear_attn(q, q, q, ld, cu_seqlens=cu, o=o)
+    assert bool((o2 == 7.0).all()) and h.shape == (0, 2, 16, 16)
+    for g in mb.mb_linear_attn_bwd(q, q, q, ld, q, cu_seqlens=cu)[:3]:
+        assert bool((g == 0).all())
+    e = torch.empty(3, 0, 2, 16).cuda()
+    h0 = torch.randn(3, 2, 16, 16).cuda()
+    o, h = mb.mb_linear_attn(e, e, e, ld, h0=h0)
+    assert o.shape == e.shape and torch.equal(h, h0)
+    assert torch.equal(mb.mb_linear_attn_bwd(e, e, e, ld, e, dh_out=h0)[3], h0)
+    o, h = mb.mb_linear_attn(e[:0], e[:0], e[:0], ld)
+    assert o.shape[0] == 0 and h.shape[0] == 0
+
+
+def test_states_behind_two_to_the_31_elements():
+    """A pool of more than 2^31 values: the last slots, chunked form and step."""
+    H, Dk, Dv, n_slots = 16, 128, 128, 8300
+    pool = torch.empty(n_slots, H, Dk, Dv, device="cuda")
+    assert pool.numel() > 2 ** 31
+    slots = torch.tensor([n_slots - 1, n_slots - 3], dtype=torch.int32)
+    d = inputs(53, 140, H, H, Dk, Dv, "bf16", 2)
+    for s, h in zip(slots.tolist(), d["h0"]):
+        pool[s] = h.cuda()
+    cu = torch.tensor([0, 70, 140], dtype=torch.int32).cuda()
+    ld, c = decays(H), {x: d[x].cuda() for x in "qkv"}
+    o, _ = mb.mb_linear_attn(c["q"], c["k"], c["v"], ld.cuda(), cu_seqlens=cu, h0=pool, slots=slots.cuda())
+    ro, rh, Mo, Mh = reference(d, ld, Dk ** -0.5, [70, 70], d["h0"])
+    close(o, ro, bound("bf16", Dk, [70], Mo, ro), "o")
+    close(pool[slots.long().cuda()], rh, bound("f32", Dk, [70], Mh, rh), "h")
+    start = pool[slots.long().cuda()].cpu()
+    one = {x: d[x][:2] for x in "qkv"}
+    o, _ = mb.mb_linear_attn_step(*(one[x].cuda() for x in "qkv"), ld.cuda(), pool, slots=slots.cuda())
+    ro, rh, Mo, Mh = reference(one, ld, Dk ** -0.5, [1, 1], start)
+    close(o, ro, (Dk + 64) * U * Mo + HB * ro.abs(), "o")
+    close(pool[slots.long().cuda()], rh, 16 * U * Mh, "h")
 
 
 def _graph(fn):

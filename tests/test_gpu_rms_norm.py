@@ -173,3 +173,20 @@ def test_norm_captured_and_replayed():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want)), "replay %d" % k
+
+
+def test_norm_rows_behind_two_to_the_31_elements():
+    D, rows = 4096, 2 ** 19 + 3
+    x = torch.empty(rows, D, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 2 ** 31
+    last = torch.randn(3, D).bfloat16()
+    x[-3:] = last.cuda()
+    y, r, rstd = mb.mb_rms_norm(x, eps=EPS)
+    ry, _, rs = lf.rms_norm(last.double(), None, None, EPS)
+    assert r is x
+    close(y[-3:], ry, rounded(ry, "bf16", 64), "y")
+    close(rstd[-3:], rs, 40 * U * rs, "rstd")
+    del y
+    q, s, _, _ = mb.mb_rms_norm_fp8(x, group=128, eps=EPS)
+    close(q[-3:].cpu().double() * s[-3:].cpu().double().repeat_interleave(128, 1), ry,
+          ry.abs() * (2.0 ** -4 + 140 * U) + s[-3:].cpu().double().repeat_interleave(128, 1) * 2.0 ** -10, "q")

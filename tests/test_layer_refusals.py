@@ -37,7 +37,7 @@ def test_linear_attn(lib):
         assert attn(lib, dt=dt) == E_DTYPE
     for kw in (dict(n=-1), dict(T=-1), dict(H=0), dict(G=0), dict(G=3), dict(Dk=0), dict(Dk=129), dict(Dv=0), dict(Dv=129), dict(T=201),
                dict(qs=255), dict(ks=127), dict(vs=1), dict(T=1 << 31), dict(n=(1 << 20) + 1), dict(H=4097, G=4097),
-               dict(qs=1 << 22), dict(ns=3), dict(slots=8 * M, ns=0), dict(slots=8 * M, ns=-1)):
+               dict(qs=1 << 22), dict(slots=8 * M, ns=1 << 31), dict(ns=3), dict(slots=8 * M, ns=0), dict(slots=8 * M, ns=-1)):
         assert attn(lib, **kw) == E_SHAPE, kw
     for kw in (dict(q=0), dict(k=0), dict(v=0), dict(o=0), dict(ld=0)):
         assert attn(lib, **kw) == E_NULL, kw
@@ -93,7 +93,8 @@ def test_linear_attn_bwd(lib):
     assert need > 0                                       # shared keys: the heads' gradients before they are added up
     assert bwd(lib, nws=need - 1) == E_WS
     assert bwd(lib, do=5 * M + 1) == E_ALIGN
-    assert bwd(lib, n=0) == OK
+    assert bwd(lib, n=0) == E_SHAPE                       # tokens, but no sequence to hold them
+    assert bwd(lib, n=0, T=0) == OK
 
 
 def norm(lib, x=M, res=2 * M, w=3 * M, y=4 * M, ro=5 * M, rs=6 * M, rows=4, D=64, xs=64, eps=1e-5, dt=BF16, rdt=F32):
@@ -107,7 +108,7 @@ def norm8(lib, sc=7 * M, group=32, y=4 * M, rows=4, D=64):
 def test_rms_norm(lib):
     for kw in (dict(dt=2), dict(rdt=3), dict(dt=F32, rdt=BF16)):
         assert norm(lib, **kw) == E_DTYPE, kw
-    for kw in (dict(rows=-1), dict(D=0), dict(D=16385, xs=16385), dict(xs=63), dict(eps=-1.0), dict(eps=INF), dict(eps=float("nan")),
+    for kw in (dict(rows=-1), dict(D=0), dict(D=16385, xs=16385), dict(xs=63), dict(xs=1 << 31), dict(eps=-1.0), dict(eps=INF), dict(eps=float("nan")),
                dict(rows=(1 << 30) + 1)):
         assert norm(lib, **kw) == E_SHAPE, kw
     for kw in (dict(x=0), dict(y=0)):
