@@ -706,9 +706,10 @@ mb_status mb_rms_norm_bwd(const void* dy, const void* r, const float* rstd, cons
  *     norm = sqrt(sum of all squares),   out = g * min(1, max_norm / (norm + eps))
  *   grads, outs, sizes : HOST arrays of n device pointers and element counts (>= 0; a pointer of
  *               a tensor of no elements is not looked at), read during the call only.  outs NULL: in
- *               place; an outs[i] may equal grads[i] and else must not overlap it.  Different
- *               tensors must not overlap.
- *   max_norm  : >= 0; INFINITY: the norm alone in place (nothing is written), a copy otherwise
+ *               place; an outs[i] may equal grads[i].  No other overlap of a tensor that is written
+ *               with any other tensor, nor the same tensor twice in place (MB_ERR_ALIAS).
+ *   max_norm  : >= 0; INFINITY: the norm alone in place (nothing is written), a copy otherwise,
+ *               whatever the norm
  *   norm      : (1) fp32 on the device
  * Squares are summed in fp64 in a fixed order.  A NaN or infinite norm scales as the formula says
  * (NaN; or zeros, and NaN where g is infinite).  Where in place and norm + eps <= max_norm, the

@@ -13,6 +13,10 @@
 // The tensors' addresses travel as kernel arguments, so a captured graph holds them
 // itself: up to kPer of them with the two passes' own launches, more through a table in the
 // workspace that launches of kPer each write first.
+#include <algorithm>
+#include <memory>
+#include <new>
+
 #include "mb_internal.h"
 
 namespace mb {
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(256) k_clip(Table t, int n, int64_t pieces, co
     const float norm = (float)sqrt(sum_block(s, lds));
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
     const float c = max_norm / (norm + eps);
-    const float f = c > 1.0f ? 1.0f : c;              // NaN stays
+    const float f = c > 1.0f || __builtin_isinf(max_norm) ? 1.0f : c;      // NaN stays
     for_pieces<T>(t, n, r, [&](const Entry& e, int64_t at, int m) {
         if (f == 1.0f && e.g == e.o) return;          // in place and nothing to scale
         scale_piece((const T*)e.g + at, (T*)e.o + at, m, f, stream);
@@ -204,6 +208,23 @@ mb_status passes(const Table& t, int n, int64_t pieces, double* part, float* nor
     if (st != MB_OK) return st;
     hipLaunchKernelGGL((k_clip<T, Table>), dim3(grid), dim3(256), 0, s, t, n, pieces, part, grid, norm, max_norm, eps, stream);
     return check_launch();
+}
+
+// Whether a tensor that is written overlaps any other one.  Tensors that are only read may.
+struct Range {
+    uintptr_t b, e;
+    bool written;
+};
+bool any_overlap(Range* r, int64_t n) {
+    const auto before = [](const Range& x, const Range& y) { return x.b < y.b; };
+    if (!std::is_sorted(r, r + n, before)) std::sort(r, r + n, before);
+    uintptr_t all = 0, out = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (r[i].b < (r[i].written ? all : out)) return true;
+        all = std::max(all, r[i].e);
+        if (r[i].written) out = std::max(out, r[i].e);
+    }
+    return false;
 }
 
 size_t table_bytes(int64_t n) { return ((size_t)n * sizeof(Entry) + 255) / 256 * 256; }
@@ -229,7 +250,12 @@ extern "C" mb_status mb_grad_norm_clip(const void* const* grads, void* const* ou
     if ((uintptr_t)norm & 3) return MB_ERR_ALIGN;
     const size_t need = grad_clip_workspace(n);
     if (n > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 255))) return MB_ERR_WORKSPACE;
-    int64_t total = 0;
+    constexpr int64_t kOnStack = 512;
+    Range few[kOnStack];
+    std::unique_ptr<Range[]> many(2 * n > kOnStack ? new (std::nothrow) Range[2 * n] : nullptr);
+    Range* const ranges = 2 * n > kOnStack ? many.get() : few;
+    if (!ranges) return MB_ERR_WORKSPACE;
+    int64_t total = 0, spans = 0;
     for (int64_t i = 0; i < n; ++i) {
         if (sizes[i] < 0 || sizes[i] > ((int64_t)1 << 40)) return MB_ERR_SHAPE;
         if (sizes[i] == 0) continue;
@@ -240,9 +266,11 @@ extern "C" mb_status mb_grad_norm_clip(const void* const* grads, void* const* ou
         if ((o != grads[i] && overlaps(o, b, grads[i], b)) || overlaps(o, b, norm, 4) || overlaps(grads[i], b, norm, 4) ||
             overlaps(ws, need, o, b) || overlaps(ws, need, grads[i], b))
             return MB_ERR_ALIAS;
+        ranges[spans++] = {(uintptr_t)o, (uintptr_t)o + b, true};
+        if (o != grads[i]) ranges[spans++] = {(uintptr_t)grads[i], (uintptr_t)grads[i] + b, false};
         total += (sizes[i] + piece - 1) / piece;
     }
-    if (n > 0 && overlaps(ws, need, norm, 4)) return MB_ERR_ALIAS;
+    if ((n > 0 && overlaps(ws, need, norm, 4)) || any_overlap(ranges, spans)) return MB_ERR_ALIAS;
     if (total == 0) return copy_state(nullptr, norm, 1, stream);
     Entry* table = (Entry*)ws;
     double* part = (double*)((char*)ws + table_bytes(n));

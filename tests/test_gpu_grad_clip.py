@@ -108,6 +108,30 @@ def test_clip_zeros_infinities_and_nan():
     assert math.isnan(float(norm)) and bool(torch.isnan(out[1]).all())
 
 
+def test_clip_without_a_limit_writes_nothing():
+    for bad in (float("inf"), float("nan"), 1.0):
+        a = torch.arange(100.0).cuda()
+        a[3] = bad
+        keep = a.clone()
+        _, norm = mb.mb_grad_norm_clip([a], float("inf"))
+        assert torch.equal(a.nan_to_num(nan=-5.0), keep.nan_to_num(nan=-5.0)) and bool(norm.isfinite()) == (bad == 1.0)
+        out, _ = mb.mb_grad_norm_clip([a], float("inf"), out=[torch.zeros_like(a)])
+        assert torch.equal(out[0].nan_to_num(nan=-5.0), keep.nan_to_num(nan=-5.0))
+
+
+def test_clip_of_tensors_that_share_memory():
+    """Gradients that are only read may; a written one may not."""
+    flat = torch.randn(5000, generator=torch.Generator().manual_seed(3)).cuda()
+    a, b = flat[:4000], flat[2000:]
+    out, norm = mb.mb_grad_norm_clip([a, b], 1.0, out=[torch.empty_like(a), torch.empty_like(b)])
+    check(out, norm, [a.cpu(), b.cpu()], 1.0, "f32")
+    for bad in (lambda: mb.mb_grad_norm_clip([a, b], 1.0), lambda: mb.mb_grad_norm_clip([a, a], 1.0),
+                lambda: mb.mb_grad_norm_clip([a, b[2000:]], 1.0, out=[torch.empty_like(a), b[1000:2000]])):
+        with pytest.raises(mb.MBError):
+            bad()
+    mb.mb_grad_norm_clip([a, a[:0], a[:0]], 1.0)
+
+
 def test_clip_captured_and_replayed():
     c = [g.cuda() for g in tensors([1000, 33, 70_000] + [5] * 200, "bf16")]
     outs = [torch.empty_like(t) for t in c]

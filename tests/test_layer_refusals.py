@@ -167,6 +167,18 @@ def test_grad_norm_clip(lib):
         assert clip(lib, **kw) == E_WS, kw
 
 
+def test_grad_norm_clip_of_tensors_that_overlap(lib):
+    """Every pair in which one is written."""
+    K = 1024
+    assert clip(lib, g=(M, M), sizes=(K, K)) == E_ALIAS                                # the same tensor twice
+    assert clip(lib, g=(M, M + 4 * K - 4), sizes=(K, K)) == E_ALIAS
+    assert clip(lib, g=(M + 4 * K - 4, M), sizes=(K, K)) == E_ALIAS                    # in either order
+    assert clip(lib, g=(M, 6 * M), o=(7 * M, M), sizes=(K, K)) == E_ALIAS              # written on another one's gradient
+    assert clip(lib, g=(M, 2 * M), o=(7 * M, 7 * M + 8), sizes=(K, K)) == E_ALIAS      # two outputs
+    assert clip(lib, g=tuple(M + 4 * K * i for i in range(400)) + (M,), sizes=(K,) * 401) == E_ALIAS
+
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(2, 8)
     q = torch.zeros(1, 3, 2, 8)
