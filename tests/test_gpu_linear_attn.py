@@ -155,6 +155,21 @@ def test_forward_split_chains(dtype):
     check_forward(torch.cat([o1, o2], 1), h, d, ld, Dk ** -0.5, [L], dtype, None)
 
 
+@pytest.mark.parametrize("few", [True, False], ids=["looked through", "table"])
+def test_long_sequences_among_short_ones(few):
+    """Sequences of more than eight segments, whose states are composed beforehand, first, last and in between;
+    offsets in front of the first token and behind the last count as these."""
+    short = [5] * (20 if few else 150)
+    lens, H, Dk, Dv = [2600] + short + [3001] + short + [2500], 2, 64, 64
+    T, n = sum(lens), len(lens)
+    d = inputs(61, T, H, H, Dk, Dv, "bf16", n)
+    ld = torch.tensor([-0.002, -0.3])
+    cu = torch.tensor([sum(lens[:i]) for i in range(n + 1)], dtype=torch.int32)
+    cu[0], cu[-1] = -70_000, T + 70_000
+    o, h = mb.mb_linear_attn(*(d[x].cuda() for x in "qkv"), ld.cuda(), cu_seqlens=cu.cuda(), h0=d["h0"].cuda())
+    check_forward(o, h, d, ld, Dk ** -0.5, lens, "bf16", d["h0"])
+
+
 def test_offsets_out_of_range_stay_inside():
     """Offsets that decrease or leave [0, T] are empty or cut sequences: nothing outside is touched."""
     T, H, D = 1100, 2, 16
