@@ -44,7 +44,9 @@ typedef float f2 __attribute__((ext_vector_type(2)));
 constexpr int kC = 64;          // tokens of a chunk
 constexpr int kV = 64;          // value columns of a workgroup
 constexpr int kMaxDim = 128;    // of keys and of values
-constexpr int kFewSegments = 8; // up to these the walk composes its entering state itself
+// Up to these the walk composes its entering state itself.  Measured at 4, 8 and 16: three sequences of 5461 tokens
+// 90 us at 8, 87 at 16; fp32 of 2 x 4095 tokens (16 segments each) 67.7 and 65.7; backward 194 us at 4, else 188.
+constexpr int kFewSegments = 16;
 constexpr int kWalkThreads = 512;
 
 // A segment of a sequence.  A sequence of L tokens is cut into ceil(L / target) segments (one if it
@@ -532,6 +534,8 @@ __device__ __forceinline__ f4* state_piece(const LaArgs& A, int at, int h, int t
 // Eight waves: a wave holds 16 value columns of the state and half of the tokens of each chunk, so
 // that the weighted values' splitting, which costs more than the products, is shared out; the two
 // halves are added up at the end.  Weights reach to the segment's end, so nothing is rescaled on the way.
+// Bound by its reads.  16384 packed tokens of nine sequences, 16 heads of 128 x 64, bf16: 30.5 us for 96 MB
+// (3.1 TB/s, matrix unit 11 % busy); 8190 tokens of 16 heads of 64 x 64 in fp32: 17.6 us for 72 MB (4.1 TB/s, 25 %).
 template <typename T, int DA, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads) k_la_state(LaArgs A) {
     constexpr int NA = DA / 16, TILES = kC * (Tiled<T, DA>::ROW + Tiled<T, kV>::ROW) * (int)sizeof(T), SUMS = NA * 4 * 64 * 16;
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(kWalkThreads) k_la_state(LaArgs A) {
 // In place over a sequence's places: the state that enters each of its segments.  A workgroup
 // takes 1024 values (256 lanes of four) of one (long sequence, head, tile).  There are at most
 // T / (kFewSegments target + 1) long sequences, so the launch does not grow with the short ones (64k tokens in
-// 2000 sequences, 16 heads: 892 -> 780 us).
+// 2000 sequences, 16 heads: the call 892 -> 780 us).  Bound by latency: 5.4 us for 16.9 MB, 5.1 us where it finds none.
 template <int DA>
 __global__ void __launch_bounds__(256) k_la_carry(LaArgs A, const int* longs) {
     constexpr int PER = DA * kV / 1024;
@@ -958,6 +962,10 @@ __device__ __forceinline__ int block_of(int wave8) {
 // next chunk's tiles into registers while this one is computed (the output waves the next
 // queries, which only they read) and put them to LDS between two barriers.
 // TO: type of the output (fp32 where several heads' gradients are still to be added up).
+// bf16 is bound by its traffic: the packed prompt above 51 us for 233 MB, 4.6 TB/s, and the backward's run for dq (4 x 4096
+// tokens, do and v to dq) 51 us for 211 MB, 4.1 TB/s, the matrix unit 16 - 19 % busy.  fp32, 46 us for 143 MB with
+// the matrix unit 41 % busy, waits for both in turn.  Two workgroups of eight waves fit a compute unit: 128
+// registers a wave.
 template <typename T, typename TO, int DA, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_la_out(LaArgs A) {
     using KL = Tiled<T, DA>;
@@ -1028,7 +1036,8 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
 // and on the same tiles and state, with queries v (X.v),
 //     dk_j = scale sum_{i>=j} lambda^{i-j} (v_j . do_i) q_i + lambda^{..} R v_j   (X.dk).
 // R's copy lies with its rows (key width) side by side: the first product reads it as it lies, the second
-// transposed.
+// transposed.  Bound by its traffic: 16384 tokens, 16 heads of 128 x 64, bf16: 81 us for 360 MB, 4.4 TB/s; the call
+// with two runs instead 231 us, so 188.
 struct SecondArgs {
     const void* v;
     void* dk;
@@ -1181,6 +1190,8 @@ struct StepArgs {
 // A workgroup owns CW = 4 LN value columns of one (row, head): LN lanes side by side hold
 // four columns each, the 256 / LN rows of lanes share out the state's rows, and their parts
 // of o are added up in LDS.  All its state reads are under way before the first is used.
+// Bound by the states' bytes: 256 rows, 16 heads of 128 x 64: 46.5 us for 272 MB, 5.8 TB/s.  One row: 4.4 us, the
+// latency of a load, a sum through LDS and a store.
 template <typename T, int LN, bool VEC>
 __global__ void __launch_bounds__(256) k_la_step(StepArgs A) {
     constexpr int RG = 256 / LN;                 // state rows at a time
@@ -1264,11 +1275,13 @@ __global__ void __launch_bounds__(256) k_la_step(StepArgs A) {
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 inline bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-constexpr int kLookThrough = 256;   // packed sequences that every workgroup looks through itself
+constexpr int kLookThrough = 256;   // packed sequences that every workgroup looks through itself (four looks of a wave)
 
 // Longest segment: as many segments as it takes to put about two workgroups on each compute unit (all
 // that fit at a time; packed sequences end in half a segment on average), no shorter than 256 tokens: a
 // segment's state makes four trips through memory.  Up to 1024 tokens in all, one segment a sequence.
+// Packed prompt and backward (above) with one workgroup a compute unit 115 and 212 us, with two 85 and 188, with
+// four and segments from 128 tokens 99 and 212; seven prompts of 1021 tokens in all 15 us, cut 19.5.
 int plan_target(int64_t n_seq, int64_t T, int64_t H, int64_t Dv, bool packed) {
     if (T <= 1024) return 1024;
     const int64_t units = H * ((Dv + kV - 1) / kV);
@@ -1602,7 +1615,8 @@ extern "C" mb_status mb_linear_attn_step(const void* q, const void* k, const voi
     StepArgs A{q, k, v, log_decay, slots, h_in, h_out, o, n, n_slots, q_stride, k_stride, v_stride,
                (int)H, (int)(H / G), (int)Dk, (int)Dv, 0, 0, scale, (size_t)n * H * Dk * Dv * 8 > kStreamBytes};
     // Few rows: narrow column tiles, so that the one token's states are read by more compute
-    // units; many rows: a tile as wide as a row of the state.
+    // units (one row of 16 heads: 4.4 us, with wide tiles 5.3); many rows: a tile as wide as a row of the
+    // state (256 rows: 46.6 us, with narrow tiles 79.5).
     const bool few = n * H < 2 * device_cu_count();
     const int ln = few ? 4 : 16, cpl = vec ? 4 : 1;
     A.cols = ln * cpl;

@@ -157,10 +157,10 @@ def test_forward_split_chains(dtype):
 
 @pytest.mark.parametrize("few", [True, False], ids=["looked through", "table"])
 def test_long_sequences_among_short_ones(few):
-    """Sequences of more than eight segments, whose states are composed beforehand, first, last and in between;
+    """Sequences of more segments than the walk composes, whose states are composed beforehand, first, last and in between;
     offsets in front of the first token and behind the last count as these."""
     short = [5] * (20 if few else 150)
-    lens, H, Dk, Dv = [2600] + short + [3001] + short + [2500], 2, 64, 64
+    lens, H, Dk, Dv = [4400] + short + [4501] + short + [2500, 4200], 2, 64, 64
     T, n = sum(lens), len(lens)
     d = inputs(61, T, H, H, Dk, Dv, "bf16", n)
     ld = torch.tensor([-0.002, -0.3])

@@ -32,7 +32,7 @@ def make(seed, rows, D, dtype, res, scale=1.0):
 
 
 TYPES = [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")]
-SHAPES = [(1, 1), (3, 7), (4, 768), (5, 512), (7, 513), (66, 1001), (3, 2048), (2, 2049), (5, 4104), (2, 8192), (3, 8200), (2, 16384)]
+SHAPES = [(1, 1), (3, 7), (4, 768), (5, 512), (7, 513), (66, 1001), (9, 1100), (5, 1840), (3, 2048), (2, 2049), (5, 4104), (2, 8192), (3, 8200), (2, 16384)]
 
 
 def rounded(v, dtype, u=1):
@@ -73,7 +73,7 @@ def test_norm_strided_unaligned_and_in_place(types):
 
 @pytest.mark.parametrize("types", TYPES, ids="-".join)
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
-@pytest.mark.parametrize("shape", [(1, 1), (5, 100), (6, 768), (4, 1001), (3, 2056), (2, 8192), (2, 9000)], ids=str)
+@pytest.mark.parametrize("shape", [(1, 1), (5, 100), (6, 768), (4, 1001), (5, 1840), (3, 2048), (3, 2056), (2, 8192), (2, 9000)], ids=str)
 def test_norm_8_bits(types, group, shape):
     (dtype, res), (rows, D) = types, shape
     x, r0, w = make(3, rows, D, dtype, res)
