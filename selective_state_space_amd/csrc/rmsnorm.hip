@@ -10,9 +10,11 @@
 // sum of squares and the scaling, and written once.  A row belongs to one wave
 // (D <= 1024, some to 2048), a workgroup of 256 (D <= 8192) or of 1024 threads (D <= 16384);
 // a thread holds E of its elements as E / VEC vectors, lanes side by side.
-// Measured: 16384 rows of 2048 bf16 with residual to 8 bits 47.4 us for 236 MB, 5.0 TB/s; 4097 rows of 1001 fp32, none of
-// them aligned to a vector, 17.6 us for 66 MB, 3.7 TB/s; four rows 3.2 us, the latency of one load, one sum and
-// one store.
+// Rows that no vector is aligned to are read and written in vectors all the same, which the memory
+// takes at any element's address; only a row's last vector goes element by element.
+// Measured: 16384 rows of 2048 bf16 with residual to 8 bits 46.5 us for 236 MB, 5.1 TB/s; 4097 rows of 1001 fp32, none of
+// them aligned, 12.7 us for 66 MB, 5.2 TB/s (one element at a time 17.6), 16384 of 1001 bf16 29.6 us (72);
+// four rows 3.2 us, the latency of one load, one sum and one store.
 #include "mb_internal.h"
 
 namespace mb {
@@ -26,56 +28,73 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kAmaxMin = 0x1p-96f;     // keeps 1 / scale and y / scale in range for a group of zeros
 constexpr int64_t kMaxD = 16384;
 
-template <int VEC>
-__device__ __forceinline__ void load_vec(const float* p, float* v) {
-    if constexpr (VEC == 1) {
-        v[0] = *p;
-    } else {
+// VEC neighbouring elements of a row, `left` of which (and at least one) are in it: those behind read as zero
+// and are not written.  AL: pointers and widths are multiples of the vector and a vector lies in the row
+// as a whole; otherwise it may start at any element, and the row's last one may be cut short.
+template <int VEC, bool AL>
+__device__ __forceinline__ void load_vec(const float* p, float* v, int left) {
+    if (AL || left >= VEC) {
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i) {
-            f4 t = reinterpret_cast<const f4*>(p)[i];
+            f4 t;
+            if constexpr (AL) t = reinterpret_cast<const f4*>(p)[i];
+            else __builtin_memcpy(&t, p + 4 * i, 16);
 #pragma unroll
             for (int k = 0; k < 4; ++k) v[4 * i + k] = t[k];
         }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = k < left ? p[k] : 0.0f;
     }
 }
 
-template <int VEC>
-__device__ __forceinline__ void load_vec(const bf16* p, float* v) {
-    if constexpr (VEC == 1) {
-        v[0] = to_f32(*p);
-    } else {
-        static_assert(VEC == 8, "bf16 vectors hold eight elements");
-        u4 t = *reinterpret_cast<const u4*>(p);
+template <int VEC, bool AL>
+__device__ __forceinline__ void load_vec(const bf16* p, float* v, int left) {
+    static_assert(VEC == 8, "bf16 vectors hold eight elements");
+    if (AL || left >= VEC) {
+        u4 t;
+        if constexpr (AL) t = *reinterpret_cast<const u4*>(p);
+        else __builtin_memcpy(&t, p, 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[2 * i] = __uint_as_float(t[i] << 16);
             v[2 * i + 1] = __uint_as_float(t[i] & 0xffff0000u);
         }
-    }
-}
-
-template <int VEC>
-__device__ __forceinline__ void store_vec(float* p, const float* v, bool stream) {
-    if constexpr (VEC == 1) {
-        *p = v[0];
     } else {
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i)
-            put(reinterpret_cast<f4*>(p) + i, f4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, stream);
+        for (int k = 0; k < VEC; ++k) v[k] = k < left ? to_f32(p[k]) : 0.0f;
     }
 }
 
-template <int VEC>
-__device__ __forceinline__ void store_vec(bf16* p, const float* v, bool stream) {
-    if constexpr (VEC == 1) {
-        *p = f32_to_bf16(v[0]);
+template <int VEC, bool AL>
+__device__ __forceinline__ void store_vec(float* p, const float* v, int left, bool stream) {
+    if (AL || left >= VEC) {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) {
+            const f4 t = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+            if constexpr (AL) put(reinterpret_cast<f4*>(p) + i, t, stream);
+            else __builtin_memcpy(p + 4 * i, &t, 16);
+        }
     } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            if (k < left) p[k] = v[k];
+    }
+}
+
+template <int VEC, bool AL>
+__device__ __forceinline__ void store_vec(bf16* p, const float* v, int left, bool stream) {
+    if (AL || left >= VEC) {
         u4 t;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             t[i] = (uint32_t)f32_to_bf16(v[2 * i]) | ((uint32_t)f32_to_bf16(v[2 * i + 1]) << 16);
-        put(reinterpret_cast<u4*>(p), t, stream);
+        if constexpr (AL) put(reinterpret_cast<u4*>(p), t, stream);
+        else __builtin_memcpy(p, &t, 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+            if (k < left) p[k] = f32_to_bf16(v[k]);
     }
 }
 
@@ -143,13 +162,12 @@ struct NormArgs {
 };
 
 // MODE 0: y in the type of x.  MODE 1: e4m3 with scales.
-template <typename TX, typename TR, int VEC, int E, int TPR, int MODE>
+template <typename TX, typename TR, int VEC, bool AL, int E, int TPR, int MODE>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) {
     constexpr int NT = TPR < 256 ? 256 : TPR;
     constexpr int ROWS = NT / TPR;
     constexpr int NV = E / VEC;
     __shared__ float red[16];
-    __shared__ uint32_t gmax[MODE == 1 && VEC == 1 ? 1024 : 1];
     const int lane = threadIdx.x % TPR, slot = threadIdx.x / TPR;
     const int64_t row = (int64_t)blockIdx.x * ROWS + slot;
     const bool live = row < a.rows;
@@ -162,10 +180,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
     for (int c = 0; c < NV; ++c) {
         const int d = (c * TPR + lane) * VEC;
         if (live && d < a.D) {
-            load_vec<VEC>(x + d, v + c * VEC);
+            load_vec<VEC, AL>(x + d, v + c * VEC, a.D - d);
             if (a.res) {
                 float t[VEC];
-                load_vec<VEC>(res + d, t);
+                load_vec<VEC, AL>(res + d, t, a.D - d);
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) v[c * VEC + k] += t[k];
             }
@@ -177,7 +195,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         const int d = (c * TPR + lane) * VEC;
-        if (a.r_out && live && d < a.D) store_vec<VEC>((TR*)a.r_out + row * a.D + d, v + c * VEC, a.stream);
+        if (a.r_out && live && d < a.D) store_vec<VEC, AL>((TR*)a.r_out + row * a.D + d, v + c * VEC, a.D - d, a.stream);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) ss = fmaf(v[c * VEC + k], v[c * VEC + k], ss);
     }
@@ -190,7 +208,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
         const int d = (c * TPR + lane) * VEC;
         float w[VEC];
         if (a.w && d < a.D) {
-            load_vec<VEC>(a.w + d, w);
+            load_vec<VEC, AL>(a.w + d, w, a.D - d);
         } else {
 #pragma unroll
             for (int k = 0; k < VEC; ++k) w[k] = 1.0f;
@@ -198,7 +216,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
 #pragma unroll
         for (int k = 0; k < VEC; ++k) v[c * VEC + k] = v[c * VEC + k] * rstd * w[k];
         if constexpr (MODE == 0) {
-            if (live && d < a.D) store_vec<VEC>((TX*)a.y + row * a.D + d, v + c * VEC, a.stream);
+            if (live && d < a.D) store_vec<VEC, AL>((TX*)a.y + row * a.D + d, v + c * VEC, a.D - d, a.stream);
         }
     }
     if constexpr (MODE == 1) {
@@ -219,7 +237,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
 #pragma unroll
             for (int c = 0; c < NV; ++c) m[c] = t;
             if (live && lane == 0) scales[0] = group_scale(t);
-        } else if constexpr (VEC > 1) {
+        } else {
             const int lanes = a.group / VEC;       // a power of two, at most 32
 #pragma unroll
             for (int c = 0; c < NV; ++c) {
@@ -227,23 +245,6 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
                 const int d = (c * TPR + lane) * VEC;
                 if (live && d < a.D && (lane & (lanes - 1)) == 0) scales[d / a.group] = group_scale(m[c]);
             }
-        } else {
-            uint32_t* gm = gmax + slot * (1024 / ROWS);
-            for (int i = lane; i < a.ngroups; i += TPR) gm[i] = 0;
-            __syncthreads();
-#pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                const int d = c * TPR + lane;
-                if (d < a.D) atomicMax(&gm[d / a.group], m[c]);    // a maximum: any order gives the same
-            }
-            __syncthreads();
-#pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                const int d = c * TPR + lane;
-                if (d < a.D) m[c] = gm[d / a.group];
-            }
-            if (live)
-                for (int i = lane; i < a.ngroups; i += TPR) scales[i] = group_scale(gm[i]);
         }
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
@@ -253,17 +254,21 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
                 float t[VEC];
 #pragma unroll
                 for (int k = 0; k < VEC; ++k) t[k] = over(v[c * VEC + k], s, inv);
-                if constexpr (VEC == 1) {
-                    q[d] = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[0], 0, false);
-                } else {
-                    uint32_t o[VEC / 4];
+                uint32_t o[VEC / 4];
 #pragma unroll
-                    for (int k = 0; k < VEC / 4; ++k) {
-                        int p = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * k], t[4 * k + 1], 0, false);
-                        o[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * k + 2], t[4 * k + 3], p, true);
-                    }
+                for (int k = 0; k < VEC / 4; ++k) {
+                    int p = __builtin_amdgcn_cvt_pk_fp8_f32(t[4 * k], t[4 * k + 1], 0, false);
+                    o[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(t[4 * k + 2], t[4 * k + 3], p, true);
+                }
+                if constexpr (AL) {
                     if constexpr (VEC == 8) put(reinterpret_cast<u2*>(q + d), u2{o[0], o[1]}, a.stream);
                     else put(reinterpret_cast<uint32_t*>(q + d), o[0], a.stream);
+                } else if (a.D - d >= VEC) {
+                    __builtin_memcpy(q + d, o, VEC);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < VEC; ++k)
+                        if (k < a.D - d) q[d + k] = (uint8_t)(o[k / 4] >> (8 * (k % 4)));
                 }
             }
         }
@@ -286,7 +291,7 @@ struct NormBwdArgs {
 // A workgroup walks rows; every thread keeps its columns' share of dw in registers
 // and the rows' slots are added up in LDS at the end.  16384 rows of 1536, bf16 with fp32 residual: 76 us for
 // 403 MB, 5.3 TB/s, and 4.7 us for the sum over workgroups.
-template <typename TX, typename TR, int VEC, int E, int TPR>
+template <typename TX, typename TR, int VEC, bool AL, int E, int TPR>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm_bwd(NormBwdArgs a) {
     constexpr int NT = TPR < 256 ? 256 : TPR;
     constexpr int ROWS = NT / TPR;
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm_bwd(NormBwdA
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             const int d = (c * TPR + lane) * VEC;
-            if (d < a.D) load_vec<VEC>(a.w + d, w + c * VEC);
+            if (d < a.D) load_vec<VEC, AL>(a.w + d, w + c * VEC, a.D - d);
         }
     }
     const float inv_d = 1.0f / (float)a.D;
@@ -314,10 +319,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm_bwd(NormBwdA
         for (int c = 0; c < NV; ++c) {
             const int d = (c * TPR + lane) * VEC;
             if (live && d < a.D) {
-                load_vec<VEC>((const TX*)a.dy + row * a.D + d, dy + c * VEC);
-                load_vec<VEC>((const TR*)a.r + row * a.D + d, xh + c * VEC);
+                load_vec<VEC, AL>((const TX*)a.dy + row * a.D + d, dy + c * VEC, a.D - d);
+                load_vec<VEC, AL>((const TR*)a.r + row * a.D + d, xh + c * VEC, a.D - d);
                 if (a.dr_in) {
-                    load_vec<VEC>((const TR*)a.dr_in + row * a.D + d, in + c * VEC);
+                    load_vec<VEC, AL>((const TR*)a.dr_in + row * a.D + d, in + c * VEC, a.D - d);
                 } else {
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) in[c * VEC + k] = 0.0f;
@@ -344,8 +349,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm_bwd(NormBwdA
 #pragma unroll
                 for (int k = 0; k < VEC; ++k)
                     o[k] = fmaf(rstd, fmaf(-xh[c * VEC + k], dot, dy[c * VEC + k]), in[c * VEC + k]);
-                if (a.dr) store_vec<VEC>((TR*)a.dr + row * a.D + d, o, false);
-                if (a.dx) store_vec<VEC>((TX*)a.dx + row * a.D + d, o, false);
+                if (a.dr) store_vec<VEC, AL>((TR*)a.dr + row * a.D + d, o, a.D - d, false);
+                if (a.dx) store_vec<VEC, AL>((TX*)a.dx + row * a.D + d, o, a.D - d, false);
             }
         }
     }
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm_bwd(NormBwdA
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
         const int d = (c * TPR + lane) * VEC;
-        if (d < a.D) store_vec<VEC>(a.part + (int64_t)blockIdx.x * a.D + d, dw + c * VEC, false);
+        if (d < a.D) store_vec<VEC, AL>(a.part + (int64_t)blockIdx.x * a.D + d, dw + c * VEC, a.D - d, false);
     }
 }
 
@@ -386,7 +391,8 @@ __global__ void __launch_bounds__(256) k_dw_sum(const float* __restrict__ part, 
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 if (i + j * SUB < n) {
-                    load_vec<VEC>(part + (int64_t)(i + j * SUB) * D + d, t[j]);
+                    if constexpr (VEC == 1) t[j][0] = part[(int64_t)(i + j * SUB) * D + d];
+                    else load_vec<VEC, true>(part + (int64_t)(i + j * SUB) * D + d, t[j], VEC);
                 } else {
 #pragma unroll
                     for (int k = 0; k < VEC; ++k) t[j][k] = 0.0f;
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(256) k_dw_sum(const float* __restrict__ part, 
 
 inline bool vec_ok(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-template <typename TX, typename TR, int MODE, int VEC>
+template <typename TX, typename TR, int MODE, int VEC, bool AL>
 void launch_norm(const NormArgs& a, hipStream_t s) {
     const int per = a.D;
     auto go = [&](auto kern, int nt, int rows) {
@@ -421,13 +427,13 @@ void launch_norm(const NormArgs& a, hipStream_t s) {
     // bf16 of 2048 columns 50.4 and 47.9 us (to 8 bits 51.0 and 47.4), of 1536 to 8 bits 41.0 and 44.3;
     // fp32 of 1280 65 and 58.4.
     constexpr bool F32 = sizeof(TX) == 4;
-    if (per <= 64 * 8) go(k_rms_norm<TX, TR, VEC, 8, 64, MODE>, 256, 4);
-    else if (per <= 64 * 16) go(k_rms_norm<TX, TR, VEC, 16, 64, MODE>, 256, 4);
-    else if (VEC > 1 && per > (F32 ? 1024 : 1792) && per <= 256 * 8) go(k_rms_norm<TX, TR, VEC, 8, 256, MODE>, 256, 1);
-    else if (per <= 64 * 32) go(k_rms_norm<TX, TR, VEC, 32, 64, MODE>, 256, 4);
-    else if (per <= 256 * 16) go(k_rms_norm<TX, TR, VEC, 16, 256, MODE>, 256, 1);
-    else if (per <= 256 * 32) go(k_rms_norm<TX, TR, VEC, 32, 256, MODE>, 256, 1);
-    else go(k_rms_norm<TX, TR, VEC, 16, 1024, MODE>, 1024, 1);
+    if (per <= 64 * 8) go(k_rms_norm<TX, TR, VEC, AL, 8, 64, MODE>, 256, 4);
+    else if (per <= 64 * 16) go(k_rms_norm<TX, TR, VEC, AL, 16, 64, MODE>, 256, 4);
+    else if (per > (F32 ? 1024 : 1792) && per <= 256 * 8) go(k_rms_norm<TX, TR, VEC, AL, 8, 256, MODE>, 256, 1);
+    else if (per <= 64 * 32) go(k_rms_norm<TX, TR, VEC, AL, 32, 64, MODE>, 256, 4);
+    else if (per <= 256 * 16) go(k_rms_norm<TX, TR, VEC, AL, 16, 256, MODE>, 256, 1);
+    else if (per <= 256 * 32) go(k_rms_norm<TX, TR, VEC, AL, 32, 256, MODE>, 256, 1);
+    else go(k_rms_norm<TX, TR, VEC, AL, 16, 1024, MODE>, 1024, 1);
 }
 
 template <int MODE>
@@ -462,11 +468,11 @@ mb_status norm(const void* x, const void* res, const float* w, void* y, float* s
     const int V = dtype == MB_BF16 ? 8 : 4;
     const bool vec = D % V == 0 && x_stride % V == 0 && vec_ok(x) && vec_ok(res) && vec_ok(w) && vec_ok(y) && vec_ok(r_out);
     if (dtype == MB_F32)
-        vec ? launch_norm<float, float, MODE, 4>(a, stream) : launch_norm<float, float, MODE, 1>(a, stream);
+        vec ? launch_norm<float, float, MODE, 4, true>(a, stream) : launch_norm<float, float, MODE, 4, false>(a, stream);
     else if (rdtype == MB_F32)
-        vec ? launch_norm<bf16, float, MODE, 8>(a, stream) : launch_norm<bf16, float, MODE, 1>(a, stream);
+        vec ? launch_norm<bf16, float, MODE, 8, true>(a, stream) : launch_norm<bf16, float, MODE, 8, false>(a, stream);
     else
-        vec ? launch_norm<bf16, bf16, MODE, 8>(a, stream) : launch_norm<bf16, bf16, MODE, 1>(a, stream);
+        vec ? launch_norm<bf16, bf16, MODE, 8, true>(a, stream) : launch_norm<bf16, bf16, MODE, 8, false>(a, stream);
     return check_launch();
 }
 
@@ -478,15 +484,15 @@ int bwd_grid(int64_t rows, int64_t D) {
     return (int)(want < cap ? want : cap);
 }
 
-template <typename TX, typename TR, int VEC>
+template <typename TX, typename TR, int VEC, bool AL>
 void launch_bwd(const NormBwdArgs& a, int grid, hipStream_t s) {
     auto go = [&](auto kern, int nt) { hipLaunchKernelGGL(kern, dim3(grid), dim3(nt), 0, s, a); };
-    if (a.D <= 64 * 8) go(k_rms_norm_bwd<TX, TR, VEC, 8, 64>, 256);
-    else if (a.D <= 64 * 16) go(k_rms_norm_bwd<TX, TR, VEC, 16, 64>, 256);
-    else if (a.D <= 64 * 32) go(k_rms_norm_bwd<TX, TR, VEC, 32, 64>, 256);
-    else if (a.D <= 256 * 16) go(k_rms_norm_bwd<TX, TR, VEC, 16, 256>, 256);
-    else if (a.D <= 256 * 32) go(k_rms_norm_bwd<TX, TR, VEC, 32, 256>, 256);
-    else go(k_rms_norm_bwd<TX, TR, VEC, 16, 1024>, 1024);
+    if (a.D <= 64 * 8) go(k_rms_norm_bwd<TX, TR, VEC, AL, 8, 64>, 256);
+    else if (a.D <= 64 * 16) go(k_rms_norm_bwd<TX, TR, VEC, AL, 16, 64>, 256);
+    else if (a.D <= 64 * 32) go(k_rms_norm_bwd<TX, TR, VEC, AL, 32, 64>, 256);
+    else if (a.D <= 256 * 16) go(k_rms_norm_bwd<TX, TR, VEC, AL, 16, 256>, 256);
+    else if (a.D <= 256 * 32) go(k_rms_norm_bwd<TX, TR, VEC, AL, 32, 256>, 256);
+    else go(k_rms_norm_bwd<TX, TR, VEC, AL, 16, 1024>, 1024);
 }
 
 }  // namespace
@@ -546,11 +552,11 @@ extern "C" mb_status mb_rms_norm_bwd(const void* dy, const void* r, const float*
     const bool vec = D % V == 0 && vec_ok(dy) && vec_ok(r) && vec_ok(weight) && vec_ok(dr_in) && vec_ok(dx) && vec_ok(dr) &&
                      vec_ok(part);
     if (dtype == MB_F32)
-        vec ? launch_bwd<float, float, 4>(a, grid, stream) : launch_bwd<float, float, 1>(a, grid, stream);
+        vec ? launch_bwd<float, float, 4, true>(a, grid, stream) : launch_bwd<float, float, 4, false>(a, grid, stream);
     else if (residual_dtype == MB_F32)
-        vec ? launch_bwd<bf16, float, 8>(a, grid, stream) : launch_bwd<bf16, float, 1>(a, grid, stream);
+        vec ? launch_bwd<bf16, float, 8, true>(a, grid, stream) : launch_bwd<bf16, float, 8, false>(a, grid, stream);
     else
-        vec ? launch_bwd<bf16, bf16, 8>(a, grid, stream) : launch_bwd<bf16, bf16, 1>(a, grid, stream);
+        vec ? launch_bwd<bf16, bf16, 8, true>(a, grid, stream) : launch_bwd<bf16, bf16, 8, false>(a, grid, stream);
     mb_status st = check_launch();
     if (st != MB_OK || !need) return st;
     const dim3 cols((unsigned)((D + 31) / 32));
