@@ -963,8 +963,8 @@ __device__ __forceinline__ int block_of(int wave8) {
 // queries, which only they read) and put them to LDS between two barriers.
 // TO: type of the output (fp32 where several heads' gradients are still to be added up).
 // bf16 is bound by its traffic: the packed prompt above 51 us for 233 MB, 4.6 TB/s, and the backward's run for dq (4 x 4096
-// tokens, do and v to dq) 51 us for 211 MB, 4.1 TB/s, the matrix unit 16 - 19 % busy.  fp32, 46 us for 143 MB with
-// the matrix unit 41 % busy, waits for both in turn.  Two workgroups of eight waves fit a compute unit: 128
+// tokens, do and v to dq) 51 us for 211 MB, 4.1 TB/s, the matrix unit 16 - 19 % busy.  fp32, 50 us for 143 MB with
+// the matrix unit 38 % busy, waits for both in turn.  Two workgroups of eight waves fit a compute unit: 128
 // registers a wave.
 template <typename T, typename TO, int DA, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_la_out(LaArgs A) {
