@@ -256,6 +256,8 @@ __device__ __forceinline__ u2 tr4(const bf16* p) {
 struct Window {
     __amdgpu_buffer_rsrc_t r;
     int row0, step;      // byte offsets: of the first row in walking order, and to the next one
+    const char* base;    // the same range as r, for vectors at any element's address
+    uint32_t bytes;
 };
 
 // p: the chunk's first token in walking order; ts: elements between tokens; n: tokens; width: elements of a row in use.
@@ -266,26 +268,33 @@ __device__ __forceinline__ Window window(const T* p, int64_t ts, bool reversed, 
     w.row0 = reversed ? (n - 1) * b : 0;
     w.step = reversed ? -b : b;
     const char* base = (const char*)p - (reversed && n > 0 ? w.row0 : 0);
-    w.r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, n > 0 ? (n - 1) * b + width * (int)sizeof(T) : 0, 0x00027000);
+    w.base = base;
+    w.bytes = n > 0 ? (n - 1) * b + width * (int)sizeof(T) : 0;
+    w.r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)w.bytes, 0x00027000);
     return w;
 }
 
-// VE elements from column c of row r; columns at and behind `width` are zero.
+// VE elements from column c of row r; columns at and behind `width` are zero.  Without VEC they may start at any
+// element's address, which the memory takes in one access; a row's last vector may be cut short (2 x 8192 tokens, 16 heads
+// of 128 x 64, bf16, from an odd address on: element by element 199 us and backward 555, so 101 and 226; aligned 72 and 196).
 template <typename T, bool VEC>
 __device__ __forceinline__ u4 load_row(const Window& w, int r, int c, int width) {
     const uint32_t off = (uint32_t)(w.row0 + r * w.step + c * (int)sizeof(T));
     u4 v;
     if constexpr (VEC) {
         v = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(w.r, c < width ? off : 0x80000000u, 0, 0));
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_raw_buffer_load_b32(w.r, c + e < width ? off + 4 * e : 0x80000000u, 0, 0);
     } else {
+        // Strides hold a row's width: an offset inside the range is in one of its rows.
+        constexpr int VE = Frag<T>::VE;
+        const int left = off < w.bytes ? width - c : 0;
+        v = u4{0, 0, 0, 0};
+        if (left >= VE) {
+            __builtin_memcpy(&v, w.base + off, 16);
+        } else if (left > 0) {
+            T part[VE];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, c + 2 * e < width ? off + 4 * e : 0x80000000u, 0, 0);
-            const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(w.r, c + 2 * e + 1 < width ? off + 4 * e + 2 : 0x80000000u, 0, 0);
-            v[e] = lo | hi << 16;
+            for (int e = 0; e < VE; ++e) part[e] = e < left ? reinterpret_cast<const T*>(w.base + off)[e] : (T)0;
+            __builtin_memcpy(&v, part, 16);
         }
     }
     return v;
@@ -852,14 +861,33 @@ __device__ __forceinline__ void store_rows(TO* base, int64_t step, int i, int n,
         }
     } else if (i < n) {
         TO* row = base + i * step;
+        if constexpr (sizeof(TO) == 4) {
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            if constexpr (VEC) {
-                if (column<TO>(x, gr) < width) *reinterpret_cast<f4*>(row + column<TO>(x, gr)) = o[x];
-            } else {
+            for (int x = 0; x < NT; ++x) {
+                const int col = column<TO>(x, gr);
+                if constexpr (VEC) {
+                    if (col < width) *reinterpret_cast<f4*>(row + col) = o[x];
+                } else if (col + 4 <= width) {
+                    __builtin_memcpy(row + col, &o[x], 16);
+                } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (column<TO>(x, gr) + r < width) store_out(row + column<TO>(x, gr) + r, o[x][r]);
+                    for (int r = 0; r < 4; ++r)
+                        if (col + r < width) row[col + r] = o[x][r];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < NT; x += 2) {
+                const int col = column<TO>(x, gr);
+                const u4 t = {pack_bf16(o[x][0], o[x][1]), pack_bf16(o[x][2], o[x][3]), pack_bf16(o[x + 1][0], o[x + 1][1]),
+                              pack_bf16(o[x + 1][2], o[x + 1][3])};
+                if (col + 8 <= width) {
+                    __builtin_memcpy(row + col, &t, 16);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        if (col + r < width) row[col + r] = (TO)(t[r / 2] >> (16 * (r % 2)));
+                }
             }
         }
     }
