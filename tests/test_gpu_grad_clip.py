@@ -119,6 +119,21 @@ def test_clip_without_a_limit_writes_nothing():
         assert torch.equal(out[0].nan_to_num(nan=-5.0), keep.nan_to_num(nan=-5.0))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("off", [(1, 0), (0, 3), (5, 2)], ids=str)
+def test_clip_from_one_address_to_another(off, dtype):
+    """Gradients and outputs at different distances from a 16-byte address; what lies beside the outputs stays."""
+    gs = tensors([40_003, 1, 17, 8], dtype, seed=9)
+    src = [torch.zeros(g.numel() + 16, dtype=DT[dtype], device="cuda") for g in gs]
+    dst = [torch.full((g.numel() + 16,), 7.0, dtype=DT[dtype], device="cuda") for g in gs]
+    a = [t[off[0]:off[0] + g.numel()].copy_(g) for t, g in zip(src, gs)]
+    o = [t[off[1]:off[1] + g.numel()] for t, g in zip(dst, gs)]
+    out, norm = mb.mb_grad_norm_clip(a, 0.5, out=o)
+    check(out, norm, gs, 0.5, dtype)
+    for t, g in zip(dst, gs):
+        assert bool((t[:off[1]] == 7.0).all()) and bool((t[off[1] + g.numel():] == 7.0).all())
+
+
 def test_clip_of_tensors_that_share_memory():
     """Gradients that are only read may; a written one may not."""
     flat = torch.randn(5000, generator=torch.Generator().manual_seed(3)).cuda()

@@ -274,6 +274,33 @@ def test_step_continues_the_chunked_form():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("widths", [(64, 64), (100, 52), (33, 127)], ids=str)
+@pytest.mark.parametrize("off", [1, 2, 3])
+def test_backward_of_views_at_any_address(off, widths, dtype):
+    """q, k and v as columns of one buffer that starts at an odd element, its rows longer than these by an odd number."""
+    (Dk, Dv), H, lens = widths, 2, [70, 1, 300]
+    T, n, ld = sum(lens), len(lens), decays(H)
+    d = inputs(71, T, H, H, Dk, Dv, dtype, n, with_do=True)
+    wide = H * (2 * Dk + Dv) + off
+    buf = torch.full((off + T * wide,), 9.0, dtype=DT[dtype]).cuda()
+    rows = buf[off:].view(T, wide)
+    at, c = 0, {}
+    for x, D in (("q", Dk), ("k", Dk), ("v", Dv)):
+        rows[:, at:at + H * D] = d[x].reshape(T, H * D).cuda()
+        c[x] = rows[:, at:at + H * D].unflatten(1, (H, D))
+        at += H * D
+    cu = torch.tensor([sum(lens[:i]) for i in range(n + 1)], dtype=torch.int32).cuda()
+    do = torch.empty(T * H * Dv + off, dtype=DT[dtype], device="cuda")[off:].view(T, H, Dv).copy_(d["do"])
+    out = mb.mb_linear_attn_bwd(c["q"], c["k"], c["v"], ld.cuda(), do, scale=0.3, cu_seqlens=cu)
+    D64 = {x: t.double() for x, t in d.items()}
+    A = {x: t.abs() for x, t in D64.items()}
+    ref = lf.attn_bwd(D64["q"], D64["k"], D64["v"], ld, 0.3, lens, D64["do"])
+    mag = lf.attn_bwd(A["q"], A["k"], A["v"], ld, 0.3, lens, A["do"])
+    for name, got, r, M in zip(("dq", "dk", "dv"), out, ref, mag):
+        close(got, r, bound(dtype, max(Dk, Dv) + 4, lens, M, r), name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_later_tokens_and_other_sequences_do_not_reach_back(dtype):
     """Infinite values and NaN keys, in the middle of a chunk: earlier tokens and the other sequences as without."""
     lens, H, D = [100, 200, 30], 2, 64
