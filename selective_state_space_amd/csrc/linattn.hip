@@ -91,9 +91,16 @@ struct LaArgs {
 
 __device__ __forceinline__ int segments_of(int len, int target) { return max((int)(((int64_t)len + target - 1) / target), 1); }
 
+// Tokens of each of a sequence's `count` segments but the last: even parts in whole chunks.  A length and
+// the number of its segments may add up to 2^31 and more: unsigned.
+__device__ __forceinline__ int segment_tokens(int len, int count) {
+    const uint32_t even = ((uint32_t)len + (uint32_t)count - 1) / (uint32_t)count;
+    return (int)((even + kC - 1) / kC * kC);
+}
+
 // Fills in p0 and n from idx and count.
 __device__ __forceinline__ void place(Seg& g) {
-    const int even = (g.len + g.count - 1) / g.count, each = (even + kC - 1) / kC * kC;
+    const int each = segment_tokens(g.len, g.count);
     g.p0 = g.idx * each;
     g.n = max(min(each, g.len - g.p0), 0);
 }
@@ -642,7 +649,7 @@ __global__ void __launch_bounds__(256) k_la_carry(LaArgs A, const int* longs) {
     int first, n, len;
     sequence(A, seq, first, n, len);
     if (n <= kFewSegments) return;
-    const float f = power(log2_decay(A, h), ((len + n - 1) / n + kC - 1) / kC * kC);
+    const float f = power(log2_decay(A, h), segment_tokens(len, n));
     f4* p = reinterpret_cast<f4*>(A.states + state_at(A, first, h, tile, DA)) + part * 256 + threadIdx.x;
     const int64_t step = state_at(A, 1, 0, 0, DA) / 4;
     f4 run = p[0];
