@@ -75,7 +75,7 @@ struct LaArgs {
     int reversed;
     int n_seq;
     int T, L;                         // tokens in all; of a sequence when they are equal
-    int target, nseg;                 // longest segment, segments launched
+    int target, seg0, nseg;           // longest segment; segments seg0 to nseg - 1 are launched
     int per_seq;                      // segments of a sequence when lengths are equal, else 0
     const int32_t* cu;
     const Seg* plan;                  // segments of many packed sequences; NULL: worked out by every workgroup
@@ -492,12 +492,16 @@ __device__ __forceinline__ Unit unit_of(const LaArgs& A) {
     Unit u;
     u.tile = i % A.nv;
     u.h = outer % groups * A.share + i / A.nv;
-    u.seg = outer / groups;
+    u.seg = A.seg0 + outer / groups;
     return u;
 }
 inline unsigned grid_of(const LaArgs& A) {
-    const int64_t outer = (int64_t)A.nseg * (A.H / A.share);
+    const int64_t outer = (int64_t)(A.nseg - A.seg0) * (A.H / A.share);
     return (unsigned)((outer + 7) / 8 * 8 * A.share * A.nv);
+}
+// Segments whose grid_of a launch may have.
+inline int64_t segments_of_launch(const LaArgs& A) {
+    return (max_workgroups(kWalkThreads) - 7 * A.share * A.nv) / ((int64_t)A.H * A.nv);
 }
 
 // ------------------------------------------------------------------ plan ----
@@ -616,7 +620,8 @@ __global__ void __launch_bounds__(kWalkThreads) k_la_state(LaArgs A) {
 // In place over a sequence's places: the state that enters each of its segments.  A workgroup
 // takes 1024 values (256 lanes of four) of one (long sequence, head, tile).  There are at most
 // T / (kFewSegments target + 1) long sequences, so the launch does not grow with the short ones (64k tokens in
-// 2000 sequences, 16 heads: the call 892 -> 780 us).  Bound by latency: 5.4 us for 16.9 MB, 5.1 us where it finds none.
+// 2000 sequences, 16 heads: the call 892 -> 780 us).  They are never more than 128: 2^23 workgroups
+// with the most heads and columns.  Bound by latency: 5.4 us for 16.9 MB, 5.1 us where it finds none.
 template <int DA>
 __global__ void __launch_bounds__(256) k_la_carry(LaArgs A, const int* longs) {
     constexpr int PER = DA * kV / 1024;
@@ -1366,10 +1371,20 @@ bool strides_ok(int64_t stride, int64_t row) { return stride >= row && stride < 
 
 template <typename T, typename TO, int DA, bool VEC>
 mb_status run_passes(const LaArgs& A, const SecondArgs* X, const Plan& p, hipStream_t s) {
-    const dim3 grid(grid_of(A)), wide(kWalkThreads);
+    const auto launch = [&](auto kern, const auto&... more) -> mb_status {
+        mb_status st = MB_OK;
+        const int64_t per = segments_of_launch(A);
+        for (int64_t at = 0; at < p.nseg && st == MB_OK; at += per) {
+            LaArgs B = A;
+            B.seg0 = (int)at;
+            B.nseg = (int)std::min<int64_t>(at + per, p.nseg);
+            hipLaunchKernelGGL(kern, dim3(grid_of(B)), dim3(kWalkThreads), 0, s, B, more...);
+            st = check_launch();
+        }
+        return st;
+    };
     if (p.states) {
-        hipLaunchKernelGGL((k_la_state<T, DA, VEC>), grid, wide, 0, s, A);
-        mb_status st = check_launch();
+        mb_status st = launch(k_la_state<T, DA, VEC>);
         if (st != MB_OK) return st;
         if (p.n_long) {
             const dim3 blocks((unsigned)((int64_t)p.n_long * A.H * A.nv * (DA * kV / 1024)));
@@ -1378,9 +1393,7 @@ mb_status run_passes(const LaArgs& A, const SecondArgs* X, const Plan& p, hipStr
             if ((st = check_launch()) != MB_OK) return st;
         }
     }
-    if (X) hipLaunchKernelGGL((k_la_dkdv<T, TO, DA, VEC>), grid, wide, 0, s, A, *X);
-    else hipLaunchKernelGGL((k_la_out<T, TO, DA, VEC>), grid, wide, 0, s, A);
-    return check_launch();
+    return X ? launch(k_la_dkdv<T, TO, DA, VEC>, *X) : launch(k_la_out<T, TO, DA, VEC>);
 }
 
 template <typename T, typename TO>
@@ -1415,12 +1428,6 @@ mb_status launch_plan(LaArgs A, const Plan& p, char* ws, hipStream_t s) {
     A.plan = nullptr;
     hipLaunchKernelGGL(k_la_plan, dim3(1), dim3(64), 0, s, A, (Seg*)ws, (int2*)(ws + p.seqs_at), (int*)(ws + p.longs_at), p.n_long);
     return check_launch();
-}
-
-// Workgroups a launch may have.
-bool grid_ok(const Plan& p, int64_t H, int64_t Dv) {
-    const int64_t nv = (Dv + kV - 1) / kV;
-    return ((int64_t)p.nseg + 8) * H * nv <= 0x7fffffff && (int64_t)p.n_long * H * nv * 8 <= 0x7fffffff;
 }
 
 // The backward: one run for dq, and for dk and dv one walk over both where one of them is at most a
@@ -1490,7 +1497,6 @@ extern "C" mb_status mb_linear_attn(const void* q, const void* k, const void* v,
         return MB_ERR_ALIGN;
     const Plan p = make_plan(n_seq, T, H, Dk, Dv, cu_seqlens != nullptr);
     const size_t need = p.table_bytes + p.states;
-    if (!grid_ok(p, H, Dv)) return MB_ERR_SHAPE;
     if (need && (!ws || ws_bytes < need || ((uintptr_t)ws & 255))) return MB_ERR_WORKSPACE;
     const size_t nh = (size_t)(slots ? n_slots : n_seq) * H * Dk * Dv * 4;
     const Span ins[8] = {{q, span_of(T, q_stride, H * Dk, es)}, {k, span_of(T, k_stride, G * Dk, es)}, {v, span_of(T, v_stride, G * Dv, es)},
@@ -1537,7 +1543,6 @@ extern "C" mb_status mb_linear_attn_bwd(const void* q, const void* k, const void
         ((uintptr_t)h0 & 3) || ((uintptr_t)dh_out & 3) || ((uintptr_t)dh0 & 3))
         return MB_ERR_ALIGN;
     const BwdPlan bp = n_seq ? bwd_plan(n_seq, T, H, G, Dk, Dv, cu_seqlens != nullptr) : BwdPlan{};
-    if (n_seq && (!grid_ok(bp.q, H, Dk) || !grid_ok(bp.v, H, Dv))) return MB_ERR_SHAPE;
     if (bp.total && (!ws || ws_bytes < bp.total || ((uintptr_t)ws & 255))) return MB_ERR_WORKSPACE;
     const size_t nh = (size_t)n_seq * H * Dk * Dv * 4;
     const Span ins[8] = {{q, span_of(T, q_stride, H * Dk, es)}, {k, span_of(T, k_stride, G * Dk, es)}, {v, span_of(T, v_stride, G * Dv, es)},

@@ -24,6 +24,9 @@ inline mb_status check_launch() {
     return MB_OK;
 }
 
+// Workgroups of one launch: HIP takes grids of fewer than 2^32 threads.
+constexpr int64_t max_workgroups(int threads) { return 0xffffffffll / threads; }
+
 // ------------------------------------------------------------ validation ----
 struct Span {
     const void* p;

@@ -50,3 +50,54 @@ def test_one_sequence_of_almost_two_to_the_31_tokens():
         ref, mag = lf.attn_bwd(*d[:3], ld, 0.5, [600], d[3]), lf.attn_bwd(*a[:3], ld, 0.5, [600], a[3])
         for name, got, r, M, part in zip(("dq", "dk", "dv"), grads, ref, mag, (slice(first, 600), slice(0, last), slice(0, last))):
             close(got[0, w][part], r[part], bound("bf16", 5, [600], M, r)[part], name + " at %d" % at)
+
+
+def _pairs(n, G, D, H, dtype, seed):
+    """Inputs of n packed sequences of zero, one or two tokens, and which row is whose."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    lens = torch.randint(0, 3, (n,), generator=g, device="cuda")
+    cu = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    cu[1:] = lens.cumsum(0)
+    T = int(cu[-1])
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda").to(dtype)
+    return lens, cu, T, rn(T, H, D), rn(T, G, D), rn(T, G, D), rn(T, H, D)
+
+
+def _pairs_forward(q, k, v, ld, scale, lens, cu):
+    """o and the end states of sequences of at most two tokens."""
+    lam = torch.exp(ld.double().cuda()).view(-1, 1)
+    first = cu[:-1][lens > 0].long()
+    second = cu[:-1][lens > 1].long() + 1
+    h = torch.zeros(lens.numel(), q.shape[1], q.shape[2], v.shape[2], dtype=F64, device="cuda")
+    h[lens > 0] = k[first].unsqueeze(3) * v[first].unsqueeze(2)
+    o = torch.zeros(q.shape[0], q.shape[1], v.shape[2], dtype=F64, device="cuda").index_add(
+        0, first, scale * (q[first] * k[first]).sum(2, keepdim=True) * v[first])
+    o = o.index_add(0, second, scale * (q[second] * k[second]).sum(2, keepdim=True) * v[second])
+    o = o.index_add(0, second, scale * lam * (q[second] * k[second - 1]).sum(2, keepdim=True) * v[second - 1])
+    h[lens > 1] = h[lens > 1] * lam.unsqueeze(2) + k[second].unsqueeze(3) * v[second].unsqueeze(2)
+    return o, h
+
+
+def test_more_workgroups_than_a_launch_takes():
+    """2^20 sequences of 8 heads: as many threads as a grid may not have, forward and backward."""
+    n, H, D, scale = 2 ** 20, 8, 4, 0.5
+    ld = -torch.arange(1.0, H + 1) / H
+    lens, cu, T, q, k, v, do = _pairs(n, H, D, H, torch.float32, 2)
+    o, h = mb.mb_linear_attn(q, k, v, ld.cuda(), scale=scale, cu_seqlens=cu)
+    grads = mb.mb_linear_attn_bwd(q, k, v, ld.cuda(), do, scale=scale, cu_seqlens=cu)
+    # magnitudes are added up over at most two tokens of four products each: 16 roundings are more than there are, and
+    # the decay's exponent is off by less than 2 u of one
+    tol = lambda M: 20 * 2.0 ** -24 * M
+    L = [t.double() for t in (q, k, v)]
+    A = [t.abs() for t in L]
+    for got, r, M, name in zip((o, h), _pairs_forward(*L, ld, scale, lens, cu), _pairs_forward(*A, ld, scale, lens, cu), "oh"):
+        assert bool(((got - r).abs() <= tol(M)).all()), name
+    del o, h, got, r, M
+    auto, mag = [], []
+    for src, d, out in ((L, do.double(), auto), (A, do.double().abs(), mag)):
+        leaves = [t.requires_grad_() for t in src]
+        (_pairs_forward(*leaves, ld, scale, lens, cu)[0] * d).sum().backward()
+        out += [t.grad for t in leaves]
+    for got, r, M, name in zip(grads, auto, mag, ("dq", "dk", "dv")):
+        assert bool(((got - r).abs() <= tol(M)).all()), name
+    assert not bool(grads[3].isnan().any())
