@@ -1221,7 +1221,7 @@ struct StepArgs {
     const float* h_in;
     float* h_out;
     void* o;
-    int64_t n, n_slots, q_ts, k_ts, v_ts;
+    int64_t row0, n_slots, q_ts, k_ts, v_ts;      // row0: first row of the launch
     int H, rep, Dk, Dv, cols, tiles;     // value columns of a workgroup, workgroups of a row's head
     float scale;
     bool stream;                         // states past the caches
@@ -1243,7 +1243,7 @@ __global__ void __launch_bounds__(256) k_la_step(StepArgs A) {
     const int tile = b % A.tiles;
     b /= A.tiles;
     const int h = b % A.H;
-    const int64_t row = b / A.H;
+    const int64_t row = A.row0 + b / A.H;
     const int ln = threadIdx.x % LN, rg = threadIdx.x / LN;
     const int col = (tile * LN + ln) * CPL;
     int64_t slot = row;
@@ -1652,7 +1652,7 @@ extern "C" mb_status mb_linear_attn_step(const void* q, const void* k, const voi
                          {log_decay, (size_t)H * 4}, {slots, (size_t)n * 4}, {h_in, nh}};
     if (overlaps_any(o, no, ins, 6) || overlaps_any(h_out, nh, ins, h_out == h_in ? 5 : 6) || overlaps(o, no, h_out, nh)) return MB_ERR_ALIAS;
     const bool vec = Dv % 4 == 0 && al16(h_in) && al16(h_out);
-    StepArgs A{q, k, v, log_decay, slots, h_in, h_out, o, n, n_slots, q_stride, k_stride, v_stride,
+    StepArgs A{q, k, v, log_decay, slots, h_in, h_out, o, 0, n_slots, q_stride, k_stride, v_stride,
                (int)H, (int)(H / G), (int)Dk, (int)Dv, 0, 0, scale, (size_t)n * H * Dk * Dv * 8 > kStreamBytes};
     // Few rows: narrow column tiles, so that the one token's states are read by more compute
     // units (one row of 16 heads: 4.4 us, with wide tiles 5.3); many rows: a tile as wide as a row of the
@@ -1661,15 +1661,19 @@ extern "C" mb_status mb_linear_attn_step(const void* q, const void* k, const voi
     const int ln = few ? 4 : 16, cpl = vec ? 4 : 1;
     A.cols = ln * cpl;
     A.tiles = (int)((Dv + A.cols - 1) / A.cols);
-    const int64_t grid = n * H * A.tiles;
-    if (grid > 0x7fffffff) return MB_ERR_SHAPE;
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(256), 0, stream, A); };
+    const auto go = [&](auto kern) -> mb_status {
+        const int64_t per = max_workgroups(256) / (H * A.tiles);     // rows of a launch
+        mb_status st = MB_OK;
+        for (; A.row0 < n && st == MB_OK; A.row0 += per) {
+            hipLaunchKernelGGL(kern, dim3((unsigned)(std::min(per, n - A.row0) * H * A.tiles)), dim3(256), 0, stream, A);
+            st = check_launch();
+        }
+        return st;
+    };
     if (dtype == MB_F32) {
-        if (vec) few ? go(k_la_step<float, 4, true>) : go(k_la_step<float, 16, true>);
-        else few ? go(k_la_step<float, 4, false>) : go(k_la_step<float, 16, false>);
-    } else {
-        if (vec) few ? go(k_la_step<bf16, 4, true>) : go(k_la_step<bf16, 16, true>);
-        else few ? go(k_la_step<bf16, 4, false>) : go(k_la_step<bf16, 16, false>);
+        if (vec) return few ? go(k_la_step<float, 4, true>) : go(k_la_step<float, 16, true>);
+        return few ? go(k_la_step<float, 4, false>) : go(k_la_step<float, 16, false>);
     }
-    return check_launch();
+    if (vec) return few ? go(k_la_step<bf16, 4, true>) : go(k_la_step<bf16, 16, true>);
+    return few ? go(k_la_step<bf16, 4, false>) : go(k_la_step<bf16, 16, false>);
 }

@@ -101,3 +101,24 @@ def test_more_workgroups_than_a_launch_takes():
     for got, r, M, name in zip(grads, auto, mag, ("dq", "dk", "dv")):
         assert bool(((got - r).abs() <= tol(M)).all()), name
     assert not bool(grads[3].isnan().any())
+
+
+def test_more_workgroups_than_a_launch_takes_step():
+    """2^20 rows of 16 heads, states in reversed slots of a pool."""
+    n, H, D, scale = 2 ** 20, 16, 4, 0.5
+    ld = -torch.arange(1.0, H + 1) / H
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn(n, H, D, generator=g, device="cuda") for _ in range(3))
+    pool = torch.randn(n, H, D, D, generator=g, device="cuda")
+    slots = torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")
+    start = pool.flip(0)
+    o, h = mb.mb_linear_attn_step(q, k, v, ld.cuda(), pool, scale=scale, slots=slots)
+    assert h is pool
+    lam = torch.exp(ld.double().cuda()).view(-1, 1, 1)
+    U = 2.0 ** -24
+    for part in torch.arange(n, device="cuda").chunk(4):
+        Q, K, V, S = (t[part].double() for t in (q, k, v, start))
+        S0, S = S.abs() * lam + (K.unsqueeze(3) * V.unsqueeze(2)).abs(), S * lam + K.unsqueeze(3) * V.unsqueeze(2)
+        assert bool(((pool.flip(0)[part] - S).abs() <= 16 * U * S0).all()), "h"
+        want, M = scale * (Q.unsqueeze(2) @ S).squeeze(2), scale * (Q.abs().unsqueeze(2) @ S0).squeeze(2)
+        assert bool(((o[part] - want).abs() <= (D + 64) * U * M).all()), "o"
