@@ -155,7 +155,7 @@ struct NormArgs {
     float* scales;
     void* r_out;
     float* rstd;
-    int64_t rows, x_stride;
+    int64_t row0, rows, x_stride;        // row0: first row of the launch
     int D, group, ngroups;
     float eps;
     bool stream;
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
     constexpr int NV = E / VEC;
     __shared__ float red[16];
     const int lane = threadIdx.x % TPR, slot = threadIdx.x / TPR;
-    const int64_t row = (int64_t)blockIdx.x * ROWS + slot;
+    const int64_t row = a.row0 + (int64_t)blockIdx.x * ROWS + slot;
     const bool live = row < a.rows;
     const TX* x = (const TX*)a.x + row * a.x_stride;
     const TR* res = (const TR*)a.res + row * a.D;
@@ -417,10 +417,16 @@ __global__ void __launch_bounds__(256) k_dw_sum(const float* __restrict__ part, 
 inline bool vec_ok(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 template <typename TX, typename TR, int MODE, int VEC, bool AL>
-void launch_norm(const NormArgs& a, hipStream_t s) {
+mb_status launch_norm(NormArgs a, hipStream_t s) {
     const int per = a.D;
+    mb_status st = MB_OK;
     auto go = [&](auto kern, int nt, int rows) {
-        hipLaunchKernelGGL(kern, dim3((unsigned)((a.rows + rows - 1) / rows)), dim3(nt), 0, s, a);
+        const int64_t most = max_workgroups(nt) * rows;              // rows of a launch
+        for (; a.row0 < a.rows && st == MB_OK; a.row0 += most) {
+            const int64_t n = a.rows - a.row0 < most ? a.rows - a.row0 : most;
+            hipLaunchKernelGGL(kern, dim3((unsigned)((n + rows - 1) / rows)), dim3(nt), 0, s, a);
+            st = check_launch();
+        }
     };
     // A whole row in one wave needs no barrier; of 32 values a thread it reads at lower rate than a
     // workgroup of 8 a thread does, as long as that leaves few threads idle.  16384 rows, wave and workgroup:
@@ -434,6 +440,7 @@ void launch_norm(const NormArgs& a, hipStream_t s) {
     else if (per <= 256 * 16) go(k_rms_norm<TX, TR, VEC, AL, 16, 256, MODE>, 256, 1);
     else if (per <= 256 * 32) go(k_rms_norm<TX, TR, VEC, AL, 32, 256, MODE>, 256, 1);
     else go(k_rms_norm<TX, TR, VEC, AL, 16, 1024, MODE>, 1024, 1);
+    return st;
 }
 
 template <int MODE>
@@ -463,17 +470,15 @@ mb_status norm(const void* x, const void* res, const float* w, void* y, float* s
         for (int j = 0; j < i; ++j)
             if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return MB_ERR_ALIAS;
     }
-    NormArgs a{x, res, w, y, scales, r_out, rstd, rows, x_stride, (int)D, (int)group, (int)ng, eps,
+    NormArgs a{x, res, w, y, scales, r_out, rstd, 0, rows, x_stride, (int)D, (int)group, (int)ng, eps,
                nx + outs[0].bytes + (res ? n * er : 0) + (r_out ? n * er : 0) > kStreamBytes};
     const int V = dtype == MB_BF16 ? 8 : 4;
     const bool vec = D % V == 0 && x_stride % V == 0 && vec_ok(x) && vec_ok(res) && vec_ok(w) && vec_ok(y) && vec_ok(r_out);
     if (dtype == MB_F32)
-        vec ? launch_norm<float, float, MODE, 4, true>(a, stream) : launch_norm<float, float, MODE, 4, false>(a, stream);
-    else if (rdtype == MB_F32)
-        vec ? launch_norm<bf16, float, MODE, 8, true>(a, stream) : launch_norm<bf16, float, MODE, 8, false>(a, stream);
-    else
-        vec ? launch_norm<bf16, bf16, MODE, 8, true>(a, stream) : launch_norm<bf16, bf16, MODE, 8, false>(a, stream);
-    return check_launch();
+        return vec ? launch_norm<float, float, MODE, 4, true>(a, stream) : launch_norm<float, float, MODE, 4, false>(a, stream);
+    if (rdtype == MB_F32)
+        return vec ? launch_norm<bf16, float, MODE, 8, true>(a, stream) : launch_norm<bf16, float, MODE, 8, false>(a, stream);
+    return vec ? launch_norm<bf16, bf16, MODE, 8, true>(a, stream) : launch_norm<bf16, bf16, MODE, 8, false>(a, stream);
 }
 
 // Workgroups of the backward: enough to fill the device twice, so that the partial

@@ -122,3 +122,31 @@ def test_more_workgroups_than_a_launch_takes_step():
         assert bool(((pool.flip(0)[part] - S).abs() <= 16 * U * S0).all()), "h"
         want, M = scale * (Q.unsqueeze(2) @ S).squeeze(2), scale * (Q.abs().unsqueeze(2) @ S0).squeeze(2)
         assert bool(((o[part] - want).abs() <= (D + 64) * U * M).all()), "o"
+
+
+@pytest.mark.parametrize("rows,D", [(2 ** 26 + 5, 2), (2 ** 26 + 5, 8), (2 ** 22 + 3, 8200)], ids=str)
+def test_more_rows_than_a_launch_takes(rows, D):
+    """A row in a wave (four to a workgroup) and in 1024 threads: rows on both sides of the border of two launches."""
+    u = 2.0 ** -24
+    x = torch.ones(rows, D, dtype=torch.bfloat16, device="cuda")
+    border = 2 ** 26 - 4 if D <= 8 else 2 ** 22 - 1
+    some = torch.cat([torch.arange(8), torch.arange(border - 8, border + 6), torch.arange(rows - 8, rows)])
+    some = some[some < rows].unique().cuda()
+    x[some] = torch.randn(some.numel(), D, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    r = x[some].double()
+    rs = (r.square().mean(1) + 1e-5).rsqrt()
+    if D <= 8:
+        y, _, rstd = mb.mb_rms_norm(x)
+        assert bool(((y[some] - r * rs[:, None]).abs() <= (2.0 ** -8 + 64 * u) * (r * rs[:, None]).abs()).all())
+        one = float((1 / torch.tensor(1 + 1e-5).double().sqrt()).bfloat16())
+        assert int((y != one).any(1).sum()) <= some.numel(), "rows that were not written"
+        del y
+    q, s, _, rstd = mb.mb_rms_norm_fp8(x, group=32)
+    assert bool(((rstd[some] - rs).abs() <= 40 * u * rs).all())
+    per = s[some].double().repeat_interleave(32, 1)[:, :D]
+    want = r * rs[:, None]
+    assert bool(((q[some].double() * per - want).abs() <= (2.0 ** -4 + 140 * u) * want.abs() + per * 2.0 ** -10).all())
+    # every other row is ones: its code is 448 everywhere
+    other = torch.cat([(part.view(torch.uint8) == 0x7e).all(1) for part in q.split(2 ** 18 if D > 8 else 2 ** 24)])
+    other[some] = True
+    assert bool(other.all()), "rows that were not written"
