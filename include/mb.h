@@ -605,7 +605,7 @@ mb_status mb_ssd_chunked_bwd(const float* X, const float* logdecay, const float*
  * three bf16 pieces).  NaN and infinities reach the outputs and states from their token on, never
  * earlier tokens or other sequences (in a state an infinity may become NaN).
  * ws: at least mb_workspace_size(MB_OP_LINEAR_ATTN, n_seq, T, H, Dv, G, Dk, 1, 0) bytes, 256-byte
- * aligned (may be 0: one segment per sequence).
+ * aligned (may be 0).
  */
 mb_status mb_linear_attn(const void* q, const void* k, const void* v, const float* log_decay,
                          const int32_t* cu_seqlens, const float* h0, const uint8_t* has_h0,

@@ -77,6 +77,7 @@ struct LaArgs {
     int T, L;                         // tokens in all; of a sequence when they are equal
     int target, seg0, nseg;           // longest segment; segments seg0 to nseg - 1 are launched
     int per_seq;                      // segments of a sequence when lengths are equal, else 0
+    int single;                       // packed sequences of one segment each, at most kOneSegment tokens in all
     const int32_t* cu;
     const Seg* plan;                  // segments of many packed sequences; NULL: worked out by every workgroup
     const int2* seqs;                 // (first state, segments) of a sequence, with plan
@@ -150,7 +151,15 @@ __device__ __forceinline__ Seg segment(const LaArgs& A, int s) {
     Seg g;
     if (A.plan) return A.plan[s];
     g.seq = -1;
-    if (A.cu) {
+    if (A.single) {
+        // Segment s is sequence s, whatever lies in front of it: one look at its own offsets.
+        g.seq = s;
+        g.first = min(max(A.cu[s], 0), A.T);
+        g.len = max(min(max(A.cu[s + 1], 0), A.T) - g.first, 0);
+        g.idx = 0;
+        g.count = 1;
+        g.state = s;
+    } else if (A.cu) {
         const int lane = threadIdx.x & 63;
         Lane64 l;
         l.reach = l.segs = l.states = 0;
@@ -1316,6 +1325,7 @@ inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 inline bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 constexpr int kLookThrough = 256;   // packed sequences that every workgroup looks through itself (four looks of a wave)
+constexpr int kOneSegment = 1024;   // tokens in all up to which every sequence is one segment
 
 // Longest segment: as many segments as it takes to put about two workgroups on each compute unit (all
 // that fit at a time; packed sequences end in half a segment on average), no shorter than 256 tokens: a
@@ -1323,7 +1333,7 @@ constexpr int kLookThrough = 256;   // packed sequences that every workgroup loo
 // Packed prompt and backward (above) with one workgroup a compute unit 115 and 212 us, with two 85 and 188, with
 // four and segments from 128 tokens 99 and 212; seven prompts of 1021 tokens in all 15 us, cut 19.5.
 int plan_target(int64_t n_seq, int64_t T, int64_t H, int64_t Dv, bool packed) {
-    if (T <= 1024) return 1024;
+    if (T <= kOneSegment) return kOneSegment;
     const int64_t units = H * ((Dv + kV - 1) / kV);
     int64_t want = (2 * (int64_t)device_cu_count() + units - 1) / units;
     if (packed) want = std::max(want - n_seq / 2, (want + 1) / 2);
@@ -1336,7 +1346,8 @@ int plan_target(int64_t n_seq, int64_t T, int64_t H, int64_t Dv, bool packed) {
 
 struct Plan {
     int target, nseg, per_seq;
-    bool table;         // more packed sequences than kLookThrough, some of several segments
+    bool single;        // packed, kOneSegment tokens at most: a workgroup's sequence is its number
+    bool table;         // more other packed sequences than kLookThrough
     size_t states, seqs_at, longs_at, table_bytes;
     int da, n_long;
 };
@@ -1347,7 +1358,8 @@ Plan make_plan(int64_t n_seq, int64_t T, int64_t H, int64_t Da, int64_t Dv, bool
     p.da = Da <= 64 ? 64 : 128;
     const int64_t L = T / n_seq;
     const bool several = packed ? T > p.target : L > p.target;
-    p.table = packed && several && n_seq > kLookThrough;
+    p.single = packed && T <= kOneSegment;
+    p.table = packed && !p.single && n_seq > kLookThrough;
     p.per_seq = packed ? 0 : several ? (int)((L + p.target - 1) / p.target) : 1;
     const int64_t nseg = !packed ? n_seq * p.per_seq : several ? T / p.target + n_seq : n_seq;
     p.nseg = (int)std::min<int64_t>(nseg, 0x7fffffff);
@@ -1412,6 +1424,7 @@ void use_plan(LaArgs& A, const Plan& p, char* ws) {
     A.target = p.target;
     A.nseg = p.nseg;
     A.per_seq = p.per_seq;
+    A.single = p.single;
     A.plan = p.table ? (const Seg*)ws : nullptr;
     A.seqs = p.table ? (const int2*)(ws + p.seqs_at) : nullptr;
     A.states = p.states ? (float*)(ws + p.table_bytes) : nullptr;

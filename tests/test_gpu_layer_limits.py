@@ -52,10 +52,11 @@ def test_one_sequence_of_almost_two_to_the_31_tokens():
             close(got[0, w][part], r[part], bound("bf16", 5, [600], M, r)[part], name + " at %d" % at)
 
 
-def _pairs(n, G, D, H, dtype, seed):
-    """Inputs of n packed sequences of zero, one or two tokens, and which row is whose."""
+def _pairs(n, G, D, H, dtype, seed, share=1.0):
+    """Inputs of n packed sequences of zero, one or two tokens; `share` of them may have some."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     lens = torch.randint(0, 3, (n,), generator=g, device="cuda")
+    lens *= torch.rand(n, generator=g, device="cuda") < share
     cu = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
     cu[1:] = lens.cumsum(0)
     T = int(cu[-1])
@@ -78,11 +79,11 @@ def _pairs_forward(q, k, v, ld, scale, lens, cu):
     return o, h
 
 
-def test_more_workgroups_than_a_launch_takes():
-    """2^20 sequences of 8 heads: as many threads as a grid may not have, forward and backward."""
-    n, H, D, scale = 2 ** 20, 8, 4, 0.5
+def _check_pairs(n, H, D, seed, share=1.0):
+    """Forward and backward of n such sequences; returns their tokens."""
+    scale = 0.5
     ld = -torch.arange(1.0, H + 1) / H
-    lens, cu, T, q, k, v, do = _pairs(n, H, D, H, torch.float32, 2)
+    lens, cu, T, q, k, v, do = _pairs(n, H, D, H, torch.float32, seed, share)
     o, h = mb.mb_linear_attn(q, k, v, ld.cuda(), scale=scale, cu_seqlens=cu)
     grads = mb.mb_linear_attn_bwd(q, k, v, ld.cuda(), do, scale=scale, cu_seqlens=cu)
     # magnitudes are added up over at most two tokens of four products each: 16 roundings are more than there are, and
@@ -101,6 +102,38 @@ def test_more_workgroups_than_a_launch_takes():
     for got, r, M, name in zip(grads, auto, mag, ("dq", "dk", "dv")):
         assert bool(((got - r).abs() <= tol(M)).all()), name
     assert not bool(grads[3].isnan().any())
+    return T
+
+
+def test_more_workgroups_than_a_launch_takes():
+    """2^20 sequences of 8 heads: as many threads as a grid may not have, forward and backward."""
+    assert _check_pairs(2 ** 20, 8, 4, 2) > 2 ** 19
+
+
+def test_many_sequences_of_few_tokens():
+    """Hundreds of thousands of sequences, nearly all empty: a workgroup finds its own without looking through the
+    others'.  And so many heads that no sequence is cut, whose segments come from the table."""
+    assert _check_pairs(300_000, 8, 4, 5, share=0.003) <= 1024
+    assert 1024 < _check_pairs(20_000, 512, 2, 6, share=0.1) < 4000
+
+
+def test_offsets_of_few_tokens_out_of_range_stay_inside():
+    """Offsets outside [0, T] where no sequence is cut count as the nearest bound, decreasing ones touch nothing outside."""
+    T, H, D = 900, 2, 16
+    g = torch.Generator().manual_seed(8)
+    q, k, v = (torch.randn(T, H, D, generator=g) for _ in range(3))
+    ld = torch.tensor([-0.1, -1.0])
+    cu = torch.tensor([-7, 300, 300, 2000, 3000], dtype=torch.int32).cuda()       # [0, 300), empty, [300, 900), empty
+    o, h = mb.mb_linear_attn(q.cuda(), k.cuda(), v.cuda(), ld.cuda(), cu_seqlens=cu)
+    a = [t.double() for t in (q, k, v)]
+    ro, rh = lf.attn(*a, ld, D ** -0.5, [300, 0, 600, 0])
+    Mo, Mh = lf.attn(*[t.abs() for t in a], ld, D ** -0.5, [300, 0, 600, 0])
+    close(o, ro, bound("f32", D, [600], Mo, ro), "o")
+    close(h, rh, bound("f32", D, [600], Mh, rh), "h")
+    room = torch.full((T + 256, H, D), 7.0, device="cuda")
+    cu = torch.tensor([900, 0, 900, 100, 2 ** 31 - 1, -2 ** 31, 5], dtype=torch.int64).to(torch.int32).cuda()
+    mb.mb_linear_attn(q.cuda(), k.cuda(), v.cuda(), ld.cuda(), cu_seqlens=cu, o=room[128:-128])
+    assert bool((room[:128] == 7.0).all()) and bool((room[-128:] == 7.0).all())
 
 
 def test_more_workgroups_than_a_launch_takes_step():
