@@ -661,7 +661,8 @@ mb_status mb_linear_attn_bwd(const void* q, const void* k, const void* v, const 
  *   residual_out : (rows, D) residual_dtype: r; NULL = not written; may equal residual
  *   rstd         : (rows) fp32, for the backward; NULL = not written
  * residual_dtype is MB_F32 or dtype (MB_ERR_DTYPE otherwise).  The norm is taken of r before
- * it is rounded to residual_dtype.  Supported: 1 <= D <= 16384, rows <= 2^30.  Any alignment of
+ * it is rounded to residual_dtype, at any size of it: squares that leave fp32's range are added up scaled
+ * (rstd itself may then be subnormal, or infinite for rows below 2^-128 with an eps of 0).  Supported: 1 <= D <= 16384, rows <= 2^30.  Any alignment of
  * the element types'; 16-byte aligned pointers with D and x_stride multiples of 8 (bf16;
  * 4 for fp32) take 16-byte accesses.
  */

@@ -137,6 +137,27 @@ __device__ __forceinline__ float group_scale(uint32_t amax) {
     return a / kE4m3Max;
 }
 
+// Sum of squares of a row whose squares as they are leave fp32's range, above or, with an eps that does not
+// cover it, below: of its values times a power of two (v is left so) that brings the larger of them and of
+// sqrt(eps) to between 1 and 4.  Returns it; 1 where there is nothing to scale by: infinities, NaN, zeros alone.
+template <int E, int TPR>
+__device__ __forceinline__ float rescale(float (&v)[E], float& ss, float eps, float* lds) {
+    uint32_t top = __float_as_uint(sqrtf(eps));
+#pragma unroll
+    for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+    top = row_max<TPR>(top, (uint32_t*)lds);
+    if (top == 0 || top >= 0x7f800000u) return 1.0f;
+    const float f = __uint_as_float((uint32_t)max(254 - (int)(top >> 23), 1) << 23);
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        v[i] *= f;
+        t = fmaf(v[i], v[i], t);
+    }
+    ss = row_sum<TPR>(t, lds);
+    return f;
+}
+
 // v / scale: the reciprocal's product with one residual correction is the
 // correctly rounded quotient but for rare cases, so values on a border of two
 // e4m3 steps fall as they do for the division.  An infinite scale (its group
@@ -200,8 +221,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_rms_norm(NormArgs a) 
         for (int k = 0; k < VEC; ++k) ss = fmaf(v[c * VEC + k], v[c * VEC + k], ss);
     }
     ss = row_sum<TPR>(ss, red);
-    const float rstd = 1.0f / sqrtf(ss / (float)a.D + a.eps);
-    if (a.rstd && live && lane == 0) a.rstd[row] = rstd;
+    float rstd = 1.0f / sqrtf(ss / (float)a.D + a.eps), rstd_out = rstd;
+    // A row's threads agree.  2^-100: squares below fp32's range are off by up to 2^-150 each.
+    if (__builtin_expect(ss > 3.0e38f || ss + a.eps < 0x1p-100f, false)) {
+        const float f = rescale<E, TPR>(v, ss, a.eps, red);
+        rstd = 1.0f / sqrtf(ss / (float)a.D + a.eps * f * f);      // of the values times f
+        rstd_out = rstd * f;
+    }
+    if (a.rstd && live && lane == 0) a.rstd[row] = rstd_out;
 
 #pragma unroll
     for (int c = 0; c < NV; ++c) {

@@ -183,3 +183,71 @@ def test_more_rows_than_a_launch_takes(rows, D):
     other = torch.cat([(part.view(torch.uint8) == 0x7e).all(1) for part in q.split(2 ** 18 if D > 8 else 2 ** 24)])
     other[some] = True
     assert bool(other.all()), "rows that were not written"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [1, 7, 600, 1500, 2048, 2049, 9000])
+def test_norm_of_rows_whose_squares_leave_the_range(D, dtype):
+    """Finite rows of 1e18 to the largest values and, without an eps that covers them, down to subnormal ones; single large
+    values among ordinary ones; ordinary rows beside them; zeros and a row with an infinity as ever."""
+    u, hb = 2.0 ** -24, 2.0 ** -8 if dtype == "bf16" else 0.0
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    sizes = [1.0, 1e18, 1e19, 1e20, 1e30, 8e37, 1e-18, 1e-20, 1e-25, 1e-37, 2.0 ** -135]
+    g = torch.Generator().manual_seed(9)
+    x = (torch.randn(len(sizes) + 2, D, generator=g).clamp(-3.0, 3.0).sign() * (0.5 + torch.rand(len(sizes) + 2, D, generator=g)))
+    x[:len(sizes)] *= torch.tensor(sizes)[:, None]
+    x[-2, D // 2] = 3e38
+    x[-1, D // 2] = -2e19
+    x, w = x.to(dt), 1 + 0.3 * torch.randn(D, generator=g)
+    for eps in (1e-5, 1e-33, 1e-41, 0.0, 1e30):
+        e = float(torch.tensor(eps))                          # what the kernel takes
+        r = x.double()
+        rs = 1 / torch.sqrt(r.square().mean(1) + e)
+        ry = r * rs[:, None] * w.double()
+        # the last size is zero in bf16: with an eps of 0 the formula itself is zero times infinity there
+        some = torch.isfinite(ry).all(1)
+        assert int(some.sum()) >= len(sizes) + (1 if dtype == "bf16" and eps == 0.0 else 2)
+        r, rs, ry = r[some], rs[some], ry[some]
+        for group in (None, 0, 32):
+            if group is None:
+                y, _, rstd = mb.mb_rms_norm(x.cuda(), w.cuda(), eps=eps)
+                assert bool(torch.isnan(y[~some]).all())
+                y = y[some]
+                # a product below the normal range is rounded to 2^-150
+                close(y, ry, (64 * u + hb) * ry.abs() + 2.0 ** (-134 if dtype == "bf16" else -148), "y, eps %g" % eps)
+            else:
+                q, s, _, rstd = mb.mb_rms_norm_fp8(x.cuda(), w.cuda(), group=group, eps=eps)
+                assert bool(torch.isnan(q[~some].float()).all()) and bool(torch.isnan(s[~some]).all())
+                q, s, n = q.cpu()[some], s[some], group or D
+                yg = torch.nn.functional.pad(ry, (0, -D % n)).view(ry.shape[0], -1, n)
+                sc = yg.abs().amax(2).clamp(min=2.0 ** -96) / 448
+                close(s, sc, 70 * u * sc, "scales, eps %g" % eps)
+                per = sc.repeat_interleave(n, 1)[:, :D]
+                close(q.cpu().double() * s.cpu().double().repeat_interleave(n, 1)[:, :D], ry,
+                      ry.abs() * (2.0 ** -4 + 140 * u) + per * 2.0 ** -10, "q, eps %g" % eps)
+            got = rstd.double().cpu()[some]
+            ok = rs < 3.4e38                                  # beyond: infinite in fp32
+            close(got[ok], rs[ok], 40 * u * rs[ok] + 2.0 ** -149, "rstd, eps %g" % eps)
+            assert bool((got[~ok] > 3.4e38).all())
+    # with the forward's rstd the gradient is that of the rows' directions
+    r32 = x.float().cuda()
+    y, _, rstd = mb.mb_rms_norm(r32[:6].contiguous(), w.cuda(), eps=1e-5)
+    dy = torch.randn(6, D, generator=g)
+    dx, _, dw = mb.mb_rms_norm_bwd(dy.cuda(), r32[:6].contiguous(), rstd, w.cuda())
+    rr, rw = lf.rms_norm_bwd(dy.double(), x[:6].double(), rstd.double().cpu(), w.double(), None)
+    xh, gw = x[:6].double() * rstd.double().cpu()[:, None], dy.double() * w.double()
+    mag = rstd.double().cpu()[:, None] * (gw.abs() + xh.abs() * (gw * xh).abs().mean(1, keepdim=True))
+    close(dx, rr, 100 * u * mag + 2.0 ** -148, "dx")
+    close(dw, rw, 106 * u * (dy.double() * xh).abs().sum(0) + 1e-30, "dw")
+
+
+def test_norm_of_zeros_and_infinities_is_the_formulas():
+    x = torch.zeros(3, 40)
+    x[1, 3], x[2, 5] = float("inf"), float("nan")
+    x[1, 4] = 3e38
+    y, _, rstd = mb.mb_rms_norm(x.cuda(), eps=1e-5)
+    assert bool((y[0] == 0).all()) and float(rstd[0]) == pytest.approx(1e5 ** 0.5, rel=1e-6)
+    assert float(rstd[1]) == 0.0 and bool(torch.isnan(y[1, 3])) and bool((y[1, 4:] == 0).all())
+    assert bool(torch.isnan(y[2]).all()) and bool(torch.isnan(rstd[2]))
+    y, _, rstd = mb.mb_rms_norm(x[:1].cuda(), eps=0.0)
+    assert bool(torch.isinf(rstd).all()) and bool(torch.isnan(y).all())
