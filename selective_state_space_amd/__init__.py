@@ -143,7 +143,7 @@ def mb_status_str(status: int) -> str:
 
 
 def mb_workspace_size(op, batch, L, H, P, G, N, R=1, chunk=0) -> int:
-    return (_lib or load_library()).mb_workspace_size(op, batch, L, H, P, G, N, R, chunk)
+    return (_lib or load_library()).mb_workspace_size(int(op), batch, L, H, P, G, N, R, chunk)
 
 
 # ----------------------------------------------------------------------------

@@ -1,0 +1,22 @@
+"""CPU: what the binding takes and hands on, without a GPU."""
+import enum
+
+import numpy as np
+import pytest
+
+import selective_state_space_amd as mb
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    import os
+    if not os.path.exists(mb.lib_path()):
+        from selective_state_space_amd import _build
+        _build.build()
+
+
+@pytest.mark.parametrize("kind", [np.int64, np.uint8, np.float64, float, enum.IntEnum("Op", {"x": mb.MB_OP_SSD_CHUNKED})], ids=str)
+def test_workspace_size_takes_what_int_takes_as_operator(kind):
+    want = mb.mb_workspace_size(mb.MB_OP_SSD_CHUNKED, 2, 100, 4, 64, 1, 64)
+    got = mb.mb_workspace_size(kind(mb.MB_OP_SSD_CHUNKED), 2, 100, 4, 64, 1, 64)
+    assert want > 0 and type(got) is int and got == want
