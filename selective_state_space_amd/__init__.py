@@ -191,8 +191,10 @@ def _ptr(t):
 
 
 def _stream(device):
-    # the handle alone: a torch.cuda.Stream object costs over a microsecond a call
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
+    # The handle alone, where torch has this call: the public one makes a torch.cuda.Stream object, over a microsecond.
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(device.index) if raw is not None else torch.cuda.current_stream(device).cuda_stream
 
 
 def _call(fn, *args):

@@ -1,8 +1,10 @@
 """CPU: what the binding takes and hands on, without a GPU."""
 import enum
+import types
 
 import numpy as np
 import pytest
+import torch
 
 import selective_state_space_amd as mb
 
@@ -20,3 +22,20 @@ def test_workspace_size_takes_what_int_takes_as_operator(kind):
     want = mb.mb_workspace_size(mb.MB_OP_SSD_CHUNKED, 2, 100, 4, 64, 1, 64)
     got = mb.mb_workspace_size(kind(mb.MB_OP_SSD_CHUNKED), 2, 100, 4, 64, 1, 64)
     assert want > 0 and type(got) is int and got == want
+
+
+def test_stream_without_torchs_private_call(monkeypatch):
+    """A torch that lacks it: the public call gives the same handle."""
+    device = torch.device("cuda", 1)
+    seen = []
+
+    def current_stream(d):
+        seen.append(d)
+        return types.SimpleNamespace(cuda_stream=1234)
+
+    public = types.SimpleNamespace(_C=types.SimpleNamespace(), cuda=types.SimpleNamespace(current_stream=current_stream))
+    monkeypatch.setattr(mb, "_torch", lambda: public)
+    assert mb._stream(device) == 1234 and seen == [device]
+    private = types.SimpleNamespace(_C=types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: 100 + i))
+    monkeypatch.setattr(mb, "_torch", lambda: private)
+    assert mb._stream(device) == 101
