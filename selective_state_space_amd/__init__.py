@@ -948,6 +948,16 @@ def mb_linear_attn_bwd(q, k, v, log_decay, do, *, scale=None, cu_seqlens=None, h
 # ----------------------------------------------------------------------------
 # root-mean-square norm, gradient clipping
 # ----------------------------------------------------------------------------
+def _row_stride(x, name):
+    """Elements between the rows of a contiguous tensor, or of a (rows, D) one with contiguous rows."""
+    D = x.shape[-1]
+    if x.is_contiguous() or x.numel() == 0:
+        return D
+    if x.dim() == 2 and (x.stride(1) == 1 or D == 1) and (x.stride(0) >= D or x.shape[0] == 1):
+        return x.stride(0) if x.shape[0] > 1 else D
+    raise ValueError("%s must be contiguous, or (rows, D) with contiguous rows" % name)
+
+
 def _norm_args(x, weight, residual, residual_out, rstd):
     """Check a norm's arguments; returns (device, code, residual code, rows, D, stride, residual dtype,
     residual_out, rstd)."""
@@ -958,12 +968,7 @@ def _norm_args(x, weight, residual, residual_out, rstd):
         raise ValueError("x must have at least one axis")
     D = x.shape[-1]
     rows = x.numel() // D if D else 0
-    if x.is_contiguous() or x.numel() == 0:
-        stride = D
-    elif x.dim() == 2 and (x.stride(1) == 1 or D == 1) and x.stride(0) >= D:
-        stride = x.stride(0) if rows > 1 else D
-    else:
-        raise ValueError("x must be contiguous, or (rows, D) with contiguous rows")
+    stride = _row_stride(x, "x")
     rdt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else x.dtype
     if rdt not in (torch.float32, x.dtype):
         raise TypeError("residual must be float32 or have the dtype of x, got %s" % rdt)
@@ -1010,8 +1015,9 @@ def mb_rms_norm_fp8(x, weight=None, residual=None, *, group=0, eps=1e-5, y=None,
 
 
 def mb_rms_norm_bwd(dy, r, rstd, weight=None, dr_in=None, *, dx=None, dr=None, dweight=None, ws=None):
-    """Backward of mb_rms_norm: dy (the gradient of y), r and rstd as the forward returned them, dr_in
-    (the gradient that reaches r from elsewhere, like r) or None.  Returns (dx, dr, dweight): dr is the
+    """Backward of mb_rms_norm: dy (the gradient of y), r and rstd as the forward returned them (an r whose rows
+    lie apart, the forward's x where it had no residual, is copied first), dr_in (the gradient that reaches
+    r from elsewhere, like r) or None.  Returns (dx, dr, dweight): dr is the
     gradient of x and of residual in the dtype of r, dx the same in the dtype of dy (the very tensor
     dr when the dtypes agree)."""
     torch = _torch()
@@ -1024,6 +1030,9 @@ def mb_rms_norm_bwd(dy, r, rstd, weight=None, dr_in=None, *, dx=None, dr=None, d
     shp, D = tuple(dy.shape), dy.shape[-1]
     rows = dy.numel() // D if D else 0
     _check(dy, "dy", shp, dy.dtype, dev)
+    if r.shape == shp and r.device == dev and not r.is_contiguous():
+        _row_stride(r, "r")
+        r = r.contiguous()
     _check(r, "r", shp, r.dtype, dev)
     _check(rstd, "rstd", shp[:-1], torch.float32, dev)
     _check(weight, "weight", (D,), torch.float32, dev)
