@@ -48,6 +48,11 @@ constexpr int kMaxDim = 128;    // of keys and of values
 // 90 us at 8, 87 at 16; fp32 of 2 x 4095 tokens (16 segments each) 67.7 and 65.7; backward 194 us at 4, else 188.
 constexpr int kFewSegments = 16;
 constexpr int kWalkThreads = 512;
+// Packed sequences that every workgroup looks through itself: one look of a wave.  More have their segments in a table, which
+// costs a launch and its own looks once.  Looked through and table, 16384 tokens of 16 heads of 128 x 64, bf16: 32 sequences 60.1 and
+// 61.4 us (backward 145.0, 143.9), 64 68.0 and 66.7 (161, 153), 128 87 and 79 (211, 180), 256 143 and 111 (344, 242); of 2 heads 9
+// sequences 32.4 and 33.4 (71, 74), 64 24.2 and 24.5 (48.7, 50.1), 128 22.1 and 23.2 (46.5, 45.3), 256 27.3 and 25.3 (63, 52).
+constexpr int kLookThrough = 64;
 
 // A segment of a sequence.  A sequence of L tokens is cut into ceil(L / target) segments (one if it
 // is empty) of equal length, rounded up to whole chunks.
@@ -163,20 +168,16 @@ __device__ __forceinline__ Seg segment(const LaArgs& A, int s) {
         const int lane = threadIdx.x & 63;
         Lane64 l;
         l.reach = l.segs = l.states = 0;
-        for (int s0 = 0; s0 < A.n_seq; s0 += 64) {
-            l.read(A, s0, lane);
-            if (s >= l.segs) continue;
-            const uint64_t hit = __ballot(l.count > 0 && l.at <= s && s < l.at + l.count);
-            const int k = __ffsll((unsigned long long)hit) - 1;
-            g.seq = s0 + k;
-            g.first = __builtin_amdgcn_readlane(l.first, k);
-            g.len = __builtin_amdgcn_readlane(l.len, k);
-            g.count = __builtin_amdgcn_readlane(l.count, k);
-            g.idx = s - __builtin_amdgcn_readlane(l.at, k);
-            g.state = __builtin_amdgcn_readlane(l.state, k) + g.idx;
-            break;
-        }
-        if (g.seq < 0) return g;
+        l.read(A, 0, lane);
+        if (s >= l.segs) return g;
+        const uint64_t hit = __ballot(l.count > 0 && l.at <= s && s < l.at + l.count);
+        const int k = __ffsll((unsigned long long)hit) - 1;
+        g.seq = k;
+        g.first = __builtin_amdgcn_readlane(l.first, k);
+        g.len = __builtin_amdgcn_readlane(l.len, k);
+        g.count = __builtin_amdgcn_readlane(l.count, k);
+        g.idx = s - __builtin_amdgcn_readlane(l.at, k);
+        g.state = __builtin_amdgcn_readlane(l.state, k) + g.idx;
     } else {
         g.seq = s / A.per_seq;
         g.idx = s - g.seq * A.per_seq;
@@ -199,10 +200,10 @@ __device__ __forceinline__ void sequence(const LaArgs& A, int seq, int& state, i
         const int lane = threadIdx.x & 63;
         Lane64 l;
         l.reach = l.segs = l.states = 0;
-        for (int s0 = 0; s0 <= seq; s0 += 64) l.read(A, s0, lane);
-        state = __builtin_amdgcn_readlane(l.state, seq & 63);
-        count = __builtin_amdgcn_readlane(l.count, seq & 63);
-        len = __builtin_amdgcn_readlane(l.len, seq & 63);
+        l.read(A, 0, lane);
+        state = __builtin_amdgcn_readlane(l.state, seq);
+        count = __builtin_amdgcn_readlane(l.count, seq);
+        len = __builtin_amdgcn_readlane(l.len, seq);
     } else {
         state = seq * A.per_seq;
         count = A.per_seq;
@@ -644,20 +645,11 @@ __global__ void __launch_bounds__(256) k_la_carry(LaArgs A, const int* longs) {
     if (A.plan) {
         seq = longs[which];
     } else if (A.cu) {
-        const int lane = threadIdx.x & 63;
-        seq = -1;
-        for (int s0 = 0; s0 < A.n_seq && seq < 0; s0 += 64) {
-            const int s = min(s0 + lane, A.n_seq - 1);
-            const int64_t len = (int64_t)min(max(A.cu[s + 1], 0), A.T) - min(max(A.cu[s], 0), A.T);
-            uint64_t many = __ballot(s0 + lane < A.n_seq && len > (int64_t)kFewSegments * A.target);
-            const int here = __popcll(many);
-            if (which < here) {
-                for (; which > 0; --which) many &= many - 1;
-                seq = s0 + __ffsll((unsigned long long)many) - 1;
-            } else {
-                which -= here;
-            }
-        }
+        const int lane = threadIdx.x & 63, s = min(lane, A.n_seq - 1);
+        const int64_t len = (int64_t)min(max(A.cu[s + 1], 0), A.T) - min(max(A.cu[s], 0), A.T);
+        uint64_t many = __ballot(lane < A.n_seq && len > (int64_t)kFewSegments * A.target);
+        for (; which > 0; --which) many &= many - 1;
+        seq = __ffsll((unsigned long long)many) - 1;             // -1: fewer are long
     }
     if (seq < 0) return;
     int first, n, len;
@@ -1324,7 +1316,6 @@ __global__ void __launch_bounds__(256) k_la_step(StepArgs A) {
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 inline bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-constexpr int kLookThrough = 256;   // packed sequences that every workgroup looks through itself (four looks of a wave)
 constexpr int kOneSegment = 1024;   // tokens in all up to which every sequence is one segment
 
 // Longest segment: as many segments as it takes to put about two workgroups on each compute unit (all

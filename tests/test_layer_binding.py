@@ -39,3 +39,13 @@ def test_stream_without_torchs_private_call(monkeypatch):
     private = types.SimpleNamespace(_C=types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: 100 + i))
     monkeypatch.setattr(mb, "_torch", lambda: private)
     assert mb._stream(device) == 101
+
+
+def test_workspace_of_packed_sequences_holds_their_table():
+    """From 65 sequences on (that a workgroup does not find in one look) the sizes allow for a table of segments, 32 bytes
+    each beside 8 a sequence; not where every sequence is one segment that its number finds."""
+    size = lambda n, T: mb.mb_workspace_size(mb.MB_OP_LINEAR_ATTN, n, T, 512, 64, 512, 64)
+    # 512 heads: two workgroups a compute unit are there without cutting a sequence, so there are no states
+    assert size(64, 4001) == 0
+    assert size(65, 4001) >= 65 * 40 and size(1000, 4001) >= 1000 * 40
+    assert size(1000, 1001) == 0 and size(100_000, 1001) == 0
