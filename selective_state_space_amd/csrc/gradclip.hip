@@ -6,8 +6,8 @@
 // Bound by HBM: the gradients are read once for the norm and once more, with a
 // write, for the scaling.  Each square is summed in fp64: no fp32 gradient's
 // square overflows or vanishes there, and the two extra fp64 operations an element
-// cost less than its load.  129 M bf16 gradients of 24 layers, which the last-level cache cannot hold: norm 48 us
-// for 258 MB (5.4 TB/s), scaling 88 us for 517 MB (5.9 TB/s); pieces of twice the size, or half or twice as many
+// cost less than its load.  129 M bf16 gradients of 24 layers, which the last-level cache cannot hold: norm 47 us
+// for 258 MB (5.5 TB/s), scaling 89 us for 517 MB (5.8 TB/s); pieces of twice the size, or half or twice as many
 // workgroups, change neither by 2 %.  A workgroup's sum goes to its own place in the
 // workspace and every reader adds these in the same order: results do not depend on
 // the order in which workgroups run.
@@ -103,7 +103,7 @@ __device__ __forceinline__ double sum_block(double v, double* lds) {
 
 // Sixteen bytes at any element's address, which the memory takes in one access: gradients are often
 // views at odd offsets of one buffer (the norm and scaling of 129 M bf16 values from an odd address on: one
-// element at a time 329 us, so 136).
+// element at a time 329 us, so 136; 266 tensors each at an odd address 147 - 158 us, aligned 145 - 148).
 typedef uint32_t any4 __attribute__((ext_vector_type(4), aligned(2)));
 template <typename T>
 __device__ __forceinline__ u4 load16(const T* p) {

@@ -26,6 +26,13 @@
 // A sequence of n segments has n places for states: end states 0 to n - 2, and in the last, which has
 // no end state to hand on, a copy of h0 (h_out may be h0, and the last segment may write it
 // before the first one reads it).
+//
+// What bf16 tensors lose beside the rounding of the output: two operands of its matrix products. The masked, decayed
+// scores are rounded to bf16 for the product with the values, the carried state for the product with the queries: each half
+// a step, 2^-8, of its terms, as the scans of the same library in bf16 have it. Against 64 bits the outputs are off by 2.3e-3
+// (root mean square, relative) where their own rounding alone leaves 1.7e-3. A second piece of each operand would take
+// that away for twice the products with them and 16 KB more LDS a workgroup. The carried state itself, the weights,
+// all sums and fp32 tensors keep 32 bits.
 #include <algorithm>
 
 #include "mb_internal.h"
@@ -402,7 +409,7 @@ struct Tile {
 // 16 w .. 16 w + 15 of the tile, all DA rows, as DA / 16 accumulators (rows 16 u +
 // 4 g + r, column lane & 15).
 //
-// bf16: w V does not fit bf16, and one rounding of it would leave 2^-9 in a state that
+// bf16: w V does not fit bf16, and one rounding of it would leave 2^-8 in a state that
 // is kept in fp32.  It is cut into three bf16 pieces (8 + 8 + 8 bits hold all 24 of the
 // product), three products on the exact K.
 // PARTS = 2: one half of the chunk's tokens, `part`; another wave adds the other half.
@@ -565,7 +572,7 @@ __device__ __forceinline__ f4* state_piece(const LaArgs& A, int at, int h, int t
 // that the weighted values' splitting, which costs more than the products, is shared out; the two
 // halves are added up at the end.  Weights reach to the segment's end, so nothing is rescaled on the way.
 // Bound by its reads.  16384 packed tokens of nine sequences, 16 heads of 128 x 64, bf16: 30.5 us for 96 MB
-// (3.1 TB/s, matrix unit 11 % busy); 8190 tokens of 16 heads of 64 x 64 in fp32: 17.6 us for 72 MB (4.1 TB/s, 25 %).
+// (3.1 TB/s, matrix unit 11 % busy); 8190 tokens of 16 heads of 64 x 64 in fp32: 17.7 us for 72 MB (4.0 TB/s, 26 %).
 template <typename T, int DA, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads) k_la_state(LaArgs A) {
     constexpr int NA = DA / 16, TILES = kC * (Tiled<T, DA>::ROW + Tiled<T, kV>::ROW) * (int)sizeof(T), SUMS = NA * 4 * 64 * 16;
@@ -630,8 +637,8 @@ __global__ void __launch_bounds__(kWalkThreads) k_la_state(LaArgs A) {
 // In place over a sequence's places: the state that enters each of its segments.  A workgroup
 // takes 1024 values (256 lanes of four) of one (long sequence, head, tile).  There are at most
 // T / (kFewSegments target + 1) long sequences, so the launch does not grow with the short ones (64k tokens in
-// 2000 sequences, 16 heads: the call 892 -> 780 us).  They are never more than 128: 2^23 workgroups
-// with the most heads and columns.  Bound by latency: 5.4 us for 16.9 MB, 5.1 us where it finds none.
+// 2000 sequences, 16 heads: the call 892 us where it did, 768 now).  They are never more than 128: 2^23 workgroups
+// with the most heads and columns.  Bound by latency: 5.4 us for 16.9 MB, 5.0 us where it finds none.
 template <int DA>
 __global__ void __launch_bounds__(256) k_la_carry(LaArgs A, const int* longs) {
     constexpr int PER = DA * kV / 1024;
@@ -1003,8 +1010,8 @@ __device__ __forceinline__ int block_of(int wave8) {
 // next chunk's tiles into registers while this one is computed (the output waves the next
 // queries, which only they read) and put them to LDS between two barriers.
 // TO: type of the output (fp32 where several heads' gradients are still to be added up).
-// bf16 is bound by its traffic: the packed prompt above 51 us for 233 MB, 4.6 TB/s, and the backward's run for dq (4 x 4096
-// tokens, do and v to dq) 51 us for 211 MB, 4.1 TB/s, the matrix unit 16 - 19 % busy.  fp32, 50 us for 143 MB with
+// bf16 is bound by its traffic: the packed prompt above 55.5 us for 233 MB, 4.2 TB/s, and the backward's run for dq (4 x 4096
+// tokens, do and v to dq) 51 us for 210 MB, 4.1 TB/s, the matrix unit 15 - 19 % busy, LDS 19 - 27 %.  fp32, 50 us for 143 MB with
 // the matrix unit 38 % busy, waits for both in turn.  Two workgroups of eight waves fit a compute unit: 128
 // registers a wave.
 template <typename T, typename TO, int DA, bool VEC>
@@ -1231,7 +1238,7 @@ struct StepArgs {
 // A workgroup owns CW = 4 LN value columns of one (row, head): LN lanes side by side hold
 // four columns each, the 256 / LN rows of lanes share out the state's rows, and their parts
 // of o are added up in LDS.  All its state reads are under way before the first is used.
-// Bound by the states' bytes: 256 rows, 16 heads of 128 x 64: 46.5 us for 272 MB, 5.8 TB/s.  One row: 4.4 us, the
+// Bound by the states' bytes: 256 rows, 16 heads of 128 x 64: 47.7 us for 272 MB, 5.7 TB/s.  One row: 4.5 us, the
 // latency of a load, a sum through LDS and a store.
 template <typename T, int LN, bool VEC>
 __global__ void __launch_bounds__(256) k_la_step(StepArgs A) {
@@ -1322,7 +1329,8 @@ constexpr int kOneSegment = 1024;   // tokens in all up to which every sequence 
 // that fit at a time; packed sequences end in half a segment on average), no shorter than 256 tokens: a
 // segment's state makes four trips through memory.  Up to 1024 tokens in all, one segment a sequence.
 // Packed prompt and backward (above) with one workgroup a compute unit 115 and 212 us, with two 85 and 188, with
-// four and segments from 128 tokens 99 and 212; seven prompts of 1021 tokens in all 15 us, cut 19.5.
+// four and segments from 128 tokens 99 and 212; seven prompts of 1021 tokens in all 15 us, cut 19.5.  The last rule goes by the sum of
+// tokens and costs a long sequence that comes alone: one prompt of 1000 tokens, 16 heads, 44 us, of 1088, cut in five, 23.
 int plan_target(int64_t n_seq, int64_t T, int64_t H, int64_t Dv, bool packed) {
     if (T <= kOneSegment) return kOneSegment;
     const int64_t units = H * ((Dv + kV - 1) / kV);

@@ -12,9 +12,10 @@
 // a thread holds E of its elements as E / VEC vectors, lanes side by side.
 // Rows that no vector is aligned to are read and written in vectors all the same, which the memory
 // takes at any element's address; only a row's last vector goes element by element.
-// Measured: 16384 rows of 2048 bf16 with residual to 8 bits 46.5 us for 236 MB, 5.1 TB/s; 4097 rows of 1001 fp32, none of
-// them aligned, 12.7 us for 66 MB, 5.2 TB/s (one element at a time 17.6), 16384 of 1001 bf16 29.6 us (72);
-// four rows 3.2 us, the latency of one load, one sum and one store.
+// Measured: 16384 rows of 2048 bf16 with residual to 8 bits 46.9 us for 237 MB, 5.0 TB/s; 4097 rows of 1001 fp32, none of
+// them aligned, 12.7 us for 66 MB, 5.2 TB/s (one element at a time 17.6), 16384 of 1001 bf16 30 us (72);
+// four rows 3.4 us, the latency of one load, one sum and one store.  Short rows leave most lanes of their wave idle: 2^20
+// rows of 64 bf16 with residual 429 us for 537 MB.
 #include "mb_internal.h"
 
 namespace mb {
