@@ -600,10 +600,10 @@ mb_status mb_ssd_chunked_bwd(const float* X, const float* logdecay, const float*
  * Supported: 1 <= Dk, Dv <= 128, H <= 4096, T < 2^31, n_seq <= 2^20.  Any alignment of the
  * element type's; 16-byte aligned pointers with Dk, Dv and strides multiples of 8
  * (bf16; 4 for fp32) take the fast path.  fp32 arithmetic runs on fp32 matrix products; with MB_BF16 the
- * products take bf16 operands with fp32 accumulation: the masked scores and a copy of the
- * state are rounded, the carried state is not (its update splits the weighted values into
- * three bf16 pieces).  NaN and infinities reach the outputs and states from their token on, never
- * earlier tokens or other sequences (in a state an infinity may become NaN).
+ * products take bf16 operands with fp32 accumulation: computed ones as several bf16 pieces (the masked
+ * scores and a copy of the state two, the weighted values of the state's update three), so that only the
+ * outputs are rounded to bf16.  NaN and infinities reach the outputs and states from their token on, never
+ * earlier tokens or other sequences (an infinity may become NaN).
  * ws: at least mb_workspace_size(MB_OP_LINEAR_ATTN, n_seq, T, H, Dv, G, Dk, 1, 0) bytes, 256-byte
  * aligned (may be 0).
  */

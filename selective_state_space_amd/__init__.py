@@ -881,9 +881,7 @@ def mb_linear_attn(q, k, v, log_decay, *, scale=None, cu_seqlens=None, h0=None, 
     (n_seq,) int32 a pool (n_slots, H, Dk, Dv) that is updated in place unless h_out is given;
     has_h0 (n_seq,) uint8 or bool marks the sequences that continue.  scale defaults to Dk ** -0.5.
     Rows of o outside all sequences are not written (an o allocated here holds anything there).
-    With bfloat16 tensors the masked scores and a copy of the state are rounded to bfloat16 for their matrix products
-    (outputs off from 64 bits by 2.3e-3 on average, where their own rounding leaves 1.7e-3); sums and the carried
-    state are float32, and float32 tensors lose nothing.  Returns (o, h_out)."""
+    Of what is computed only o is rounded to its dtype; states are float32.  Returns (o, h_out)."""
     torch = _torch()
     dev, code, lead, n, T, H, G, Dk, Dv, st = _attn_args(q, k, v, log_decay, cu_seqlens)
     n_slots, hs = _pool_args(h0, h_out, slots, n, H, Dk, Dv, dev)
@@ -929,8 +927,7 @@ def mb_linear_attn_bwd(q, k, v, log_decay, do, *, scale=None, cu_seqlens=None, h
                        dv=None, dh0=None, ws=None):
     """Backward of mb_linear_attn: the gradients of sum do . o + sum dh_out . h_out with respect to q,
     k, v and h0.  do like o; h0, dh_out (n_seq, H, Dk, Dv) float32 or None (zeros).  Rows of tokens
-    outside all sequences are zero.  bfloat16 tensors: dq, dk and dv with the roundings of mb_linear_attn's o.
-    Returns (dq, dk, dv, dh0)."""
+    outside all sequences are zero.  Returns (dq, dk, dv, dh0)."""
     torch = _torch()
     dev, code, lead, n, T, H, G, Dk, Dv, st = _attn_args(q, k, v, log_decay, cu_seqlens)
     f32, dt, hs = torch.float32, q.dtype, (n, H, Dk, Dv)

@@ -27,12 +27,12 @@
 // no end state to hand on, a copy of h0 (h_out may be h0, and the last segment may write it
 // before the first one reads it).
 //
-// What bf16 tensors lose beside the rounding of the output: two operands of its matrix products. The masked, decayed
-// scores are rounded to bf16 for the product with the values, the carried state for the product with the queries: each half
-// a step, 2^-8, of its terms, as the scans of the same library in bf16 have it. Against 64 bits the outputs are off by 2.3e-3
-// (root mean square, relative) where their own rounding alone leaves 1.7e-3. A second piece of each operand would take
-// that away for twice the products with them and 16 KB more LDS a workgroup. The carried state itself, the weights,
-// all sums and fp32 tensors keep 32 bits.
+// bf16 tensors lose nothing beside the rounding of their outputs: what is computed and has to be an operand of a bf16 product
+// once more is cut into bf16 pieces, the masked, decayed scores and the state's copy into two (2^-16 of a term is left), the
+// weighted values of the state's update into three.  With one piece of the first two the outputs were off from 64 bits by
+// 2.3e-3 (root mean square, relative), so by the 1.7e-3 of their own rounding, for twice the products with them: packed prompt
+// 85.1 -> 83.1 us and backward 189 -> 191, both with the registers' use mended (forget_lane), seven short prompts 16.5 -> 17.5.
+// An infinity in one piece leaves NaN in the next.
 #include <algorithm>
 
 #include "mb_internal.h"
@@ -364,6 +364,13 @@ struct Tiled {
 // Hides how a lane's place came about, once a chunk: the places derived from it are then worked out
 // where they are used instead of being held in registers over the whole walk.
 __device__ __forceinline__ void forget(int& x) { asm volatile("" : "+v"(x)); }
+// The lane itself, where a walk's registers do not reach for what follows from it: a reload from scratch also waits for the
+// loads of the next chunk.  With and without: packed prompt 82.4 and 86.9 us, backward 190 and 193, 4 groups of heads 274 and
+// 283; key width 64 and fp32, which have registers left, lose by it: seven prompts 18.2 and 17.8, fp32 66.0 and 64.8.
+template <typename T, int DA>
+__device__ __forceinline__ void forget_lane(int& x) {
+    if constexpr (sizeof(T) == 2 && DA == 128) forget(x);
+}
 
 // A tile of kC tokens by W columns: its global reads into registers, and from there to LDS.
 template <typename T, int W, bool VEC, int NT>
@@ -682,13 +689,14 @@ __global__ void __launch_bounds__(256) k_la_carry(LaArgs A, const int* longs) {
 }
 
 // ----------------------------------------------------------------- walk ----
-// N rows of 16x16 products with the NK fragments of `q`: y = sum_s fetch(x, s) q[s], handed to use(x, y).
+// N rows of 16x16 products with the NK fragments of `q`: y = sum_s fetch(x, s) q[s], handed to use(x, y).  With PIECES = 2
+// the other operand comes in two pieces, fetch(x, 2 s) and fetch(x, 2 s + 1).
 // bf16 reads two operands ahead of the ones it multiplies; fp32 four at a time, whose 16
 // instructions cover the next read themselves.
 // fp32, bound by its products, leaves out the rows from `end` on (scores of later tokens): use gets zeros.
-template <typename T, int N, int NK, typename Fetch, typename Use>
+template <typename T, int N, int PIECES, int NK, typename Fetch, typename Use>
 __device__ __forceinline__ void products(const u4 (&q)[NK], int end, Fetch fetch, Use use) {
-    constexpr int GS = sizeof(T) == 2 ? 2 : 4, NG = NK / GS, NB = sizeof(T) == 2 ? 2 : 1;
+    constexpr int GS = sizeof(T) == 2 ? 2 : 4, NG = NK * PIECES / GS, NB = sizeof(T) == 2 ? 2 : 1;
     u4 fr[NB][GS];
     auto read = [&](int z) {
 #pragma unroll
@@ -708,7 +716,7 @@ __device__ __forceinline__ void products(const u4 (&q)[NK], int end, Fetch fetch
             else if (z + 1 < N * NG) read(z + 1);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int s = 0; s < GS; ++s) y = Frag<T>::mma(fr[z % NB][s], q[z % NG * GS + s], y);
+            for (int s = 0; s < GS; ++s) y = Frag<T>::mma(fr[z % NB][s], q[(z % NG * GS + s) / PIECES], y);
         }
         use(x, y);
     }
@@ -721,12 +729,18 @@ __device__ __forceinline__ constexpr int column(int x, int g) {
     return sizeof(TO) == 2 ? 32 * (x >> 1) + 8 * g + 4 * (x & 1) : 16 * x + 4 * g;
 }
 
-// Masked, decayed scores P^T (rows j, column i = 16 wave + m): what a lane holds of them is the operand
+// fp32 values as two bf16 pieces, the second what the first leaves: 16 of the 24 bits.
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16(a, b);
+    lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+}
+template <typename T> constexpr int kPieces = sizeof(T) == 2 ? 2 : 1;
+
+// Masked, decayed scores P^T (rows j, column i = 16 wave + m) of TOKENS tokens: what a lane holds of them is the operand
 // of the product with the values as it stands, tokens in the same order on both sides.
-template <typename T>
+template <typename T, int TOKENS>
 struct Scores {
-    static constexpr int N = sizeof(T) == 2 ? 2 : 4;
-    u4 p[N];
+    u4 p[TOKENS / 16];                       // bf16: two pieces for every 32 tokens; fp32: 16 tokens each
 };
 // s_in lambda^{i - j} with j = 16 t + 4 gr + r: on the diagonal block (t = wave) as it is, in front of it
 // through the power of the next block's distance, between 1 and 31, times lambda^{16 (wave - 1 - t)}.
@@ -745,17 +759,23 @@ struct Decay {
         for (int t = 0; t < 4; ++t) far[t] = power(l2, 16 * max(wave - 1 - t, 0));
     }
     __device__ __forceinline__ f4 weights(int t, int wave) const { return lds[t == wave ? 0 : 64]; }
-    template <typename T>
-    __device__ __forceinline__ void apply(Scores<T>& P, int t, f4 y, int wave, int m, int gr) const {
+    // t: the block of 16 tokens in the chunk, x: in P
+    template <typename T, int TOKENS>
+    __device__ __forceinline__ void apply(Scores<T, TOKENS>& P, int x, int t, f4 y, int wave, int m, int gr) const {
         const f4 w = weights(t, wave);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             y[r] = t > wave || (t == wave && 4 * gr + r > m) ? 0.0f : y[r] * (t == wave ? w[r] : w[r] * far[t]);
         if constexpr (sizeof(T) == 2) {
-            P.p[t >> 1][2 * (t & 1)] = pack_bf16(y[0], y[1]);
-            P.p[t >> 1][2 * (t & 1) + 1] = pack_bf16(y[2], y[3]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t hi, lo;
+                split_bf16(y[2 * k], y[2 * k + 1], hi, lo);
+                P.p[x & ~1][2 * (x & 1) + k] = hi;
+                P.p[x | 1][2 * (x & 1) + k] = lo;
+            }
         } else {
-            P.p[t] = __builtin_bit_cast(u4, y);
+            P.p[x] = __builtin_bit_cast(u4, y);
         }
     }
 };
@@ -776,15 +796,16 @@ __device__ __forceinline__ u4 value_fragment(const T* vt, int va, int x, int t, 
     }
 }
 
-// o[x] += V^T P^T for NT accumulators, V a tile of W columns.  The matrix product multiplies the zero
-// scores of later tokens with whatever those hold: where the chunk has infinities or NaN among its values
+// o[x] += V^T P^T for NT accumulators and the scores' tokens, from t0 on; V a tile of W columns.  The matrix product multiplies
+// the zero scores of later tokens with whatever those hold: where the chunk has infinities or NaN among its values
 // (`odd`), it is made once for each of the 16 tokens, later ones cleared from the tile's fragments.
-template <typename T, typename TO, int W, int NT>
-__device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, const T* vt, bool odd, int wave, int m, int gr) {
+template <typename T, typename TO, int W, int TOKENS, int NT>
+__device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T, TOKENS>& P, const T* vt, int t0, bool odd, int wave, int m, int gr) {
     using VL = Tiled<T, W>;
     constexpr int STEP = sizeof(T) == 2 ? 32 : 16;       // tokens of a fragment
     if (__builtin_expect(odd, false)) {
-        const int va = sizeof(T) == 2 ? VL::at(4 * gr + (m >> 2), column<TO>(0, m & 3)) : 0;
+        int va = sizeof(T) == 2 ? VL::at(4 * gr + (m >> 2), column<TO>(0, m & 3)) : 0;
+        forget(va);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             f4 own = o[x];
@@ -792,9 +813,9 @@ __device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, cons
             for (int i = 0; i < 16; ++i) {
                 f4 y = o[x];
 #pragma unroll
-                for (int s = 0; s < Scores<T>::N; ++s) {
-                    u4 a = value_fragment<T, TO, W>(vt, va, x, STEP * s, m, gr);
-                    const int left = 16 * wave + i - STEP * s - 4 * gr;      // the fragment's tokens up to the i-th
+                for (int s = 0; s < TOKENS / STEP; ++s) {
+                    u4 a = value_fragment<T, TO, W>(vt, va, x, t0 + STEP * s, m, gr);
+                    const int left = 16 * wave + i - t0 - STEP * s - 4 * gr;      // the fragment's tokens up to the i-th
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         if constexpr (sizeof(T) == 2)
@@ -802,7 +823,8 @@ __device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, cons
                         else
                             a[e] = left >= e ? a[e] : 0u;
                     }
-                    y = Frag<T>::mma(a, P.p[s], y);
+#pragma unroll
+                    for (int k = 0; k < kPieces<T>; ++k) y = Frag<T>::mma(a, P.p[kPieces<T> * s + k], y);
                 }
                 if (m == i) own = y;
             }
@@ -815,16 +837,16 @@ __device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, cons
         forget(va);
 #pragma unroll
         for (int h = 0; h < NT; h += 4) {
-            u4 a[2][4];
+            u4 a[TOKENS / 32][4];
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < TOKENS / 32; ++s)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) a[s][x] = value_fragment<T, TO, W>(vt, va, h + x, 32 * s, m, gr);
+                for (int x = 0; x < 4; ++x) a[s][x] = value_fragment<T, TO, W>(vt, va, h + x, t0 + 32 * s, m, gr);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+            for (int s = 0; s < TOKENS / 16; ++s)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) o[h + x] = Frag<T>::mma(a[s][x], P.p[s], o[h + x]);
+                for (int x = 0; x < 4; ++x) o[h + x] = Frag<T>::mma(a[s / 2][x], P.p[s], o[h + x]);
         }
     } else {
 #pragma unroll
@@ -839,6 +861,27 @@ __device__ __forceinline__ void add_values(f4 (&o)[NT], const Scores<T>& P, cons
                 for (int x = 0; x < 4; ++x) o[h + x] = Frag<T>::mma(a[x], P.p[t], o[h + x]);
             }
         }
+    }
+}
+
+// o += the chunk's own part for this wave's 16 tokens: the scores of `kt`, a tile of KW columns, with the fragments q, times the
+// values in `vt`, a tile of W columns.  TOKENS: of the chunk at a time, none that are all later ones.  All 64 wait less (seven
+// short prompts 17.7 us, 32 at a time 18.5); 32 take half the registers, which k_la_dkdv does not have.
+template <typename T, typename TO, int KW, int W, int TOKENS, int NK, int NT>
+__device__ __forceinline__ void add_chunk(f4 (&o)[NT], const u4 (&q)[NK], const Decay& dec, const T* kt, const T* vt, bool odd, int wave,
+                                          int m, int gr) {
+    using KL = Tiled<T, KW>;
+    constexpr int N = TOKENS / 16;
+    int ka = KL::at(m, Frag<T>::VE * gr);
+    forget(ka);
+#pragma unroll
+    for (int c = 0; c < kC / TOKENS; ++c) {
+        if (N * c > wave) break;
+        Scores<T, TOKENS> P;
+        products<T, N, 1>(
+            q, 1 + wave, [&](int x, int s) { return *reinterpret_cast<const u4*>(kt + KL::go(ka, TOKENS * c + 16 * x, Frag<T>::K * s)); },
+            [&](int x, f4 y) { dec.apply(P, x, N * c + x, y, wave, m, gr); });
+        add_values<T, TO, W>(o, P, vt, TOKENS * c, odd, wave, m, gr);
     }
 }
 
@@ -919,7 +962,7 @@ template <typename T, int DA, bool VEC>
 __device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const Unit& un, float l2, T* kt, T* vt, T* st, float* wt,
                                             int* odd, int wave, int lane) {
     using SL = Tiled<T, DA>;
-    const int m = lane & 15, gr = lane >> 4, thread = threadIdx.x & 255;
+    int thread = threadIdx.x & 255;
     const int64_t bs = A.reversed ? -A.b_ts : A.b_ts, cs = A.reversed ? -A.c_ts : A.c_ts;
     const T* kp = rows_of<T>(A.b, A, g, g.p0, A.b_ts, (un.h / A.b_rep) * A.Da);
     const T* vp = rows_of<T>(A.c, A, g, g.p0, A.c_ts, (un.h / A.c_rep) * A.Dv + un.tile * kV);
@@ -950,8 +993,9 @@ __device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const
         }
     }
     float f = power(l2, kC);
-    const int sw = SL::at_state(16 * wave + m, 4 * gr);
     for (int c0 = 0; c0 < g.n; c0 += kC) {
+        forget_lane<T, DA>(thread);
+        const int lane = thread & 63, sw = SL::at_state(16 * wave + (lane & 15), 4 * (lane >> 4));
         const int n = min(kC, g.n - c0);
         const bool more = c0 + kC < g.n;
         k.store(kt, thread);
@@ -966,7 +1010,16 @@ __device__ __forceinline__ void carry_state(const LaArgs& A, const Seg& g, const
         for (int i = 0; i < DA / 16; ++i) {      // the copy that this chunk's products read
             T* p = st + SL::go_state(sw, 0, 16 * i, false);
             if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<u2*>(p) = u2{pack_bf16(S[i][0], S[i][1]), pack_bf16(S[i][2], S[i][3])};
+                u2 hi, lo;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t a, b;
+                    split_bf16(S[i][2 * k], S[i][2 * k + 1], a, b);
+                    hi[k] = a;
+                    lo[k] = b;
+                }
+                *reinterpret_cast<u2*>(p) = hi;
+                *reinterpret_cast<u2*>(p + kV * SL::ROW) = lo;
             } else {
                 *reinterpret_cast<f4*>(p) = S[i];
             }
@@ -1017,10 +1070,10 @@ __device__ __forceinline__ int block_of(int wave8) {
 template <typename T, typename TO, int DA, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_la_out(LaArgs A) {
     using KL = Tiled<T, DA>;
-    constexpr int NK = DA / Frag<T>::K;
+    constexpr int NK = DA / Frag<T>::K, P = kPieces<T>;
     __shared__ __attribute__((aligned(16))) T kt[kC * Tiled<T, DA>::ROW];
     __shared__ __attribute__((aligned(16))) T vt[kC * Tiled<T, kV>::ROW];
-    __shared__ __attribute__((aligned(16))) T st[kV * KL::ROW];      // the state's copy [value column][row]
+    __shared__ __attribute__((aligned(16))) T st[kPieces<T> * kV * KL::ROW];      // the state's copy [piece][value column][row]
     __shared__ __attribute__((aligned(16))) float wt[kC];
     __shared__ __attribute__((aligned(16))) f4 powers[128];
     __shared__ int odd[4];                       // infinities or NaN in the chunk: in the V tile 1, in the K tile 2
@@ -1055,24 +1108,18 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
         lds_barrier();
         if (c0 + kC < g.n) load_q(c0 + kC);
 
-        // the carried part O^T = S^T Q^T (four accumulators of value columns), then the scores K Q^T
+        // the carried part O^T = S^T Q^T (four accumulators of value columns), then the chunk's own
         f4 o[4];
-        Scores<T> P;
-        int sa = KL::at_state(column<TO>(0, m >> 2) + (m & 3), Frag<T>::VE * gr), ka = KL::at(m, Frag<T>::VE * gr);
+        int sa = KL::at_state(column<TO>(0, m >> 2) + (m & 3), Frag<T>::VE * gr);
         forget(sa);
-        forget(ka);
-        products<T, 8, NK>(
-            q, 5 + wave,
+        products<T, 4, kPieces<T>>(
+            q, 4,
             [&](int x, int s) {
-                const int c = Frag<T>::K * s;
-                return *reinterpret_cast<const u4*>(x < 4 ? st + KL::go_state(sa, column<TO>(x, 0), c, x & 1) : kt + KL::go(ka, 16 * (x - 4), c));
+                return *reinterpret_cast<const u4*>(st + s % P * (kV * KL::ROW) + KL::go_state(sa, column<TO>(x, 0), Frag<T>::K * (s / P), x & 1));
             },
-            [&](int x, f4 y) {
-                if (x < 4) o[x] = y * at_q;      // lambda^{i + shift} of the lane's token
-                else dec.apply(P, x - 4, y, wave, m, gr);
-            });
+            [&](int x, f4 y) { o[x] = y * at_q; });      // lambda^{i + shift} of the lane's token
         const int has = odd[0] | odd[1] | odd[2] | odd[3];
-        add_values<T, TO, kV>(o, P, vt, has & 1, wave, m, gr);
+        add_chunk<T, TO, DA, kV, kC>(o, q, dec, kt, vt, has & 1, wave, m, gr);
         store_rows<TO, VEC, true>(op + c0 * os, os, qi, g.n - c0, o, A.Dv - un.tile * kV, gr);
         lds_barrier();
     }
@@ -1096,10 +1143,10 @@ template <typename T, typename TO, int DA, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkdv(LaArgs A, SecondArgs X) {
     using KL = Tiled<T, DA>;
     using VL = Tiled<T, kV>;
-    constexpr int NK = DA / Frag<T>::K, NV = kV / Frag<T>::K, NA = DA / 16;
+    constexpr int NK = DA / Frag<T>::K, NV = kV / Frag<T>::K, NA = DA / 16, P = kPieces<T>, TOK = sizeof(T) == 2 ? 32 : kC;
     __shared__ __attribute__((aligned(16))) T kt[kC * Tiled<T, DA>::ROW];
     __shared__ __attribute__((aligned(16))) T vt[kC * Tiled<T, kV>::ROW];
-    __shared__ __attribute__((aligned(16))) T st[kV * KL::ROW];
+    __shared__ __attribute__((aligned(16))) T st[kPieces<T> * kV * KL::ROW];
     __shared__ __attribute__((aligned(16))) float wt[kC];
     __shared__ __attribute__((aligned(16))) f4 powers[128];
     __shared__ int odd[4];                       // infinities or NaN in the chunk: in the V tile 1, in the K tile 2
@@ -1107,7 +1154,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
     if (un.seg >= A.nseg) return;
     const Seg g = segment(A, un.seg);
     if (g.seq < 0) return;
-    const int lane = threadIdx.x & 63, m = lane & 15, gr = lane >> 4;
+    const int lane = threadIdx.x & 63;
     const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = block_of<T>(wave8);
     const float l2 = log2_decay(A, un.h);
     if (wave8 >= 4) {
@@ -1118,17 +1165,17 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
     const T* vp = rows_of<T>(X.v, A, g, g.p0, X.v_ts, (un.h / X.v_rep) * A.Dv);
     TO* dv = const_cast<TO*>(rows_of<TO>(A.o, A, g, g.p0, A.o_ts, un.h * A.Dv));
     TO* dk = const_cast<TO*>(rows_of<TO>(X.dk, A, g, g.p0, X.dk_ts, un.h * A.Da));
-    const int qi = 16 * wave + m;
-    const float at_q = A.s_carry * power(l2, qi + A.shift);
+    const float at_q = A.s_carry * power(l2, 16 * wave + (lane & 15) + A.shift);
     const Decay dec(powers, l2, A.s_in, wave, lane);
     u4 q[NK], qn[NK], v[NV], vn[NV];
+    int me = lane;
     auto load = [&](int c0) {
-        const int n = min(kC, g.n - c0);
+        const int n = min(kC, g.n - c0), i = 16 * wave + (me & 15), e = Frag<T>::VE * (me >> 4);
         const Window wq = window(ap - c0 * A.a_ts, A.a_ts, true, n, A.Da), wv = window(vp - c0 * X.v_ts, X.v_ts, true, n, A.Dv);
 #pragma unroll
-        for (int s = 0; s < NK; ++s) qn[s] = load_row<T, VEC>(wq, qi, Frag<T>::K * s + Frag<T>::VE * gr, A.Da);
+        for (int s = 0; s < NK; ++s) qn[s] = load_row<T, VEC>(wq, i, Frag<T>::K * s + e, A.Da);
 #pragma unroll
-        for (int s = 0; s < NV; ++s) vn[s] = load_row<T, VEC>(wv, qi, Frag<T>::K * s + Frag<T>::VE * gr, A.Dv);
+        for (int s = 0; s < NV; ++s) vn[s] = load_row<T, VEC>(wv, i, Frag<T>::K * s + e, A.Dv);
     };
     load(0);
     for (int c0 = 0; c0 < g.n; c0 += kC) {
@@ -1137,55 +1184,46 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
 #pragma unroll
         for (int s = 0; s < NV; ++s) v[s] = vn[s];
         lds_barrier();
+        forget_lane<T, DA>(me);
+        const int m = me & 15, gr = me >> 4, qi = 16 * wave + m;
         if (c0 + kC < g.n) load(c0 + kC);
         const int has = odd[0] | odd[1] | odd[2] | odd[3];
         {
             f4 o[4];
-            Scores<T> P;
-            int sa = KL::at_state(column<TO>(0, m >> 2) + (m & 3), Frag<T>::VE * gr), ka = KL::at(m, Frag<T>::VE * gr);
+            int sa = KL::at_state(column<TO>(0, m >> 2) + (m & 3), Frag<T>::VE * gr);
             forget(sa);
-            forget(ka);
-            products<T, 8, NK>(
-                q, 5 + wave,
+            products<T, 4, kPieces<T>>(
+                q, 4,
                 [&](int x, int s) {
-                    const int c = Frag<T>::K * s;
-                    return *reinterpret_cast<const u4*>(x < 4 ? st + KL::go_state(sa, column<TO>(x, 0), c, x & 1) : kt + KL::go(ka, 16 * (x - 4), c));
+                    return *reinterpret_cast<const u4*>(st + s % P * (kV * KL::ROW) + KL::go_state(sa, column<TO>(x, 0), Frag<T>::K * (s / P), x & 1));
                 },
-                [&](int x, f4 y) {
-                    if (x < 4) o[x] = y * at_q;
-                    else dec.apply(P, x - 4, y, wave, m, gr);
-                });
-            add_values<T, TO, kV>(o, P, vt, has & 1, wave, m, gr);
+                [&](int x, f4 y) { o[x] = y * at_q; });
+            add_chunk<T, TO, DA, kV, TOK>(o, q, dec, kt, vt, has & 1, wave, m, gr);
             store_rows<TO, VEC, false>(dv - c0 * A.o_ts, -A.o_ts, qi, g.n - c0, o, A.Dv, gr);
         }
         {
             f4 o[NA];
-            Scores<T> P;
-            int va = VL::at(m, Frag<T>::VE * gr);
             int sa = KL::at_state(8 * gr + (m >> 2), column<TO>(0, m & 3));
-            forget(va);
             forget(sa);
-            products<T, NA + 4, NV>(
-                v, NA + 1 + wave,
-                [&](int x, int s) {
-                    if (x >= NA) return *reinterpret_cast<const u4*>(vt + VL::go(va, 16 * (x - NA), Frag<T>::K * s));
+            products<T, NA, kPieces<T>>(
+                v, NA,
+                [&](int x, int sp) {
+                    const int s = sp / P;
+                    const T* copy = st + sp % P * (kV * KL::ROW);
                     if constexpr (sizeof(T) == 2) {      // rows of R: key columns of the copy, eight value columns a lane
-                        const u2 a0 = tr4(st + KL::go_state(sa, 32 * s, column<TO>(x, 0), false));
-                        const u2 a1 = tr4(st + KL::go_state(sa, 32 * s + 4, column<TO>(x, 0), true));
+                        const u2 a0 = tr4(copy + KL::go_state(sa, 32 * s, column<TO>(x, 0), false));
+                        const u2 a1 = tr4(copy + KL::go_state(sa, 32 * s + 4, column<TO>(x, 0), true));
                         return u4{a0[0], a0[1], a1[0], a1[1]};
                     } else {
                         u4 a;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            a[e] = __float_as_uint(st[KL::at_state(16 * s + 4 * gr + e, column<TO>(x, m >> 2) + (m & 3))]);
+                            a[e] = __float_as_uint(copy[KL::at_state(16 * s + 4 * gr + e, column<TO>(x, m >> 2) + (m & 3))]);
                         return a;
                     }
                 },
-                [&](int x, f4 y) {
-                    if (x < NA) o[x] = y * at_q;
-                    else dec.apply(P, x - NA, y, wave, m, gr);
-                });
-            add_values<T, TO, DA>(o, P, kt, has & 2, wave, m, gr);
+                [&](int x, f4 y) { o[x] = y * at_q; });
+            add_chunk<T, TO, kV, DA, TOK>(o, v, dec, vt, kt, has & 2, wave, m, gr);
             store_rows<TO, VEC, false>(dk - c0 * X.dk_ts, -X.dk_ts, qi, g.n - c0, o, A.Da, gr);
         }
         lds_barrier();
