@@ -262,6 +262,12 @@ template <> struct Frag<float> {
     }
 };
 
+// 16 bytes of LDS on a 16-byte border.  Said once more, since the compiler loses sight of it and reads fp32 in four pieces.
+template <typename T>
+__device__ __forceinline__ u4 fragment_at(const T* p) {
+    return *reinterpret_cast<const u4*>(__builtin_assume_aligned(p, 16));
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const f2 v = {lo, hi};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));   // nearest even
@@ -879,7 +885,7 @@ __device__ __forceinline__ void add_chunk(f4 (&o)[NT], const u4 (&q)[NK], const 
         if (N * c > wave) break;
         Scores<T, TOKENS> P;
         products<T, N, 1>(
-            q, 1 + wave, [&](int x, int s) { return *reinterpret_cast<const u4*>(kt + KL::go(ka, TOKENS * c + 16 * x, Frag<T>::K * s)); },
+            q, 1 + wave, [&](int x, int s) { return fragment_at(kt + KL::go(ka, TOKENS * c + 16 * x, Frag<T>::K * s)); },
             [&](int x, f4 y) { dec.apply(P, x, N * c + x, y, wave, m, gr); });
         add_values<T, TO, W>(o, P, vt, TOKENS * c, odd, wave, m, gr);
     }
@@ -1115,7 +1121,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
         products<T, 4, kPieces<T>>(
             q, 4,
             [&](int x, int s) {
-                return *reinterpret_cast<const u4*>(st + s % P * (kV * KL::ROW) + KL::go_state(sa, column<TO>(x, 0), Frag<T>::K * (s / P), x & 1));
+                return fragment_at(st + s % P * (kV * KL::ROW) + KL::go_state(sa, column<TO>(x, 0), Frag<T>::K * (s / P), x & 1));
             },
             [&](int x, f4 y) { o[x] = y * at_q; });      // lambda^{i + shift} of the lane's token
         const int has = odd[0] | odd[1] | odd[2] | odd[3];
@@ -1195,7 +1201,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 4 ? 2 : 4) k_la_dkd
             products<T, 4, kPieces<T>>(
                 q, 4,
                 [&](int x, int s) {
-                    return *reinterpret_cast<const u4*>(st + s % P * (kV * KL::ROW) + KL::go_state(sa, column<TO>(x, 0), Frag<T>::K * (s / P), x & 1));
+                    return fragment_at(st + s % P * (kV * KL::ROW) + KL::go_state(sa, column<TO>(x, 0), Frag<T>::K * (s / P), x & 1));
                 },
                 [&](int x, f4 y) { o[x] = y * at_q; });
             add_chunk<T, TO, DA, kV, TOK>(o, q, dec, kt, vt, has & 1, wave, m, gr);
