@@ -306,7 +306,7 @@ __device__ __forceinline__ Window window(const T* p, int64_t ts, bool reversed, 
 
 // VE elements from column c of row r; columns at and behind `width` are zero.  Without VEC they may start at any
 // element's address, which the memory takes in one access; a row's last vector may be cut short (2 x 8192 tokens, 16 heads
-// of 128 x 64, bf16, from an odd address on: element by element 199 us and backward 555, so 101 and 226; aligned 72 and 196).
+// of 128 x 64, bf16, from an odd address on: element by element 199 us and backward 555, so 102 and 254; aligned 78 and 194).
 template <typename T, bool VEC>
 __device__ __forceinline__ u4 load_row(const Window& w, int r, int c, int width) {
     const uint32_t off = (uint32_t)(w.row0 + r * w.step + c * (int)sizeof(T));
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kWalkThreads) k_la_state(LaArgs A) {
 // In place over a sequence's places: the state that enters each of its segments.  A workgroup
 // takes 1024 values (256 lanes of four) of one (long sequence, head, tile).  There are at most
 // T / (kFewSegments target + 1) long sequences, so the launch does not grow with the short ones (64k tokens in
-// 2000 sequences, 16 heads: the call 892 us where it did, 768 now).  They are never more than 128: 2^23 workgroups
+// 2000 sequences, 16 heads: the call 892 us where it did, 780 so; 721 now).  They are never more than 128: 2^23 workgroups
 // with the most heads and columns.  Bound by latency: 5.4 us for 16.9 MB, 5.0 us where it finds none.
 template <int DA>
 __global__ void __launch_bounds__(256) k_la_carry(LaArgs A, const int* longs) {
@@ -1069,8 +1069,8 @@ __device__ __forceinline__ int block_of(int wave8) {
 // next chunk's tiles into registers while this one is computed (the output waves the next
 // queries, which only they read) and put them to LDS between two barriers.
 // TO: type of the output (fp32 where several heads' gradients are still to be added up).
-// bf16 is bound by its traffic: the packed prompt above 55.5 us for 233 MB, 4.2 TB/s, and the backward's run for dq (4 x 4096
-// tokens, do and v to dq) 51 us for 210 MB, 4.1 TB/s, the matrix unit 15 - 19 % busy, LDS 19 - 27 %.  fp32, 50 us for 143 MB with
+// bf16 is bound by its traffic: the packed prompt above 54 us for 222 MB, 4.1 TB/s, and the backward's run for dq (4 x 4096
+// tokens, do and v to dq) 55 us for 210 MB, 3.8 TB/s, the matrix unit 21 - 24 % busy, LDS 26 - 32 %.  fp32, 49 us for 143 MB with
 // the matrix unit 38 % busy, waits for both in turn.  Two workgroups of eight waves fit a compute unit: 128
 // registers a wave.
 template <typename T, typename TO, int DA, bool VEC>
@@ -1137,7 +1137,8 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) * DA > 256 ? 2 : 4) k_
 // and on the same tiles and state, with queries v (X.v),
 //     dk_j = scale sum_{i>=j} lambda^{i-j} (v_j . do_i) q_i + lambda^{..} R v_j   (X.dk).
 // R's copy lies with its rows (key width) side by side: the first product reads it as it lies, the second
-// transposed.  Bound by its traffic: 16384 tokens, 16 heads of 128 x 64, bf16: 81 us for 360 MB, 4.4 TB/s; the call
+// transposed.  Bound by its traffic: 16384 tokens, 16 heads of 128 x 64, bf16: 86 us for 352 MB, 4.1 TB/s (matrix unit 20 % busy,
+// LDS 36 %); before the operands came in two pieces 81 us, and the call
 // with two runs instead 231 us, so 188.
 struct SecondArgs {
     const void* v;
@@ -1282,7 +1283,7 @@ struct StepArgs {
 // A workgroup owns CW = 4 LN value columns of one (row, head): LN lanes side by side hold
 // four columns each, the 256 / LN rows of lanes share out the state's rows, and their parts
 // of o are added up in LDS.  All its state reads are under way before the first is used.
-// Bound by the states' bytes: 256 rows, 16 heads of 128 x 64: 47.7 us for 272 MB, 5.7 TB/s.  One row: 4.5 us, the
+// Bound by the states' bytes: 256 rows, 16 heads of 128 x 64: 48 us for 272 MB, 5.6 TB/s.  One row: 4.4 us, the
 // latency of a load, a sum through LDS and a store.
 template <typename T, int LN, bool VEC>
 __global__ void __launch_bounds__(256) k_la_step(StepArgs A) {
@@ -1374,7 +1375,7 @@ constexpr int kOneSegment = 1024;   // tokens in all up to which every sequence 
 // segment's state makes four trips through memory.  Up to 1024 tokens in all, one segment a sequence.
 // Packed prompt and backward (above) with one workgroup a compute unit 115 and 212 us, with two 85 and 188, with
 // four and segments from 128 tokens 99 and 212; seven prompts of 1021 tokens in all 15 us, cut 19.5.  The last rule goes by the sum of
-// tokens and costs a long sequence that comes alone: one prompt of 1000 tokens, 16 heads, 44 us, of 1088, cut in five, 23.
+// tokens and costs a long sequence that comes alone: one prompt of 1000 tokens, 16 heads, 44 us, of 1088, cut in five, 24.
 int plan_target(int64_t n_seq, int64_t T, int64_t H, int64_t Dv, bool packed) {
     if (T <= kOneSegment) return kOneSegment;
     const int64_t units = H * ((Dv + kV - 1) / kV);
