@@ -71,7 +71,10 @@ typedef enum {
     MB_OP_LINEAR_ATTN = 11,     /* sizes (n_seq, T, H, Dv, G, Dk) in (batch, L, H, P, G, N) */
     MB_OP_LINEAR_ATTN_BWD = 12, /* likewise */
     MB_OP_RMS_NORM_BWD = 13,    /* sizes (rows, D) in (batch, H) */
-    MB_OP_GRAD_NORM_CLIP = 14   /* the number of tensors in batch */
+    MB_OP_GRAD_NORM_CLIP = 14,  /* the number of tensors in batch */
+    MB_OP_GATED_SCAN = 15,      /* sizes (n_seq, T, D) in (batch, L, H) */
+    MB_OP_GATED_SCAN_BWD = 16,  /* likewise */
+    MB_OP_QK_NORM_ROPE_BWD = 17 /* sizes (T, Hq, Hk, D) in (batch, H, G, P) */
 } mb_op;
 
 /*
@@ -720,6 +723,125 @@ mb_status mb_rms_norm_bwd(const void* dy, const void* r, const float* rstd, cons
 mb_status mb_grad_norm_clip(const void* const* grads, void* const* outs, const int64_t* sizes,
                             int64_t n, float max_norm, float eps, float* norm, mb_dtype dtype,
                             void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Gated linear recurrence: every channel of every token has a decay of its own from a gate, and an
+ * input that a second gate opens and that is scaled so that the state keeps its variance.  Per
+ * sequence and channel c, with sigma(v) = 1 / (1 + e^-v):
+ *     s_t = sigma(a_gate_t + a_bias),  la_t = -decay s_t,  a_t = e^{la_t}
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigma(x_gate_t + x_bias) x_t,   y_t = h_t
+ *   x, a_gate, x_gate, y : (T, D)  dtype   the tokens of all sequences, one after another; x_gate
+ *                 NULL: no input gate (its factor is 1; x_bias is then NULL too)
+ *   x_stride, a_stride, g_stride : elements between the tokens of x, a_gate, x_gate, at least D and
+ *                 below 2^22: they may be columns of one projection's output.  y is contiguous.
+ *   decay       : (D) fp32, >= 0 (a negative one gives NaN; infinity: no memory)
+ *   a_bias, x_bias : (D) fp32 or NULL (zeros)
+ *   cu_seqlens, has_h0, slots, n_seq, n_slots : as mb_linear_attn (rows of y outside all sequences are
+ *                 left as they were; offsets outside [0, T] are taken as the nearest bound; decreasing ones
+ *                 give unspecified results, but no access outside the tensors)
+ *   h0, h_out   : (n_seq, D) fp32, or (n_slots, D) with slots; h0 NULL = zeros; h_out NULL = not
+ *                 written; h_out may equal h0.  A sequence of no tokens leaves its h0 (or zeros).
+ *   states      : (ceil(T / 64), D) fp32, for the backward: row j is the state that token 64 j starts
+ *                 from (h0 or zeros where it is the first of its sequence; unspecified outside all
+ *                 sequences); NULL = not written
+ * Arithmetic and states are fp32; 1 - a^2 keeps its digits where a is next to 1.  NaN and infinities
+ * reach the outputs and states of their channel from their token on, never earlier tokens, other
+ * channels or other sequences (an infinity may become NaN).  Deterministic.
+ * Supported: 1 <= D < 2^22, T < 2^31, n_seq <= 2^20, ceil(T / 128) ceil(D / 64) < 2^24.  Any alignment of the
+ * element type's; even D and strides with pointers aligned to two elements read and write in pairs.
+ * ws: at least mb_workspace_size(MB_OP_GATED_SCAN, n_seq, T, D, 1, 1, 1, 1, 0) bytes, 256-byte
+ * aligned (may be 0).  Two calls that run at the same time need a workspace each.
+ */
+mb_status mb_gated_scan(const void* x, const void* a_gate, const void* x_gate, const float* decay,
+                        const float* a_bias, const float* x_bias, const int32_t* cu_seqlens,
+                        const float* h0, const uint8_t* has_h0, const int32_t* slots, void* y,
+                        float* h_out, float* states, int64_t n_seq, int64_t T, int64_t D,
+                        int64_t n_slots, int64_t x_stride, int64_t a_stride, int64_t g_stride,
+                        mb_dtype dtype, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * One token of mb_gated_scan for n independent sequences (decode):
+ *     h[s] <- a h[s] + sqrt(1 - a^2) sigma(x_gate + x_bias) x,   y = h[s]
+ *   x, a_gate, x_gate, y (n, D) dtype; strides as above
+ *   h_in, h_out : (n, D) fp32, or (n_slots, D) with slots; h_in NULL = zeros; h_out == h_in (in
+ *                 place) is allowed; rows of h_out that no slot names are left alone
+ *   slots       : as mb_linear_attn_step (outside [0, n_slots): starts from zeros, nothing stored)
+ * n <= 2^20.  No workspace.
+ */
+mb_status mb_gated_scan_step(const void* x, const void* a_gate, const void* x_gate,
+                             const float* decay, const float* a_bias, const float* x_bias,
+                             const int32_t* slots, const float* h_in, float* h_out, void* y,
+                             int64_t n, int64_t D, int64_t n_slots, int64_t x_stride,
+                             int64_t a_stride, int64_t g_stride, mb_dtype dtype, hipStream_t stream);
+
+/*
+ * Backward of mb_gated_scan: given dy (gradient of the loss with respect to y) and dh_out (with
+ * respect to h_out; NULL = zero), the gradients of sum dy . y + sum dh_out . h_out.  With i the input
+ * gate, beta = sqrt(1 - a^2), b = beta i x and G the adjoint of the state (G = dh_out behind the last token):
+ *     G_t = dy_t + G;   dh = a_t G_t;   dx = G_t beta i;   dx_gate = G_t b (1 - i)
+ *     dla = G_t (a_t h_{t-1} - a_t^2 b / beta^2);   da_gate = dla la (1 - s);   ddecay = -sum dla s
+ *     G = dh for the token before;  dh0 = G at the end;  da_bias = sum da_gate,  dx_bias = sum dx_gate
+ * A step whose beta^2 is below 2^-120 (no decay at all) passes nothing through beta to ddecay and da_gate, where
+ * the root has no derivative.
+ *   dy, dx, da_gate, dx_gate : (T, D) dtype, contiguous; dx_gate NULL exactly where x_gate is
+ *   ddecay, da_bias, dx_bias : (D) fp32; NULL = not wanted
+ *   h0, dh_out, dh0 : (n_seq, D) fp32; h0, dh_out NULL = zeros; dh0 NULL = not wanted
+ *   states      : what mb_gated_scan wrote for the same arguments, or NULL: they are made again
+ * Rows of dx, da_gate, dx_gate of tokens outside all sequences are zero.  Sums in a fixed order (deterministic).
+ * Other arguments and limits as mb_gated_scan.  No output may overlap an input, another output or the
+ * workspace (MB_ERR_ALIAS).
+ * ws: at least mb_workspace_size(MB_OP_GATED_SCAN_BWD, n_seq, T, D, 1, 1, 1, 1, 0) bytes.
+ */
+mb_status mb_gated_scan_bwd(const void* x, const void* a_gate, const void* x_gate, const float* decay,
+                            const float* a_bias, const float* x_bias, const int32_t* cu_seqlens,
+                            const float* h0, const void* dy, const float* dh_out, const float* states,
+                            void* dx, void* da_gate, void* dx_gate, float* ddecay, float* da_bias,
+                            float* dx_bias, float* dh0, int64_t n_seq, int64_t T, int64_t D,
+                            int64_t x_stride, int64_t a_stride, int64_t g_stride, mb_dtype dtype,
+                            void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * Root-mean-square norm of every head of queries and keys, and the rotation by their position, in
+ * one pass: what stands in front of mb_linear_attn and mb_linear_attn_step.  Per token and head,
+ *     n_d = x_d / sqrt(mean_d x_d^2 + eps) * weight_d
+ *     pairs (u, v) of n at (2j, 2j+1) with interleaved, at (j, j + R/2) without, j < R/2:
+ *     (u cos - v sin, u sin + v cos) of the angle position freqs[j];  columns R to D - 1 keep n
+ *   q, q_out : (T, Hq, D)  dtype;   k, k_out : (T, Hk, D)  dtype; Hk = 0: no keys (k, k_out ignored)
+ *   q_stride, k_stride, q_out_stride, k_out_stride : elements between tokens, at least Hq*D and Hk*D and
+ *                 below 2^22.  q_out may be q, k_out k (same stride): in place, in a projection's output.
+ *   q_weight, k_weight : (D) fp32 or NULL (ones)
+ *   freqs       : (R / 2) fp32, radians per position; NULL with R = 0 (no rotation)
+ *   positions   : (T) int32, any value; NULL: token t has position t mod L
+ *   L           : tokens of a sequence where positions is NULL (L >= 1; ignored otherwise)
+ * Angles are made of the product in 64 bits, so far positions keep their place.  Arithmetic is fp32,
+ * outputs are rounded once; sums of squares outside fp32's range are taken scaled, as in mb_rms_norm.
+ * Supported: 1 <= D <= 512, R even, 0 <= R <= D, 1 <= Hq <= 4096, Hk <= 4096, T <= 2^30.  Any alignment of the element type's;
+ * 16-byte aligned pointers with D and strides multiples of 8 (bf16; 4 for fp32) and R of 16 (8) take vector accesses.
+ */
+mb_status mb_qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                          const float* freqs, const int32_t* positions, void* q_out, void* k_out,
+                          int64_t T, int64_t L, int64_t Hq, int64_t Hk, int64_t D, int64_t R,
+                          int64_t q_stride, int64_t k_stride, int64_t q_out_stride,
+                          int64_t k_out_stride, int interleaved, float eps, mb_dtype dtype,
+                          hipStream_t stream);
+
+/*
+ * Backward of mb_qk_norm_rope: given dq_out and dk_out, and the inputs q and k (not the
+ * outputs), with e the gradient rotated back, xh = x / sqrt(mean x^2 + eps) and g = e weight,
+ *     dx = (g - xh mean_d(g xh)) / sqrt(mean x^2 + eps),   dweight_d = sum over tokens and heads e_d xh_d
+ *   dq_out, dq : (T, Hq, D) dtype;  dk_out, dk : (T, Hk, D) dtype, contiguous
+ *   dq_weight, dk_weight : (D) fp32; NULL = not wanted (dk_weight ignored with Hk = 0)
+ * Sums in a fixed order (deterministic).  Other arguments and limits as mb_qk_norm_rope.  No output may
+ * overlap an input, another output or the workspace (MB_ERR_ALIAS).
+ * ws: with dq_weight or dk_weight, at least mb_workspace_size(MB_OP_QK_NORM_ROPE_BWD, T, 1, Hq, D, Hk, 1, 1, 0)
+ * bytes, 256-byte aligned (may be 0).
+ */
+mb_status mb_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                              const float* q_weight, const float* k_weight, const float* freqs,
+                              const int32_t* positions, void* dq, void* dk, float* dq_weight,
+                              float* dk_weight, int64_t T, int64_t L, int64_t Hq, int64_t Hk, int64_t D,
+                              int64_t R, int64_t q_stride, int64_t k_stride, int interleaved, float eps,
+                              mb_dtype dtype, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /*
  * Bytes of device workspace an entry point needs for the given sizes (0 if it

@@ -24,6 +24,8 @@ __all__ = [
     "mb_linear_attn", "mb_linear_attn_step", "mb_linear_attn_bwd", "mb_rms_norm", "mb_rms_norm_fp8",
     "mb_rms_norm_bwd", "mb_grad_norm_clip", "MB_OP_LINEAR_ATTN", "MB_OP_LINEAR_ATTN_BWD",
     "MB_OP_RMS_NORM_BWD", "MB_OP_GRAD_NORM_CLIP",
+    "mb_gated_scan", "mb_gated_scan_step", "mb_gated_scan_bwd", "mb_qk_norm_rope", "mb_qk_norm_rope_bwd",
+    "MB_OP_GATED_SCAN", "MB_OP_GATED_SCAN_BWD", "MB_OP_QK_NORM_ROPE_BWD",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,7 +37,8 @@ MB_F32, MB_BF16 = 0, 1
 (MB_OP_SELECTIVE_SCAN, MB_OP_SSM_STEP, MB_OP_SSD_CHUNKED, MB_OP_TRAP_SSD,
  MB_OP_MIMO_SSD, MB_OP_SSD_CHUNKED_BWD, MB_OP_SELECTIVE_SCAN_BWD, MB_OP_TRAP_SSD_BWD,
  MB_OP_MIMO_SSD_BWD, MB_OP_SSD_BLOCK, MB_OP_SSD_BLOCK_BF16, MB_OP_LINEAR_ATTN,
- MB_OP_LINEAR_ATTN_BWD, MB_OP_RMS_NORM_BWD, MB_OP_GRAD_NORM_CLIP) = range(15)
+ MB_OP_LINEAR_ATTN_BWD, MB_OP_RMS_NORM_BWD, MB_OP_GRAD_NORM_CLIP, MB_OP_GATED_SCAN, MB_OP_GATED_SCAN_BWD,
+ MB_OP_QK_NORM_ROPE_BWD) = range(18)
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -127,6 +130,15 @@ def load_library():
             lib.mb_grad_norm_clip.argtypes = [_vp] * 3 + [_i64, fl, fl, _vp, it, _vp, sz, _vp]
             for f in ("mb_linear_attn", "mb_linear_attn_step", "mb_linear_attn_bwd", "mb_rms_norm", "mb_rms_norm_fp8",
                       "mb_rms_norm_bwd", "mb_grad_norm_clip"):
+                getattr(lib, f).restype = ctypes.c_int
+        if hasattr(lib, "mb_gated_scan"):
+            sz, fl, it = ctypes.c_size_t, ctypes.c_float, ctypes.c_int
+            lib.mb_gated_scan.argtypes = [_vp] * 13 + [_i64] * 7 + [it, _vp, sz, _vp]
+            lib.mb_gated_scan_step.argtypes = [_vp] * 10 + [_i64] * 6 + [it, _vp]
+            lib.mb_gated_scan_bwd.argtypes = [_vp] * 18 + [_i64] * 6 + [it, _vp, sz, _vp]
+            lib.mb_qk_norm_rope.argtypes = [_vp] * 8 + [_i64] * 10 + [it, fl, it, _vp]
+            lib.mb_qk_norm_rope_bwd.argtypes = [_vp] * 12 + [_i64] * 8 + [it, fl, it, _vp, sz, _vp]
+            for f in ("mb_gated_scan", "mb_gated_scan_step", "mb_gated_scan_bwd", "mb_qk_norm_rope", "mb_qk_norm_rope_bwd"):
                 getattr(lib, f).restype = ctypes.c_int
         lib.mb_status_str.argtypes = [ctypes.c_int]
         lib.mb_status_str.restype = ctypes.c_char_p
@@ -942,6 +954,230 @@ def mb_linear_attn_bwd(q, k, v, log_decay, do, *, scale=None, cu_seqlens=None, h
     _call_on(dev, "mb_linear_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(cu_seqlens), _ptr(h0), _ptr(do),
              _ptr(dh_out), *[_ptr(t) for t in out], n, T, H, G, Dk, Dv, *st, Dk ** -0.5 if scale is None else scale, code,
              _ptr(ws), nws)
+    return tuple(out)
+
+
+# ----------------------------------------------------------------------------
+# gated linear recurrence
+# ----------------------------------------------------------------------------
+MB_GATED_SCAN_EVERY = 64     # tokens between the rows of `states`
+
+
+def _channels(t, name, lead, D, dtype, device):
+    """_tokens of a (*lead, D) tensor."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if tuple(t.shape) != tuple(lead) + (D,):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(lead) + (D,)))
+    return _tokens(t.unsqueeze(-2), name, lead, 1, D, dtype, device)
+
+
+def _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, lead):
+    """Check the inputs that every form of the recurrence has: (device, code, strides)."""
+    torch = _torch()
+    dev = _device_of(x)
+    code = _dtype_code(x, "x")
+    D = x.shape[-1]
+    st = [_channels(x, "x", lead, D, x.dtype, dev), _channels(a_gate, "a_gate", lead, D, x.dtype, dev),
+          D if x_gate is None else _channels(x_gate, "x_gate", lead, D, x.dtype, dev)]
+    if x_gate is None and x_bias is not None:
+        raise ValueError("x_bias needs an x_gate")
+    for t, name in ((decay, "decay"), (a_bias, "a_bias"), (x_bias, "x_bias")):
+        _check(t, name, (D,), torch.float32, dev)
+    return dev, code, st
+
+
+def _gated_sequences(x, cu_seqlens, dev):
+    """(leading axes, sequences, tokens) of x (T, D) with cu_seqlens, (batch, L, D) without."""
+    if x.dim() != (2 if cu_seqlens is not None else 3):
+        raise ValueError("x must be (T, D) with cu_seqlens, (batch, L, D) without")
+    lead = tuple(x.shape[:-1])
+    if cu_seqlens is None:
+        return lead, lead[0], lead[0] * lead[1]
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must hold n_seq + 1 offsets")
+    _check(cu_seqlens, "cu_seqlens", tuple(cu_seqlens.shape), _torch().int32, dev)
+    return lead, cu_seqlens.shape[0] - 1, lead[0]
+
+
+def _gated_pool(h0, h_out, slots, n, D, dev):
+    """Check the slots; returns (n_slots, state shape)."""
+    if slots is None:
+        return 0, (n, D)
+    _check(slots, "slots", (n,), _torch().int32, dev)
+    pool = h0 if h0 is not None else h_out
+    if pool is None or pool.dim() != 2 or pool.shape[0] < 1:
+        raise ValueError("slots need a pool of states (n_slots, D)")
+    return pool.shape[0], (pool.shape[0], D)
+
+
+def mb_gated_scan(x, a_gate, decay, x_gate=None, *, a_bias=None, x_bias=None, cu_seqlens=None, h0=None, has_h0=None,
+                  slots=None, y=None, h_out=None, states=False, ws=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(x_gate + x_bias) x_t with a_t =
+    exp(-decay sigmoid(a_gate + a_bias)), y = h.  x, a_gate, x_gate (batch, L, D), or (T, D) with cu_seqlens
+    (n_seq + 1,) int32, in one dtype (float32 or bfloat16), views with one stride between tokens allowed;
+    x_gate None: no input gate; decay (D,) float32 >= 0, a_bias, x_bias (D,) float32 or None.  h0 (n_seq,
+    D) float32, or with slots (n_seq,) int32 a pool (n_slots, D) that is updated in place unless h_out is
+    given; has_h0 (n_seq,) uint8 or bool marks the sequences that continue.  Rows of y outside all
+    sequences are not written.  Returns (y, h_out), and with states=True (or a tensor for them) also the
+    states (ceil(T / 64), D) float32 that mb_gated_scan_bwd takes."""
+    torch = _torch()
+    dev = _device_of(x)
+    lead, n, T = _gated_sequences(x, cu_seqlens, dev)
+    dev, code, st = _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, lead)
+    D, f32 = x.shape[-1], torch.float32
+    n_slots, hs = _gated_pool(h0, h_out, slots, n, D, dev)
+    _check(h0, "h0", hs, f32, dev)
+    if has_h0 is not None:
+        _check(has_h0, "has_h0", (n,), torch.bool if has_h0.dtype == torch.bool else torch.uint8, dev)
+    y = x.new_empty(lead + (D,)) if y is None else _check(y, "y", lead + (D,), x.dtype, dev)
+    if h_out is None:
+        h_out = h0 if slots is not None else decay.new_empty(hs)
+    _check(h_out, "h_out", hs, f32, dev)
+    kept = None
+    if states is not None and states is not False:
+        ss = (-(-T // MB_GATED_SCAN_EVERY), D)
+        kept = decay.new_empty(ss) if states is True else _check(states, "states", ss, f32, dev)
+    ws, nws = _scratch(MB_OP_GATED_SCAN, dev, ws, (n, T, D, 1, 1, 1, 1, 0))
+    _call_on(dev, "mb_gated_scan", _ptr(x), _ptr(a_gate), _ptr(x_gate), _ptr(decay), _ptr(a_bias), _ptr(x_bias), _ptr(cu_seqlens),
+             _ptr(h0), _ptr(has_h0), _ptr(slots), _ptr(y), _ptr(h_out), _ptr(kept), n, T, D, n_slots, *st, code, _ptr(ws), nws)
+    return (y, h_out) if kept is None else (y, h_out, kept)
+
+
+def mb_gated_scan_step(x, a_gate, decay, h, x_gate=None, *, a_bias=None, x_bias=None, slots=None, y=None, h_out=None):
+    """One token of mb_gated_scan per sequence.  x, a_gate, x_gate (n, D); h (n, D) float32, or with slots
+    (n,) int32 a pool (n_slots, D).  With h_out=None the states are updated in place.  Returns (y, h_out)."""
+    torch = _torch()
+    _device_of(x)
+    if x.dim() != 2:
+        raise ValueError("x must be (n, D)")
+    n, D = x.shape
+    dev, code, st = _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, (n,))
+    n_slots, hs = _gated_pool(h, h_out, slots, n, D, dev)
+    _check(h, "h", hs, torch.float32, dev)
+    h_out = h if h_out is None else _check(h_out, "h_out", hs, torch.float32, dev)
+    y = x.new_empty((n, D)) if y is None else _check(y, "y", (n, D), x.dtype, dev)
+    _call_on(dev, "mb_gated_scan_step", _ptr(x), _ptr(a_gate), _ptr(x_gate), _ptr(decay), _ptr(a_bias), _ptr(x_bias), _ptr(slots),
+             _ptr(h), _ptr(h_out), _ptr(y), n, D, n_slots, *st, code)
+    return y, h_out
+
+
+def mb_gated_scan_bwd(x, a_gate, decay, dy, x_gate=None, *, a_bias=None, x_bias=None, cu_seqlens=None, h0=None, dh_out=None,
+                      states=None, dx=None, da_gate=None, dx_gate=None, ddecay=None, da_bias=None, dx_bias=None, dh0=None,
+                      ws=None):
+    """Backward of mb_gated_scan: the gradients of sum dy . y + sum dh_out . h_out.  dy (contiguous) like x; h0, dh_out
+    (n_seq, D) float32 or None (zeros); states as the forward returned them for the same arguments, or
+    None (they are made again).  Rows of tokens outside all sequences are zero.  Returns (dx, da_gate,
+    dx_gate, ddecay, da_bias, dx_bias, dh0), None for what belongs to a gate or bias that is None."""
+    torch = _torch()
+    dev = _device_of(x)
+    lead, n, T = _gated_sequences(x, cu_seqlens, dev)
+    dev, code, st = _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, lead)
+    D, f32, dt = x.shape[-1], torch.float32, x.dtype
+    _check(dy, "dy", lead + (D,), dt, dev)
+    for t, name in ((h0, "h0"), (dh_out, "dh_out")):
+        _check(t, name, (n, D), f32, dev)
+    _check(states, "states", (-(-T // MB_GATED_SCAN_EVERY), D), f32, dev)
+    out = []
+    for t, name, shp, d, there in ((dx, "dx", lead + (D,), dt, x), (da_gate, "da_gate", lead + (D,), dt, x),
+                                   (dx_gate, "dx_gate", lead + (D,), dt, x_gate), (ddecay, "ddecay", (D,), f32, x),
+                                   (da_bias, "da_bias", (D,), f32, a_bias), (dx_bias, "dx_bias", (D,), f32, x_bias),
+                                   (dh0, "dh0", (n, D), f32, x)):
+        if there is None:
+            if t is not None:
+                raise ValueError("%s is the gradient of an argument that is None" % name)
+            out.append(None)
+        else:
+            out.append(x.new_empty(shp, dtype=d) if t is None else _check(t, name, shp, d, dev))
+    ws, nws = _scratch(MB_OP_GATED_SCAN_BWD, dev, ws, (n, T, D, 1, 1, 1, 1, 0))
+    _call_on(dev, "mb_gated_scan_bwd", _ptr(x), _ptr(a_gate), _ptr(x_gate), _ptr(decay), _ptr(a_bias), _ptr(x_bias),
+             _ptr(cu_seqlens), _ptr(h0), _ptr(dy), _ptr(dh_out), _ptr(states), *[_ptr(t) for t in out], n, T, D, *st, code,
+             _ptr(ws), nws)
+    return tuple(out)
+
+
+# ----------------------------------------------------------------------------
+# norm of queries and keys with the position rotation
+# ----------------------------------------------------------------------------
+def _qk_args(q, k, freqs, positions, q_weight, k_weight):
+    """Check the inputs: (device, code, leading axes, T, L, Hq, Hk, D, R, strides)."""
+    torch = _torch()
+    dev = _device_of(q)
+    code = _dtype_code(q, "q")
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be (T, heads, D) or (batch, L, heads, D)")
+    lead, (Hq, D) = tuple(q.shape[:-2]), q.shape[-2:]
+    if k is not None and k.dim() != q.dim():
+        raise ValueError("q and k must have the same number of axes")
+    Hk = 0 if k is None else k.shape[-2]
+    if k is not None and Hk < 1:
+        raise ValueError("k must have at least one head")
+    st = (_tokens(q, "q", lead, Hq, D, q.dtype, dev), 0 if k is None else _tokens(k, "k", lead, Hk, D, q.dtype, dev))
+    if k is None and k_weight is not None:
+        raise ValueError("k_weight needs a k")
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _check(t, name, (D,), torch.float32, dev)
+    R = 0
+    if freqs is not None:
+        if freqs.dim() != 1:
+            raise ValueError("freqs must have one axis")
+        R = 2 * freqs.shape[0]
+        _check(freqs, "freqs", tuple(freqs.shape), torch.float32, dev)
+    _check(positions, "positions", lead, torch.int32, dev)
+    T = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    return dev, code, lead, T, max(lead[-1], 1), Hq, Hk, D, R, st
+
+
+def mb_qk_norm_rope(q, k=None, freqs=None, positions=None, *, q_weight=None, k_weight=None, interleaved=False, eps=1e-5, q_out=None,
+                    k_out=None):
+    """Root-mean-square norm of every head of q (batch, L, Hq, D) or (T, Hq, D) and k (the same with Hk heads, or None),
+    times q_weight, k_weight (D,) float32 or None, then the rotation of the first 2 len(freqs)
+    columns by position * freqs (float32): pairs (2j, 2j+1) with interleaved, (j, j + len(freqs)) without.
+    positions: int32, shaped like a token, None: the place on the last token axis.  q and k float32 or
+    bfloat16, views with one stride between tokens allowed; q_out and k_out may be q and k themselves.
+    Returns (q_out, k_out)."""
+    dev, code, lead, T, L, Hq, Hk, D, R, st = _qk_args(q, k, freqs, positions, q_weight, k_weight)
+    out, so = [], []
+    for t, name, H in ((q_out, "q_out", Hq), (k_out, "k_out", Hk)):
+        if not H and name == "k_out":
+            if t is not None:
+                raise ValueError("k_out needs a k")
+            out.append(None)
+            so.append(0)
+            continue
+        t = q.new_empty(lead + (H, D)) if t is None else t
+        so.append(_tokens(t, name, lead, H, D, q.dtype, dev))
+        out.append(t)
+    _call_on(dev, "mb_qk_norm_rope", _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(freqs) if R else None, _ptr(positions),
+             _ptr(out[0]), _ptr(out[1]), T, L, Hq, Hk, D, R, *st, *so, int(bool(interleaved)), float(eps), code)
+    return tuple(out)
+
+
+def mb_qk_norm_rope_bwd(dq_out, dk_out, q, k=None, freqs=None, positions=None, *, q_weight=None, k_weight=None, interleaved=False,
+                        eps=1e-5, dq=None, dk=None, dq_weight=None, dk_weight=None, ws=None):
+    """Backward of mb_qk_norm_rope: dq_out, dk_out (contiguous, like q and k) the gradients of its outputs, q and k its
+    inputs.  Returns (dq, dk, dq_weight, dk_weight), None for what belongs to an argument that is None."""
+    torch = _torch()
+    dev, code, lead, T, L, Hq, Hk, D, R, st = _qk_args(q, k, freqs, positions, q_weight, k_weight)
+    if (dk_out is None) != (k is None):
+        raise ValueError("dk_out belongs to k")
+    out = []
+    _check(dq_out, "dq_out", lead + (Hq, D), q.dtype, dev)
+    _check(dk_out, "dk_out", lead + (Hk, D), q.dtype, dev)
+    for t, name, shp, d, there in ((dq, "dq", lead + (Hq, D), q.dtype, q), (dk, "dk", lead + (Hk, D), q.dtype, k),
+                                   (dq_weight, "dq_weight", (D,), torch.float32, q_weight),
+                                   (dk_weight, "dk_weight", (D,), torch.float32, k_weight)):
+        if there is None:
+            if t is not None:
+                raise ValueError("%s is the gradient of an argument that is None" % name)
+            out.append(None)
+        else:
+            out.append(q.new_empty(shp, dtype=d) if t is None else _check(t, name, shp, d, dev))
+    ws, nws = _scratch(MB_OP_QK_NORM_ROPE_BWD, dev, ws, (T, 1, Hq, D, Hk, 1, 1, 0)) if out[2] is not None or out[3] is not None else (None, 0)
+    _call_on(dev, "mb_qk_norm_rope_bwd", _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+             _ptr(freqs) if R else None, _ptr(positions), *[_ptr(t) for t in out], T, L, Hq, Hk, D, R, *st, int(bool(interleaved)),
+             float(eps), code, _ptr(ws), nws)
     return tuple(out)
 
 

@@ -75,6 +75,12 @@ size_t linear_attn_bwd_workspace(int64_t n_seq, int64_t T, int64_t H, int64_t G,
 size_t rms_norm_bwd_workspace(int64_t rows, int64_t D);
 size_t grad_clip_workspace(int64_t n);
 
+// Workspace bytes of the gated recurrence, forward and backward, and of the backward of the norm of queries and keys
+// (0 for unsupported sizes).
+size_t gated_scan_workspace(int64_t n_seq, int64_t T, int64_t D);
+size_t gated_scan_bwd_workspace(int64_t n_seq, int64_t T, int64_t D);
+size_t qk_norm_rope_bwd_workspace(int64_t T, int64_t Hq, int64_t Hk, int64_t D);
+
 // Copy h0 (or zeros) into h_out; used for zero-length sequences.
 mb_status copy_state(const float* h0, float* h_out, int64_t n, hipStream_t stream);
 

@@ -3274,6 +3274,10 @@ extern "C" size_t mb_workspace_size(mb_op op, int64_t batch, int64_t L, int64_t 
     // linear attention: (n_seq, T, H, Dv, G, Dk) travel as (batch, L, H, P, G, N)
     if (op == MB_OP_LINEAR_ATTN) return linear_attn_workspace(batch, L, H, G, N, P);
     if (op == MB_OP_LINEAR_ATTN_BWD) return linear_attn_bwd_workspace(batch, L, H, G, N, P);
+    // gated recurrence: (n_seq, T, D) travel as (batch, L, H); norm of queries and keys: (T, Hq, Hk, D) as (batch, H, G, P)
+    if (op == MB_OP_GATED_SCAN) return gated_scan_workspace(batch, L, H);
+    if (op == MB_OP_GATED_SCAN_BWD) return gated_scan_bwd_workspace(batch, L, H);
+    if (op == MB_OP_QK_NORM_ROPE_BWD) return qk_norm_rope_bwd_workspace(batch, H, G, P);
     // Mamba-1 scan: the sizes (batch, L, D, N) travel as (batch, L, H, N)
     if (op == MB_OP_SELECTIVE_SCAN) return m1_scan_workspace(batch, L, H, N);
     if (op == MB_OP_SSD_CHUNKED_BWD) return ssd_bwd_workspace(batch, L, H, P, G, N);
