@@ -2,14 +2,49 @@
 //
 //     s = sigma(a_gate + a_bias), la = -decay s, a = e^la, beta = sqrt(1 - a^2)
 //     b = beta sigma(x_gate + x_bias) x,  h_t = a_t h_{t-1} + b_t,  y = h
+//     backward: G_t = dy_t + a_{t+1} G_{t+1}, and every gradient a product of G_t and what the token's gates give
 //
-// A lane walks one channel of one sequence.
+// A span of tokens acts on the state that enters it as h -> e^S h + U, S the sum of its la, and two spans one behind the other as
+// (S1 + S2, e^S2 U1 + U2).  The tokens of all sequences, one after another, are cut into tiles of 128 (backward: 64)
+// tokens by 64 channels.  A workgroup reads its tile once, keeps a and b in registers, makes the tile's (S, U), hands it
+// to the tiles behind it, takes the state that enters from those in front, and walks its tokens a second time in registers:
+// one pass over memory, where cutting the sequence into a pass for end states and one for outputs reads everything twice.
+//
+// Handing on.  Workgroups take their tile from a counter, so that every tile in front of a taken one has been taken by a workgroup that
+// runs; a wait for a tile in front therefore ends.  A tile publishes (S, U) for each channel in one 64-bit store, which
+// readers poll until it is no longer the pattern that the first launch left there.  16 tiles make a group, whose last
+// tile also publishes the state behind it.  The state that enters a tile is composed of the state behind the group
+// before and the (S, U) of the group's tiles in front, always in this order: results do not depend on who came first.
+// Tiles in front of the one in which the first token's sequence starts are not looked at.
+#include <algorithm>
+#include <initializer_list>
+#include <type_traits>
+
 #include "mb_internal.h"
 
 namespace mb {
 namespace {
 
-constexpr int kEvery = 64;       // tokens between the rows of states
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+
+constexpr int kEvery = 64;                  // tokens between the rows of states
+constexpr int kCols = 64;                   // channels of a tile
+constexpr int kTile = 128, kTileBack = 64;  // its tokens, forward and backward
+constexpr int kGroup = 16;                  // tiles of a group
+constexpr uint64_t kNone = ~0ull;           // not published yet
+// Polls of one wait before it is given up (the result is NaN then): some seconds, which only a workspace
+// that something else writes to at the same time can bring about.
+constexpr int kPolls = 1 << 22;
+
+// What the tiles of one direction hand on to each other, in the workspace.
+struct Chain {
+    uint64_t* agg;       // (tiles, columns): (S, U) of a tile
+    uint32_t* incl;      // (groups, columns): the state behind a group
+    int* first;          // (tiles + 1): the last offset of cu at or before the tile's first token
+    uint32_t* ticket;
+};
 
 struct GsArgs {
     const void *x, *a, *g;
@@ -23,159 +58,821 @@ struct GsArgs {
     void* y;
     float *h_out, *states;
     const void* dy;
-    const float* dh_out;
+    const float *dh_out, *kept;
     void *dx, *da, *dg;
-    float* dh0;
-    float *before, *part;
+    float *dh0, *part;
     int n_seq, T, L, D;
+    int tiles, cols;     // tiles along the tokens, columns of tiles
+    Chain ch;
 };
 
+// ---------------------------------------------------------------- gates ----
+// Logarithms are held in base 2: x2 = la log2(e).
 struct Gate {
-    float s, la, a, b1, beta, i;     // b1 = 1 - a^2
+    float x2, a, less, beta;     // less = 1 - a^2
 };
 
-template <typename T>
-__device__ __forceinline__ Gate gate(const GsArgs& A, int64_t t, int c) {
+// e^la - 1 next to zero, from x2 = la log2(e): the series of 2^x - 1, off by x^6 / 5040 of itself at |la| = 1/4, 2^-24.3.
+// Further away 2^x - 1 loses two bits at most.
+__device__ __forceinline__ float less_one(float x2, float a) {
+    float p = fmaf(x2, 1.5403530394e-4f, 1.3333558146e-3f);
+    p = fmaf(x2, p, 9.6181291076e-3f);
+    p = fmaf(x2, p, 5.5504108665e-2f);
+    p = fmaf(x2, p, 2.4022650696e-1f);
+    p = fmaf(x2, p, 6.9314718056e-1f);
+    return x2 > -0.36f ? p * x2 : a - 1.0f;
+}
+
+// s: sigma of the gate; nd: -decay log2(e).
+__device__ __forceinline__ Gate gate(float s, float nd) {
     Gate r;
-    const float va = to_f32(((const T*)A.a)[t * A.a_ts + c]) + (A.a_bias ? A.a_bias[c] : 0.0f);
-    r.s = 1.0f / (1.0f + expf(-va));
-    r.la = -A.decay[c] * r.s;
-    const float e = expm1f(r.la);
-    r.a = expf(r.la);                 // 1 + e has lost the digits of a small a
-    r.b1 = -e * (2.0f + e);
-    r.beta = sqrtf(r.b1);
-    r.i = 1.0f;
-    if (A.g) r.i = 1.0f / (1.0f + expf(-(to_f32(((const T*)A.g)[t * A.g_ts + c]) + (A.x_bias ? A.x_bias[c] : 0.0f))));
+    r.x2 = nd * s;
+    r.a = exp2_fast(r.x2);
+    const float e = less_one(r.x2, r.a);
+    r.less = -e * (2.0f + e);
+    r.beta = __builtin_amdgcn_sqrtf(r.less);
     return r;
 }
 
-__device__ __forceinline__ void range(const GsArgs& A, int s, int& b, int& e) {
+// e^-(v + bias), nb = -bias log2(e)
+__device__ __forceinline__ float exp_minus(float v, float nb) { return exp2_fast(fmaf(v, -kLog2e, nb)); }
+__device__ __forceinline__ float sigma(float v, float nb) { return __builtin_amdgcn_rcpf(1.0f + exp_minus(v, nb)); }
+
+// sigma and 1 - sigma, both with all their digits.  The bound keeps e^-v finite (and NaN as it is).
+__device__ __forceinline__ void sigma2(float v, float nb, float& s, float& not_s) {
+    const float e = __builtin_elementwise_minimum(exp_minus(v, nb), 0x1p120f);
+    s = __builtin_amdgcn_rcpf(1.0f + e);
+    not_s = e * s;
+}
+
+// --------------------------------------------------------------- memory ----
+// Two channels beside each other, as they lie in memory.
+template <typename T> struct Raw;
+template <> struct Raw<bf16> { typedef uint32_t type; };
+template <> struct Raw<float> { typedef f2 type; };
+
+__device__ __forceinline__ float half_of(uint32_t v, int i) { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
+__device__ __forceinline__ float half_of(f2 v, int i) { return v[i]; }
+
+// `n` rows of a tile as a buffer: what lies outside reads zero.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* p, int64_t t0, int64_t ts, int n, int D) {
+    const uint32_t bytes = n > 0 ? (uint32_t)(n - 1) * (uint32_t)ts * sizeof(T) + (uint32_t)D * sizeof(T) : 0;
+    return __builtin_amdgcn_make_buffer_rsrc((void*)((const T*)p + t0 * ts), 0, (int)bytes, 0x00027000);
+}
+
+// PAIR: two channels start on a border of two elements.
+template <typename T, bool PAIR>
+__device__ __forceinline__ typename Raw<T>::type load2(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    if constexpr (sizeof(T) == 2) {
+        if constexpr (PAIR) return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+        const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+        const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off + 2, 0, 0);
+        return lo | hi << 16;
+    } else {
+        if constexpr (PAIR) return __builtin_bit_cast(f2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+        f2 v;
+        v[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+        v[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off + 4, 0, 0));
+        return v;
+    }
+}
+
+// The first `n` (1 or 2) of two channels; rounds to nearest even.
+template <typename T, bool PAIR>
+__device__ __forceinline__ void store2(__amdgpu_buffer_rsrc_t r, uint32_t off, float lo, float hi, int n) {
+    if constexpr (sizeof(T) == 2) {
+        const f2 v = {lo, hi};
+        const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));
+        if constexpr (PAIR) {
+            __builtin_amdgcn_raw_buffer_store_b32(w, r, off, 0, 0);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b16((short)(w & 0xffffu), r, off, 0, 0);
+            if (n > 1) __builtin_amdgcn_raw_buffer_store_b16((short)(w >> 16), r, off + 2, 0, 0);
+        }
+    } else {
+        if constexpr (PAIR) {
+            typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+            __builtin_amdgcn_raw_buffer_store_b64(u2{__float_as_uint(lo), __float_as_uint(hi)}, r, off, 0, 0);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lo), r, off, 0, 0);
+            if (n > 1) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(hi), r, off + 4, 0, 0);
+        }
+    }
+}
+
+// A barrier for what waves share through LDS: loads and stores to memory stay under way.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);          // lgkmcnt(0), no other counter
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// ------------------------------------------------------------ sequences ----
+__device__ __forceinline__ int offset_at(const GsArgs& A, int i) { return min(max(A.cu[i], 0), A.T); }
+
+// Tokens of sequence s.
+__device__ __forceinline__ void range_of(const GsArgs& A, int s, int& b, int& e) {
     if (A.cu) {
-        b = min(max(A.cu[s], 0), A.T);
-        e = min(max(A.cu[s + 1], 0), A.T);
+        b = offset_at(A, s);
+        e = offset_at(A, s + 1);
     } else {
         b = s * A.L;
         e = b + A.L;
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_gs_walk(GsArgs A) {
-    const int c = blockIdx.x * 256 + threadIdx.x, s = blockIdx.y;
-    if (c >= A.D) return;
-    int b, e;
-    range(A, s, b, e);
-    int64_t row = s;
-    if (A.slots) {
-        row = A.slots[s];
-        if (row < 0 || row >= A.n_slots) row = -1;
-    }
-    float h = A.h0 && row >= 0 && (!A.has_h0 || A.has_h0[s]) ? A.h0[row * A.D + c] : 0.0f;
-    for (int t = b; t < e; ++t) {
-        const Gate r = gate<T>(A, t, c);
-        if (A.states && t % kEvery == 0) A.states[(int64_t)(t / kEvery) * A.D + c] = h;
-        h = fmaf(r.a, h, r.beta * r.i * to_f32(((const T*)A.x)[t * A.x_ts + c]));
-        store_out((T*)A.y + (int64_t)t * A.D + c, h);
-    }
-    if (A.h_out && row >= 0) A.h_out[row * A.D + c] = h;
+// Row of h0 and h_out of a sequence, or -1 where it has none.
+__device__ __forceinline__ int row_of(const GsArgs& A, int s) {
+    if (!A.slots) return s;
+    const int r = A.slots[s];
+    return r >= 0 && r < A.n_slots ? r : -1;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_gs_back(GsArgs A) {
-    const int c = blockIdx.x * 256 + threadIdx.x, s = blockIdx.y;
-    if (c >= A.D) return;
-    int b, e;
-    range(A, s, b, e);
-    float h = A.h0 ? A.h0[(int64_t)s * A.D + c] : 0.0f;
-    for (int t = b; t < e; ++t) {
-        const Gate r = gate<T>(A, t, c);
-        A.before[(int64_t)t * A.D + c] = h;
-        h = fmaf(r.a, h, r.beta * r.i * to_f32(((const T*)A.x)[t * A.x_ts + c]));
-    }
-    float G = A.dh_out ? A.dh_out[(int64_t)s * A.D + c] : 0.0f;
-    float sd = 0.0f, sa = 0.0f, sx = 0.0f;
-    for (int t = e - 1; t >= b; --t) {
-        const Gate r = gate<T>(A, t, c);
-        const int64_t at = (int64_t)t * A.D + c;
-        const float x = to_f32(((const T*)A.x)[t * A.x_ts + c]);
-        G += to_f32(((const T*)A.dy)[at]);
-        const float bb = r.beta * r.i * x, root = r.b1 < 0x1p-120f ? 0.0f : bb / r.b1;
-        const float dla = G * (r.a * A.before[at] - r.a * r.a * root);
-        const float va = to_f32(((const T*)A.a)[t * A.a_ts + c]) + (A.a_bias ? A.a_bias[c] : 0.0f);
-        const float da = dla * r.la / (1.0f + expf(va));
-        store_out((T*)A.dx + at, G * r.beta * r.i);
-        store_out((T*)A.da + at, da);
-        sd -= dla * r.s;
-        sa += da;
-        if (A.g) {
-            const float vg = to_f32(((const T*)A.g)[t * A.g_ts + c]) + (A.x_bias ? A.x_bias[c] : 0.0f);
-            const float dg = G * bb / (1.0f + expf(vg));
-            store_out((T*)A.dg + at, dg);
-            sx += dg;
+// A tile's place, the same in all threads.
+struct Place {
+    int t0, n;           // first token, tokens
+    int sa, sb;          // sequences that may begin or end in it
+    int src;             // tile in which the first (backward: last) token's sequence begins (ends); its own: nothing enters
+    int lo, hi;          // its tokens that belong to a sequence
+    bool plain;          // all its tokens belong to one sequence that neither begins nor ends in it
+};
+
+template <int TT, bool BACK>
+__device__ __forceinline__ Place place(const GsArgs& A, int j) {
+    Place p;
+    p.t0 = j * TT;
+    p.n = min(A.T - p.t0, TT);
+    p.lo = 0;
+    p.hi = p.n;
+    p.src = j;
+    const int end = p.t0 + p.n;
+    if (A.cu) {
+        int f0 = -1, f1 = A.n_seq;
+        if (A.tiles > 1) {
+            f0 = A.ch.first[j];
+            f1 = A.ch.first[j + 1];
         }
-        G *= r.a;
+        p.sa = j == 0 ? 0 : max(f0, 0);
+        p.sb = min(f1, A.n_seq - 1);
+        p.plain = f0 == f1 && f0 >= 0 && f0 < A.n_seq && offset_at(A, f0) < p.t0 && p.n == TT;
+        if (!p.plain) {
+            p.lo = max(offset_at(A, 0) - p.t0, 0);
+            p.hi = min(offset_at(A, A.n_seq) - p.t0, p.n);
+        }
+        if constexpr (BACK) {
+            // the sequence of the last token: f1, but where it begins right behind the tile
+            if (j + 1 < A.tiles && f1 >= 0) {
+                int s = f1;
+                if (offset_at(A, f1) >= end) s = -1;      // another one begins there: the last token ends its own
+                if (s >= 0 && s < A.n_seq) p.src = max((offset_at(A, s + 1) - 1) / TT, j);
+            }
+        } else if (f0 >= 0 && f0 < A.n_seq) {
+            p.src = min(offset_at(A, f0) / TT, j);
+        }
+    } else if (A.L == 0) {
+        p.sa = 0;
+        p.sb = A.n_seq - 1;
+        p.plain = false;
+    } else {
+        p.sa = p.t0 / A.L;
+        p.sb = (end - 1) / A.L;
+        p.plain = p.sa == p.sb && p.sa * A.L < p.t0 && (p.sb + 1) * (int64_t)A.L > end && p.n == TT;
+        p.src = BACK ? (int)(((p.sb + 1) * (int64_t)A.L - 1) / TT) : p.sa * A.L / TT;
     }
-    if (A.dh0) A.dh0[(int64_t)s * A.D + c] = G;
-    float* p = A.part + (int64_t)s * 3 * A.D + c;
-    p[0] = sd;
-    p[A.D] = sa;
-    p[2 * (int64_t)A.D] = sx;
+    return p;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_gs_clear(GsArgs A) {
-    const int64_t t = blockIdx.x;
-    const int b = A.n_seq ? min(max(A.cu[0], 0), A.T) : A.T, e = min(max(A.cu[A.n_seq], 0), A.T);
-    if (t >= b && t < e) return;
-    for (int c = threadIdx.x; c < A.D; c += 256) {
-        const int64_t at = t * A.D + c;
-        store_out((T*)A.dx + at, 0.0f);
-        store_out((T*)A.da + at, 0.0f);
-        if (A.g) store_out((T*)A.dg + at, 0.0f);
+// Where sequences begin and end in a tile: for each token -2, or the row of the sequence (-1: none) that it is the first or the last of.
+template <int TT>
+struct Events {
+    int begin[TT], end[TT];
+};
+
+// Fills them in (a barrier on either side is the caller's) and settles the sequences of no tokens: `from` rows, or
+// zeros, go to `to`.  BACK: rows are the sequences' numbers.
+template <int TT, int NT, bool BACK>
+__device__ __forceinline__ void find_events(const GsArgs& A, const Place& p, Events<TT>& ev, int c, int n, const float* from, float* to) {
+    const int lane = threadIdx.x & 31;
+    for (int s = p.sa + (int)(threadIdx.x >> 5); s <= p.sb; s += NT / 32) {
+        int b, e;
+        range_of(A, s, b, e);
+        const int row = BACK ? s : row_of(A, s);
+        const bool has = BACK || (row >= 0 && A.h0 && (!A.has_h0 || A.has_h0[s]));
+        if (b < e) {
+            if (lane == 0) {
+                if (b >= p.t0 && b < p.t0 + p.n) ev.begin[b - p.t0] = has ? row : -1;
+                if (e > p.t0 && e <= p.t0 + p.n) ev.end[e - 1 - p.t0] = row;
+            }
+        } else if (to && row >= 0) {
+            for (int i = 0; i < n; ++i) {
+                const int64_t at = (int64_t)row * A.D + c + i;
+                to[at] = from && has ? from[at] : 0.0f;
+            }
+        }
     }
 }
 
-__global__ void __launch_bounds__(256) k_gs_sums(const float* part, int n, int D, float* d0, float* d1, float* d2) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= D) return;
-    float s[3] = {0.0f, 0.0f, 0.0f};
-    for (int i = 0; i < n; ++i)
-        for (int k = 0; k < 3; ++k) s[k] += part[((int64_t)i * 3 + k) * D + c];
-    if (d0) d0[c] = s[0];
-    if (d1) d1[c] = s[1];
-    if (d2) d2[c] = s[2];
+// -------------------------------------------------------------- handing on ----
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ uint32_t peek(const uint32_t* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// One NaN for all: none looks like kNone.
+__device__ __forceinline__ uint32_t plain_bits(float v) { return v == v ? __float_as_uint(v) : 0x7fc00000u; }
+
+__device__ __forceinline__ void publish(const GsArgs& A, int j, int c, float S, float U) {
+    const uint64_t w = (uint64_t)plain_bits(S) | (uint64_t)plain_bits(U) << 32;
+    __hip_atomic_store(A.ch.agg + (int64_t)j * A.cols * kCols + c, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_gs_step(GsArgs A, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n * A.D) return;
-    const int64_t r = i / A.D;
-    const int c = (int)(i - r * A.D);
-    int64_t row = r;
+__device__ __forceinline__ void publish_state(const GsArgs& A, int group, int c, float h) {
+    __hip_atomic_store(A.ch.incl + (int64_t)group * A.cols * kCols + c, plain_bits(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// What enters tile j of the chain (tiles counted in walking order), in one wave, a channel a lane.  src: the tile whose own U
+// starts it.  A tile's group is looked at as a whole: all its words are under way at a time.
+__device__ __forceinline__ float entering(const GsArgs& A, int j, int src, int c) {
+    const int group = j / kGroup, lo = max(src, group * kGroup);
+    const int64_t row = (int64_t)A.cols * kCols;
+    const uint64_t* agg = A.ch.agg + lo * row + c;
+    uint64_t w[kGroup - 1];
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i) w[i] = lo + i < j ? peek(agg + i * row) : 0;
+    float h = 0.0f;
+    int polls = 0;
+    if (src < lo) {
+        const uint32_t* p = A.ch.incl + (group - 1) * row + c;
+        uint32_t v = peek(p);
+        while (v == (uint32_t)kNone && ++polls < kPolls) {
+            __builtin_amdgcn_s_sleep(1);
+            v = peek(p);
+        }
+        h = __uint_as_float(v);
+    }
+#pragma unroll
+    for (int i = 0; i < kGroup - 1; ++i) {
+        if (lo + i < j) {
+            while (w[i] == kNone && ++polls < kPolls) {
+                __builtin_amdgcn_s_sleep(1);
+                w[i] = peek(agg + i * row);
+            }
+            const float U = __uint_as_float((uint32_t)(w[i] >> 32));
+            h = src == lo + i ? U : fmaf(exp2_fast(__uint_as_float((uint32_t)w[i])), h, U);
+        }
+    }
+    return h;
+}
+
+// Clears what the chains hand on and finds every tile's place among the offsets.
+struct Setup {
+    Chain ch[2];
+    int tiles[2], tokens[2];     // 0 tiles: no chain
+    const int32_t* cu;
+    int n_seq, T, columns;
+};
+
+__global__ void __launch_bounds__(256) k_gs_setup(Setup S) {
+    const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (S.tiles[k] < 2) continue;
+        const int64_t words = (int64_t)S.tiles[k] * S.columns, states = (int64_t)((S.tiles[k] + kGroup - 1) / kGroup) * S.columns;
+        for (int64_t i = i0; i < words; i += step) S.ch[k].agg[i] = kNone;
+        for (int64_t i = i0; i < states; i += step) S.ch[k].incl[i] = (uint32_t)kNone;
+        if (i0 == 0) *S.ch[k].ticket = 0;
+        if (S.cu)
+            for (int64_t i = i0; i <= S.tiles[k]; i += step) {
+                const int64_t t = i * S.tokens[k];
+                int lo = 0, hi = S.n_seq + 1;              // offsets at or before t
+                while (lo < hi) {
+                    const int m = (lo + hi) >> 1;
+                    if (min(max(S.cu[m], 0), S.T) <= t) lo = m + 1;
+                    else hi = m;
+                }
+                S.ch[k].first[i] = lo - 1;
+            }
+    }
+}
+
+// The next tile of the launch: its number in walking order and its column.
+__device__ __forceinline__ void take_tile(const GsArgs& A, int* shared, int& j, int& col) {
+    if (A.tiles == 1) {
+        j = 0;
+        col = blockIdx.x;
+        return;
+    }
+    if (threadIdx.x == 0) *shared = (int)__hip_atomic_fetch_add(A.ch.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    const int t = __builtin_amdgcn_readfirstlane(*shared);
+    j = t / A.cols;
+    col = t - j * A.cols;
+}
+
+// -------------------------------------------------------------- forward ----
+// A thread holds K tokens of two channels; 32 threads side by side make a group's rows of 64 channels, NT / 32 groups the tile.
+// OUT: outputs and end states are written; otherwise the states for the backward alone.
+template <typename T, bool PAIR, int K, bool OUT>
+__global__ void __launch_bounds__(kTile / K * 32) k_gs_forward(GsArgs A) {
+    constexpr int NG = kTile / K, NT = NG * 32;
+    __shared__ f2 comp[NG][kCols];
+    __shared__ float entry[NG][kCols];
+    __shared__ Events<kTile> ev;
+    __shared__ int taken;
+    int j, col;
+    take_tile(A, &taken, j, col);
+    const Place p = place<kTile, false>(A, j);
+    const int c = col * kCols + (threadIdx.x & 31) * 2, grp = threadIdx.x >> 5;
+    const int live = min(max(A.D - c, 0), 2);              // channels of this thread
+    typename Raw<T>::type rx[K], ra[K], rg[K];
+    {
+        const __amdgpu_buffer_rsrc_t bx = rows_at<T>(A.x, p.t0, A.x_ts, p.n, A.D), ba = rows_at<T>(A.a, p.t0, A.a_ts, p.n, A.D);
+        const uint32_t sx = (uint32_t)A.x_ts * sizeof(T), sa = (uint32_t)A.a_ts * sizeof(T);
+        const uint32_t ox = grp * K * sx + c * sizeof(T), oa = grp * K * sa + c * sizeof(T);
+#pragma unroll
+        for (int k = 0; k < K; ++k) ra[k] = load2<T, PAIR>(ba, oa + k * sa);
+#pragma unroll
+        for (int k = 0; k < K; ++k) rx[k] = load2<T, PAIR>(bx, ox + k * sx);
+        if (A.g) {
+            const __amdgpu_buffer_rsrc_t bg = rows_at<T>(A.g, p.t0, A.g_ts, p.n, A.D);
+            const uint32_t sg = (uint32_t)A.g_ts * sizeof(T), og = grp * K * sg + c * sizeof(T);
+#pragma unroll
+            for (int k = 0; k < K; ++k) rg[k] = load2<T, PAIR>(bg, og + k * sg);
+        }
+    }
+    float nd[2], nab[2], nxb[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool in = i < live;
+        nd[i] = in ? -A.decay[c + i] * kLog2e : 0.0f;
+        nab[i] = in && A.a_bias ? -A.a_bias[c + i] * kLog2e : 0.0f;
+        nxb[i] = in && A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f;
+    }
+    if (!p.plain) {
+        for (int i = threadIdx.x; i < kTile; i += NT) ev.begin[i] = ev.end[i] = -2;
+        lds_barrier();
+        find_events<kTile, NT, false>(A, p, ev, c, live, A.h0, OUT ? A.h_out : nullptr);
+        lds_barrier();
+    }
+    const auto state0 = [&](int row, int i) { return row >= 0 && i < live ? A.h0[(int64_t)row * A.D + c + i] : 0.0f; };
+
+    float a[K][2], b[K][2];
+    f2 S[2];                               // (S, U) of this thread's tokens
+#pragma unroll
+    for (int i = 0; i < 2; ++i) S[i] = f2{0.0f, 0.0f};
+    bool cut = false;                      // a sequence begins among them: what enters is lost
+    const auto gates = [&](auto plain) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            int row = -2;
+            if constexpr (!decltype(plain)::value) row = ev.begin[grp * K + k];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const Gate q = gate(sigma(half_of(ra[k], i), nab[i]), nd[i]);
+                const float x = half_of(rx[k], i);
+                a[k][i] = q.a;
+                b[k][i] = q.beta * (A.g ? sigma(half_of(rg[k], i), nxb[i]) * x : x);
+                if (row != -2) {
+                    // The only read of h0: a row that is updated in place may be written by the thread that holds its last token.
+                    const float h0 = state0(row, i);
+                    if (k == 0 && A.states && i < live && (grp * K) % kEvery == 0) A.states[(int64_t)((p.t0 + grp * K) / kEvery) * A.D + c + i] = h0;
+                    b[k][i] = fmaf(q.a, h0, b[k][i]);
+                    S[i] = f2{0.0f, b[k][i]};
+                    cut = true;
+                } else {
+                    S[i] = f2{S[i][0] + q.x2, fmaf(q.a, S[i][1], b[k][i])};
+                }
+            }
+        }
+    };
+    if (p.plain) gates(std::true_type{});
+    else gates(std::false_type{});
+    // a logarithm above zero marks what is cut off from the state that enters
+    *reinterpret_cast<f4*>(&comp[grp][(threadIdx.x & 31) * 2]) = f4{cut ? 1.0f : S[0][0], S[0][1], cut ? 1.0f : S[1][0], S[1][1]};
+    lds_barrier();
+    if (threadIdx.x < kCols) {
+        const int at = col * kCols + threadIdx.x;
+        float E[NG], U[NG], St = 0.0f, Ut = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const f2 v = comp[i][threadIdx.x];
+            const bool off = v[0] > 0.0f;
+            E[i] = off ? -1.0f : exp2_fast(v[0]);
+            U[i] = v[1];
+            St += off ? 0.0f : v[0];
+            Ut = off ? U[i] : fmaf(E[i], Ut, U[i]);
+        }
+        float h = 0.0f;
+        if (A.tiles > 1) {
+            publish(A, j, at, St, Ut);
+            if (p.src < j) h = entering(A, j, p.src, at);
+        }
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            entry[i][threadIdx.x] = h;
+            h = E[i] < 0.0f ? U[i] : fmaf(E[i], h, U[i]);
+        }
+        if (A.tiles > 1 && j % kGroup == kGroup - 1) publish_state(A, j / kGroup, at, h);
+    }
+    lds_barrier();
+    float h[2] = {entry[grp][(threadIdx.x & 31) * 2], entry[grp][(threadIdx.x & 31) * 2 + 1]};
+    const __amdgpu_buffer_rsrc_t by = rows_at<T>(A.y, p.t0, A.D, OUT ? p.n : 0, A.D);
+    const uint32_t sy = (uint32_t)A.D * sizeof(T), oy = grp * K * sy + c * sizeof(T);
+    const auto walk = [&](auto plain) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int t = grp * K + k;
+            int begin = -2, end = -2;
+            if constexpr (!decltype(plain)::value) {
+                begin = ev.begin[t];
+                end = ev.end[t];
+            }
+            if (k == 0 && A.states && (grp * K) % kEvery == 0 && t < p.n && begin == -2) {
+                float* s = A.states + (int64_t)((p.t0 + t) / kEvery) * A.D + c;
+                if (live > 0) s[0] = h[0];
+                if (live > 1) s[1] = h[1];
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) h[i] = begin != -2 ? b[k][i] : fmaf(a[k][i], h[i], b[k][i]);
+            if constexpr (OUT) {
+                if (live > 0 && (decltype(plain)::value || (t >= p.lo && t < p.hi))) store2<T, PAIR>(by, oy + k * sy, h[0], h[1], live);
+                if (end >= 0 && A.h_out) {
+                    float* o = A.h_out + (int64_t)end * A.D + c;
+                    if (live > 0) o[0] = h[0];
+                    if (live > 1) o[1] = h[1];
+                }
+            }
+        }
+    };
+    if (p.plain) walk(std::true_type{});
+    else walk(std::false_type{});
+}
+
+// ------------------------------------------------------------- backward ----
+// Tiles from the last to the first.  A tile needs the state that enters it, which the forward kept for every 64th token, and
+// the gradient that comes back out of the tiles behind, handed on like the states forward.  The tokens are walked three times in
+// registers: forward and back for what the tile hands on, forward for h_{t-1}, back for G and the gradients.
+template <typename T, bool PAIR, int K>
+__global__ void __launch_bounds__(kTileBack / K * 32) k_gs_backward(GsArgs A) {
+    constexpr int NG = kTileBack / K, NT = NG * 32;
+    __shared__ f4 comp[NG][kCols];          // of every group: (S, U) forward, (S, V) backward
+    __shared__ f2 entry[NG][kCols];         // the state in front of it, the gradient from behind it
+    __shared__ Events<kTileBack> ev;
+    __shared__ int taken;
+    static_assert(kTileBack == kEvery, "a tile starts from a kept state");
+    int jr, col;
+    take_tile(A, &taken, jr, col);
+    const int j = A.tiles - 1 - jr;
+    const Place p = place<kTileBack, true>(A, j);
+    const int c2 = (threadIdx.x & 31) * 2, c = col * kCols + c2, grp = threadIdx.x >> 5;
+    const int live = min(max(A.D - c, 0), 2);
+    typename Raw<T>::type rx[K], ra[K], rg[K], rd[K];
+    {
+        const __amdgpu_buffer_rsrc_t bx = rows_at<T>(A.x, p.t0, A.x_ts, p.n, A.D), ba = rows_at<T>(A.a, p.t0, A.a_ts, p.n, A.D);
+        const __amdgpu_buffer_rsrc_t bd = rows_at<T>(A.dy, p.t0, A.D, p.n, A.D);
+        const uint32_t sx = (uint32_t)A.x_ts * sizeof(T), sa = (uint32_t)A.a_ts * sizeof(T), sd = (uint32_t)A.D * sizeof(T);
+        const uint32_t ox = grp * K * sx + c * sizeof(T), oa = grp * K * sa + c * sizeof(T), od = grp * K * sd + c * sizeof(T);
+#pragma unroll
+        for (int k = 0; k < K; ++k) ra[k] = load2<T, PAIR>(ba, oa + k * sa);
+#pragma unroll
+        for (int k = 0; k < K; ++k) rx[k] = load2<T, PAIR>(bx, ox + k * sx);
+        if (A.g) {
+            const __amdgpu_buffer_rsrc_t bg = rows_at<T>(A.g, p.t0, A.g_ts, p.n, A.D);
+            const uint32_t sg = (uint32_t)A.g_ts * sizeof(T), og = grp * K * sg + c * sizeof(T);
+#pragma unroll
+            for (int k = 0; k < K; ++k) rg[k] = load2<T, PAIR>(bg, og + k * sg);
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k) rd[k] = load2<T, PAIR>(bd, od + k * sd);
+    }
+    float nd[2], nab[2], nxb[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool in = i < live;
+        nd[i] = in ? -A.decay[c + i] * kLog2e : 0.0f;
+        nab[i] = in && A.a_bias ? -A.a_bias[c + i] * kLog2e : 0.0f;
+        nxb[i] = in && A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f;
+    }
+    if (!p.plain) {
+        for (int i = threadIdx.x; i < kTileBack; i += NT) ev.begin[i] = ev.end[i] = -2;
+        lds_barrier();
+        find_events<kTileBack, NT, true>(A, p, ev, c, live, A.dh_out, A.dh0);
+        lds_barrier();
+    }
+    const auto row_value = [&](const float* q, int row, int i) { return q && row >= 0 && i < live ? q[(int64_t)row * A.D + c + i] : 0.0f; };
+
+    // of every token: a, b, beta i, a^2 b / (1 - a^2) and then dla / G, s, la (1 - s), b (1 - i)
+    float a[K][2], b[K][2], bi[K][2], r[K][2], s[K][2], w[K][2], bn[K][2];
+    float S[2] = {0.0f, 0.0f}, U[2] = {0.0f, 0.0f}, V[2] = {0.0f, 0.0f};
+    bool cut = false, cut_back = false;
+    const auto gates = [&](auto plain) {
+        constexpr bool P = decltype(plain)::value;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int row = P ? -2 : ev.begin[grp * K + k];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float not_s, ig = 1.0f, not_i = 0.0f;
+                sigma2(half_of(ra[k], i), nab[i], s[k][i], not_s);
+                const Gate q = gate(s[k][i], nd[i]);
+                if (A.g) sigma2(half_of(rg[k], i), nxb[i], ig, not_i);
+                a[k][i] = q.a;
+                bi[k][i] = q.beta * ig;
+                b[k][i] = bi[k][i] * half_of(rx[k], i);
+                bn[k][i] = b[k][i] * not_i;
+                w[k][i] = q.x2 * 0.69314718056f * not_s;
+                const float root = q.a * q.a * b[k][i] * __builtin_amdgcn_rcpf(q.less);
+                r[k][i] = q.less < 0x1p-120f ? 0.0f : root;
+                S[i] += q.x2;
+                if (row != -2) {
+                    U[i] = fmaf(q.a, row_value(A.h0, row, i), b[k][i]);
+                    cut = true;
+                } else {
+                    U[i] = fmaf(q.a, U[i], b[k][i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k) {
+            const int row = P ? -2 : ev.end[grp * K + k];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (row != -2) {
+                    V[i] = row_value(A.dh_out, row, i);
+                    cut_back = true;
+                }
+                V[i] = a[k][i] * (half_of(rd[k], i) + V[i]);
+            }
+        }
+    };
+    if (p.plain) gates(std::true_type{});
+    else gates(std::false_type{});
+#pragma unroll
+    for (int i = 0; i < 2; ++i) comp[grp][c2 + i] = f4{cut ? 1.0f : S[i], U[i], cut_back ? 1.0f : S[i], V[i]};
+    lds_barrier();
+    if (threadIdx.x < kCols) {
+        const int at = col * kCols + threadIdx.x, src = A.tiles - 1 - p.src;
+        float E[NG], v[NG], St = 0.0f, Vt = 0.0f;
+#pragma unroll
+        for (int i = NG - 1; i >= 0; --i) {
+            const f4 q = comp[i][threadIdx.x];
+            const bool off = q[2] > 0.0f;
+            E[i] = off ? -1.0f : exp2_fast(q[2]);
+            v[i] = q[3];
+            St += off ? 0.0f : q[2];
+            Vt = off ? v[i] : fmaf(E[i], Vt, v[i]);
+        }
+        float g = 0.0f;
+        if (A.tiles > 1) {
+            publish(A, jr, at, St, Vt);
+            if (src < jr) g = entering(A, jr, src, at);
+        }
+#pragma unroll
+        for (int i = NG - 1; i >= 0; --i) {
+            entry[i][threadIdx.x][1] = g;
+            g = E[i] < 0.0f ? v[i] : fmaf(E[i], g, v[i]);
+        }
+        if (A.tiles > 1 && jr % kGroup == kGroup - 1) publish_state(A, jr / kGroup, at, g);
+    } else if (threadIdx.x < 2 * kCols) {
+        const int lane = threadIdx.x - kCols, at = col * kCols + lane;
+        float h = at < A.D && p.n > 0 ? A.kept[(int64_t)j * A.D + at] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            const f4 q = comp[i][lane];
+            entry[i][lane][0] = h;
+            h = q[0] > 0.0f ? q[1] : fmaf(exp2_fast(q[0]), h, q[1]);
+        }
+    }
+    lds_barrier();
+    float h[2], g[2], sum[3][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        h[i] = entry[grp][c2 + i][0];
+        g[i] = entry[grp][c2 + i][1];
+        sum[0][i] = sum[1][i] = sum[2][i] = 0.0f;
+    }
+    const __amdgpu_buffer_rsrc_t bdx = rows_at<T>(A.dx, p.t0, A.D, p.n, A.D), bda = rows_at<T>(A.da, p.t0, A.D, p.n, A.D);
+    const __amdgpu_buffer_rsrc_t bdg = rows_at<T>(A.dg, p.t0, A.D, A.g ? p.n : 0, A.D);
+    const uint32_t sd = (uint32_t)A.D * sizeof(T), od = grp * K * sd + c * sizeof(T);
+    const auto walk = [&](auto plain) {
+        constexpr bool P = decltype(plain)::value;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int row = P ? -2 : ev.begin[grp * K + k];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (row != -2) h[i] = row_value(A.h0, row, i);
+                r[k][i] = fmaf(a[k][i], h[i], -r[k][i]);
+                h[i] = fmaf(a[k][i], h[i], b[k][i]);
+            }
+        }
+#pragma unroll
+        for (int k = K - 1; k >= 0; --k) {
+            const int t = grp * K + k;
+            const int begin = P ? -2 : ev.begin[t], end = P ? -2 : ev.end[t];
+            const bool in = P || (t >= p.lo && t < p.hi);
+            float dx[2], da[2], dg[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (end != -2) g[i] = row_value(A.dh_out, end, i);
+                const float G = half_of(rd[k], i) + g[i];
+                g[i] = a[k][i] * G;
+                const float dla = in ? G * r[k][i] : 0.0f;
+                dx[i] = in ? G * bi[k][i] : 0.0f;
+                dg[i] = in ? G * bn[k][i] : 0.0f;
+                da[i] = in ? dla * w[k][i] : 0.0f;
+                sum[0][i] = in ? fmaf(-dla, s[k][i], sum[0][i]) : sum[0][i];
+                sum[1][i] += da[i];
+                sum[2][i] += dg[i];
+                if (begin >= 0 && A.dh0 && i < live) A.dh0[(int64_t)begin * A.D + c + i] = g[i];
+            }
+            if (live > 0) {
+                store2<T, PAIR>(bdx, od + k * sd, dx[0], dx[1], live);
+                store2<T, PAIR>(bda, od + k * sd, da[0], da[1], live);
+                if (A.g) store2<T, PAIR>(bdg, od + k * sd, dg[0], dg[1], live);
+            }
+        }
+    };
+    if (p.plain) walk(std::true_type{});
+    else walk(std::false_type{});
+    if (!A.part) return;
+    float (*red)[3][kCols] = reinterpret_cast<float (*)[3][kCols]>(&comp[0][0]);       // comp has been read
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) red[grp][q][c2 + i] = sum[q][i];
+    lds_barrier();
+    for (int i = threadIdx.x; i < 3 * kCols; i += NT) {
+        float v = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) v += red[n][i / kCols][i % kCols];
+        A.part[((int64_t)j * 3 + i / kCols) * A.cols * kCols + col * kCols + i % kCols] = v;
+    }
+}
+
+// The sums over tokens of ddecay, da_bias and dx_bias from the tiles' shares: a workgroup adds up 64 columns of one of them, its 16
+// groups of lanes dealing the tiles out.
+__global__ void __launch_bounds__(1024) k_gs_sums(const float* __restrict__ part, int tiles, int cols, int D, float* d0, float* d1, float* d2) {
+    __shared__ float red[16][kCols];
+    const int which = blockIdx.y, lane = threadIdx.x & 63, grp = threadIdx.x >> 6, c = blockIdx.x * kCols + lane;
+    float* d = which == 0 ? d0 : which == 1 ? d1 : d2;
+    if (!d) return;
+    const int64_t row = (int64_t)cols * kCols;
+    float s = 0.0f;
+    for (int i = grp; i < tiles; i += 16 * 8) {
+        float t[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = i + 16 * k < tiles ? part[((int64_t)(i + 16 * k) * 3 + which) * row + c] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += t[k];
+    }
+    red[grp][lane] = s;
+    __syncthreads();
+    if (grp == 0 && c < D) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += red[i][lane];
+        d[c] = s;
+    }
+}
+
+// ----------------------------------------------------------------- step ----
+// Two channels of one sequence a thread.
+template <typename T, bool PAIR>
+__global__ void __launch_bounds__(256) k_gs_step(GsArgs A, int64_t n0, int blocks) {
+    const int64_t n = n0 + blockIdx.x / blocks;
+    const int c = ((int)(blockIdx.x % blocks) * 256 + threadIdx.x) * 2, live = min(A.D - c, 2);
+    if (live <= 0) return;
+    const __amdgpu_buffer_rsrc_t bx = rows_at<T>(A.x, n, A.x_ts, 1, A.D), ba = rows_at<T>(A.a, n, A.a_ts, 1, A.D);
+    const __amdgpu_buffer_rsrc_t bg = rows_at<T>(A.g, n, A.g_ts, A.g ? 1 : 0, A.D), by = rows_at<T>(A.y, n, A.D, 1, A.D);
+    const auto rx = load2<T, PAIR>(bx, c * sizeof(T)), ra = load2<T, PAIR>(ba, c * sizeof(T)), rg = load2<T, PAIR>(bg, c * sizeof(T));
+    int64_t row = n;
     if (A.slots) {
-        row = A.slots[r];
+        row = A.slots[n];
         if (row < 0 || row >= A.n_slots) row = -1;
     }
-    const Gate q = gate<T>(A, r, c);
-    const float h0 = A.h0 && row >= 0 ? A.h0[row * A.D + c] : 0.0f;
-    const float h = fmaf(q.a, h0, q.beta * q.i * to_f32(((const T*)A.x)[r * A.x_ts + c]));
-    store_out((T*)A.y + i, h);
-    if (row >= 0) A.h_out[row * A.D + c] = h;
+    float h[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        h[i] = 0.0f;
+        if (i < live) {
+            if (A.h0 && row >= 0) h[i] = A.h0[row * A.D + c + i];
+            const Gate q = gate(sigma(half_of(ra, i), A.a_bias ? -A.a_bias[c + i] * kLog2e : 0.0f), -A.decay[c + i] * kLog2e);
+            const float x = half_of(rx, i);
+            const float u = A.g ? sigma(half_of(rg, i), A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f) * x : x;
+            h[i] = fmaf(q.a, h[i], q.beta * u);
+            if (row >= 0) A.h_out[row * A.D + c + i] = h[i];
+        }
+    }
+    store2<T, PAIR>(by, c * sizeof(T), h[0], h[1], live);
 }
 
 // ------------------------------------------------------------------ host ----
-constexpr int kTile = 128, kCols = 64;      // tokens and channels of a tile
-
 bool sizes_ok(int64_t n_seq, int64_t T, int64_t D) {
     if (n_seq < 0 || T < 0 || D < 1 || D >= 1 << 22 || n_seq > 1 << 20 || T >= (int64_t)1 << 31) return false;
-    return ((T + kTile - 1) / kTile) * ((D + kCols - 1) / kCols) < (int64_t)1 << 24;
+    return ((T + kTileBack - 1) / kTileBack) * ((D + kCols - 1) / kCols) < (int64_t)1 << 23;
 }
 
 bool stride_ok(int64_t s, int64_t D) { return s >= D && s < 1 << 22; }
 
 size_t span_of(int64_t tokens, int64_t stride, int64_t row, size_t es) {
     return tokens > 0 ? ((size_t)(tokens - 1) * stride + row) * es : 0;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+int64_t tiles_of(int64_t T, int tokens) { return T > 0 ? (T + tokens - 1) / tokens : 1; }
+int64_t columns_of(int64_t D) { return (D + kCols - 1) / kCols * kCols; }
+
+// Where a chain's parts lie in the workspace from `at` on; returns the bytes it takes (none for one tile).
+size_t lay_out(Chain* ch, char* at, int64_t tiles, int64_t columns) {
+    if (tiles < 2) return 0;
+    const size_t agg = up256((size_t)tiles * columns * 8), incl = up256((size_t)((tiles + kGroup - 1) / kGroup) * columns * 4);
+    const size_t first = up256((size_t)(tiles + 1) * 4);
+    if (ch) {
+        ch->agg = (uint64_t*)at;
+        ch->incl = (uint32_t*)(at + agg);
+        ch->first = (int*)(at + agg + incl);
+        ch->ticket = (uint32_t*)(at + agg + incl + first);
+    }
+    return agg + incl + first + 256;
+}
+
+// The backward's workspace: both chains, the tiles' shares of the sums, the states where they are made again.
+struct BackPlan {
+    int64_t tiles, tiles_back, columns;
+    size_t back_at, part_at, states_at, bytes;
+};
+
+BackPlan back_plan(int64_t T, int64_t D) {
+    BackPlan b;
+    b.tiles = tiles_of(T, kTile);
+    b.tiles_back = tiles_of(T, kTileBack);
+    b.columns = columns_of(D);
+    b.back_at = lay_out(nullptr, nullptr, b.tiles, b.columns);
+    b.part_at = b.back_at + lay_out(nullptr, nullptr, b.tiles_back, b.columns);
+    b.states_at = b.part_at + up256((size_t)b.tiles_back * 3 * b.columns * 4);
+    b.bytes = b.states_at + up256((size_t)((T + kEvery - 1) / kEvery) * D * 4);
+    return b;
+}
+
+template <typename T>
+bool pairs_ok(const GsArgs& A, std::initializer_list<const void*> more) {
+    constexpr uintptr_t M = 2 * sizeof(T) - 1;
+    bool ok = A.D % 2 == 0 && A.x_ts % 2 == 0 && A.a_ts % 2 == 0 && (!A.g || A.g_ts % 2 == 0) && !((uintptr_t)A.x & M) && !((uintptr_t)A.a & M) &&
+              !((uintptr_t)A.g & M);
+    for (const void* p : more) ok = ok && !((uintptr_t)p & M);
+    return ok;
+}
+
+mb_status launch_setup(const GsArgs& A, const Chain& fwd, int64_t tiles, const Chain& back, int64_t tiles_back, hipStream_t s) {
+    Setup S{};
+    S.ch[0] = fwd;
+    S.ch[1] = back;
+    S.tiles[0] = (int)tiles;
+    S.tiles[1] = (int)tiles_back;
+    S.tokens[0] = kTile;
+    S.tokens[1] = kTileBack;
+    S.cu = A.cu;
+    S.n_seq = A.n_seq;
+    S.T = A.T;
+    S.columns = A.cols * kCols;
+    const int64_t most = std::max(tiles, tiles_back);
+    if (most < 2) return MB_OK;
+    const int64_t words = most * S.columns;
+    hipLaunchKernelGGL(k_gs_setup, dim3((unsigned)std::min<int64_t>((words + 1023) / 1024, 1024)), dim3(256), 0, s, S);
+    return check_launch();
+}
+
+template <typename T, bool OUT>
+mb_status run_forward(const GsArgs& A, hipStream_t s) {
+    constexpr int K = sizeof(T) == 2 ? 16 : 8;
+    const dim3 grid((unsigned)(A.tiles * A.cols)), block(kTile / K * 32);
+    if (pairs_ok<T>(A, {A.y})) hipLaunchKernelGGL((k_gs_forward<T, true, K, OUT>), grid, block, 0, s, A);
+    else hipLaunchKernelGGL((k_gs_forward<T, false, K, OUT>), grid, block, 0, s, A);
+    return check_launch();
+}
+
+template <typename T>
+mb_status run_step(const GsArgs& A, int64_t n, hipStream_t s) {
+    const int64_t blocks = (A.D + 511) / 512, most = max_workgroups(256) / blocks;       // rows of a launch
+    const bool pairs = pairs_ok<T>(A, {A.y});
+    for (int64_t at = 0; at < n; at += most) {
+        const dim3 grid((unsigned)(std::min(most, n - at) * blocks));
+        if (pairs) hipLaunchKernelGGL((k_gs_step<T, true>), grid, dim3(256), 0, s, A, at, (int)blocks);
+        else hipLaunchKernelGGL((k_gs_step<T, false>), grid, dim3(256), 0, s, A, at, (int)blocks);
+        const mb_status st = check_launch();
+        if (st != MB_OK) return st;
+    }
+    return MB_OK;
+}
+
+template <typename T>
+mb_status run_backward(const GsArgs& A, hipStream_t s) {
+    constexpr int K = sizeof(T) == 2 ? 8 : 4;
+    const dim3 grid((unsigned)(A.tiles * A.cols)), block(kTileBack / K * 32);
+    if (pairs_ok<T>(A, {A.dy, A.dx, A.da, A.dg})) hipLaunchKernelGGL((k_gs_backward<T, true, K>), grid, block, 0, s, A);
+    else hipLaunchKernelGGL((k_gs_backward<T, false, K>), grid, block, 0, s, A);
+    return check_launch();
 }
 
 // What every entry point takes: sizes, pointers and alignment of the inputs.
@@ -191,12 +888,13 @@ mb_status check_inputs(const GsArgs& A, int64_t T, mb_dtype dtype) {
 }  // namespace
 
 size_t gated_scan_workspace(int64_t n_seq, int64_t T, int64_t D) {
-    return 0;
+    if (!sizes_ok(n_seq, T, D)) return 0;
+    return lay_out(nullptr, nullptr, tiles_of(T, kTile), columns_of(D));
 }
 
 size_t gated_scan_bwd_workspace(int64_t n_seq, int64_t T, int64_t D) {
     if (!sizes_ok(n_seq, T, D)) return 0;
-    return (size_t)T * D * 4 + (size_t)n_seq * 3 * D * 4;
+    return back_plan(T, D).bytes;
 }
 
 }  // namespace mb
@@ -237,10 +935,11 @@ extern "C" mb_status mb_gated_scan(const void* x, const void* a_gate, const void
         if (overlaps_any(outs[i].p, outs[i].bytes, outs, i)) return MB_ERR_ALIAS;
     }
     if (need && (overlaps_any(ws, need, ins, 10) || overlaps_any(ws, need, outs, 3))) return MB_ERR_ALIAS;
-    const dim3 grid((unsigned)((D + 255) / 256), (unsigned)n_seq);
-    if (dtype == MB_F32) hipLaunchKernelGGL(k_gs_walk<float>, grid, dim3(256), 0, stream, A);
-    else hipLaunchKernelGGL(k_gs_walk<bf16>, grid, dim3(256), 0, stream, A);
-    return check_launch();
+    A.tiles = (int)tiles_of(T, kTile);
+    A.cols = (int)(columns_of(D) / kCols);
+    lay_out(&A.ch, (char*)ws, A.tiles, columns_of(D));
+    if ((st = launch_setup(A, A.ch, A.tiles, Chain{}, 0, stream)) != MB_OK) return st;
+    return dtype == MB_F32 ? run_forward<float, true>(A, stream) : run_forward<bf16, true>(A, stream);
 }
 
 extern "C" mb_status mb_gated_scan_step(const void* x, const void* a_gate, const void* x_gate, const float* decay, const float* a_bias,
@@ -267,10 +966,7 @@ extern "C" mb_status mb_gated_scan_step(const void* x, const void* a_gate, const
     const Span ins[8] = {{x, span_of(n, x_stride, D, es)}, {a_gate, span_of(n, a_stride, D, es)}, {x_gate, span_of(n, g_stride, D, es)},
                          {decay, (size_t)D * 4}, {a_bias, (size_t)D * 4}, {x_bias, (size_t)D * 4}, {slots, (size_t)n * 4}, {h_in, nh}};
     if (overlaps_any(y, no, ins, 8) || overlaps_any(h_out, nh, ins, h_out == h_in ? 7 : 8) || overlaps(y, no, h_out, nh)) return MB_ERR_ALIAS;
-    const dim3 grid((unsigned)((n * D + 255) / 256));
-    if (dtype == MB_F32) hipLaunchKernelGGL(k_gs_step<float>, grid, dim3(256), 0, stream, A, n);
-    else hipLaunchKernelGGL(k_gs_step<bf16>, grid, dim3(256), 0, stream, A, n);
-    return check_launch();
+    return dtype == MB_F32 ? run_step<float>(A, n, stream) : run_step<bf16>(A, n, stream);
 }
 
 extern "C" mb_status mb_gated_scan_bwd(const void* x, const void* a_gate, const void* x_gate, const float* decay, const float* a_bias,
@@ -285,7 +981,7 @@ extern "C" mb_status mb_gated_scan_bwd(const void* x, const void* a_gate, const 
     A.x = x; A.a = a_gate; A.g = x_gate;
     A.x_ts = x_stride; A.a_ts = a_stride; A.g_ts = g_stride;
     A.decay = decay; A.a_bias = a_bias; A.x_bias = x_bias;
-    A.cu = cu_seqlens; A.h0 = h0; A.dy = dy; A.dh_out = dh_out; A.states = const_cast<float*>(states);
+    A.cu = cu_seqlens; A.h0 = h0; A.dy = dy; A.dh_out = dh_out; A.kept = states;
     A.dx = dx; A.da = da_gate; A.dg = dx_gate; A.dh0 = dh0;
     A.n_seq = (int)n_seq; A.T = (int)T; A.L = n_seq ? (int)(T / n_seq) : 0; A.D = (int)D;
     mb_status st = check_inputs(A, T, dtype);
@@ -304,20 +1000,26 @@ extern "C" mb_status mb_gated_scan_bwd(const void* x, const void* a_gate, const 
     for (int i = 0; i < 7; ++i)
         if (overlaps_any(outs[i].p, outs[i].bytes, ins, 11) || overlaps_any(outs[i].p, outs[i].bytes, outs, i)) return MB_ERR_ALIAS;
     if (need && (overlaps_any(ws, need, ins, 11) || overlaps_any(ws, need, outs, 7))) return MB_ERR_ALIAS;
-    A.before = (float*)ws;
-    A.part = A.before + T * D;
-    const unsigned cols = (unsigned)((D + 255) / 256);
-    if (n_seq) {
-        const dim3 grid(cols, (unsigned)n_seq);
-        if (dtype == MB_F32) hipLaunchKernelGGL(k_gs_back<float>, grid, dim3(256), 0, stream, A);
-        else hipLaunchKernelGGL(k_gs_back<bf16>, grid, dim3(256), 0, stream, A);
-        if ((st = check_launch()) != MB_OK) return st;
+    const BackPlan bp = back_plan(T, D);
+    char* base = (char*)ws;
+    A.cols = (int)(bp.columns / kCols);
+    Chain fwd{}, back{};
+    if (!states) lay_out(&fwd, base, bp.tiles, bp.columns);
+    lay_out(&back, base + bp.back_at, bp.tiles_back, bp.columns);
+    if ((st = launch_setup(A, fwd, states ? 0 : bp.tiles, back, bp.tiles_back, stream)) != MB_OK) return st;
+    if (!states) {
+        GsArgs F = A;
+        F.states = (float*)(base + bp.states_at);
+        F.tiles = (int)bp.tiles;
+        F.ch = fwd;
+        if (T && (st = dtype == MB_F32 ? run_forward<float, false>(F, stream) : run_forward<bf16, false>(F, stream)) != MB_OK) return st;
+        A.kept = F.states;
     }
-    if (cu_seqlens && T) {
-        if (dtype == MB_F32) hipLaunchKernelGGL(k_gs_clear<float>, dim3((unsigned)T), dim3(256), 0, stream, A);
-        else hipLaunchKernelGGL(k_gs_clear<bf16>, dim3((unsigned)T), dim3(256), 0, stream, A);
-        if ((st = check_launch()) != MB_OK) return st;
-    }
-    hipLaunchKernelGGL(k_gs_sums, dim3(cols), dim3(256), 0, stream, A.part, A.n_seq, A.D, ddecay, da_bias, dx_bias);
+    A.tiles = (int)bp.tiles_back;
+    A.ch = back;
+    A.part = ddecay || da_bias || dx_bias ? (float*)(base + bp.part_at) : nullptr;
+    if ((st = dtype == MB_F32 ? run_backward<float>(A, stream) : run_backward<bf16>(A, stream)) != MB_OK) return st;
+    if (!A.part) return MB_OK;
+    hipLaunchKernelGGL(k_gs_sums, dim3((unsigned)A.cols, 3), dim3(1024), 0, stream, A.part, A.tiles, A.cols, A.D, ddecay, da_bias, dx_bias);
     return check_launch();
 }
