@@ -5,137 +5,398 @@
 //     backward: e = the gradient turned back, xh = x rstd, g = e w:
 //         dx = rstd (g - xh mean(g xh)),  dw = sum e xh
 //
-// A wave takes one head of one token at a time.
+// Bound by HBM: a head's row is read once, kept in registers between the sum of squares and the turn, and written once.
+// LPR lanes (the power of two that holds D / 8) share a row, eight columns each as four pairs: the pairs' members lie in
+// one lane whichever way they are paired, two pieces of four neighbouring columns.  A workgroup takes some tokens with all
+// their heads, and makes the tokens' sines and cosines once, in LDS, for all of them.
+#include <algorithm>
+
 #include "mb_internal.h"
 
 namespace mb {
 namespace {
 
-constexpr int kMaxD = 512, kE = kMaxD / 64;
-constexpr int kParts = 256;       // workgroups of the backward, each with its own share of dw
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+
+constexpr int kMaxD = 512;
+constexpr int kTokens = 16;       // most tokens of a workgroup at a time
+constexpr int kParts = 1024;      // most workgroups of the backward, each with its own share of dw
+constexpr int kBatch = 4;         // rows of a lane under way at a time
 
 struct QkArgs {
     const void* in[2];        // queries, keys
     void* out[2];
     const void* d[2];         // backward: their outputs' gradients
     const float* w[2];
-    float* part[2];
+    float* part;              // (workgroups, 2, D) shares of dw
     int64_t in_ts[2], out_ts[2];
     const float* freqs;
     const int32_t* positions;
     int64_t T, L;
     int H[2], D, R, inter;
+    int tokens, heads;        // of a workgroup at a time
     float eps;
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+// Sum (or maximum) over the LPR lanes of a row, the same in all of them.
+template <int LPR, bool MAX = false>
+__device__ __forceinline__ float row_all(float v) {
+    const auto with = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+#define MB_DPP(ctrl) with(v, __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), ctrl, 0xf, 0xf, true)))
+    v = MB_DPP(0xB1);                            // neighbour
+    v = MB_DPP(0x4E);                            // neighbouring pair
+    if constexpr (LPR > 4) v = MB_DPP(0x141);    // mirrored in eight lanes
+    if constexpr (LPR > 8) v = MB_DPP(0x140);    // mirrored in sixteen
+#undef MB_DPP
+    if constexpr (LPR > 16) v = with(v, __shfl_xor(v, 16));
+    if constexpr (LPR > 32) v = with(v, __shfl_xor(v, 32));
     return v;
 }
 
-// Columns of element i of lane: pairs' members beside each other in a lane.  -1: none.
-__device__ __forceinline__ int column(const QkArgs& A, int lane, int i) {
-    const int p = (i / 2) * 64 + lane, o = i & 1;
-    if (2 * p < A.R) return A.inter ? 2 * p + o : p + o * (A.R / 2);
-    return 2 * p + o < A.D ? 2 * p + o : -1;
-}
-
-__device__ __forceinline__ void turn(const QkArgs& A, int64_t pos, int lane, int i, float& c, float& s) {
-    const int p = i * 64 + lane;
-    c = 1.0f;
-    s = 0.0f;
-    if (2 * p < A.R) {
-        const double r = (double)pos * (double)A.freqs[p] * 0.15915494309189533577;
-        sincospif(2.0f * (float)(r - rint(r)), &s, &c);
+// Four neighbouring columns as they lie in memory.
+template <typename T> struct Four;
+template <> struct Four<bf16> {
+    typedef u2 type;
+    static __device__ __forceinline__ float get(u2 v, int i) { return __uint_as_float(i & 1 ? v[i >> 1] & 0xffff0000u : v[i >> 1] << 16); }
+    static __device__ __forceinline__ u2 make(float a, float b, float c, float d) {
+        const f2 x = {a, b}, y = {c, d};
+        return u2{__builtin_bit_cast(uint32_t, __builtin_convertvector(x, b2)), __builtin_bit_cast(uint32_t, __builtin_convertvector(y, b2))};
     }
-}
+};
+template <> struct Four<float> {
+    typedef f4 type;
+    static __device__ __forceinline__ float get(f4 v, int i) { return v[i]; }
+    static __device__ __forceinline__ f4 make(float a, float b, float c, float d) { return f4{a, b, c, d}; }
+};
 
-template <typename T, bool BACK>
-__global__ void __launch_bounds__(256) k_qk(QkArgs A) {
-    __shared__ float red[4][2][kMaxD];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int heads = A.H[0] + A.H[1];
-    float dw[2][kE];
-    for (int i = 0; i < kE; ++i) dw[0][i] = dw[1][i] = 0.0f;
-    for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < A.T * heads; r += (int64_t)gridDim.x * 4) {
-        const int64_t t = r / heads;
-        const int hh = (int)(r - t * heads), k = hh >= A.H[0], h = hh - (k ? A.H[0] : 0);
-        const int64_t pos = A.positions ? A.positions[t] : t % A.L;
-        const T* x = (const T*)A.in[k] + t * A.in_ts[k] + (int64_t)h * A.D;
-        float v[kE], top = 0.0f, ss = 0.0f;
-        for (int i = 0; i < kE; ++i) {
-            const int d = column(A, lane, i);
-            v[i] = d >= 0 ? to_f32(x[d]) : 0.0f;
-            ss = fmaf(v[i], v[i], ss);
-            top = fmaxf(top, fabsf(v[i]));
-        }
-        ss = wave_sum(ss);
-        float rs = 1.0f / sqrtf(ss / (float)A.D + A.eps);
-        if (ss > 3.0e38f || ss + A.eps < 0x1p-100f) {
-            for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-            top = fmaxf(top, sqrtf(A.eps));
-            if (top > 0.0f && top < 3.4e38f) {
-                const float f = exp2f(-(float)ilogbf(top));
-                ss = 0.0f;
-                for (int i = 0; i < kE; ++i) ss = fmaf(v[i] * f, v[i] * f, ss);
-                rs = f / sqrtf(wave_sum(ss) / (float)A.D + A.eps * f * f);
-            }
-        }
-        float w[kE], c[kE / 2], s[kE / 2];
-        for (int i = 0; i < kE; ++i) {
-            const int d = column(A, lane, i);
-            w[i] = A.w[k] && d >= 0 ? A.w[k][d] : 1.0f;
-        }
-        for (int i = 0; i < kE / 2; ++i) turn(A, pos, lane, i, c[i], s[i]);
-        const int64_t at = t * A.out_ts[k] + (int64_t)h * A.D;
-        if (!BACK) {
-            for (int i = 0; i < kE; i += 2) {
-                const float a = v[i] * rs * w[i], b = v[i + 1] * rs * w[i + 1];
-                const int d0 = column(A, lane, i), d1 = column(A, lane, i + 1);
-                if (d0 >= 0) store_out((T*)A.out[k] + at + d0, 2 * ((i / 2) * 64 + lane) < A.R ? a * c[i / 2] - b * s[i / 2] : a);
-                if (d1 >= 0) store_out((T*)A.out[k] + at + d1, 2 * ((i / 2) * 64 + lane) < A.R ? a * s[i / 2] + b * c[i / 2] : b);
-            }
+// A lane's columns: member o of its pair i lies at at<VEC>(i, o), or nowhere (-1).  VEC: two pieces of four.
+struct Columns {
+    int first, second;       // the pieces
+    int pair, R, D, inter;   // its first pair
+    template <bool VEC>
+    __device__ __forceinline__ int at(int i, int o) const {
+        int d;
+        if constexpr (VEC) {
+            d = inter ? first + 2 * i + o : (o ? second : first) + i;
         } else {
-            float dot = 0.0f, g[kE];
-            for (int i = 0; i < kE; i += 2) {
-                const int d0 = column(A, lane, i), d1 = column(A, lane, i + 1);
-                const float a = d0 >= 0 ? to_f32(((const T*)A.d[k])[at + d0]) : 0.0f, b = d1 >= 0 ? to_f32(((const T*)A.d[k])[at + d1]) : 0.0f;
-                g[i] = a * c[i / 2] + b * s[i / 2];
-                g[i + 1] = b * c[i / 2] - a * s[i / 2];
+            const int p = pair + i;
+            d = 2 * p < R && !inter ? p + o * (R / 2) : 2 * p + o;
+        }
+        return d < D ? d : -1;
+    }
+    __device__ __forceinline__ bool turns(int i) const { return 2 * (pair + i) < R; }
+};
+
+__device__ __forceinline__ Columns columns(const QkArgs& A, int lane) {
+    Columns c;
+    c.pair = 4 * lane;
+    c.R = A.R;
+    c.D = A.D;
+    c.inter = A.inter;
+    const bool apart = !A.inter && 8 * lane < A.R;
+    c.first = apart ? 4 * lane : 8 * lane;
+    c.second = apart ? A.R / 2 + 4 * lane : 8 * lane + 4;
+    return c;
+}
+
+// A weight's values for a lane's columns.
+template <bool VEC>
+__device__ __forceinline__ void load_weights(const float* w, const Columns& c, float (&u)[4], float (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int d = c.at<VEC>(i, 0), e = c.at<VEC>(i, 1);
+        u[i] = w && d >= 0 ? w[d] : 1.0f;
+        v[i] = w && e >= 0 ? w[e] : 1.0f;
+    }
+}
+
+// A lane's part of a row, before it is taken apart.
+template <typename T, bool VEC> struct Part {
+    typename Four<T>::type a, b;
+    __device__ __forceinline__ void load(const T* p, const Columns& c) {
+        if (c.first < c.D) {
+            a = *reinterpret_cast<const typename Four<T>::type*>(p + c.first);
+            b = *reinterpret_cast<const typename Four<T>::type*>(p + c.second);
+        } else {
+            a = b = typename Four<T>::type{};
+        }
+    }
+    // pairs (u, v)
+    __device__ __forceinline__ void get(float (&u)[4], float (&v)[4], const Columns& c) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u[i] = c.inter ? Four<T>::get(i < 2 ? a : b, 2 * (i & 1)) : Four<T>::get(a, i);
+            v[i] = c.inter ? Four<T>::get(i < 2 ? a : b, 2 * (i & 1) + 1) : Four<T>::get(b, i);
+        }
+    }
+    static __device__ __forceinline__ void store(T* p, const float (&u)[4], const float (&v)[4], const Columns& c) {
+        if (c.first >= c.D) return;
+        typedef typename Four<T>::type F;
+        const bool x = c.inter;
+        *reinterpret_cast<F*>(p + c.first) = x ? Four<T>::make(u[0], v[0], u[1], v[1]) : Four<T>::make(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<F*>(p + c.second) = x ? Four<T>::make(u[2], v[2], u[3], v[3]) : Four<T>::make(v[0], v[1], v[2], v[3]);
+    }
+};
+template <typename T> struct Part<T, false> {
+    T e[4][2];
+    __device__ __forceinline__ void load(const T* p, const Columns& c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const int d = c.at<false>(i, o);
+                e[i][o] = d >= 0 ? p[d] : (T)0;
             }
-            for (int i = 0; i < kE; ++i) {
-                v[i] *= rs;
-                dw[k][i] += g[i] * v[i];
-                g[i] *= w[i];
-                dot = fmaf(g[i], v[i], dot);
+    }
+    __device__ __forceinline__ void get(float (&u)[4], float (&v)[4], const Columns&) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u[i] = to_f32(e[i][0]);
+            v[i] = to_f32(e[i][1]);
+        }
+    }
+    static __device__ __forceinline__ void store(T* p, const float (&u)[4], const float (&v)[4], const Columns& c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int d = c.at<false>(i, 0), e = c.at<false>(i, 1);
+            if (d >= 0) store_out(p + d, u[i]);
+            if (e >= 0) store_out(p + e, v[i]);
+        }
+    }
+};
+
+// 1 / sqrt(mean x^2 + eps) of a row of the sum of squares ss.  Squares that leave fp32's range, above or, with an eps that does not
+// cover it, below (2^-100: those below the range are off by up to 2^-150 each), are summed once more of the values times a power of two
+// that brings the larger of them and of sqrt(eps) to between 1 and 4: `up`, which the result belongs to; 1 otherwise.
+template <int LPR>
+__device__ __forceinline__ float inverse_rms(float ss, const float (&u)[4], const float (&v)[4], int D, float eps, float& up) {
+    up = 1.0f;
+    if (__builtin_expect(ss > 3.0e38f || ss + eps < 0x1p-100f, false)) {
+        float top = sqrtf(eps);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(u[i]), fabsf(v[i])));
+        const uint32_t bits = __float_as_uint(row_all<LPR, true>(top));
+        if (bits != 0 && bits < 0x7f800000u) {       // neither zeros alone nor infinities; NaN does not come here
+            up = __uint_as_float((uint32_t)max(254 - (int)(bits >> 23), 1) << 23);
+            ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ss = fmaf(u[i] * up, u[i] * up, fmaf(v[i] * up, v[i] * up, ss));
+            ss = row_all<LPR>(ss);
+        }
+    }
+    return 1.0f / sqrtf(ss / (float)D + eps * up * up);
+}
+
+// Sines and cosines of `n` tokens from t0 on, LPR * 4 pairs each; pairs that do not turn are left out.  The angle in turns
+// is reduced in 64 bits: at a position of 2^31 it is off by 2^-24 of a turn.
+template <int LPR>
+__device__ __forceinline__ void fill_turns(const QkArgs& A, int64_t t0, int n, f2* cs) {
+    const int half = A.R / 2;
+    for (int i = threadIdx.x; i < n * LPR * 4; i += 256) {
+        const int t = i / (LPR * 4), p = i % (LPR * 4);
+        if (p >= half || t0 + t >= A.T) continue;
+        const int64_t pos = A.positions ? A.positions[t0 + t] : (t0 + t) % A.L;
+        const double r = (double)pos * (double)A.freqs[p] * 0.15915494309189533577;
+        float s, c;
+        sincospif(2.0f * (float)(r - rint(r)), &s, &c);
+        cs[i] = f2{c, s};
+    }
+}
+
+// (u, v) turned by (cos, sin)
+__device__ __forceinline__ void turn(float& u, float& v, float c, float s) {
+    const float a = u;
+    u = fmaf(-v, s, a * c);
+    v = fmaf(v, c, a * s);
+}
+
+template <typename T, int LPR, bool VEC>
+__global__ void __launch_bounds__(256) k_qk_forward(QkArgs A) {
+    constexpr int RS = 256 / LPR;
+    __shared__ f2 cs[kTokens * LPR * 4];
+    const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const Columns c = columns(A, lane);
+    const int64_t t0 = (int64_t)blockIdx.x * A.tokens;
+    const int all = A.H[0] + A.H[1], h0 = blockIdx.y * A.heads, nh = min(A.heads, all - h0);
+    const int rows = (int)min((int64_t)A.tokens, A.T - t0) * nh;
+    const float inv_nh = 1.0f / (float)nh;
+    const auto place = [&](int r, int& t, int& k, int& h) {
+        t = (int)(((float)r + 0.5f) * inv_nh);       // at most 16 tokens and 8192 heads: off by less than 0.5 / nh
+        h = h0 + r - t * nh;
+        k = h >= A.H[0];
+        h -= k ? A.H[0] : 0;
+    };
+    float wu[2][4], wv[2][4];
+    Part<T, VEC> x[kBatch];
+    const auto fetch = [&](int r0) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int r = r0 + b * RS;
+            if (r < rows) {
+                int t, k, h;
+                place(r, t, k, h);
+                x[b].load((const T*)(k ? A.in[1] : A.in[0]) + (t0 + t) * (k ? A.in_ts[1] : A.in_ts[0]) + h * A.D, c);
             }
-            dot = wave_sum(dot) / (float)A.D;
-            for (int i = 0; i < kE; ++i) {
-                const int d = column(A, lane, i);
-                if (d >= 0) store_out((T*)A.out[k] + at + d, rs * (g[i] - v[i] * dot));
+        }
+    };
+    fetch(slot);
+    load_weights<VEC>(A.w[0], c, wu[0], wv[0]);
+    load_weights<VEC>(A.w[1], c, wu[1], wv[1]);
+    if (A.R) fill_turns<LPR>(A, t0, A.tokens, cs);
+    __syncthreads();
+    for (int r0 = slot; r0 < rows; r0 += kBatch * RS) {
+        if (r0 != slot) fetch(r0);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int r = r0 + b * RS;
+            if (r >= rows) continue;
+            int t, k, h;
+            place(r, t, k, h);
+            float u[4], v[4], ss = 0.0f, up;
+            x[b].get(u, v, c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ss = fmaf(u[i], u[i], fmaf(v[i], v[i], ss));
+            const float rs = inverse_rms<LPR>(row_all<LPR>(ss), u, v, A.D, A.eps, up);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                u[i] = u[i] * up * rs * (k ? wu[1][i] : wu[0][i]);
+                v[i] = v[i] * up * rs * (k ? wv[1][i] : wv[0][i]);
+                if (c.turns(i)) {
+                    const f2 q = cs[t * LPR * 4 + c.pair + i];
+                    turn(u[i], v[i], q[0], q[1]);
+                }
+            }
+            Part<T, VEC>::store((T*)(k ? A.out[1] : A.out[0]) + (t0 + t) * (k ? A.out_ts[1] : A.out_ts[0]) + h * A.D, u, v, c);
+        }
+    }
+}
+
+// A workgroup walks over blocks of tokens; a lane keeps its columns' shares of both weights' gradients in registers, which are added up
+// in LDS at the end.
+template <typename T, int LPR, bool VEC>
+__global__ void __launch_bounds__(256) k_qk_backward(QkArgs A) {
+    constexpr int RS = 256 / LPR, B = 2;
+    __shared__ f2 cs[kTokens * LPR * 4];
+    __shared__ float red[RS][LPR * 8 + 1];
+    const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const Columns c = columns(A, lane);
+    const int nh = A.H[0] + A.H[1];
+    float wu[2][4], wv[2][4], du[2][4], dv[2][4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) du[k][i] = dv[k][i] = 0.0f;
+        load_weights<VEC>(A.w[k], c, wu[k], wv[k]);
+    }
+    const float inv_d = 1.0f / (float)A.D, inv_nh = 1.0f / (float)nh;
+    for (int64_t t0 = (int64_t)blockIdx.x * A.tokens; t0 < A.T; t0 += (int64_t)gridDim.x * A.tokens) {
+        const int rows = (int)min((int64_t)A.tokens, A.T - t0) * nh;
+        __syncthreads();                          // the turns of the block before have been read
+        if (A.R) fill_turns<LPR>(A, t0, A.tokens, cs);
+        __syncthreads();
+        for (int r0 = slot; r0 < rows; r0 += B * RS) {
+            Part<T, VEC> x[B], d[B];
+            int t[B], k[B], h[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int r = r0 + b * RS;
+                if (r < rows) {
+                    t[b] = (int)(((float)r + 0.5f) * inv_nh);
+                    h[b] = r - t[b] * nh;
+                    k[b] = h[b] >= A.H[0];
+                    h[b] -= k[b] ? A.H[0] : 0;
+                    x[b].load((const T*)(k[b] ? A.in[1] : A.in[0]) + (t0 + t[b]) * (k[b] ? A.in_ts[1] : A.in_ts[0]) + h[b] * A.D, c);
+                    d[b].load((const T*)(k[b] ? A.d[1] : A.d[0]) + (t0 + t[b]) * (k[b] ? A.out_ts[1] : A.out_ts[0]) + h[b] * A.D, c);
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (r0 + b * RS >= rows) continue;
+                float u[4], v[4], eu[4], ev[4], ss = 0.0f, dot = 0.0f, up;
+                x[b].get(u, v, c);
+                d[b].get(eu, ev, c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ss = fmaf(u[i], u[i], fmaf(v[i], v[i], ss));
+                    if (c.turns(i)) {
+                        const f2 q = cs[t[b] * LPR * 4 + c.pair + i];
+                        turn(eu[i], ev[i], q[0], -q[1]);
+                    }
+                }
+                const float rs = inverse_rms<LPR>(row_all<LPR>(ss), u, v, A.D, A.eps, up);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    u[i] = u[i] * up * rs;
+                    v[i] = v[i] * up * rs;
+                    if (k[b]) {
+                        du[1][i] = fmaf(eu[i], u[i], du[1][i]);
+                        dv[1][i] = fmaf(ev[i], v[i], dv[1][i]);
+                    } else {
+                        du[0][i] = fmaf(eu[i], u[i], du[0][i]);
+                        dv[0][i] = fmaf(ev[i], v[i], dv[0][i]);
+                    }
+                    eu[i] *= k[b] ? wu[1][i] : wu[0][i];
+                    ev[i] *= k[b] ? wv[1][i] : wv[0][i];
+                    dot = fmaf(eu[i], u[i], fmaf(ev[i], v[i], dot));
+                }
+                dot = row_all<LPR>(dot) * inv_d;
+                const float scale = rs * up;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    eu[i] = scale * fmaf(-u[i], dot, eu[i]);
+                    ev[i] = scale * fmaf(-v[i], dot, ev[i]);
+                }
+                Part<T, VEC>::store((T*)(k[b] ? A.out[1] : A.out[0]) + (t0 + t[b]) * (k[b] ? A.out_ts[1] : A.out_ts[0]) + h[b] * A.D, eu, ev, c);
             }
         }
     }
-    if (BACK) {
-        for (int k = 0; k < 2; ++k)
-            for (int i = 0; i < kE; ++i) {
-                const int d = column(A, lane, i);
-                if (d >= 0) red[wave][k][d] = dw[k][i];
+    if (!A.part) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                const int d = c.at<VEC>(i, o);
+                if (d >= 0) red[slot][d] = o ? dv[k][i] : du[k][i];
             }
         __syncthreads();
-        for (int k = 0; k < 2; ++k)
-            for (int d = threadIdx.x; d < A.D; d += 256)
-                if (A.part[k]) A.part[k][(int64_t)blockIdx.x * A.D + d] = red[0][k][d] + red[1][k][d] + red[2][k][d] + red[3][k][d];
+        for (int d = threadIdx.x; d < A.D; d += 256) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < RS; ++i) s += red[i][d];
+            A.part[((int64_t)blockIdx.x * 2 + k) * A.D + d] = s;
+        }
     }
 }
 
-__global__ void __launch_bounds__(256) k_qk_sum(const float* part, int n, int D, float* dw) {
-    const int d = blockIdx.x * 256 + threadIdx.x;
-    if (d >= D) return;
+// dw from the workgroups' shares, in a fixed order: 64 columns a workgroup, its 16 groups of lanes dealing the shares out.
+__global__ void __launch_bounds__(1024) k_qk_sum(const float* __restrict__ part, int n, int D, float* dq, float* dk) {
+    __shared__ float red[16][64];
+    float* dw = blockIdx.y ? dk : dq;
+    if (!dw) return;
+    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6, d = blockIdx.x * 64 + lane;
     float s = 0.0f;
-    for (int i = 0; i < n; ++i) s += part[(int64_t)i * D + d];
-    dw[d] = s;
+    if (d < D)
+        for (int i = grp; i < n; i += 16 * 8) {
+            float t[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t[k] = i + 16 * k < n ? part[((int64_t)(i + 16 * k) * 2 + blockIdx.y) * D + d] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += t[k];
+        }
+    red[grp][lane] = s;
+    __syncthreads();
+    if (grp == 0 && d < D) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s += red[i][lane];
+        dw[d] = s;
+    }
 }
 
 // ------------------------------------------------------------------ host ----
@@ -166,11 +427,64 @@ bool rows_overlap(const Rows& a, const Rows& b, int64_t T, size_t es) {
     return off < a.row * (int64_t)es || off + b.row * (int64_t)es > s;
 }
 
+// Lanes of a row: the power of two that holds its width, four at least.
+int lanes_of(int64_t D) {
+    int l = 4;
+    while (l * 8 < D) l *= 2;
+    return l;
+}
+
+// Tokens that a workgroup takes at a time: eight rows for every place that it has, no more than leaves two workgroups a
+// compute unit.
+int tokens_of(int64_t T, int64_t heads, int64_t D) {
+    const int64_t places = 256 / lanes_of(D), want = 2 * (int64_t)device_cu_count();
+    int64_t n = std::min<int64_t>(std::max<int64_t>((8 * places + heads - 1) / heads, 1), kTokens);
+    while (n > 1 && (T + n - 1) / n < want) n = (n + 1) / 2;
+    return (int)n;
+}
+
+// Pieces of four columns may be read as they are.
+bool pieces_ok(const QkArgs& A, size_t es) {
+    bool ok = A.D % 8 == 0 && A.R % 8 == 0;
+    for (int i = 0; i < 2; ++i)
+        ok = ok && A.in_ts[i] % 4 == 0 && A.out_ts[i] % 4 == 0 && (uintptr_t)A.in[i] % (4 * es) == 0 && (uintptr_t)A.out[i] % (4 * es) == 0 &&
+             (uintptr_t)A.d[i] % (4 * es) == 0;
+    return ok;
+}
+
+template <typename T, bool VEC>
+void launch_forward(const QkArgs& A, dim3 grid, hipStream_t s) {
+    switch (lanes_of(A.D)) {
+        case 4: hipLaunchKernelGGL((k_qk_forward<T, 4, VEC>), grid, dim3(256), 0, s, A); break;
+        case 8: hipLaunchKernelGGL((k_qk_forward<T, 8, VEC>), grid, dim3(256), 0, s, A); break;
+        case 16: hipLaunchKernelGGL((k_qk_forward<T, 16, VEC>), grid, dim3(256), 0, s, A); break;
+        case 32: hipLaunchKernelGGL((k_qk_forward<T, 32, VEC>), grid, dim3(256), 0, s, A); break;
+        default: hipLaunchKernelGGL((k_qk_forward<T, 64, VEC>), grid, dim3(256), 0, s, A);
+    }
+}
+
+template <typename T, bool VEC>
+void launch_backward(const QkArgs& A, dim3 grid, hipStream_t s) {
+    switch (lanes_of(A.D)) {
+        case 4: hipLaunchKernelGGL((k_qk_backward<T, 4, VEC>), grid, dim3(256), 0, s, A); break;
+        case 8: hipLaunchKernelGGL((k_qk_backward<T, 8, VEC>), grid, dim3(256), 0, s, A); break;
+        case 16: hipLaunchKernelGGL((k_qk_backward<T, 16, VEC>), grid, dim3(256), 0, s, A); break;
+        case 32: hipLaunchKernelGGL((k_qk_backward<T, 32, VEC>), grid, dim3(256), 0, s, A); break;
+        default: hipLaunchKernelGGL((k_qk_backward<T, 64, VEC>), grid, dim3(256), 0, s, A);
+    }
+}
+
+// Workgroups of the backward.
+int64_t parts_of(int64_t T, int64_t heads, int64_t D) {
+    const int64_t n = tokens_of(T, heads, D);
+    return std::min<int64_t>((T + n - 1) / n, kParts);
+}
+
 }  // namespace
 
 size_t qk_norm_rope_bwd_workspace(int64_t T, int64_t Hq, int64_t Hk, int64_t D) {
     if (!sizes_ok(T, Hq, Hk, D, 0) || T == 0) return 0;
-    return (size_t)kParts * D * 4 * 2;
+    return (size_t)parts_of(T, Hq + Hk, D) * D * 4 * 2;
 }
 
 }  // namespace mb
@@ -209,10 +523,16 @@ extern "C" mb_status mb_qk_norm_rope(const void* q, const void* k, const float* 
     A.in_ts[0] = q_stride; A.in_ts[1] = k_stride; A.out_ts[0] = q_out_stride; A.out_ts[1] = k_out_stride;
     A.freqs = freqs; A.positions = positions;
     A.T = T; A.L = L < 1 ? 1 : L; A.H[0] = (int)Hq; A.H[1] = (int)Hk; A.D = (int)D; A.R = (int)R; A.inter = interleaved; A.eps = eps;
-    const int64_t rows = T * (Hq + Hk);
-    const dim3 grid((unsigned)(rows < 4 * 65536 ? (rows + 3) / 4 : 65536));
-    if (dtype == MB_F32) hipLaunchKernelGGL((k_qk<float, false>), grid, dim3(256), 0, stream, A);
-    else hipLaunchKernelGGL((k_qk<bf16, false>), grid, dim3(256), 0, stream, A);
+    // Few tokens: their heads are dealt out to several workgroups.
+    A.tokens = tokens_of(T, Hq + Hk, D);
+    int64_t parts = 1;
+    const int64_t blocks = (T + A.tokens - 1) / A.tokens, places = 256 / lanes_of(D);
+    while (blocks * parts < 2 * device_cu_count() && (Hq + Hk + parts - 1) / parts > places) parts *= 2;
+    A.heads = (int)((Hq + Hk + parts - 1) / parts);
+    const dim3 grid((unsigned)blocks, (unsigned)((Hq + Hk + A.heads - 1) / A.heads));
+    const bool vec = pieces_ok(A, es);
+    if (dtype == MB_F32) vec ? launch_forward<float, true>(A, grid, stream) : launch_forward<float, false>(A, grid, stream);
+    else vec ? launch_forward<bf16, true>(A, grid, stream) : launch_forward<bf16, false>(A, grid, stream);
     return check_launch();
 }
 
@@ -250,19 +570,19 @@ extern "C" mb_status mb_qk_norm_rope_bwd(const void* dq_out, const void* dk_out,
     A.in_ts[0] = q_stride; A.in_ts[1] = k_stride; A.out_ts[0] = Hq * D; A.out_ts[1] = Hk * D;
     A.freqs = freqs; A.positions = positions;
     A.T = T; A.L = L < 1 ? 1 : L; A.H[0] = (int)Hq; A.H[1] = (int)Hk; A.D = (int)D; A.R = (int)R; A.inter = interleaved; A.eps = eps;
-    A.part[0] = dq_weight ? (float*)ws : nullptr;
-    A.part[1] = dk_weight ? (float*)ws + (size_t)kParts * D : nullptr;
     mb_status st;
+    const int64_t parts = T ? parts_of(T, Hq + Hk, D) : 0;
+    A.part = need ? (float*)ws : nullptr;
     if (T) {
-        if (dtype == MB_F32) hipLaunchKernelGGL((k_qk<float, true>), dim3(kParts), dim3(256), 0, stream, A);
-        else hipLaunchKernelGGL((k_qk<bf16, true>), dim3(kParts), dim3(256), 0, stream, A);
+        A.tokens = tokens_of(T, Hq + Hk, D);
+        const dim3 grid((unsigned)parts);
+        const bool vec = pieces_ok(A, es);
+        if (dtype == MB_F32) vec ? launch_backward<float, true>(A, grid, stream) : launch_backward<float, false>(A, grid, stream);
+        else vec ? launch_backward<bf16, true>(A, grid, stream) : launch_backward<bf16, false>(A, grid, stream);
         if ((st = check_launch()) != MB_OK) return st;
     }
-    float* dw[2] = {dq_weight, dk_weight};
-    for (int i = 0; i < 2; ++i)
-        if (dw[i]) {
-            hipLaunchKernelGGL(k_qk_sum, dim3((unsigned)((D + 255) / 256)), dim3(256), 0, stream, A.part[i], T ? kParts : 0, (int)D, dw[i]);
-            if ((st = check_launch()) != MB_OK) return st;
-        }
-    return MB_OK;
+    if (!dq_weight && !dk_weight) return MB_OK;
+    hipLaunchKernelGGL(k_qk_sum, dim3((unsigned)((D + 63) / 64), 2), dim3(1024), 0, stream, (const float*)A.part, (int)parts, (int)D, dq_weight,
+                       dk_weight);
+    return check_launch();
 }
