@@ -32,7 +32,9 @@ typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 constexpr int kEvery = 64;                  // tokens between the rows of states
 constexpr int kCols = 64;                   // channels of a tile
 constexpr int kTile = 128, kTileBack = 64;  // its tokens, forward and backward
+constexpr int kPer = 16, kPerBack = 8;      // tokens of a thread
 constexpr int kGroup = 16;                  // tiles of a group
+constexpr int kCounter = 32;                // words between the counters of two columns
 constexpr uint64_t kNone = ~0ull;           // not published yet
 // Polls of one wait before it is given up (the result is NaN then): some seconds, which only a workspace
 // that something else writes to at the same time can bring about.
@@ -108,8 +110,14 @@ __device__ __forceinline__ void sigma2(float v, float nb, float& s, float& not_s
 // --------------------------------------------------------------- memory ----
 // Two channels beside each other, as they lie in memory.
 template <typename T> struct Raw;
-template <> struct Raw<bf16> { typedef uint32_t type; };
-template <> struct Raw<float> { typedef f2 type; };
+template <> struct Raw<bf16> {
+    typedef uint32_t type;
+    static __device__ __forceinline__ type open() { return 0x7f807f80u; }
+};
+template <> struct Raw<float> {
+    typedef f2 type;
+    static __device__ __forceinline__ type open() { return f2{__builtin_inff(), __builtin_inff()}; }
+};
 
 __device__ __forceinline__ float half_of(uint32_t v, int i) { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
 __device__ __forceinline__ float half_of(f2 v, int i) { return v[i]; }
@@ -121,42 +129,54 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* p, int64_t
     return __builtin_amdgcn_make_buffer_rsrc((void*)((const T*)p + t0 * ts), 0, (int)bytes, 0x00027000);
 }
 
-// PAIR: two channels start on a border of two elements.
+// `row`: the same in all lanes, a scalar operand (a sum in a vector register for each row would be held over the whole walk); the
+// buffer's range holds for the sum.  PAIR: two channels start on a border of two elements.
 template <typename T, bool PAIR>
-__device__ __forceinline__ typename Raw<T>::type load2(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+__device__ __forceinline__ typename Raw<T>::type load2(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t row) {
     if constexpr (sizeof(T) == 2) {
-        if constexpr (PAIR) return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
-        const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
-        const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off + 2, 0, 0);
+        if constexpr (PAIR) return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
+        const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
+        const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off + 2, row, 0);
         return lo | hi << 16;
     } else {
-        if constexpr (PAIR) return __builtin_bit_cast(f2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+        if constexpr (PAIR) return __builtin_bit_cast(f2, __builtin_amdgcn_raw_buffer_load_b64(r, off, row, 0));
         f2 v;
-        v[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-        v[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off + 4, 0, 0));
+        v[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0));
+        v[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off + 4, row, 0));
         return v;
     }
 }
 
-// The first `n` (1 or 2) of two channels; rounds to nearest even.
+// Where two channels of a thread are stored: channels that are not there lie outside every buffer.
+struct Place2 {
+    uint32_t lo, hi;
+};
+constexpr uint32_t kNowhere = 0x80000000u;
+
+template <typename T>
+__device__ __forceinline__ Place2 place2(uint32_t off, int live) {
+    return Place2{live > 0 ? off : kNowhere, live > 1 ? off + (uint32_t)sizeof(T) : kNowhere};
+}
+
+// Rounds to nearest even.
 template <typename T, bool PAIR>
-__device__ __forceinline__ void store2(__amdgpu_buffer_rsrc_t r, uint32_t off, float lo, float hi, int n) {
+__device__ __forceinline__ void store2(__amdgpu_buffer_rsrc_t r, Place2 at, uint32_t row, float lo, float hi) {
     if constexpr (sizeof(T) == 2) {
         const f2 v = {lo, hi};
         const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, b2));
         if constexpr (PAIR) {
-            __builtin_amdgcn_raw_buffer_store_b32(w, r, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(w, r, at.lo, row, 0);
         } else {
-            __builtin_amdgcn_raw_buffer_store_b16((short)(w & 0xffffu), r, off, 0, 0);
-            if (n > 1) __builtin_amdgcn_raw_buffer_store_b16((short)(w >> 16), r, off + 2, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((short)(w & 0xffffu), r, at.lo, row, 0);
+            __builtin_amdgcn_raw_buffer_store_b16((short)(w >> 16), r, at.hi, row, 0);
         }
     } else {
         if constexpr (PAIR) {
             typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-            __builtin_amdgcn_raw_buffer_store_b64(u2{__float_as_uint(lo), __float_as_uint(hi)}, r, off, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(u2{__float_as_uint(lo), __float_as_uint(hi)}, r, at.lo, row, 0);
         } else {
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lo), r, off, 0, 0);
-            if (n > 1) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(hi), r, off + 4, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(lo), r, at.lo, row, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(hi), r, at.hi, row, 0);
         }
     }
 }
@@ -244,26 +264,36 @@ __device__ __forceinline__ Place place(const GsArgs& A, int j) {
     return p;
 }
 
-// Where sequences begin and end in a tile: for each token -2, or the row of the sequence (-1: none) that it is the first or the last of.
-template <int TT>
+// Where sequences begin and end in a tile: a bit for each of a group's tokens, and the rows (-1: none) of the sequences that begin and end.
+template <int TT, int NG>
 struct Events {
+    uint32_t begins[NG], ends[NG];
     int begin[TT], end[TT];
 };
 
-// Fills them in (a barrier on either side is the caller's) and settles the sequences of no tokens: `from` rows, or
-// zeros, go to `to`.  BACK: rows are the sequences' numbers.
-template <int TT, int NT, bool BACK>
-__device__ __forceinline__ void find_events(const GsArgs& A, const Place& p, Events<TT>& ev, int c, int n, const float* from, float* to) {
+// Fills them in, all threads together, and settles the sequences of no tokens: `from` rows, or zeros, go to `to`.  BACK: rows are the
+// sequences' numbers.
+template <int TT, int NG, bool BACK>
+__device__ __forceinline__ void find_events(const GsArgs& A, const Place& p, Events<TT, NG>& ev, int c, int n, const float* from, float* to) {
+    constexpr int K = TT / NG;
     const int lane = threadIdx.x & 31;
-    for (int s = p.sa + (int)(threadIdx.x >> 5); s <= p.sb; s += NT / 32) {
+    if (threadIdx.x < NG) ev.begins[threadIdx.x] = ev.ends[threadIdx.x] = 0;
+    lds_barrier();
+    for (int s = p.sa + (int)(threadIdx.x >> 5); s <= p.sb; s += NG) {
         int b, e;
         range_of(A, s, b, e);
         const int row = BACK ? s : row_of(A, s);
         const bool has = BACK || (row >= 0 && A.h0 && (!A.has_h0 || A.has_h0[s]));
         if (b < e) {
-            if (lane == 0) {
-                if (b >= p.t0 && b < p.t0 + p.n) ev.begin[b - p.t0] = has ? row : -1;
-                if (e > p.t0 && e <= p.t0 + p.n) ev.end[e - 1 - p.t0] = row;
+            b -= p.t0;
+            e -= p.t0 + 1;
+            if (lane == 0 && b >= 0 && b < p.n) {
+                ev.begin[b] = has ? row : -1;
+                atomicOr(&ev.begins[b / K], 1u << b % K);
+            }
+            if (lane == 0 && e >= 0 && e < p.n) {
+                ev.end[e] = row;
+                atomicOr(&ev.ends[e / K], 1u << e % K);
             }
         } else if (to && row >= 0) {
             for (int i = 0; i < n; ++i) {
@@ -272,6 +302,7 @@ __device__ __forceinline__ void find_events(const GsArgs& A, const Place& p, Eve
             }
         }
     }
+    lds_barrier();
 }
 
 // -------------------------------------------------------------- handing on ----
@@ -290,36 +321,44 @@ __device__ __forceinline__ void publish_state(const GsArgs& A, int group, int c,
     __hip_atomic_store(A.ch.incl + (int64_t)group * A.cols * kCols + c, plain_bits(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// What enters tile j of the chain (tiles counted in walking order), in one wave, a channel a lane.  src: the tile whose own U
-// starts it.  A tile's group is looked at as a whole: all its words are under way at a time.
-__device__ __forceinline__ float entering(const GsArgs& A, int j, int src, int c) {
-    const int group = j / kGroup, lo = max(src, group * kGroup);
+// What enters tile j of the chain (tiles counted in walking order): all waves fetch what the tiles of its group in front of it, from `src`
+// on, and the group before published, `look`; behind a barrier compose() puts it together, a channel a lane.
+template <int NW>
+__device__ __forceinline__ void fetch_look(const GsArgs& A, int j, int src, int col, uint64_t (*look)[kCols]) {
+    const int group = j / kGroup, lo = max(src, group * kGroup), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t row = (int64_t)A.cols * kCols;
-    const uint64_t* agg = A.ch.agg + lo * row + c;
-    uint64_t w[kGroup - 1];
-#pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i) w[i] = lo + i < j ? peek(agg + i * row) : 0;
-    float h = 0.0f;
+    const uint64_t* agg = A.ch.agg + lo * row + col * kCols;
+    const uint32_t* incl = A.ch.incl + (group - 1) * row + col * kCols;
+    constexpr int N = kGroup / NW;
+    uint64_t w[N];
     int polls = 0;
-    if (src < lo) {
-        const uint32_t* p = A.ch.incl + (group - 1) * row + c;
-        uint32_t v = peek(p);
-        while (v == (uint32_t)kNone && ++polls < kPolls) {
-            __builtin_amdgcn_s_sleep(1);
-            v = peek(p);
+    const auto read = [&](int i) -> uint64_t {
+        if (i == kGroup - 1) {
+            const uint32_t v = src < lo ? peek(incl + lane) : 0;
+            return v == (uint32_t)kNone ? kNone : v;
         }
-        h = __uint_as_float(v);
-    }
+        return lo + i < j ? peek(agg + i * row + lane) : 0;
+    };
 #pragma unroll
-    for (int i = 0; i < kGroup - 1; ++i) {
-        if (lo + i < j) {
-            while (w[i] == kNone && ++polls < kPolls) {
-                __builtin_amdgcn_s_sleep(1);
-                w[i] = peek(agg + i * row);
-            }
-            const float U = __uint_as_float((uint32_t)(w[i] >> 32));
-            h = src == lo + i ? U : fmaf(exp2_fast(__uint_as_float((uint32_t)w[i])), h, U);
+    for (int n = 0; n < N; ++n) w[n] = read(wave + n * NW);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        while (w[n] == kNone && ++polls < kPolls) {
+            __builtin_amdgcn_s_sleep(1);
+            w[n] = read(wave + n * NW);
         }
+        look[wave + n * NW][lane] = w[n];
+    }
+}
+
+__device__ __forceinline__ float compose(int j, int src, const uint64_t (*look)[kCols]) {
+    const int group = j / kGroup, lo = max(src, group * kGroup), lane = threadIdx.x & 63;
+    float h = src < lo ? __uint_as_float((uint32_t)look[kGroup - 1][lane]) : 0.0f;
+#pragma unroll 4
+    for (int i = 0; lo + i < j; ++i) {
+        const uint64_t w = look[i][lane];
+        const float U = __uint_as_float((uint32_t)(w >> 32));
+        h = src == lo + i ? U : fmaf(exp2_fast(__uint_as_float((uint32_t)w)), h, U);
     }
     return h;
 }
@@ -340,7 +379,7 @@ __global__ void __launch_bounds__(256) k_gs_setup(Setup S) {
         const int64_t words = (int64_t)S.tiles[k] * S.columns, states = (int64_t)((S.tiles[k] + kGroup - 1) / kGroup) * S.columns;
         for (int64_t i = i0; i < words; i += step) S.ch[k].agg[i] = kNone;
         for (int64_t i = i0; i < states; i += step) S.ch[k].incl[i] = (uint32_t)kNone;
-        if (i0 == 0) *S.ch[k].ticket = 0;
+        for (int64_t i = i0; i < S.columns / kCols; i += step) S.ch[k].ticket[i * kCounter] = 0;
         if (S.cu)
             for (int64_t i = i0; i <= S.tiles[k]; i += step) {
                 const int64_t t = i * S.tokens[k];
@@ -355,157 +394,209 @@ __global__ void __launch_bounds__(256) k_gs_setup(Setup S) {
     }
 }
 
-// The next tile of the launch: its number in walking order and its column.
-__device__ __forceinline__ void take_tile(const GsArgs& A, int* shared, int& j, int& col) {
-    if (A.tiles == 1) {
-        j = 0;
-        col = blockIdx.x;
-        return;
-    }
-    if (threadIdx.x == 0) *shared = (int)__hip_atomic_fetch_add(A.ch.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    const int t = __builtin_amdgcn_readfirstlane(*shared);
-    j = t / A.cols;
-    col = t - j * A.cols;
+// Workgroup b has column b % cols, and takes the column's tiles, in walking order, from a counter: the least unfinished one is
+// then always in work.  One counter for all columns would be slower: their adds, one after the other at one address, took
+// 12 us of the 62 that 3072 tiles of a packed prompt take without waits.
+
+__device__ __forceinline__ int take(const GsArgs& A, int col) {
+    if (A.tiles == 1) return 0;
+    return (int)__hip_atomic_fetch_add(A.ch.ticket + col * kCounter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// -decay log2(e) and the biases times -log2(e) of two channels; those behind the last are zero.
+struct Params {
+    float nd[2], nab[2], nxb[2];
+    __device__ __forceinline__ void load(const GsArgs& A, int c, int live) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool in = i < live;
+            nd[i] = in ? -A.decay[c + i] * kLog2e : 0.0f;
+            nab[i] = in && A.a_bias ? -A.a_bias[c + i] * kLog2e : 0.0f;
+            nxb[i] = in && A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f;
+        }
+    }
+};
+
+// A thread's K tokens of several tensors, token by token: work on the first ones begins while the others are on their way.
+template <typename T>
+struct Source {
+    __amdgpu_buffer_rsrc_t rows;
+    uint32_t off, step;
+    __device__ __forceinline__ Source(const void* p, int64_t t0, int64_t ts, int n, int D, int first, int c) {
+        rows = rows_at<T>(p, t0, ts, n, D);
+        step = (uint32_t)ts * sizeof(T);
+        off = first * step + c * sizeof(T);
+    }
+    template <bool PAIR>
+    __device__ __forceinline__ typename Raw<T>::type get(int k) const {
+        return load2<T, PAIR>(rows, off, k * step);
+    }
+};
+
 // -------------------------------------------------------------- forward ----
-// A thread holds K tokens of two channels; 32 threads side by side make a group's rows of 64 channels, NT / 32 groups the tile.
+// A thread holds K tokens of two channels; 32 threads side by side make a group's rows of 64 channels, NG groups the tile.
 // OUT: outputs and end states are written; otherwise the states for the backward alone.
 template <typename T, bool PAIR, int K, bool OUT>
-__global__ void __launch_bounds__(kTile / K * 32) k_gs_forward(GsArgs A) {
-    constexpr int NG = kTile / K, NT = NG * 32;
+__global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
+    constexpr int NG = kTile / K;
     __shared__ f2 comp[NG][kCols];
     __shared__ float entry[NG][kCols];
-    __shared__ Events<kTile> ev;
+    __shared__ uint64_t look[kGroup][kCols];
+    __shared__ Events<kTile, NG> ev;
     __shared__ int taken;
-    int j, col;
-    take_tile(A, &taken, j, col);
-    const Place p = place<kTile, false>(A, j);
-    const int c = col * kCols + (threadIdx.x & 31) * 2, grp = threadIdx.x >> 5;
-    const int live = min(max(A.D - c, 0), 2);              // channels of this thread
+    const int c2 = (threadIdx.x & 31) * 2, grp = threadIdx.x >> 5;
     typename Raw<T>::type rx[K], ra[K], rg[K];
+    Params par;
+    const int col = blockIdx.x % A.cols;
+    if (threadIdx.x == 0) taken = take(A, col);
+    __syncthreads();
+    const int j = __builtin_amdgcn_readfirstlane(taken);
     {
-        const __amdgpu_buffer_rsrc_t bx = rows_at<T>(A.x, p.t0, A.x_ts, p.n, A.D), ba = rows_at<T>(A.a, p.t0, A.a_ts, p.n, A.D);
-        const uint32_t sx = (uint32_t)A.x_ts * sizeof(T), sa = (uint32_t)A.a_ts * sizeof(T);
-        const uint32_t ox = grp * K * sx + c * sizeof(T), oa = grp * K * sa + c * sizeof(T);
+        const int c = col * kCols + c2, live = min(max(A.D - c, 0), 2);          // channels of this thread
+        {
+            const int t0 = j * kTile, n = min(A.T - t0, kTile);
+            par.load(A, c, live);
+            const Source<T> sa(A.a, t0, A.a_ts, n, A.D, grp * K, c), sx(A.x, t0, A.x_ts, n, A.D, grp * K, c);
+            const Source<T> sg(A.g, t0, A.g_ts, A.g ? n : 0, A.D, grp * K, c);
+            if (A.g) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) ra[k] = load2<T, PAIR>(ba, oa + k * sa);
+                for (int k = 0; k < K; ++k) {
+                    ra[k] = sa.template get<PAIR>(k);
+                    rg[k] = sg.template get<PAIR>(k);
+                    rx[k] = sx.template get<PAIR>(k);
+                }
+            } else {
 #pragma unroll
-        for (int k = 0; k < K; ++k) rx[k] = load2<T, PAIR>(bx, ox + k * sx);
-        if (A.g) {
-            const __amdgpu_buffer_rsrc_t bg = rows_at<T>(A.g, p.t0, A.g_ts, p.n, A.D);
-            const uint32_t sg = (uint32_t)A.g_ts * sizeof(T), og = grp * K * sg + c * sizeof(T);
-#pragma unroll
-            for (int k = 0; k < K; ++k) rg[k] = load2<T, PAIR>(bg, og + k * sg);
+                for (int k = 0; k < K; ++k) {
+                    ra[k] = sa.template get<PAIR>(k);
+                    rg[k] = Raw<T>::open();           // infinity: a gate of exactly one
+                    rx[k] = sx.template get<PAIR>(k);
+                }
+            }
         }
-    }
-    float nd[2], nab[2], nxb[2];
+        const Place p = place<kTile, false>(A, j);
+        uint32_t begins = 0, ends = 0;         // of this thread's tokens: first and last ones of a sequence
+        if (!p.plain) {
+            find_events<kTile, NG, false>(A, p, ev, c, live, A.h0, OUT ? A.h_out : nullptr);
+            begins = ev.begins[grp];
+            ends = ev.ends[grp];
+        }
+        float a[K][2], b[K][2], S[2] = {0.0f, 0.0f}, U[2] = {0.0f, 0.0f};        // (S, U) of this thread's tokens
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool in = i < live;
-        nd[i] = in ? -A.decay[c + i] * kLog2e : 0.0f;
-        nab[i] = in && A.a_bias ? -A.a_bias[c + i] * kLog2e : 0.0f;
-        nxb[i] = in && A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f;
-    }
-    if (!p.plain) {
-        for (int i = threadIdx.x; i < kTile; i += NT) ev.begin[i] = ev.end[i] = -2;
-        lds_barrier();
-        find_events<kTile, NT, false>(A, p, ev, c, live, A.h0, OUT ? A.h_out : nullptr);
-        lds_barrier();
-    }
-    const auto state0 = [&](int row, int i) { return row >= 0 && i < live ? A.h0[(int64_t)row * A.D + c + i] : 0.0f; };
-
-    float a[K][2], b[K][2];
-    f2 S[2];                               // (S, U) of this thread's tokens
-#pragma unroll
-    for (int i = 0; i < 2; ++i) S[i] = f2{0.0f, 0.0f};
-    bool cut = false;                      // a sequence begins among them: what enters is lost
-    const auto gates = [&](auto plain) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            int row = -2;
-            if constexpr (!decltype(plain)::value) row = ev.begin[grp * K + k];
+        for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const Gate q = gate(sigma(half_of(ra[k], i), nab[i]), nd[i]);
+                const Gate q = gate(sigma(half_of(ra[k], i), par.nab[i]), par.nd[i]);
                 const float x = half_of(rx[k], i);
                 a[k][i] = q.a;
-                b[k][i] = q.beta * (A.g ? sigma(half_of(rg[k], i), nxb[i]) * x : x);
-                if (row != -2) {
-                    // The only read of h0: a row that is updated in place may be written by the thread that holds its last token.
-                    const float h0 = state0(row, i);
-                    if (k == 0 && A.states && i < live && (grp * K) % kEvery == 0) A.states[(int64_t)((p.t0 + grp * K) / kEvery) * A.D + c + i] = h0;
-                    b[k][i] = fmaf(q.a, h0, b[k][i]);
-                    S[i] = f2{0.0f, b[k][i]};
-                    cut = true;
-                } else {
-                    S[i] = f2{S[i][0] + q.x2, fmaf(q.a, S[i][1], b[k][i])};
+                b[k][i] = q.beta * sigma(half_of(rg[k], i), par.nxb[i]) * x;
+                S[i] += q.x2;
+            }
+        // A first token's b takes in what its h0 gives, and its a is marked by -1: nothing of the token before.  This is the only read
+        // of h0: a row that is updated in place may be written by the thread that holds its last token.
+        for (uint32_t m = begins; m; m &= m - 1) {
+            const int at = __builtin_ctz(m), row = ev.begin[grp * K + at];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float h0 = row >= 0 && i < live ? A.h0[(int64_t)row * A.D + c + i] : 0.0f;
+                if (at == 0 && A.states && i < live && grp * K % kEvery == 0) A.states[(int64_t)((p.t0 + grp * K) / kEvery) * A.D + c + i] = h0;
+                float av = 0.0f, bv = 0.0f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    av = k == at ? a[k][i] : av;
+                    bv = k == at ? b[k][i] : bv;
+                }
+                bv = fmaf(av, h0, bv);
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    b[k][i] = k == at ? bv : b[k][i];
+                    a[k][i] = k == at ? -1.0f : a[k][i];
                 }
             }
         }
-    };
-    if (p.plain) gates(std::true_type{});
-    else gates(std::false_type{});
-    // a logarithm above zero marks what is cut off from the state that enters
-    *reinterpret_cast<f4*>(&comp[grp][(threadIdx.x & 31) * 2]) = f4{cut ? 1.0f : S[0][0], S[0][1], cut ? 1.0f : S[1][0], S[1][1]};
-    lds_barrier();
-    if (threadIdx.x < kCols) {
-        const int at = col * kCols + threadIdx.x;
-        float E[NG], U[NG], St = 0.0f, Ut = 0.0f;
+        if (p.plain) {
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            const f2 v = comp[i][threadIdx.x];
-            const bool off = v[0] > 0.0f;
-            E[i] = off ? -1.0f : exp2_fast(v[0]);
-            U[i] = v[1];
-            St += off ? 0.0f : v[0];
-            Ut = off ? U[i] : fmaf(E[i], Ut, U[i]);
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) U[i] = fmaf(a[k][i], U[i], b[k][i]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) U[i] = a[k][i] < 0.0f ? b[k][i] : fmaf(a[k][i], U[i], b[k][i]);
+            if (begins) S[0] = S[1] = 1.0f;      // a logarithm above zero marks what is cut off from the state that enters
         }
-        float h = 0.0f;
+        *reinterpret_cast<f4*>(&comp[grp][c2]) = f4{S[0], U[0], S[1], U[1]};
+        lds_barrier();
         if (A.tiles > 1) {
-            publish(A, j, at, St, Ut);
-            if (p.src < j) h = entering(A, j, p.src, at);
-        }
-#pragma unroll
-        for (int i = 0; i < NG; ++i) {
-            entry[i][threadIdx.x] = h;
-            h = E[i] < 0.0f ? U[i] : fmaf(E[i], h, U[i]);
-        }
-        if (A.tiles > 1 && j % kGroup == kGroup - 1) publish_state(A, j / kGroup, at, h);
-    }
-    lds_barrier();
-    float h[2] = {entry[grp][(threadIdx.x & 31) * 2], entry[grp][(threadIdx.x & 31) * 2 + 1]};
-    const __amdgpu_buffer_rsrc_t by = rows_at<T>(A.y, p.t0, A.D, OUT ? p.n : 0, A.D);
-    const uint32_t sy = (uint32_t)A.D * sizeof(T), oy = grp * K * sy + c * sizeof(T);
-    const auto walk = [&](auto plain) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int t = grp * K + k;
-            int begin = -2, end = -2;
-            if constexpr (!decltype(plain)::value) {
-                begin = ev.begin[t];
-                end = ev.end[t];
+            if (threadIdx.x < kCols) {
+                float St = 0.0f, Ut = 0.0f;
+#pragma unroll 4
+                for (int i = 0; i < NG; ++i) {
+                    const f2 v = comp[i][threadIdx.x];
+                    const bool off = v[0] > 0.0f;
+                    St += off ? 0.0f : v[0];
+                    Ut = off ? v[1] : fmaf(exp2_fast(v[0]), Ut, v[1]);
+                }
+                publish(A, j, col * kCols + threadIdx.x, St, Ut);
             }
-            if (k == 0 && A.states && (grp * K) % kEvery == 0 && t < p.n && begin == -2) {
-                float* s = A.states + (int64_t)((p.t0 + t) / kEvery) * A.D + c;
-                if (live > 0) s[0] = h[0];
-                if (live > 1) s[1] = h[1];
+            if (p.src < j) fetch_look<NG / 2>(A, j, p.src, col, look);
+            lds_barrier();
+        }
+        if (threadIdx.x < kCols) {
+            float h = p.src < j ? compose(j, p.src, look) : 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < NG; ++i) {
+                const f2 v = comp[i][threadIdx.x];
+                entry[i][threadIdx.x] = h;
+                h = v[0] > 0.0f ? v[1] : fmaf(exp2_fast(v[0]), h, v[1]);
             }
+            if (A.tiles > 1 && j % kGroup == kGroup - 1) publish_state(A, j / kGroup, col * kCols + threadIdx.x, h);
+        }
+        lds_barrier();
+        const f2 enter = *reinterpret_cast<const f2*>(&entry[grp][c2]);
+        float h[2] = {enter[0], enter[1]};
+        if (A.states && grp * K % kEvery == 0 && grp * K < p.n && !(begins & 1)) {
+            float* s = A.states + (int64_t)((p.t0 + grp * K) / kEvery) * A.D + c;
+            if (live > 0) s[0] = h[0];
+            if (live > 1) s[1] = h[1];
+        }
+        if constexpr (OUT) {
+            const __amdgpu_buffer_rsrc_t by = rows_at<T>(A.y, p.t0, A.D, p.n, A.D);
+            const uint32_t sy = (uint32_t)A.D * sizeof(T);
+            const Place2 oy = place2<T>(grp * K * sy + c * sizeof(T), live);
+            if (p.plain) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) h[i] = begin != -2 ? b[k][i] : fmaf(a[k][i], h[i], b[k][i]);
-            if constexpr (OUT) {
-                if (live > 0 && (decltype(plain)::value || (t >= p.lo && t < p.hi))) store2<T, PAIR>(by, oy + k * sy, h[0], h[1], live);
-                if (end >= 0 && A.h_out) {
-                    float* o = A.h_out + (int64_t)end * A.D + c;
-                    if (live > 0) o[0] = h[0];
-                    if (live > 1) o[1] = h[1];
+                for (int k = 0; k < K; ++k) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) h[i] = fmaf(a[k][i], h[i], b[k][i]);
+                    store2<T, PAIR>(by, oy, k * sy, h[0], h[1]);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        h[i] = a[k][i] < 0.0f ? b[k][i] : fmaf(a[k][i], h[i], b[k][i]);
+                        b[k][i] = h[i];                 // for the end states
+                    }
+                    const bool in = grp * K + k >= p.lo && grp * K + k < p.hi;
+                    store2<T, PAIR>(by, in ? oy : Place2{kNowhere, kNowhere}, k * sy, h[0], h[1]);
+                }
+                for (uint32_t m = ends; m; m &= m - 1) {
+                    const int at = __builtin_ctz(m), row = ev.end[grp * K + at];
+                    if (row < 0 || !A.h_out) continue;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float v = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < K; ++k) v = k == at ? b[k][i] : v;
+                        if (i < live) A.h_out[(int64_t)row * A.D + c + i] = v;
+                    }
                 }
             }
         }
-    };
-    if (p.plain) walk(std::true_type{});
-    else walk(std::false_type{});
+    }
 }
 
 // ------------------------------------------------------------- backward ----
@@ -513,130 +604,120 @@ __global__ void __launch_bounds__(kTile / K * 32) k_gs_forward(GsArgs A) {
 // the gradient that comes back out of the tiles behind, handed on like the states forward.  The tokens are walked three times in
 // registers: forward and back for what the tile hands on, forward for h_{t-1}, back for G and the gradients.
 template <typename T, bool PAIR, int K>
-__global__ void __launch_bounds__(kTileBack / K * 32) k_gs_backward(GsArgs A) {
+__global__ void __launch_bounds__(kTileBack / K * 32, 2) k_gs_backward(GsArgs A) {
     constexpr int NG = kTileBack / K, NT = NG * 32;
     __shared__ f4 comp[NG][kCols];          // of every group: (S, U) forward, (S, V) backward
     __shared__ f2 entry[NG][kCols];         // the state in front of it, the gradient from behind it
-    __shared__ Events<kTileBack> ev;
+    __shared__ uint64_t look[kGroup][kCols];
+    __shared__ Events<kTileBack, NG> ev;
     __shared__ int taken;
     static_assert(kTileBack == kEvery, "a tile starts from a kept state");
-    int jr, col;
-    take_tile(A, &taken, jr, col);
-    const int j = A.tiles - 1 - jr;
-    const Place p = place<kTileBack, true>(A, j);
-    const int c2 = (threadIdx.x & 31) * 2, c = col * kCols + c2, grp = threadIdx.x >> 5;
-    const int live = min(max(A.D - c, 0), 2);
+    const int c2 = (threadIdx.x & 31) * 2, grp = threadIdx.x >> 5;
     typename Raw<T>::type rx[K], ra[K], rg[K], rd[K];
+    Params par;
+    const int col = blockIdx.x % A.cols;
+    if (threadIdx.x == 0) taken = take(A, col);
+    __syncthreads();
+    const int jr = __builtin_amdgcn_readfirstlane(taken), j = A.tiles - 1 - jr;
+    const int c = col * kCols + c2, live = min(max(A.D - c, 0), 2);
     {
-        const __amdgpu_buffer_rsrc_t bx = rows_at<T>(A.x, p.t0, A.x_ts, p.n, A.D), ba = rows_at<T>(A.a, p.t0, A.a_ts, p.n, A.D);
-        const __amdgpu_buffer_rsrc_t bd = rows_at<T>(A.dy, p.t0, A.D, p.n, A.D);
-        const uint32_t sx = (uint32_t)A.x_ts * sizeof(T), sa = (uint32_t)A.a_ts * sizeof(T), sd = (uint32_t)A.D * sizeof(T);
-        const uint32_t ox = grp * K * sx + c * sizeof(T), oa = grp * K * sa + c * sizeof(T), od = grp * K * sd + c * sizeof(T);
+        const int t0 = j * kTileBack, n = min(A.T - t0, kTileBack);
+        par.load(A, c, live);
+        const Source<T> sa(A.a, t0, A.a_ts, n, A.D, grp * K, c), sx(A.x, t0, A.x_ts, n, A.D, grp * K, c);
+        const Source<T> sg(A.g, t0, A.g_ts, A.g ? n : 0, A.D, grp * K, c), sd(A.dy, t0, A.D, n, A.D, grp * K, c);
 #pragma unroll
-        for (int k = 0; k < K; ++k) ra[k] = load2<T, PAIR>(ba, oa + k * sa);
-#pragma unroll
-        for (int k = 0; k < K; ++k) rx[k] = load2<T, PAIR>(bx, ox + k * sx);
-        if (A.g) {
-            const __amdgpu_buffer_rsrc_t bg = rows_at<T>(A.g, p.t0, A.g_ts, p.n, A.D);
-            const uint32_t sg = (uint32_t)A.g_ts * sizeof(T), og = grp * K * sg + c * sizeof(T);
-#pragma unroll
-            for (int k = 0; k < K; ++k) rg[k] = load2<T, PAIR>(bg, og + k * sg);
+        for (int k = 0; k < K; ++k) {
+            ra[k] = sa.template get<PAIR>(k);
+            rg[k] = A.g ? sg.template get<PAIR>(k) : Raw<T>::open();
+            rx[k] = sx.template get<PAIR>(k);
         }
 #pragma unroll
-        for (int k = 0; k < K; ++k) rd[k] = load2<T, PAIR>(bd, od + k * sd);
+        for (int k = K - 1; k >= 0; --k) rd[k] = sd.template get<PAIR>(k);
     }
-    float nd[2], nab[2], nxb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bool in = i < live;
-        nd[i] = in ? -A.decay[c + i] * kLog2e : 0.0f;
-        nab[i] = in && A.a_bias ? -A.a_bias[c + i] * kLog2e : 0.0f;
-        nxb[i] = in && A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f;
-    }
+    const Place p = place<kTileBack, true>(A, j);
+    uint32_t begins = 0, ends = 0;
     if (!p.plain) {
-        for (int i = threadIdx.x; i < kTileBack; i += NT) ev.begin[i] = ev.end[i] = -2;
-        lds_barrier();
-        find_events<kTileBack, NT, true>(A, p, ev, c, live, A.dh_out, A.dh0);
-        lds_barrier();
+        find_events<kTileBack, NG, true>(A, p, ev, c, live, A.dh_out, A.dh0);
+        begins = ev.begins[grp];
+        ends = ev.ends[grp];
     }
-    const auto row_value = [&](const float* q, int row, int i) { return q && row >= 0 && i < live ? q[(int64_t)row * A.D + c + i] : 0.0f; };
+    // A row's values in place of what comes from the neighbouring token.  Not before its turn: rows of many tokens would be held.
+    const auto set = [&](float (&v)[2], const float* q, int row) {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 2; ++i) v[i] = q && i < live ? q[(int64_t)row * A.D + c + i] : 0.0f;
+    };
 
     // of every token: a, b, beta i, a^2 b / (1 - a^2) and then dla / G, s, la (1 - s), b (1 - i)
     float a[K][2], b[K][2], bi[K][2], r[K][2], s[K][2], w[K][2], bn[K][2];
     float S[2] = {0.0f, 0.0f}, U[2] = {0.0f, 0.0f}, V[2] = {0.0f, 0.0f};
-    bool cut = false, cut_back = false;
-    const auto gates = [&](auto plain) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float not_s, ig, not_i;
+            sigma2(half_of(ra[k], i), par.nab[i], s[k][i], not_s);
+            const Gate q = gate(s[k][i], par.nd[i]);
+            sigma2(half_of(rg[k], i), par.nxb[i], ig, not_i);
+            a[k][i] = q.a;
+            bi[k][i] = q.beta * ig;
+            b[k][i] = bi[k][i] * half_of(rx[k], i);
+            bn[k][i] = b[k][i] * not_i;
+            w[k][i] = q.x2 * 0.69314718056f * not_s;
+            const float root = q.a * q.a * b[k][i] * __builtin_amdgcn_rcpf(q.less);
+            r[k][i] = q.less < 0x1p-120f ? 0.0f : root;
+            S[i] += q.x2;
+        }
+    const auto spans = [&](auto plain) {
         constexpr bool P = decltype(plain)::value;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int row = P ? -2 : ev.begin[grp * K + k];
+            if (!P && (begins >> k & 1)) set(U, A.h0, ev.begin[grp * K + k]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float not_s, ig = 1.0f, not_i = 0.0f;
-                sigma2(half_of(ra[k], i), nab[i], s[k][i], not_s);
-                const Gate q = gate(s[k][i], nd[i]);
-                if (A.g) sigma2(half_of(rg[k], i), nxb[i], ig, not_i);
-                a[k][i] = q.a;
-                bi[k][i] = q.beta * ig;
-                b[k][i] = bi[k][i] * half_of(rx[k], i);
-                bn[k][i] = b[k][i] * not_i;
-                w[k][i] = q.x2 * 0.69314718056f * not_s;
-                const float root = q.a * q.a * b[k][i] * __builtin_amdgcn_rcpf(q.less);
-                r[k][i] = q.less < 0x1p-120f ? 0.0f : root;
-                S[i] += q.x2;
-                if (row != -2) {
-                    U[i] = fmaf(q.a, row_value(A.h0, row, i), b[k][i]);
-                    cut = true;
-                } else {
-                    U[i] = fmaf(q.a, U[i], b[k][i]);
-                }
-            }
+            for (int i = 0; i < 2; ++i) U[i] = fmaf(a[k][i], U[i], b[k][i]);
         }
 #pragma unroll
         for (int k = K - 1; k >= 0; --k) {
-            const int row = P ? -2 : ev.end[grp * K + k];
+            if (!P && (ends >> k & 1)) set(V, A.dh_out, ev.end[grp * K + k]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (row != -2) {
-                    V[i] = row_value(A.dh_out, row, i);
-                    cut_back = true;
-                }
-                V[i] = a[k][i] * (half_of(rd[k], i) + V[i]);
-            }
+            for (int i = 0; i < 2; ++i) V[i] = a[k][i] * (half_of(rd[k], i) + V[i]);
         }
     };
-    if (p.plain) gates(std::true_type{});
-    else gates(std::false_type{});
+    if (p.plain) spans(std::true_type{});
+    else spans(std::false_type{});
+    const bool cut = begins != 0, cut_back = ends != 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) comp[grp][c2 + i] = f4{cut ? 1.0f : S[i], U[i], cut_back ? 1.0f : S[i], V[i]};
     lds_barrier();
+    const int src = A.tiles - 1 - p.src;
+    if (A.tiles > 1) {
+        if (threadIdx.x < kCols) {
+            float St = 0.0f, Vt = 0.0f;
+#pragma unroll 4
+            for (int i = NG - 1; i >= 0; --i) {
+                const f4 q = comp[i][threadIdx.x];
+                const bool off = q[2] > 0.0f;
+                St += off ? 0.0f : q[2];
+                Vt = off ? q[3] : fmaf(exp2_fast(q[2]), Vt, q[3]);
+            }
+            publish(A, jr, col * kCols + threadIdx.x, St, Vt);
+        }
+        if (src < jr) fetch_look<NG / 2>(A, jr, src, col, look);
+        lds_barrier();
+    }
     if (threadIdx.x < kCols) {
-        const int at = col * kCols + threadIdx.x, src = A.tiles - 1 - p.src;
-        float E[NG], v[NG], St = 0.0f, Vt = 0.0f;
-#pragma unroll
+        float g = src < jr ? compose(jr, src, look) : 0.0f;
+#pragma unroll 4
         for (int i = NG - 1; i >= 0; --i) {
             const f4 q = comp[i][threadIdx.x];
-            const bool off = q[2] > 0.0f;
-            E[i] = off ? -1.0f : exp2_fast(q[2]);
-            v[i] = q[3];
-            St += off ? 0.0f : q[2];
-            Vt = off ? v[i] : fmaf(E[i], Vt, v[i]);
-        }
-        float g = 0.0f;
-        if (A.tiles > 1) {
-            publish(A, jr, at, St, Vt);
-            if (src < jr) g = entering(A, jr, src, at);
-        }
-#pragma unroll
-        for (int i = NG - 1; i >= 0; --i) {
             entry[i][threadIdx.x][1] = g;
-            g = E[i] < 0.0f ? v[i] : fmaf(E[i], g, v[i]);
+            g = q[2] > 0.0f ? q[3] : fmaf(exp2_fast(q[2]), g, q[3]);
         }
-        if (A.tiles > 1 && jr % kGroup == kGroup - 1) publish_state(A, jr / kGroup, at, g);
+        if (A.tiles > 1 && jr % kGroup == kGroup - 1) publish_state(A, jr / kGroup, col * kCols + threadIdx.x, g);
     } else if (threadIdx.x < 2 * kCols) {
         const int lane = threadIdx.x - kCols, at = col * kCols + lane;
         float h = at < A.D && p.n > 0 ? A.kept[(int64_t)j * A.D + at] : 0.0f;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < NG; ++i) {
             const f4 q = comp[i][lane];
             entry[i][lane][0] = h;
@@ -653,15 +734,15 @@ __global__ void __launch_bounds__(kTileBack / K * 32) k_gs_backward(GsArgs A) {
     }
     const __amdgpu_buffer_rsrc_t bdx = rows_at<T>(A.dx, p.t0, A.D, p.n, A.D), bda = rows_at<T>(A.da, p.t0, A.D, p.n, A.D);
     const __amdgpu_buffer_rsrc_t bdg = rows_at<T>(A.dg, p.t0, A.D, A.g ? p.n : 0, A.D);
-    const uint32_t sd = (uint32_t)A.D * sizeof(T), od = grp * K * sd + c * sizeof(T);
+    const uint32_t sd = (uint32_t)A.D * sizeof(T);
+    const Place2 od = place2<T>(grp * K * sd + c * sizeof(T), live);
     const auto walk = [&](auto plain) {
         constexpr bool P = decltype(plain)::value;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int row = P ? -2 : ev.begin[grp * K + k];
+            if (!P && (begins >> k & 1)) set(h, A.h0, ev.begin[grp * K + k]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (row != -2) h[i] = row_value(A.h0, row, i);
                 r[k][i] = fmaf(a[k][i], h[i], -r[k][i]);
                 h[i] = fmaf(a[k][i], h[i], b[k][i]);
             }
@@ -669,14 +750,14 @@ __global__ void __launch_bounds__(kTileBack / K * 32) k_gs_backward(GsArgs A) {
 #pragma unroll
         for (int k = K - 1; k >= 0; --k) {
             const int t = grp * K + k;
-            const int begin = P ? -2 : ev.begin[t], end = P ? -2 : ev.end[t];
             const bool in = P || (t >= p.lo && t < p.hi);
             float dx[2], da[2], dg[2];
+            if (!P && (ends >> k & 1)) set(g, A.dh_out, ev.end[t]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (end != -2) g[i] = row_value(A.dh_out, end, i);
                 const float G = half_of(rd[k], i) + g[i];
                 g[i] = a[k][i] * G;
+                // tokens of no sequence have no gradients, whatever they hold
                 const float dla = in ? G * r[k][i] : 0.0f;
                 dx[i] = in ? G * bi[k][i] : 0.0f;
                 dg[i] = in ? G * bn[k][i] : 0.0f;
@@ -684,13 +765,11 @@ __global__ void __launch_bounds__(kTileBack / K * 32) k_gs_backward(GsArgs A) {
                 sum[0][i] = in ? fmaf(-dla, s[k][i], sum[0][i]) : sum[0][i];
                 sum[1][i] += da[i];
                 sum[2][i] += dg[i];
-                if (begin >= 0 && A.dh0 && i < live) A.dh0[(int64_t)begin * A.D + c + i] = g[i];
+                if (!P && (begins >> k & 1) && A.dh0 && i < live) A.dh0[(int64_t)ev.begin[t] * A.D + c + i] = g[i];
             }
-            if (live > 0) {
-                store2<T, PAIR>(bdx, od + k * sd, dx[0], dx[1], live);
-                store2<T, PAIR>(bda, od + k * sd, da[0], da[1], live);
-                if (A.g) store2<T, PAIR>(bdg, od + k * sd, dg[0], dg[1], live);
-            }
+            store2<T, PAIR>(bdx, od, k * sd, dx[0], dx[1]);
+            store2<T, PAIR>(bda, od, k * sd, da[0], da[1]);
+            store2<T, PAIR>(bdg, od, k * sd, dg[0], dg[1]);
         }
     };
     if (p.plain) walk(std::true_type{});
@@ -745,7 +824,8 @@ __global__ void __launch_bounds__(256) k_gs_step(GsArgs A, int64_t n0, int block
     if (live <= 0) return;
     const __amdgpu_buffer_rsrc_t bx = rows_at<T>(A.x, n, A.x_ts, 1, A.D), ba = rows_at<T>(A.a, n, A.a_ts, 1, A.D);
     const __amdgpu_buffer_rsrc_t bg = rows_at<T>(A.g, n, A.g_ts, A.g ? 1 : 0, A.D), by = rows_at<T>(A.y, n, A.D, 1, A.D);
-    const auto rx = load2<T, PAIR>(bx, c * sizeof(T)), ra = load2<T, PAIR>(ba, c * sizeof(T)), rg = load2<T, PAIR>(bg, c * sizeof(T));
+    const auto rx = load2<T, PAIR>(bx, c * sizeof(T), 0), ra = load2<T, PAIR>(ba, c * sizeof(T), 0);
+    const auto rg = A.g ? load2<T, PAIR>(bg, c * sizeof(T), 0) : Raw<T>::open();
     int64_t row = n;
     if (A.slots) {
         row = A.slots[n];
@@ -759,12 +839,12 @@ __global__ void __launch_bounds__(256) k_gs_step(GsArgs A, int64_t n0, int block
             if (A.h0 && row >= 0) h[i] = A.h0[row * A.D + c + i];
             const Gate q = gate(sigma(half_of(ra, i), A.a_bias ? -A.a_bias[c + i] * kLog2e : 0.0f), -A.decay[c + i] * kLog2e);
             const float x = half_of(rx, i);
-            const float u = A.g ? sigma(half_of(rg, i), A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f) * x : x;
-            h[i] = fmaf(q.a, h[i], q.beta * u);
+            const float ig = sigma(half_of(rg, i), A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f);
+            h[i] = fmaf(q.a, h[i], q.beta * ig * x);
             if (row >= 0) A.h_out[row * A.D + c + i] = h[i];
         }
     }
-    store2<T, PAIR>(by, c * sizeof(T), h[0], h[1], live);
+    store2<T, PAIR>(by, place2<T>(c * sizeof(T), live), 0, h[0], h[1]);
 }
 
 // ------------------------------------------------------------------ host ----
@@ -794,7 +874,7 @@ size_t lay_out(Chain* ch, char* at, int64_t tiles, int64_t columns) {
         ch->first = (int*)(at + agg + incl);
         ch->ticket = (uint32_t*)(at + agg + incl + first);
     }
-    return agg + incl + first + 256;
+    return agg + incl + first + up256((size_t)(columns / kCols) * kCounter * 4);
 }
 
 // The backward's workspace: both chains, the tiles' shares of the sums, the states where they are made again.
@@ -845,7 +925,7 @@ mb_status launch_setup(const GsArgs& A, const Chain& fwd, int64_t tiles, const C
 
 template <typename T, bool OUT>
 mb_status run_forward(const GsArgs& A, hipStream_t s) {
-    constexpr int K = sizeof(T) == 2 ? 16 : 8;
+    constexpr int K = kPer;
     const dim3 grid((unsigned)(A.tiles * A.cols)), block(kTile / K * 32);
     if (pairs_ok<T>(A, {A.y})) hipLaunchKernelGGL((k_gs_forward<T, true, K, OUT>), grid, block, 0, s, A);
     else hipLaunchKernelGGL((k_gs_forward<T, false, K, OUT>), grid, block, 0, s, A);
@@ -868,7 +948,7 @@ mb_status run_step(const GsArgs& A, int64_t n, hipStream_t s) {
 
 template <typename T>
 mb_status run_backward(const GsArgs& A, hipStream_t s) {
-    constexpr int K = sizeof(T) == 2 ? 8 : 4;
+    constexpr int K = kPerBack;
     const dim3 grid((unsigned)(A.tiles * A.cols)), block(kTileBack / K * 32);
     if (pairs_ok<T>(A, {A.dy, A.dx, A.da, A.dg})) hipLaunchKernelGGL((k_gs_backward<T, true, K>), grid, block, 0, s, A);
     else hipLaunchKernelGGL((k_gs_backward<T, false, K>), grid, block, 0, s, A);
