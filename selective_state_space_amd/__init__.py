@@ -964,28 +964,36 @@ MB_GATED_SCAN_EVERY = 64     # tokens between the rows of `states`
 
 
 def _channels(t, name, lead, D, dtype, device):
-    """_tokens of a (*lead, D) tensor."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    """Check a (*lead, D) tensor whose tokens lie at one stride; returns that stride in elements.  The plain case comes
+    first, one look at each property: a step's kernel takes a few microseconds."""
+    shape = lead + (D,)
+    if isinstance(t, _torch().Tensor) and t.shape == shape and t.dtype is dtype and t.device == device:
+        if t.is_contiguous():
+            return D
+        if len(shape) == 2 and D > 1 and shape[0] > 1:
+            st = t.stride()
+            if st[1] == 1 and st[0] >= D:
+                return st[0]
+        return _tokens(t.unsqueeze(-2), name, lead, 1, D, dtype, device)
+    if not isinstance(t, _torch().Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if tuple(t.shape) != tuple(lead) + (D,):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(lead) + (D,)))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), shape))
     return _tokens(t.unsqueeze(-2), name, lead, 1, D, dtype, device)
 
 
-def _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, lead):
-    """Check the inputs that every form of the recurrence has: (device, code, strides)."""
-    torch = _torch()
-    dev = _device_of(x)
-    code = _dtype_code(x, "x")
-    D = x.shape[-1]
-    st = [_channels(x, "x", lead, D, x.dtype, dev), _channels(a_gate, "a_gate", lead, D, x.dtype, dev),
-          D if x_gate is None else _channels(x_gate, "x_gate", lead, D, x.dtype, dev)]
+def _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, lead, dev):
+    """Check the inputs that every form of the recurrence has: (dtype code, strides)."""
+    code, dt, D = _dtype_code(x, "x"), x.dtype, x.shape[-1]
+    st = [_channels(x, "x", lead, D, dt, dev), _channels(a_gate, "a_gate", lead, D, dt, dev),
+          D if x_gate is None else _channels(x_gate, "x_gate", lead, D, dt, dev)]
     if x_gate is None and x_bias is not None:
         raise ValueError("x_bias needs an x_gate")
-    for t, name in ((decay, "decay"), (a_bias, "a_bias"), (x_bias, "x_bias")):
-        _check(t, name, (D,), torch.float32, dev)
-    return dev, code, st
+    f32 = _torch().float32
+    _check(decay, "decay", (D,), f32, dev)
+    _check(a_bias, "a_bias", (D,), f32, dev)
+    _check(x_bias, "x_bias", (D,), f32, dev)
+    return code, st
 
 
 def _gated_sequences(x, cu_seqlens, dev):
@@ -1025,7 +1033,7 @@ def mb_gated_scan(x, a_gate, decay, x_gate=None, *, a_bias=None, x_bias=None, cu
     torch = _torch()
     dev = _device_of(x)
     lead, n, T = _gated_sequences(x, cu_seqlens, dev)
-    dev, code, st = _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, lead)
+    code, st = _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, lead, dev)
     D, f32 = x.shape[-1], torch.float32
     n_slots, hs = _gated_pool(h0, h_out, slots, n, D, dev)
     _check(h0, "h0", hs, f32, dev)
@@ -1049,11 +1057,11 @@ def mb_gated_scan_step(x, a_gate, decay, h, x_gate=None, *, a_bias=None, x_bias=
     """One token of mb_gated_scan per sequence.  x, a_gate, x_gate (n, D); h (n, D) float32, or with slots
     (n,) int32 a pool (n_slots, D).  With h_out=None the states are updated in place.  Returns (y, h_out)."""
     torch = _torch()
-    _device_of(x)
+    dev = _device_of(x)
     if x.dim() != 2:
         raise ValueError("x must be (n, D)")
     n, D = x.shape
-    dev, code, st = _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, (n,))
+    code, st = _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, (n,), dev)
     n_slots, hs = _gated_pool(h, h_out, slots, n, D, dev)
     _check(h, "h", hs, torch.float32, dev)
     h_out = h if h_out is None else _check(h_out, "h_out", hs, torch.float32, dev)
@@ -1073,7 +1081,7 @@ def mb_gated_scan_bwd(x, a_gate, decay, dy, x_gate=None, *, a_bias=None, x_bias=
     torch = _torch()
     dev = _device_of(x)
     lead, n, T = _gated_sequences(x, cu_seqlens, dev)
-    dev, code, st = _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, lead)
+    code, st = _gated_args(x, a_gate, decay, x_gate, a_bias, x_bias, lead, dev)
     D, f32, dt = x.shape[-1], torch.float32, x.dtype
     _check(dy, "dy", lead + (D,), dt, dev)
     for t, name in ((h0, "h0"), (dh_out, "dh_out")):
@@ -1146,8 +1154,11 @@ def mb_qk_norm_rope(q, k=None, freqs=None, positions=None, *, q_weight=None, k_w
             out.append(None)
             so.append(0)
             continue
-        t = q.new_empty(lead + (H, D)) if t is None else t
-        so.append(_tokens(t, name, lead, H, D, q.dtype, dev))
+        if t is None:
+            t = q.new_empty(lead + (H, D))
+            so.append(H * D)
+        else:
+            so.append(_tokens(t, name, lead, H, D, q.dtype, dev))
         out.append(t)
     _call_on(dev, "mb_qk_norm_rope", _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(freqs) if R else None, _ptr(positions),
              _ptr(out[0]), _ptr(out[1]), T, L, Hq, Hk, D, R, *st, *so, int(bool(interleaved)), float(eps), code)

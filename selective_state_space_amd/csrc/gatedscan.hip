@@ -329,8 +329,6 @@ __device__ __forceinline__ void fetch_look(const GsArgs& A, int j, int src, int 
     const int64_t row = (int64_t)A.cols * kCols;
     const uint64_t* agg = A.ch.agg + lo * row + col * kCols;
     const uint32_t* incl = A.ch.incl + (group - 1) * row + col * kCols;
-    constexpr int N = kGroup / NW;
-    uint64_t w[N];
     int polls = 0;
     const auto read = [&](int i) -> uint64_t {
         if (i == kGroup - 1) {
@@ -339,15 +337,22 @@ __device__ __forceinline__ void fetch_look(const GsArgs& A, int j, int src, int 
         }
         return lo + i < j ? peek(agg + i * row + lane) : 0;
     };
+    // All reads are under way at a time; what came too early is read again, one word after the other.
+    constexpr int N = kGroup / NW;
+    uint64_t w[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) w[n] = read(wave + n * NW);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        while (w[n] == kNone && ++polls < kPolls) {
+    for (int n = 0; n < N; ++n) look[wave + n * NW][lane] = w[n];
+#pragma unroll 1
+    for (int i = wave; i < kGroup; i += NW) {
+        uint64_t v = look[i][lane];
+        if (v != kNone) continue;
+        while (v == kNone && ++polls < kPolls) {
             __builtin_amdgcn_s_sleep(1);
-            w[n] = read(wave + n * NW);
+            v = read(i);
         }
-        look[wave + n * NW][lane] = w[n];
+        look[i][lane] = v;
     }
 }
 
@@ -380,7 +385,15 @@ __global__ void __launch_bounds__(256) k_gs_setup(Setup S) {
         for (int64_t i = i0; i < words; i += step) S.ch[k].agg[i] = kNone;
         for (int64_t i = i0; i < states; i += step) S.ch[k].incl[i] = (uint32_t)kNone;
         for (int64_t i = i0; i < S.columns / kCols; i += step) S.ch[k].ticket[i * kCounter] = 0;
-        if (S.cu)
+        if (S.cu && S.n_seq < 64) {
+            // one look at all offsets, a lane each
+            const int lane = threadIdx.x & 63;
+            const int own = lane <= S.n_seq ? min(max(S.cu[lane], 0), S.T) : 0x7fffffff;
+            for (int64_t i = i0 >> 6; i <= S.tiles[k]; i += step >> 6) {
+                const int n = __popcll(__ballot(own <= i * S.tokens[k]));
+                if (lane == 0) S.ch[k].first[i] = n - 1;
+            }
+        } else if (S.cu)
             for (int64_t i = i0; i <= S.tiles[k]; i += step) {
                 const int64_t t = i * S.tokens[k];
                 int lo = 0, hi = S.n_seq + 1;              // offsets at or before t
@@ -666,6 +679,8 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 2) k_gs_backward(GsArgs A)
             w[k][i] = q.x2 * 0.69314718056f * not_s;
             const float root = q.a * q.a * b[k][i] * __builtin_amdgcn_rcpf(q.less);
             r[k][i] = q.less < 0x1p-120f ? 0.0f : root;
+            // made here and held, rather than their factors, of which there are more
+            asm volatile("" : "+v"(w[k][i]), "+v"(r[k][i]), "+v"(bn[k][i]));
             S[i] += q.x2;
         }
     const auto spans = [&](auto plain) {
@@ -789,19 +804,19 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 2) k_gs_backward(GsArgs A)
     }
 }
 
-// The sums over tokens of ddecay, da_bias and dx_bias from the tiles' shares: a workgroup adds up 64 columns of one of them, its 16
-// groups of lanes dealing the tiles out.
+// The sums over tokens of ddecay, da_bias and dx_bias from the tiles' shares, in a fixed order: a workgroup adds up 32 columns of one of
+// them, its 32 groups of lanes dealing the tiles out.
 __global__ void __launch_bounds__(1024) k_gs_sums(const float* __restrict__ part, int tiles, int cols, int D, float* d0, float* d1, float* d2) {
-    __shared__ float red[16][kCols];
-    const int which = blockIdx.y, lane = threadIdx.x & 63, grp = threadIdx.x >> 6, c = blockIdx.x * kCols + lane;
+    __shared__ float red[32][33];
+    const int which = blockIdx.y, lane = threadIdx.x & 31, grp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float* d = which == 0 ? d0 : which == 1 ? d1 : d2;
     if (!d) return;
     const int64_t row = (int64_t)cols * kCols;
     float s = 0.0f;
-    for (int i = grp; i < tiles; i += 16 * 8) {
+    for (int i = grp; i < tiles; i += 32 * 8) {
         float t[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t[k] = i + 16 * k < tiles ? part[((int64_t)(i + 16 * k) * 3 + which) * row + c] : 0.0f;
+        for (int k = 0; k < 8; ++k) t[k] = i + 32 * k < tiles ? part[((int64_t)(i + 32 * k) * 3 + which) * row + c] : 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) s += t[k];
     }
@@ -810,7 +825,7 @@ __global__ void __launch_bounds__(1024) k_gs_sums(const float* __restrict__ part
     if (grp == 0 && c < D) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s += red[i][lane];
+        for (int i = 0; i < 32; ++i) s += red[i][lane];
         d[c] = s;
     }
 }
@@ -1100,6 +1115,6 @@ extern "C" mb_status mb_gated_scan_bwd(const void* x, const void* a_gate, const 
     A.part = ddecay || da_bias || dx_bias ? (float*)(base + bp.part_at) : nullptr;
     if ((st = dtype == MB_F32 ? run_backward<float>(A, stream) : run_backward<bf16>(A, stream)) != MB_OK) return st;
     if (!A.part) return MB_OK;
-    hipLaunchKernelGGL(k_gs_sums, dim3((unsigned)A.cols, 3), dim3(1024), 0, stream, A.part, A.tiles, A.cols, A.D, ddecay, da_bias, dx_bias);
+    hipLaunchKernelGGL(k_gs_sums, dim3((unsigned)A.cols * (kCols / 32), 3), dim3(1024), 0, stream, A.part, A.tiles, A.cols, A.D, ddecay, da_bias, dx_bias);
     return check_launch();
 }

@@ -10,6 +10,7 @@
 // one lane whichever way they are paired, two pieces of four neighbouring columns.  A workgroup takes some tokens with all
 // their heads, and makes the tokens' sines and cosines once, in LDS, for all of them.
 #include <algorithm>
+#include <type_traits>
 
 #include "mb_internal.h"
 
@@ -283,7 +284,6 @@ __global__ void __launch_bounds__(256) k_qk_backward(QkArgs A) {
     __shared__ float red[RS][LPR * 8 + 1];
     const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
     const Columns c = columns(A, lane);
-    const int nh = A.H[0] + A.H[1];
     float wu[2][4], wv[2][4], du[2][4], dv[2][4];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -291,31 +291,30 @@ __global__ void __launch_bounds__(256) k_qk_backward(QkArgs A) {
         for (int i = 0; i < 4; ++i) du[k][i] = dv[k][i] = 0.0f;
         load_weights<VEC>(A.w[k], c, wu[k], wv[k]);
     }
-    const float inv_d = 1.0f / (float)A.D, inv_nh = 1.0f / (float)nh;
-    for (int64_t t0 = (int64_t)blockIdx.x * A.tokens; t0 < A.T; t0 += (int64_t)gridDim.x * A.tokens) {
-        const int rows = (int)min((int64_t)A.tokens, A.T - t0) * nh;
-        __syncthreads();                          // the turns of the block before have been read
-        if (A.R) fill_turns<LPR>(A, t0, A.tokens, cs);
-        __syncthreads();
+    const float inv_d = 1.0f / (float)A.D;
+    // The rows of n tokens from t0 on of queries or of keys: which of both is known where it is compiled.
+    const auto rows_of = [&](auto which, int64_t t0, int n) {
+        constexpr int k = decltype(which)::value;
+        const int nh = A.H[k], rows = n * nh;
+        const float inv_nh = 1.0f / (float)nh;
+        const T* in = (const T*)A.in[k] + t0 * A.in_ts[k];
+        const T* up = (const T*)A.d[k] + t0 * A.out_ts[k];
+        T* out = (T*)A.out[k] + t0 * A.out_ts[k];
         for (int r0 = slot; r0 < rows; r0 += B * RS) {
             Part<T, VEC> x[B], d[B];
-            int t[B], k[B], h[B];
+            int t[B], h[B];
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                const int r = r0 + b * RS;
-                if (r < rows) {
-                    t[b] = (int)(((float)r + 0.5f) * inv_nh);
-                    h[b] = r - t[b] * nh;
-                    k[b] = h[b] >= A.H[0];
-                    h[b] -= k[b] ? A.H[0] : 0;
-                    x[b].load((const T*)(k[b] ? A.in[1] : A.in[0]) + (t0 + t[b]) * (k[b] ? A.in_ts[1] : A.in_ts[0]) + h[b] * A.D, c);
-                    d[b].load((const T*)(k[b] ? A.d[1] : A.d[0]) + (t0 + t[b]) * (k[b] ? A.out_ts[1] : A.out_ts[0]) + h[b] * A.D, c);
-                }
+                const int r = min(r0 + b * RS, rows - 1);           // rows behind the last are the last one again, and not written
+                t[b] = (int)(((float)r + 0.5f) * inv_nh);
+                h[b] = (r - t[b] * nh) * A.D;
+                x[b].load(in + t[b] * A.in_ts[k] + h[b], c);
+                d[b].load(up + t[b] * A.out_ts[k] + h[b], c);
             }
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                if (r0 + b * RS >= rows) continue;
-                float u[4], v[4], eu[4], ev[4], ss = 0.0f, dot = 0.0f, up;
+                const bool live = r0 + b * RS < rows;
+                float u[4], v[4], eu[4], ev[4], ss = 0.0f, dot = 0.0f, scale_up;
                 x[b].get(u, v, c);
                 d[b].get(eu, ev, c);
 #pragma unroll
@@ -326,32 +325,35 @@ __global__ void __launch_bounds__(256) k_qk_backward(QkArgs A) {
                         turn(eu[i], ev[i], q[0], -q[1]);
                     }
                 }
-                const float rs = inverse_rms<LPR>(row_all<LPR>(ss), u, v, A.D, A.eps, up);
+                const float rs = inverse_rms<LPR>(row_all<LPR>(ss), u, v, A.D, A.eps, scale_up);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    u[i] = u[i] * up * rs;
-                    v[i] = v[i] * up * rs;
-                    if (k[b]) {
-                        du[1][i] = fmaf(eu[i], u[i], du[1][i]);
-                        dv[1][i] = fmaf(ev[i], v[i], dv[1][i]);
-                    } else {
-                        du[0][i] = fmaf(eu[i], u[i], du[0][i]);
-                        dv[0][i] = fmaf(ev[i], v[i], dv[0][i]);
-                    }
-                    eu[i] *= k[b] ? wu[1][i] : wu[0][i];
-                    ev[i] *= k[b] ? wv[1][i] : wv[0][i];
+                    u[i] = u[i] * scale_up * rs;
+                    v[i] = v[i] * scale_up * rs;
+                    du[k][i] = live ? fmaf(eu[i], u[i], du[k][i]) : du[k][i];
+                    dv[k][i] = live ? fmaf(ev[i], v[i], dv[k][i]) : dv[k][i];
+                    eu[i] *= wu[k][i];
+                    ev[i] *= wv[k][i];
                     dot = fmaf(eu[i], u[i], fmaf(ev[i], v[i], dot));
                 }
                 dot = row_all<LPR>(dot) * inv_d;
-                const float scale = rs * up;
+                const float scale = rs * scale_up;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     eu[i] = scale * fmaf(-u[i], dot, eu[i]);
                     ev[i] = scale * fmaf(-v[i], dot, ev[i]);
                 }
-                Part<T, VEC>::store((T*)(k[b] ? A.out[1] : A.out[0]) + (t0 + t[b]) * (k[b] ? A.out_ts[1] : A.out_ts[0]) + h[b] * A.D, eu, ev, c);
+                if (live) Part<T, VEC>::store(out + t[b] * A.out_ts[k] + h[b], eu, ev, c);
             }
         }
+    };
+    for (int64_t t0 = (int64_t)blockIdx.x * A.tokens; t0 < A.T; t0 += (int64_t)gridDim.x * A.tokens) {
+        const int n = (int)min((int64_t)A.tokens, A.T - t0);
+        __syncthreads();                          // the turns of the block before have been read
+        if (A.R) fill_turns<LPR>(A, t0, A.tokens, cs);
+        __syncthreads();
+        rows_of(std::integral_constant<int, 0>{}, t0, n);
+        if (A.H[1]) rows_of(std::integral_constant<int, 1>{}, t0, n);
     }
     if (!A.part) return;
 #pragma unroll
@@ -374,18 +376,18 @@ __global__ void __launch_bounds__(256) k_qk_backward(QkArgs A) {
     }
 }
 
-// dw from the workgroups' shares, in a fixed order: 64 columns a workgroup, its 16 groups of lanes dealing the shares out.
+// dw from the workgroups' shares, in a fixed order: 32 columns a workgroup, its 32 groups of lanes dealing the shares out.
 __global__ void __launch_bounds__(1024) k_qk_sum(const float* __restrict__ part, int n, int D, float* dq, float* dk) {
-    __shared__ float red[16][64];
+    __shared__ float red[32][33];
     float* dw = blockIdx.y ? dk : dq;
     if (!dw) return;
-    const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6, d = blockIdx.x * 64 + lane;
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5, d = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (d < D)
-        for (int i = grp; i < n; i += 16 * 8) {
+        for (int i = grp; i < n; i += 32 * 8) {
             float t[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t[k] = i + 16 * k < n ? part[((int64_t)(i + 16 * k) * 2 + blockIdx.y) * D + d] : 0.0f;
+            for (int k = 0; k < 8; ++k) t[k] = i + 32 * k < n ? part[((int64_t)(i + 32 * k) * 2 + blockIdx.y) * D + d] : 0.0f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) s += t[k];
         }
@@ -394,7 +396,7 @@ __global__ void __launch_bounds__(1024) k_qk_sum(const float* __restrict__ part,
     if (grp == 0 && d < D) {
         s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s += red[i][lane];
+        for (int i = 0; i < 32; ++i) s += red[i][lane];
         dw[d] = s;
     }
 }
@@ -582,7 +584,7 @@ extern "C" mb_status mb_qk_norm_rope_bwd(const void* dq_out, const void* dk_out,
         if ((st = check_launch()) != MB_OK) return st;
     }
     if (!dq_weight && !dk_weight) return MB_OK;
-    hipLaunchKernelGGL(k_qk_sum, dim3((unsigned)((D + 63) / 64), 2), dim3(1024), 0, stream, (const float*)A.part, (int)parts, (int)D, dq_weight,
+    hipLaunchKernelGGL(k_qk_sum, dim3((unsigned)((D + 31) / 32), 2), dim3(1024), 0, stream, (const float*)A.part, (int)parts, (int)D, dq_weight,
                        dk_weight);
     return check_launch();
 }
