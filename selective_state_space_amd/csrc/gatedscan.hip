@@ -125,8 +125,11 @@ __device__ __forceinline__ float half_of(f2 v, int i) { return v[i]; }
 // `n` rows of a tile as a buffer: what lies outside reads zero.
 template <typename T>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* p, int64_t t0, int64_t ts, int n, int D) {
+    // The same in all lanes, and known to be: a descriptor in vector registers costs a loop for every access.
+    n = __builtin_amdgcn_readfirstlane(n);
+    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane((int)t0);
     const uint32_t bytes = n > 0 ? (uint32_t)(n - 1) * (uint32_t)ts * sizeof(T) + (uint32_t)D * sizeof(T) : 0;
-    return __builtin_amdgcn_make_buffer_rsrc((void*)((const T*)p + t0 * ts), 0, (int)bytes, 0x00027000);
+    return __builtin_amdgcn_make_buffer_rsrc((void*)((const T*)p + row0 * ts), 0, (int)bytes, 0x00027000);
 }
 
 // `row`: the same in all lanes, a scalar operand (a sum in a vector register for each row would be held over the whole walk); the
@@ -134,12 +137,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* p, int64_t
 template <typename T, bool PAIR>
 __device__ __forceinline__ typename Raw<T>::type load2(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t row) {
     if constexpr (sizeof(T) == 2) {
-        if constexpr (PAIR) return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0);
+        if constexpr (PAIR) return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 2);
         const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
         const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off + 2, row, 0);
         return lo | hi << 16;
     } else {
-        if constexpr (PAIR) return __builtin_bit_cast(f2, __builtin_amdgcn_raw_buffer_load_b64(r, off, row, 0));
+        if constexpr (PAIR) return __builtin_bit_cast(f2, __builtin_amdgcn_raw_buffer_load_b64(r, off, row, 2));
         f2 v;
         v[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0));
         v[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off + 4, row, 0));
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
 // the gradient that comes back out of the tiles behind, handed on like the states forward.  The tokens are walked three times in
 // registers: forward and back for what the tile hands on, forward for h_{t-1}, back for G and the gradients.
 template <typename T, bool PAIR, int K>
-__global__ void __launch_bounds__(kTileBack / K * 32, 2) k_gs_backward(GsArgs A) {
+__global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A) {
     constexpr int NG = kTileBack / K, NT = NG * 32;
     __shared__ f4 comp[NG][kCols];          // of every group: (S, U) forward, (S, V) backward
     __shared__ f2 entry[NG][kCols];         // the state in front of it, the gradient from behind it
@@ -653,6 +656,15 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 2) k_gs_backward(GsArgs A)
         find_events<kTileBack, NG, true>(A, p, ev, c, live, A.dh_out, A.dh0);
         begins = ev.begins[grp];
         ends = ev.ends[grp];
+        // Tokens of no sequence count as zeros, whatever they hold: nothing comes to them and they give nothing.
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const bool in = grp * K + k >= p.lo && grp * K + k < p.hi;
+            ra[k] = in ? ra[k] : typename Raw<T>::type{};
+            rx[k] = in ? rx[k] : typename Raw<T>::type{};
+            rg[k] = in ? rg[k] : typename Raw<T>::type{};
+            rd[k] = in ? rd[k] : typename Raw<T>::type{};
+        }
     }
     // A row's values in place of what comes from the neighbouring token.  Not before its turn: rows of many tokens would be held.
     const auto set = [&](float (&v)[2], const float* q, int row) {
@@ -662,44 +674,39 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 2) k_gs_backward(GsArgs A)
     };
 
     // of every token: a, b, beta i, a^2 b / (1 - a^2) and then dla / G, s, la (1 - s), b (1 - i)
-    float a[K][2], b[K][2], bi[K][2], r[K][2], s[K][2], w[K][2], bn[K][2];
+    float a[K][2], bi[K][2], r[K][2], sm[K][2], bn[K][2];
     float S[2] = {0.0f, 0.0f}, U[2] = {0.0f, 0.0f}, V[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float not_s, ig, not_i;
-            sigma2(half_of(ra[k], i), par.nab[i], s[k][i], not_s);
-            const Gate q = gate(s[k][i], par.nd[i]);
+            float s, not_s, ig, not_i;
+            sigma2(half_of(ra[k], i), par.nab[i], s, not_s);
+            const Gate q = gate(s, par.nd[i]);
             sigma2(half_of(rg[k], i), par.nxb[i], ig, not_i);
             a[k][i] = q.a;
             bi[k][i] = q.beta * ig;
-            b[k][i] = bi[k][i] * half_of(rx[k], i);
-            bn[k][i] = b[k][i] * not_i;
-            w[k][i] = q.x2 * 0.69314718056f * not_s;
-            const float root = q.a * q.a * b[k][i] * __builtin_amdgcn_rcpf(q.less);
+            const float b = bi[k][i] * half_of(rx[k], i);
+            bn[k][i] = b * not_i;
+            sm[k][i] = s > not_s ? -not_s : s;
+            const float root = q.a * q.a * b * __builtin_amdgcn_rcpf(q.less);
             r[k][i] = q.less < 0x1p-120f ? 0.0f : root;
             // made here and held, rather than their factors, of which there are more
-            asm volatile("" : "+v"(w[k][i]), "+v"(r[k][i]), "+v"(bn[k][i]));
+            asm volatile("" : "+v"(sm[k][i]), "+v"(r[k][i]), "+v"(bn[k][i]));
             S[i] += q.x2;
         }
-    const auto spans = [&](auto plain) {
-        constexpr bool P = decltype(plain)::value;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (!P && (begins >> k & 1)) set(U, A.h0, ev.begin[grp * K + k]);
+    for (int k = 0; k < K; ++k) {
+        if (!p.plain && (begins >> k & 1)) set(U, A.h0, ev.begin[grp * K + k]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) U[i] = fmaf(a[k][i], U[i], b[k][i]);
-        }
+        for (int i = 0; i < 2; ++i) U[i] = fmaf(a[k][i], U[i], bi[k][i] * half_of(rx[k], i));
+    }
 #pragma unroll
-        for (int k = K - 1; k >= 0; --k) {
-            if (!P && (ends >> k & 1)) set(V, A.dh_out, ev.end[grp * K + k]);
+    for (int k = K - 1; k >= 0; --k) {
+        if (!p.plain && (ends >> k & 1)) set(V, A.dh_out, ev.end[grp * K + k]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) V[i] = a[k][i] * (half_of(rd[k], i) + V[i]);
-        }
-    };
-    if (p.plain) spans(std::true_type{});
-    else spans(std::false_type{});
+        for (int i = 0; i < 2; ++i) V[i] = a[k][i] * (half_of(rd[k], i) + V[i]);
+    }
     const bool cut = begins != 0, cut_back = ends != 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) comp[grp][c2 + i] = f4{cut ? 1.0f : S[i], U[i], cut_back ? 1.0f : S[i], V[i]};
@@ -751,44 +758,43 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 2) k_gs_backward(GsArgs A)
     const __amdgpu_buffer_rsrc_t bdg = rows_at<T>(A.dg, p.t0, A.D, A.g ? p.n : 0, A.D);
     const uint32_t sd = (uint32_t)A.D * sizeof(T);
     const Place2 od = place2<T>(grp * K * sd + c * sizeof(T), live);
-    const auto walk = [&](auto plain) {
-        constexpr bool P = decltype(plain)::value;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (!P && (begins >> k & 1)) set(h, A.h0, ev.begin[grp * K + k]);
+    for (int k = 0; k < K; ++k) {
+        if (!p.plain && (begins >> k & 1)) set(h, A.h0, ev.begin[grp * K + k]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            r[k][i] = fmaf(a[k][i], h[i], -r[k][i]);
+            h[i] = fmaf(a[k][i], h[i], bi[k][i] * half_of(rx[k], i));
+        }
+    }
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+        float dx[2], da[2], dg[2];
+        if (!p.plain && (ends >> k & 1)) set(g, A.dh_out, ev.end[grp * K + k]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float G = half_of(rd[k], i) + g[i], dla = G * r[k][i];
+            g[i] = a[k][i] * G;
+            dx[i] = G * bi[k][i];
+            dg[i] = G * bn[k][i];
+            const float m = sm[k][i], s = m < 0.0f ? 1.0f + m : m, not_s = m < 0.0f ? -m : 1.0f - m;
+            da[i] = dla * (par.nd[i] * 0.69314718056f * s * not_s);
+            sum[0][i] = fmaf(-dla, s, sum[0][i]);
+            sum[1][i] += da[i];
+            sum[2][i] += dg[i];
+        }
+        store2<T, PAIR>(bdx, od, k * sd, dx[0], dx[1]);
+        store2<T, PAIR>(bda, od, k * sd, da[0], da[1]);
+        store2<T, PAIR>(bdg, od, k * sd, dg[0], dg[1]);
+        if (!p.plain && (begins >> k & 1)) {
+            const int64_t at = (int64_t)ev.begin[grp * K + k] * A.D + c;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                r[k][i] = fmaf(a[k][i], h[i], -r[k][i]);
-                h[i] = fmaf(a[k][i], h[i], b[k][i]);
+                if (A.dh0 && i < live) A.dh0[at + i] = g[i];
+                g[i] = 0.0f;            // for tokens of no sequence in front of it
             }
         }
-#pragma unroll
-        for (int k = K - 1; k >= 0; --k) {
-            const int t = grp * K + k;
-            const bool in = P || (t >= p.lo && t < p.hi);
-            float dx[2], da[2], dg[2];
-            if (!P && (ends >> k & 1)) set(g, A.dh_out, ev.end[t]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float G = half_of(rd[k], i) + g[i];
-                g[i] = a[k][i] * G;
-                // tokens of no sequence have no gradients, whatever they hold
-                const float dla = in ? G * r[k][i] : 0.0f;
-                dx[i] = in ? G * bi[k][i] : 0.0f;
-                dg[i] = in ? G * bn[k][i] : 0.0f;
-                da[i] = in ? dla * w[k][i] : 0.0f;
-                sum[0][i] = in ? fmaf(-dla, s[k][i], sum[0][i]) : sum[0][i];
-                sum[1][i] += da[i];
-                sum[2][i] += dg[i];
-                if (!P && (begins >> k & 1) && A.dh0 && i < live) A.dh0[(int64_t)ev.begin[t] * A.D + c + i] = g[i];
-            }
-            store2<T, PAIR>(bdx, od, k * sd, dx[0], dx[1]);
-            store2<T, PAIR>(bda, od, k * sd, da[0], da[1]);
-            store2<T, PAIR>(bdg, od, k * sd, dg[0], dg[1]);
-        }
-    };
-    if (p.plain) walk(std::true_type{});
-    else walk(std::false_type{});
+    }
     if (!A.part) return;
     float (*red)[3][kCols] = reinterpret_cast<float (*)[3][kCols]>(&comp[0][0]);       // comp has been read
 #pragma unroll
