@@ -127,9 +127,10 @@ template <typename T>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* p, int64_t t0, int64_t ts, int n, int D) {
     // The same in all lanes, and known to be: a descriptor in vector registers costs a loop for every access.
     n = __builtin_amdgcn_readfirstlane(n);
-    const int64_t row0 = (int64_t)__builtin_amdgcn_readfirstlane((int)t0);
+    int row0 = __builtin_amdgcn_readfirstlane((int)t0);
+    asm("" : "+s"(n), "+s"(row0));
     const uint32_t bytes = n > 0 ? (uint32_t)(n - 1) * (uint32_t)ts * sizeof(T) + (uint32_t)D * sizeof(T) : 0;
-    return __builtin_amdgcn_make_buffer_rsrc((void*)((const T*)p + row0 * ts), 0, (int)bytes, 0x00027000);
+    return __builtin_amdgcn_make_buffer_rsrc((void*)((const T*)p + (int64_t)row0 * ts), 0, (int)bytes, 0x00027000);
 }
 
 // `row`: the same in all lanes, a scalar operand (a sum in a vector register for each row would be held over the whole walk); the
@@ -570,6 +571,8 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
             if (A.tiles > 1 && j % kGroup == kGroup - 1) publish_state(A, j / kGroup, col * kCols + threadIdx.x, h);
         }
         lds_barrier();
+        // made here: behind the branch below it would come to lie in vector registers
+        const __amdgpu_buffer_rsrc_t by = rows_at<T>(A.y, p.t0, A.D, p.n, A.D);
         const f2 enter = *reinterpret_cast<const f2*>(&entry[grp][c2]);
         float h[2] = {enter[0], enter[1]};
         if (A.states && grp * K % kEvery == 0 && grp * K < p.n && !(begins & 1)) {
@@ -578,7 +581,6 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
             if (live > 1) s[1] = h[1];
         }
         if constexpr (OUT) {
-            const __amdgpu_buffer_rsrc_t by = rows_at<T>(A.y, p.t0, A.D, p.n, A.D);
             const uint32_t sy = (uint32_t)A.D * sizeof(T);
             const Place2 oy = place2<T>(grp * K * sy + c * sizeof(T), live);
             if (p.plain) {
