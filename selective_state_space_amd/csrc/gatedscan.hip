@@ -108,7 +108,15 @@ __device__ __forceinline__ void sigma2(float v, float nb, float& s, float& not_s
 }
 
 // --------------------------------------------------------------- memory ----
-// Two channels beside each other, as they lie in memory.
+// A thread's two channels: beside each other where both can be read at a time (PAIR: they start on a border of two elements everywhere),
+// otherwise half a tile apart, so that a row's threads read neighbouring elements with each of two reads.  16384 tokens of 1001 bf16
+// channels, forward and backward: channels beside each other 55.7 and 107 us read one by one, 64 and 114 read in pairs from odd
+// addresses, half a tile apart 51.6 and 103.
+template <bool PAIR> constexpr int kNext = PAIR ? 1 : kCols / 2;
+template <bool PAIR> __device__ __forceinline__ int first_channel() { return (threadIdx.x & 31) * (PAIR ? 2 : 1); }
+template <bool PAIR> __device__ __forceinline__ int channels_of(int D, int c) { return (c < D) + (c + kNext<PAIR> < D); }
+
+// Two channels as they come from memory.
 template <typename T> struct Raw;
 template <> struct Raw<bf16> {
     typedef uint32_t type;
@@ -140,13 +148,13 @@ __device__ __forceinline__ typename Raw<T>::type load2(__amdgpu_buffer_rsrc_t r,
     if constexpr (sizeof(T) == 2) {
         if constexpr (PAIR) return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 2);
         const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
-        const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off + 2, row, 0);
+        const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off + 2 * kNext<PAIR>, row, 0);
         return lo | hi << 16;
     } else {
         if constexpr (PAIR) return __builtin_bit_cast(f2, __builtin_amdgcn_raw_buffer_load_b64(r, off, row, 2));
         f2 v;
         v[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0));
-        v[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off + 4, row, 0));
+        v[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off + 4 * kNext<PAIR>, row, 0));
         return v;
     }
 }
@@ -157,9 +165,9 @@ struct Place2 {
 };
 constexpr uint32_t kNowhere = 0x80000000u;
 
-template <typename T>
+template <typename T, bool PAIR>
 __device__ __forceinline__ Place2 place2(uint32_t off, int live) {
-    return Place2{live > 0 ? off : kNowhere, live > 1 ? off + (uint32_t)sizeof(T) : kNowhere};
+    return Place2{live > 0 ? off : kNowhere, live > 1 ? off + (uint32_t)sizeof(T) * kNext<PAIR> : kNowhere};
 }
 
 // Rounds to nearest even.
@@ -277,7 +285,7 @@ struct Events {
 
 // Fills them in, all threads together, and settles the sequences of no tokens: `from` rows, or zeros, go to `to`.  BACK: rows are the
 // sequences' numbers.
-template <int TT, int NG, bool BACK>
+template <int TT, int NG, bool BACK, bool PAIR>
 __device__ __forceinline__ void find_events(const GsArgs& A, const Place& p, Events<TT, NG>& ev, int c, int n, const float* from, float* to) {
     constexpr int K = TT / NG;
     const int lane = threadIdx.x & 31;
@@ -301,7 +309,7 @@ __device__ __forceinline__ void find_events(const GsArgs& A, const Place& p, Eve
             }
         } else if (to && row >= 0) {
             for (int i = 0; i < n; ++i) {
-                const int64_t at = (int64_t)row * A.D + c + i;
+                const int64_t at = (int64_t)row * A.D + c + i * kNext<PAIR>;
                 to[at] = from && has ? from[at] : 0.0f;
             }
         }
@@ -421,15 +429,17 @@ __device__ __forceinline__ int take(const GsArgs& A, int col) {
 }
 
 // -decay log2(e) and the biases times -log2(e) of two channels; those behind the last are zero.
+template <bool PAIR>
 struct Params {
     float nd[2], nab[2], nxb[2];
     __device__ __forceinline__ void load(const GsArgs& A, int c, int live) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const bool in = i < live;
-            nd[i] = in ? -A.decay[c + i] * kLog2e : 0.0f;
-            nab[i] = in && A.a_bias ? -A.a_bias[c + i] * kLog2e : 0.0f;
-            nxb[i] = in && A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f;
+            const int at = c + i * kNext<PAIR>;
+            nd[i] = in ? -A.decay[at] * kLog2e : 0.0f;
+            nab[i] = in && A.a_bias ? -A.a_bias[at] * kLog2e : 0.0f;
+            nxb[i] = in && A.x_bias ? -A.x_bias[at] * kLog2e : 0.0f;
         }
     }
 };
@@ -455,21 +465,21 @@ struct Source {
 // OUT: outputs and end states are written; otherwise the states for the backward alone.
 template <typename T, bool PAIR, int K, bool OUT>
 __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
-    constexpr int NG = kTile / K;
+    constexpr int NG = kTile / K, NX = kNext<PAIR>;
     __shared__ f2 comp[NG][kCols];
     __shared__ float entry[NG][kCols];
     __shared__ uint64_t look[kGroup][kCols];
     __shared__ Events<kTile, NG> ev;
     __shared__ int taken;
-    const int c2 = (threadIdx.x & 31) * 2, grp = threadIdx.x >> 5;
+    const int c2 = first_channel<PAIR>(), grp = threadIdx.x >> 5;
     typename Raw<T>::type rx[K], ra[K], rg[K];
-    Params par;
+    Params<PAIR> par;
     const int col = blockIdx.x % A.cols;
     if (threadIdx.x == 0) taken = take(A, col);
     __syncthreads();
     const int j = __builtin_amdgcn_readfirstlane(taken);
     {
-        const int c = col * kCols + c2, live = min(max(A.D - c, 0), 2);          // channels of this thread
+        const int c = col * kCols + c2, live = channels_of<PAIR>(A.D, c);          // channels of this thread
         {
             const int t0 = j * kTile, n = min(A.T - t0, kTile);
             par.load(A, c, live);
@@ -494,7 +504,7 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
         const Place p = place<kTile, false>(A, j);
         uint32_t begins = 0, ends = 0;         // of this thread's tokens: first and last ones of a sequence
         if (!p.plain) {
-            find_events<kTile, NG, false>(A, p, ev, c, live, A.h0, OUT ? A.h_out : nullptr);
+            find_events<kTile, NG, false, PAIR>(A, p, ev, c, live, A.h0, OUT ? A.h_out : nullptr);
             begins = ev.begins[grp];
             ends = ev.ends[grp];
         }
@@ -515,8 +525,8 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
             const int at = __builtin_ctz(m), row = ev.begin[grp * K + at];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float h0 = row >= 0 && i < live ? A.h0[(int64_t)row * A.D + c + i] : 0.0f;
-                if (at == 0 && A.states && i < live && grp * K % kEvery == 0) A.states[(int64_t)((p.t0 + grp * K) / kEvery) * A.D + c + i] = h0;
+                const float h0 = row >= 0 && i < live ? A.h0[(int64_t)row * A.D + c + i * NX] : 0.0f;
+                if (at == 0 && A.states && i < live && grp * K % kEvery == 0) A.states[(int64_t)((p.t0 + grp * K) / kEvery) * A.D + c + i * NX] = h0;
                 float av = 0.0f, bv = 0.0f;
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
@@ -543,7 +553,8 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
                 for (int i = 0; i < 2; ++i) U[i] = a[k][i] < 0.0f ? b[k][i] : fmaf(a[k][i], U[i], b[k][i]);
             if (begins) S[0] = S[1] = 1.0f;      // a logarithm above zero marks what is cut off from the state that enters
         }
-        *reinterpret_cast<f4*>(&comp[grp][c2]) = f4{S[0], U[0], S[1], U[1]};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) comp[grp][c2 + i * NX] = f2{S[i], U[i]};
         lds_barrier();
         if (A.tiles > 1) {
             if (threadIdx.x < kCols) {
@@ -573,16 +584,15 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
         lds_barrier();
         // made here: behind the branch below it would come to lie in vector registers
         const __amdgpu_buffer_rsrc_t by = rows_at<T>(A.y, p.t0, A.D, p.n, A.D);
-        const f2 enter = *reinterpret_cast<const f2*>(&entry[grp][c2]);
-        float h[2] = {enter[0], enter[1]};
+        float h[2] = {entry[grp][c2], entry[grp][c2 + NX]};
         if (A.states && grp * K % kEvery == 0 && grp * K < p.n && !(begins & 1)) {
             float* s = A.states + (int64_t)((p.t0 + grp * K) / kEvery) * A.D + c;
             if (live > 0) s[0] = h[0];
-            if (live > 1) s[1] = h[1];
+            if (live > 1) s[NX] = h[1];
         }
         if constexpr (OUT) {
             const uint32_t sy = (uint32_t)A.D * sizeof(T);
-            const Place2 oy = place2<T>(grp * K * sy + c * sizeof(T), live);
+            const Place2 oy = place2<T, PAIR>(grp * K * sy + c * sizeof(T), live);
             if (p.plain) {
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
@@ -609,7 +619,7 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
                         float v = 0.0f;
 #pragma unroll
                         for (int k = 0; k < K; ++k) v = k == at ? b[k][i] : v;
-                        if (i < live) A.h_out[(int64_t)row * A.D + c + i] = v;
+                        if (i < live) A.h_out[(int64_t)row * A.D + c + i * NX] = v;
                     }
                 }
             }
@@ -623,21 +633,21 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
 // registers: forward and back for what the tile hands on, forward for h_{t-1}, back for G and the gradients.
 template <typename T, bool PAIR, int K>
 __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A) {
-    constexpr int NG = kTileBack / K, NT = NG * 32;
+    constexpr int NG = kTileBack / K, NT = NG * 32, NX = kNext<PAIR>;
     __shared__ f4 comp[NG][kCols];          // of every group: (S, U) forward, (S, V) backward
     __shared__ f2 entry[NG][kCols];         // the state in front of it, the gradient from behind it
     __shared__ uint64_t look[kGroup][kCols];
     __shared__ Events<kTileBack, NG> ev;
     __shared__ int taken;
     static_assert(kTileBack == kEvery, "a tile starts from a kept state");
-    const int c2 = (threadIdx.x & 31) * 2, grp = threadIdx.x >> 5;
+    const int c2 = first_channel<PAIR>(), grp = threadIdx.x >> 5;
     typename Raw<T>::type rx[K], ra[K], rg[K], rd[K];
-    Params par;
+    Params<PAIR> par;
     const int col = blockIdx.x % A.cols;
     if (threadIdx.x == 0) taken = take(A, col);
     __syncthreads();
     const int jr = __builtin_amdgcn_readfirstlane(taken), j = A.tiles - 1 - jr;
-    const int c = col * kCols + c2, live = min(max(A.D - c, 0), 2);
+    const int c = col * kCols + c2, live = channels_of<PAIR>(A.D, c);
     {
         const int t0 = j * kTileBack, n = min(A.T - t0, kTileBack);
         par.load(A, c, live);
@@ -655,7 +665,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
     const Place p = place<kTileBack, true>(A, j);
     uint32_t begins = 0, ends = 0;
     if (!p.plain) {
-        find_events<kTileBack, NG, true>(A, p, ev, c, live, A.dh_out, A.dh0);
+        find_events<kTileBack, NG, true, PAIR>(A, p, ev, c, live, A.dh_out, A.dh0);
         begins = ev.begins[grp];
         ends = ev.ends[grp];
         // Tokens of no sequence count as zeros, whatever they hold: nothing comes to them and they give nothing.
@@ -672,7 +682,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
     const auto set = [&](float (&v)[2], const float* q, int row) {
         asm volatile("" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < 2; ++i) v[i] = q && i < live ? q[(int64_t)row * A.D + c + i] : 0.0f;
+        for (int i = 0; i < 2; ++i) v[i] = q && i < live ? q[(int64_t)row * A.D + c + i * NX] : 0.0f;
     };
 
     // of every token: a, b, beta i, a^2 b / (1 - a^2) and then dla / G, s, la (1 - s), b (1 - i)
@@ -711,7 +721,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
     }
     const bool cut = begins != 0, cut_back = ends != 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) comp[grp][c2 + i] = f4{cut ? 1.0f : S[i], U[i], cut_back ? 1.0f : S[i], V[i]};
+    for (int i = 0; i < 2; ++i) comp[grp][c2 + i * NX] = f4{cut ? 1.0f : S[i], U[i], cut_back ? 1.0f : S[i], V[i]};
     lds_barrier();
     const int src = A.tiles - 1 - p.src;
     if (A.tiles > 1) {
@@ -752,14 +762,14 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
     float h[2], g[2], sum[3][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        h[i] = entry[grp][c2 + i][0];
-        g[i] = entry[grp][c2 + i][1];
+        h[i] = entry[grp][c2 + i * NX][0];
+        g[i] = entry[grp][c2 + i * NX][1];
         sum[0][i] = sum[1][i] = sum[2][i] = 0.0f;
     }
     const __amdgpu_buffer_rsrc_t bdx = rows_at<T>(A.dx, p.t0, A.D, p.n, A.D), bda = rows_at<T>(A.da, p.t0, A.D, p.n, A.D);
     const __amdgpu_buffer_rsrc_t bdg = rows_at<T>(A.dg, p.t0, A.D, A.g ? p.n : 0, A.D);
     const uint32_t sd = (uint32_t)A.D * sizeof(T);
-    const Place2 od = place2<T>(grp * K * sd + c * sizeof(T), live);
+    const Place2 od = place2<T, PAIR>(grp * K * sd + c * sizeof(T), live);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         if (!p.plain && (begins >> k & 1)) set(h, A.h0, ev.begin[grp * K + k]);
@@ -792,7 +802,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
             const int64_t at = (int64_t)ev.begin[grp * K + k] * A.D + c;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (A.dh0 && i < live) A.dh0[at + i] = g[i];
+                if (A.dh0 && i < live) A.dh0[at + i * NX] = g[i];
                 g[i] = 0.0f;            // for tokens of no sequence in front of it
             }
         }
@@ -802,7 +812,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
 #pragma unroll
     for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) red[grp][q][c2 + i] = sum[q][i];
+        for (int i = 0; i < 2; ++i) red[grp][q][c2 + i * NX] = sum[q][i];
     lds_barrier();
     for (int i = threadIdx.x; i < 3 * kCols; i += NT) {
         float v = 0.0f;
@@ -843,8 +853,9 @@ __global__ void __launch_bounds__(1024) k_gs_sums(const float* __restrict__ part
 template <typename T, bool PAIR>
 __global__ void __launch_bounds__(256) k_gs_step(GsArgs A, int64_t n0, int blocks) {
     const int64_t n = n0 + blockIdx.x / blocks;
-    const int c = ((int)(blockIdx.x % blocks) * 256 + threadIdx.x) * 2, live = min(A.D - c, 2);
-    if (live <= 0) return;
+    constexpr int NX = kNext<PAIR>;
+    const int c = ((int)(blockIdx.x % blocks) * 8 + (threadIdx.x >> 5)) * kCols + first_channel<PAIR>(), live = channels_of<PAIR>(A.D, c);
+    if (live == 0) return;
     const __amdgpu_buffer_rsrc_t bx = rows_at<T>(A.x, n, A.x_ts, 1, A.D), ba = rows_at<T>(A.a, n, A.a_ts, 1, A.D);
     const __amdgpu_buffer_rsrc_t bg = rows_at<T>(A.g, n, A.g_ts, A.g ? 1 : 0, A.D), by = rows_at<T>(A.y, n, A.D, 1, A.D);
     const auto rx = load2<T, PAIR>(bx, c * sizeof(T), 0), ra = load2<T, PAIR>(ba, c * sizeof(T), 0);
@@ -857,17 +868,17 @@ __global__ void __launch_bounds__(256) k_gs_step(GsArgs A, int64_t n0, int block
     float h[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        const int at = c + i * NX;
         h[i] = 0.0f;
         if (i < live) {
-            if (A.h0 && row >= 0) h[i] = A.h0[row * A.D + c + i];
-            const Gate q = gate(sigma(half_of(ra, i), A.a_bias ? -A.a_bias[c + i] * kLog2e : 0.0f), -A.decay[c + i] * kLog2e);
-            const float x = half_of(rx, i);
-            const float ig = sigma(half_of(rg, i), A.x_bias ? -A.x_bias[c + i] * kLog2e : 0.0f);
-            h[i] = fmaf(q.a, h[i], q.beta * ig * x);
-            if (row >= 0) A.h_out[row * A.D + c + i] = h[i];
+            if (A.h0 && row >= 0) h[i] = A.h0[row * A.D + at];
+            const Gate q = gate(sigma(half_of(ra, i), A.a_bias ? -A.a_bias[at] * kLog2e : 0.0f), -A.decay[at] * kLog2e);
+            const float ig = sigma(half_of(rg, i), A.x_bias ? -A.x_bias[at] * kLog2e : 0.0f);
+            h[i] = fmaf(q.a, h[i], q.beta * ig * half_of(rx, i));
+            if (row >= 0) A.h_out[row * A.D + at] = h[i];
         }
     }
-    store2<T, PAIR>(by, place2<T>(c * sizeof(T), live), 0, h[0], h[1]);
+    store2<T, PAIR>(by, place2<T, PAIR>(c * sizeof(T), live), 0, h[0], h[1]);
 }
 
 // ------------------------------------------------------------------ host ----
