@@ -283,35 +283,51 @@ struct Events {
     int begin[TT], end[TT];
 };
 
-// Fills them in, all threads together, and settles the sequences of no tokens: `from` rows, or zeros, go to `to`.  BACK: rows are the
-// sequences' numbers.
-template <int TT, int NG, bool BACK, bool PAIR>
-__device__ __forceinline__ void find_events(const GsArgs& A, const Place& p, Events<TT, NG>& ev, int c, int n, const float* from, float* to) {
+// Fills them in, all threads together, a sequence each, and settles the sequences of no tokens: their `from` rows, or zeros, go to `to`, four
+// rows of the column's 64 channels at a time in a wave (offsets padded to a thousand sequences and more are all in one tile).  BACK: rows
+// are the sequences' numbers.
+template <int TT, int NG, bool BACK>
+__device__ __forceinline__ void find_events(const GsArgs& A, const Place& p, Events<TT, NG>& ev, int col, const float* from, float* to) {
     constexpr int K = TT / NG;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 63;
     if (threadIdx.x < NG) ev.begins[threadIdx.x] = ev.ends[threadIdx.x] = 0;
     lds_barrier();
-    for (int s = p.sa + (int)(threadIdx.x >> 5); s <= p.sb; s += NG) {
-        int b, e;
-        range_of(A, s, b, e);
-        const int row = BACK ? s : row_of(A, s);
-        const bool has = BACK || (row >= 0 && A.h0 && (!A.has_h0 || A.has_h0[s]));
-        if (b < e) {
-            b -= p.t0;
-            e -= p.t0 + 1;
-            if (lane == 0 && b >= 0 && b < p.n) {
-                ev.begin[b] = has ? row : -1;
-                atomicOr(&ev.begins[b / K], 1u << b % K);
+    for (int s0 = p.sa; s0 <= p.sb; s0 += NG * 32) {
+        const int s = s0 + (int)threadIdx.x;
+        int row = -1;
+        bool has = false, copy = false;
+        if (s <= p.sb) {
+            int b, e;
+            range_of(A, s, b, e);
+            row = BACK ? s : row_of(A, s);
+            has = BACK || (row >= 0 && A.h0 && (!A.has_h0 || A.has_h0[s]));
+            copy = b >= e && to && row >= 0 && !(has && from == to);
+            if (b < e) {
+                b -= p.t0;
+                e -= p.t0 + 1;
+                if (b >= 0 && b < p.n) {
+                    ev.begin[b] = has ? row : -1;
+                    atomicOr(&ev.begins[b / K], 1u << b % K);
+                }
+                if (e >= 0 && e < p.n) {
+                    ev.end[e] = row;
+                    atomicOr(&ev.ends[e / K], 1u << e % K);
+                }
             }
-            if (lane == 0 && e >= 0 && e < p.n) {
-                ev.end[e] = row;
-                atomicOr(&ev.ends[e / K], 1u << e % K);
-            }
-        } else if (to && row >= 0) {
-            for (int i = 0; i < n; ++i) {
-                const int64_t at = (int64_t)row * A.D + c + i * kNext<PAIR>;
-                to[at] = from && has ? from[at] : 0.0f;
-            }
+        }
+        const uint64_t rows = __ballot(copy);
+        const int with = (has && from) ? row : ~row;       // below zero: zeros
+        for (int i = 0; i < 64; i += 4) {
+            if ((rows >> i & 0xf) == 0) continue;
+            const int src = i + (lane >> 4), r = __shfl(with, src), c = col * kCols + (lane & 15);
+            if (!(rows >> src & 1)) continue;
+            const int64_t at = (int64_t)(r < 0 ? ~r : r) * A.D + c;
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = r >= 0 && c + 16 * k < A.D ? from[at + 16 * k] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c + 16 * k < A.D) to[at + 16 * k] = v[k];
         }
     }
     lds_barrier();
@@ -504,7 +520,7 @@ __global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
         const Place p = place<kTile, false>(A, j);
         uint32_t begins = 0, ends = 0;         // of this thread's tokens: first and last ones of a sequence
         if (!p.plain) {
-            find_events<kTile, NG, false, PAIR>(A, p, ev, c, live, A.h0, OUT ? A.h_out : nullptr);
+            find_events<kTile, NG, false>(A, p, ev, col, A.h0, OUT ? A.h_out : nullptr);
             begins = ev.begins[grp];
             ends = ev.ends[grp];
         }
@@ -665,7 +681,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
     const Place p = place<kTileBack, true>(A, j);
     uint32_t begins = 0, ends = 0;
     if (!p.plain) {
-        find_events<kTileBack, NG, true, PAIR>(A, p, ev, c, live, A.dh_out, A.dh0);
+        find_events<kTileBack, NG, true>(A, p, ev, col, A.dh_out, A.dh0);
         begins = ev.begins[grp];
         ends = ev.ends[grp];
         // Tokens of no sequence count as zeros, whatever they hold: nothing comes to them and they give nothing.

@@ -420,3 +420,41 @@ def test_long_cache_offsets():
     ref, bound = gf.scan_bwd(*wide(d), [T], d["dy"].double(), d["h0"].double())
     close(out[0], ref["dx"], tol(bound["dx"], ref["dx"], "bf16"), "dx")
     close(out[3], ref["ddecay"], tol(bound["ddecay"], ref["ddecay"], "f32"), "ddecay")
+
+
+@pytest.mark.parametrize("T", [100, 700])
+def test_padded_offsets(T):
+    """Offsets padded to many more sequences than there are, as a captured graph has them: the padded ones have no tokens, and
+    no row in the pool or one of their own; without a pool every one's state is written."""
+    D, lens = 70, [T - 40, 0, 40] + [0] * 1500
+    n = len(lens)
+    d = make(91, T, D, "bf16", n)
+    c = [d[k].cuda() for k in ("x", "a_gate", "decay", "x_gate")]
+    bias = dict(a_bias=d["a_bias"].cuda(), x_bias=d["x_bias"].cuda(), cu_seqlens=offsets(lens).cuda())
+    ry, rh, _, ty, th, _ = gf.scan(*wide(d), lens, d["h0"].double())
+    y, h = mb.mb_gated_scan(*c, h0=d["h0"].cuda(), **bias)
+    close(y, ry, tol(ty, ry, "bf16"), "y")
+    close(h, rh, tol(th, rh, "f32"), "h")
+    assert torch.equal(h[3:].cpu(), d["h0"][3:]) and torch.equal(h[1].cpu(), d["h0"][1])
+    y, h = mb.mb_gated_scan(*c, **bias)
+    assert bool((h[3:] == 0).all()) and bool((h[1] == 0).all())
+    slots = torch.full((n,), -1, dtype=torch.int32)
+    slots[:3], slots[900] = torch.tensor([2, 5, 0], dtype=torch.int32), 7
+    has = torch.ones(n, dtype=torch.bool)
+    has[900] = has[1] = False
+    pool = torch.randn(9, D, generator=torch.Generator().manual_seed(1))
+    start = torch.stack([pool[2], torch.zeros(D), pool[0]] + [torch.zeros(D)] * 1500).double()
+    got = pool.clone().cuda()
+    y, _ = mb.mb_gated_scan(*c, h0=got, slots=slots.cuda(), has_h0=has.cuda(), **bias)
+    ry, rh, _, ty, th, _ = gf.scan(*wide(d), lens, start)
+    close(y, ry, tol(ty, ry, "bf16"), "y")
+    for s, row in ((0, 2), (2, 0)):
+        close(got[row], rh[s], tol(th[s], rh[s], "f32"), "slot")
+    assert bool((got[7] == 0).all()) and bool((got[5] == 0).all())
+    for row in (1, 3, 4, 6, 8):
+        assert torch.equal(got[row].cpu(), pool[row])
+    out = mb.mb_gated_scan_bwd(*c[:3], d["dy"].cuda(), c[3], h0=d["h0"].cuda(), dh_out=d["dh"].cuda(), **bias)
+    ref, bound = gf.scan_bwd(*wide(d), lens, d["dy"].double(), d["h0"].double(), d["dh"].double())
+    for name, o in zip(("dx", "da_gate", "dx_gate", "ddecay", "da_bias", "dx_bias", "dh0"), out):
+        close(o, ref[name], tol(bound[name], ref[name], "bf16" if o.dtype == torch.bfloat16 else "f32"), name)
+    assert torch.equal(out[6][3:].cpu(), d["dh"][3:])
