@@ -1087,17 +1087,16 @@ def mb_gated_scan_bwd(x, a_gate, decay, dy, x_gate=None, *, a_bias=None, x_bias=
     for t, name in ((h0, "h0"), (dh_out, "dh_out")):
         _check(t, name, (n, D), f32, dev)
     _check(states, "states", (-(-T // MB_GATED_SCAN_EVERY), D), f32, dev)
-    out = []
-    for t, name, shp, d, there in ((dx, "dx", lead + (D,), dt, x), (da_gate, "da_gate", lead + (D,), dt, x),
-                                   (dx_gate, "dx_gate", lead + (D,), dt, x_gate), (ddecay, "ddecay", (D,), f32, x),
-                                   (da_bias, "da_bias", (D,), f32, a_bias), (dx_bias, "dx_bias", (D,), f32, x_bias),
-                                   (dh0, "dh0", (n, D), f32, x)):
+    out, like = [], torch.empty_like
+    for t, name, model, there in ((dx, "dx", dy, x), (da_gate, "da_gate", dy, x), (dx_gate, "dx_gate", dy, x_gate), (ddecay, "ddecay", decay, x),
+                                  (da_bias, "da_bias", decay, a_bias), (dx_bias, "dx_bias", decay, x_bias)):
         if there is None:
             if t is not None:
                 raise ValueError("%s is the gradient of an argument that is None" % name)
             out.append(None)
         else:
-            out.append(x.new_empty(shp, dtype=d) if t is None else _check(t, name, shp, d, dev))
+            out.append(like(model) if t is None else _check(t, name, model.shape, model.dtype, dev))
+    out.append(decay.new_empty((n, D)) if dh0 is None else _check(dh0, "dh0", (n, D), f32, dev))
     ws, nws = _scratch(MB_OP_GATED_SCAN_BWD, dev, ws, (n, T, D, 1, 1, 1, 1, 0))
     _call_on(dev, "mb_gated_scan_bwd", _ptr(x), _ptr(a_gate), _ptr(x_gate), _ptr(decay), _ptr(a_bias), _ptr(x_bias),
              _ptr(cu_seqlens), _ptr(h0), _ptr(dy), _ptr(dh_out), _ptr(states), *[_ptr(t) for t in out], n, T, D, *st, code,
