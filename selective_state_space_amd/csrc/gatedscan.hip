@@ -684,7 +684,8 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
         find_events<kTileBack, NG, true>(A, p, ev, col, A.dh_out, A.dh0);
         begins = ev.begins[grp];
         ends = ev.ends[grp];
-        // Tokens of no sequence count as zeros, whatever they hold: nothing comes to them and they give nothing.
+        // Tokens of no sequence count as zeros, whatever they hold; no gradient comes to them (the walks back are cut where a
+        // sequence begins) and no state that is not finite, so that they add nothing to the sums.
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const bool in = grp * K + k >= p.lo && grp * K + k < p.hi;
@@ -734,8 +735,9 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
         if (!p.plain && (ends >> k & 1)) set(V, A.dh_out, ev.end[grp * K + k]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) V[i] = a[k][i] * (half_of(rd[k], i) + V[i]);
+        if (!p.plain && (begins >> k & 1)) V[0] = V[1] = 0.0f;
     }
-    const bool cut = begins != 0, cut_back = ends != 0;
+    const bool cut = begins != 0, cut_back = (begins | ends) != 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) comp[grp][c2 + i * NX] = f4{cut ? 1.0f : S[i], U[i], cut_back ? 1.0f : S[i], V[i]};
     lds_barrier();
@@ -766,7 +768,8 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
         if (A.tiles > 1 && jr % kGroup == kGroup - 1) publish_state(A, jr / kGroup, col * kCols + threadIdx.x, g);
     } else if (threadIdx.x < 2 * kCols) {
         const int lane = threadIdx.x - kCols, at = col * kCols + lane;
-        float h = at < A.D && p.n > 0 ? A.kept[(int64_t)j * A.D + at] : 0.0f;
+        // no state is kept where the first token is in no sequence
+        float h = at < A.D && p.lo == 0 && p.hi > 0 ? A.kept[(int64_t)j * A.D + at] : 0.0f;
 #pragma unroll 4
         for (int i = 0; i < NG; ++i) {
             const f4 q = comp[i][lane];
@@ -821,6 +824,15 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
                 if (A.dh0 && i < live) A.dh0[at + i * NX] = g[i];
                 g[i] = 0.0f;            // for tokens of no sequence in front of it
             }
+        }
+    }
+    if (p.lo > 0 || p.hi < p.n) {          // their rows: zeros, also behind a state that is not finite
+#pragma unroll 1
+        for (int k = 0; k < K; ++k) {
+            if (grp * K + k >= p.lo && grp * K + k < p.hi) continue;
+            store2<T, PAIR>(bdx, od, k * sd, 0.0f, 0.0f);
+            store2<T, PAIR>(bda, od, k * sd, 0.0f, 0.0f);
+            store2<T, PAIR>(bdg, od, k * sd, 0.0f, 0.0f);
         }
     }
     if (!A.part) return;

@@ -458,3 +458,39 @@ def test_padded_offsets(T):
     for name, o in zip(("dx", "da_gate", "dx_gate", "ddecay", "da_bias", "dx_bias", "dh0"), out):
         close(o, ref[name], tol(bound[name], ref[name], "bf16" if o.dtype == torch.bfloat16 else "f32"), name)
     assert torch.equal(out[6][3:].cpu(), d["dh"][3:])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("head,tail,D", [(20, 100, 64), (150, 300, 33), (64, 128, 6), (1000, 1, 64)])
+def test_tokens_of_no_sequence(head, tail, D, dtype):
+    """Many tokens in front of the first and behind the last sequence, whole tiles of them and parts of one, NaN in all that is theirs:
+    the gradients are those of the sequences, and zero outside."""
+    lens = [100, 37]
+    n, T = len(lens), sum([100, 37])
+    d = make(101, T, D, dtype, n)
+    wrap = lambda t, v: torch.cat([torch.full((head, D), v, dtype=t.dtype), t, torch.full((tail, D), v, dtype=t.dtype)]).cuda()  # noqa: E731
+    ins = [wrap(d["x"], float("nan")), wrap(d["a_gate"], float("nan")), d["decay"].cuda()]
+    g, dy = wrap(d["x_gate"], float("nan")), wrap(d["dy"], float("nan"))
+    kw = dict(a_bias=d["a_bias"].cuda(), x_bias=d["x_bias"].cuda(), cu_seqlens=(offsets(lens) + head).int().cuda(), h0=d["h0"].cuda())
+    y, h, kept = mb.mb_gated_scan(*ins, g, y=wrap(torch.zeros_like(d["x"]), 7.0), states=True, **kw)
+    ry, rh, _, ty, th, _ = gf.scan(*wide(d), lens, d["h0"].double())
+    assert bool((y[:head] == 7.0).all()) and bool((y[head + T:] == 7.0).all())
+    close(y[head:head + T], ry, tol(ty, ry, dtype), "y")
+    close(h, rh, tol(th, rh, "f32"), "h")
+    ref, bound = gf.scan_bwd(*wide(d), lens, d["dy"].double(), d["h0"].double(), d["dh"].double())
+    for filled in (float("nan"), 3.0):
+        kept[:head // 64], kept[-(-(head + T) // 64):] = filled, filled
+        for bad in (g, dy, ins[0], ins[1]):
+            bad[:head], bad[head + T:] = filled, filled
+        for states in (None, kept):
+            out = mb.mb_gated_scan_bwd(*ins, dy, g, dh_out=d["dh"].cuda(), states=states, **kw)
+            for name, got in zip(("dx", "da_gate", "dx_gate", "ddecay", "da_bias", "dx_bias", "dh0"), out):
+                if name in ("dx", "da_gate", "dx_gate"):
+                    assert bool((got[:head] == 0).all()) and bool((got[head + T:] == 0).all()), name
+                    got = got[head:head + T]
+                close(got, ref[name], tol(bound[name], ref[name], dtype if got.dtype == DT[dtype] else "f32"), name)
+    # a state that is not finite at the end of the last sequence
+    ins[0][head + T - 1, 0] = float("nan")
+    out = mb.mb_gated_scan_bwd(*ins, dy, g, dh_out=d["dh"].cuda(), **kw)
+    for got in out[:3]:
+        assert bool((got[:head] == 0).all()) and bool((got[head + T:] == 0).all())
