@@ -37,6 +37,7 @@ struct QkArgs {
     const float* freqs;
     const int32_t* positions;
     int64_t T, L;
+    int64_t first;            // forward: the launch's first token
     int H[2], D, R, inter;
     int tokens, heads;        // of a workgroup at a time
     float eps;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(256) k_qk_forward(QkArgs A) {
     __shared__ f2 cs[kTokens * LPR * 4];
     const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
     const Columns c = columns(A, lane);
-    const int64_t t0 = (int64_t)blockIdx.x * A.tokens;
+    const int64_t t0 = A.first + (int64_t)blockIdx.x * A.tokens;
     const int all = A.H[0] + A.H[1], h0 = blockIdx.y * A.heads, nh = min(A.heads, all - h0);
     const int rows = (int)min((int64_t)A.tokens, A.T - t0) * nh;
     const float inv_nh = 1.0f / (float)nh;
@@ -531,11 +532,17 @@ extern "C" mb_status mb_qk_norm_rope(const void* q, const void* k, const float* 
     const int64_t blocks = (T + A.tokens - 1) / A.tokens, places = 256 / lanes_of(D);
     while (blocks * parts < 2 * device_cu_count() && (Hq + Hk + parts - 1) / parts > places) parts *= 2;
     A.heads = (int)((Hq + Hk + parts - 1) / parts);
-    const dim3 grid((unsigned)blocks, (unsigned)((Hq + Hk + A.heads - 1) / A.heads));
+    const int64_t groups = (Hq + Hk + A.heads - 1) / A.heads, most = max_workgroups(256) / groups;        // blocks of a launch
     const bool vec = pieces_ok(A, es);
-    if (dtype == MB_F32) vec ? launch_forward<float, true>(A, grid, stream) : launch_forward<float, false>(A, grid, stream);
-    else vec ? launch_forward<bf16, true>(A, grid, stream) : launch_forward<bf16, false>(A, grid, stream);
-    return check_launch();
+    for (int64_t at = 0; at < blocks; at += most) {
+        A.first = at * A.tokens;
+        const dim3 grid((unsigned)std::min(most, blocks - at), (unsigned)groups);
+        if (dtype == MB_F32) vec ? launch_forward<float, true>(A, grid, stream) : launch_forward<float, false>(A, grid, stream);
+        else vec ? launch_forward<bf16, true>(A, grid, stream) : launch_forward<bf16, false>(A, grid, stream);
+        const mb_status st = check_launch();
+        if (st != MB_OK) return st;
+    }
+    return MB_OK;
 }
 
 extern "C" mb_status mb_qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const float* q_weight,

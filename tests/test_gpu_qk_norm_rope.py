@@ -224,3 +224,18 @@ def test_rows_past_32_bit_offsets():
     q.copy_(d["q"])
     mb.mb_qk_norm_rope(q, None, d["freqs"].cuda(), d["pos"].cuda(), q_weight=d["wq"].cuda(), eps=EPS, q_out=q)
     check(d, q.contiguous(), "q", "bf16", False)
+
+
+def test_more_tokens_than_a_launch_takes():
+    """2^28 tokens and some: more threads than one grid has; in place, one head of one pair."""
+    T, D, n = (1 << 28) + 37, 2, 300
+    q = torch.ones(T, 1, D, dtype=torch.bfloat16, device="cuda")                   # 1 GB
+    f = torch.full((1,), 0.37).cuda()
+    places = torch.cat([torch.arange(n), torch.arange(T - n, T)])
+    q[places.cuda()] = torch.randn(2 * n, 1, D, generator=torch.Generator().manual_seed(3)).bfloat16().cuda()
+    want, _ = mb.mb_qk_norm_rope(q[places.cuda()], None, f, places.int().cuda(), eps=EPS)
+    mb.mb_qk_norm_rope(q, None, f, eps=EPS, q_out=q)
+    assert torch.equal(q[places.cuda()], want)
+    rest = q[n:T - n:1021, 0].float()
+    # (1, 1) turned: two squares that add up to 2 / (1 + EPS), each value off by half a step, (1 + HB)^2 of its square
+    assert bool((((rest * rest).sum(1) - 2.0).abs() <= 2 * (2 * HB + HB * HB) + 3 * EPS).all())
