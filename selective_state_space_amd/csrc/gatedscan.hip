@@ -244,7 +244,7 @@ __device__ __forceinline__ Place place(const GsArgs& A, int j) {
         int f0 = -1, f1 = A.n_seq;
         if (A.tiles > 1) {
             f0 = A.ch.first[j];
-            f1 = A.ch.first[j + 1];
+            f1 = min(A.ch.first[j + 1], A.n_seq);
         }
         p.sa = j == 0 ? 0 : max(f0, 0);
         p.sb = min(f1, A.n_seq - 1);
@@ -436,12 +436,13 @@ __global__ void __launch_bounds__(256) k_gs_setup(Setup S) {
 }
 
 // Workgroup b has column b % cols, and takes the column's tiles, in walking order, from a counter: the least unfinished one is
-// then always in work.  One counter for all columns would be slower: their adds, one after the other at one address, took
-// 12 us of the 62 that 3072 tiles of a packed prompt take without waits.
-
+// then always in work.  One counter for all columns is slower: their adds come one after the other at one address, 12 us of the 73
+// that 16384 tokens of 1536 bf16 channels took with it; with a counter each, 128 bytes apart, 3 to 5.
+// The bound holds it in range where something else writes to the workspace at the same time.
 __device__ __forceinline__ int take(const GsArgs& A, int col) {
     if (A.tiles == 1) return 0;
-    return (int)__hip_atomic_fetch_add(A.ch.ticket + col * kCounter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t j = __hip_atomic_fetch_add(A.ch.ticket + col * kCounter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return (int)min(j, (uint32_t)A.tiles - 1);
 }
 
 // -decay log2(e) and the biases times -log2(e) of two channels; those behind the last are zero.
@@ -479,8 +480,10 @@ struct Source {
 // -------------------------------------------------------------- forward ----
 // A thread holds K tokens of two channels; 32 threads side by side make a group's rows of 64 channels, NG groups the tile.
 // OUT: outputs and end states are written; otherwise the states for the backward alone.
+// Four workgroups a compute unit; three where fp32 channels come in pairs, whose registers would not hold it all otherwise (16384 tokens of
+// 2048 channels 113 us with four and 24 bytes of scratch, 106 with three; 8192 of 1536 47.5 and 43.2).
 template <typename T, bool PAIR, int K, bool OUT>
-__global__ void __launch_bounds__(kTile / K * 32, 4) k_gs_forward(GsArgs A) {
+__global__ void __launch_bounds__(kTile / K * 32, sizeof(T) == 4 && PAIR ? 3 : 4) k_gs_forward(GsArgs A) {
     constexpr int NG = kTile / K, NX = kNext<PAIR>;
     __shared__ f2 comp[NG][kCols];
     __shared__ float entry[NG][kCols];
