@@ -435,9 +435,17 @@ __global__ void __launch_bounds__(256) k_gs_setup(Setup S) {
     }
 }
 
-// Workgroup b has column b % cols, and takes the column's tiles, in walking order, from a counter: the least unfinished one is
+// A workgroup has a column by its number, and takes the column's tiles, in walking order, from a counter: the least unfinished one is
 // then always in work.  One counter for all columns is slower: their adds come one after the other at one address, 12 us of the 73
 // that 16384 tokens of 1536 bf16 channels took with it; with a counter each, 128 bytes apart, 3 to 5.
+// Workgroups go to the eight dies in turn: a die, or two or four together where eight does not divide the columns, has columns that lie
+// beside each other, whose rows share lines where they are not aligned and pages of memory everywhere.  Against column b % cols, 16384 tokens of
+// 1536 bf16 channels: forward 60.1 and 57.3 us, backward 114 and 108; 16380 tokens of 1001 fp32 channels 36.8 and 34.2.
+__device__ __forceinline__ int column_of(const GsArgs& A) {
+    const uint32_t b = blockIdx.x, cols = A.cols, shift = cols & 1 ? 0 : cols & 2 ? 1 : cols & 4 ? 2 : 3, per = cols >> shift;
+    return (int)((b & ((1u << shift) - 1)) * per + (b >> shift) % per);
+}
+
 // The bound holds it in range where something else writes to the workspace at the same time.
 __device__ __forceinline__ int take(const GsArgs& A, int col) {
     if (A.tiles == 1) return 0;
@@ -493,7 +501,7 @@ __global__ void __launch_bounds__(kTile / K * 32, sizeof(T) == 4 && PAIR ? 3 : 4
     const int c2 = first_channel<PAIR>(), grp = threadIdx.x >> 5;
     typename Raw<T>::type rx[K], ra[K], rg[K];
     Params<PAIR> par;
-    const int col = blockIdx.x % A.cols;
+    const int col = column_of(A);
     if (threadIdx.x == 0) taken = take(A, col);
     __syncthreads();
     const int j = __builtin_amdgcn_readfirstlane(taken);
@@ -662,7 +670,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
     const int c2 = first_channel<PAIR>(), grp = threadIdx.x >> 5;
     typename Raw<T>::type rx[K], ra[K], rg[K], rd[K];
     Params<PAIR> par;
-    const int col = blockIdx.x % A.cols;
+    const int col = column_of(A);
     if (threadIdx.x == 0) taken = take(A, col);
     __syncthreads();
     const int jr = __builtin_amdgcn_readfirstlane(taken), j = A.tiles - 1 - jr;
