@@ -112,9 +112,12 @@ __device__ __forceinline__ void sigma2(float v, float nb, float& s, float& not_s
 // otherwise half a tile apart, so that a row's threads read neighbouring elements with each of two reads.  16384 tokens of 1001 bf16
 // channels, forward and backward: channels beside each other 55.7 and 107 us read one by one, 64 and 114 read in pairs from odd
 // addresses, half a tile apart 51.6 and 103.
-template <bool PAIR> constexpr int kNext = PAIR ? 1 : kCols / 2;
-template <bool PAIR> __device__ __forceinline__ int first_channel() { return (threadIdx.x & 31) * (PAIR ? 2 : 1); }
-template <bool PAIR> __device__ __forceinline__ int channels_of(int D, int c) { return (c < D) + (c + kNext<PAIR> < D); }
+// PAIR: 0 half a tile apart, 1 pairs, 2 pairs whose tiles' rows are whole lines of memory, 128 bytes.  Those are read past the caches; lines
+// that two tiles share are not.  16384 tokens of 1536 bf16 channels (whole lines): forward 57.7 us past the caches and 58.9 through
+// them, backward 106 and 114; of 1000 (shared): 48.7 and 45.0, 90 and 84; 8192 of 1530 fp32 channels (shared): 49.8 and 51.9, 87 and 81.
+template <int PAIR> constexpr int kNext = PAIR ? 1 : kCols / 2;
+template <int PAIR> __device__ __forceinline__ int first_channel() { return (threadIdx.x & 31) * (PAIR ? 2 : 1); }
+template <int PAIR> __device__ __forceinline__ int channels_of(int D, int c) { return (c < D) + (c + kNext<PAIR> < D); }
 
 // Two channels as they come from memory.
 template <typename T> struct Raw;
@@ -143,15 +146,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_at(const void* p, int64_t
 
 // `row`: the same in all lanes, a scalar operand (a sum in a vector register for each row would be held over the whole walk); the
 // buffer's range holds for the sum.  PAIR: two channels start on a border of two elements.
-template <typename T, bool PAIR>
+template <typename T, int PAIR>
 __device__ __forceinline__ typename Raw<T>::type load2(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t row) {
+    constexpr int kAux = PAIR == 2 ? 2 : 0;          // non-temporal
     if constexpr (sizeof(T) == 2) {
-        if constexpr (PAIR) return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, 2);
+        if constexpr (PAIR) return __builtin_amdgcn_raw_buffer_load_b32(r, off, row, kAux);
         const uint32_t lo = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, row, 0);
         const uint32_t hi = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off + 2 * kNext<PAIR>, row, 0);
         return lo | hi << 16;
     } else {
-        if constexpr (PAIR) return __builtin_bit_cast(f2, __builtin_amdgcn_raw_buffer_load_b64(r, off, row, 2));
+        if constexpr (PAIR) return __builtin_bit_cast(f2, __builtin_amdgcn_raw_buffer_load_b64(r, off, row, kAux));
         f2 v;
         v[0] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, row, 0));
         v[1] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off + 4 * kNext<PAIR>, row, 0));
@@ -165,13 +169,13 @@ struct Place2 {
 };
 constexpr uint32_t kNowhere = 0x80000000u;
 
-template <typename T, bool PAIR>
+template <typename T, int PAIR>
 __device__ __forceinline__ Place2 place2(uint32_t off, int live) {
     return Place2{live > 0 ? off : kNowhere, live > 1 ? off + (uint32_t)sizeof(T) * kNext<PAIR> : kNowhere};
 }
 
 // Rounds to nearest even.
-template <typename T, bool PAIR>
+template <typename T, int PAIR>
 __device__ __forceinline__ void store2(__amdgpu_buffer_rsrc_t r, Place2 at, uint32_t row, float lo, float hi) {
     if constexpr (sizeof(T) == 2) {
         const f2 v = {lo, hi};
@@ -454,7 +458,7 @@ __device__ __forceinline__ int take(const GsArgs& A, int col) {
 }
 
 // -decay log2(e) and the biases times -log2(e) of two channels; those behind the last are zero.
-template <bool PAIR>
+template <int PAIR>
 struct Params {
     float nd[2], nab[2], nxb[2];
     __device__ __forceinline__ void load(const GsArgs& A, int c, int live) {
@@ -479,7 +483,7 @@ struct Source {
         step = (uint32_t)ts * sizeof(T);
         off = first * step + c * sizeof(T);
     }
-    template <bool PAIR>
+    template <int PAIR>
     __device__ __forceinline__ typename Raw<T>::type get(int k) const {
         return load2<T, PAIR>(rows, off, k * step);
     }
@@ -490,7 +494,7 @@ struct Source {
 // OUT: outputs and end states are written; otherwise the states for the backward alone.
 // Four workgroups a compute unit; three where fp32 channels come in pairs, whose registers would not hold it all otherwise (16384 tokens of
 // 2048 channels 113 us with four and 24 bytes of scratch, 106 with three; 8192 of 1536 47.5 and 43.2).
-template <typename T, bool PAIR, int K, bool OUT>
+template <typename T, int PAIR, int K, bool OUT>
 __global__ void __launch_bounds__(kTile / K * 32, sizeof(T) == 4 && PAIR ? 3 : 4) k_gs_forward(GsArgs A) {
     constexpr int NG = kTile / K, NX = kNext<PAIR>;
     __shared__ f2 comp[NG][kCols];
@@ -658,7 +662,7 @@ __global__ void __launch_bounds__(kTile / K * 32, sizeof(T) == 4 && PAIR ? 3 : 4
 // Tiles from the last to the first.  A tile needs the state that enters it, which the forward kept for every 64th token, and
 // the gradient that comes back out of the tiles behind, handed on like the states forward.  The tokens are walked three times in
 // registers: forward and back for what the tile hands on, forward for h_{t-1}, back for G and the gradients.
-template <typename T, bool PAIR, int K>
+template <typename T, int PAIR, int K>
 __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A) {
     constexpr int NG = kTileBack / K, NT = NG * 32, NX = kNext<PAIR>;
     __shared__ f4 comp[NG][kCols];          // of every group: (S, U) forward, (S, V) backward
@@ -889,7 +893,7 @@ __global__ void __launch_bounds__(1024) k_gs_sums(const float* __restrict__ part
 
 // ----------------------------------------------------------------- step ----
 // Two channels of one sequence a thread.
-template <typename T, bool PAIR>
+template <typename T, int PAIR>
 __global__ void __launch_bounds__(256) k_gs_step(GsArgs A, int64_t n0, int blocks) {
     const int64_t n = n0 + blockIdx.x / blocks;
     constexpr int NX = kNext<PAIR>;
@@ -968,13 +972,13 @@ BackPlan back_plan(int64_t T, int64_t D) {
     return b;
 }
 
+// Which of the kernels' PAIR holds for a call: `more` are the outputs, contiguous.
 template <typename T>
-bool pairs_ok(const GsArgs& A, std::initializer_list<const void*> more) {
-    constexpr uintptr_t M = 2 * sizeof(T) - 1;
-    bool ok = A.D % 2 == 0 && A.x_ts % 2 == 0 && A.a_ts % 2 == 0 && (!A.g || A.g_ts % 2 == 0) && !((uintptr_t)A.x & M) && !((uintptr_t)A.a & M) &&
-              !((uintptr_t)A.g & M);
-    for (const void* p : more) ok = ok && !((uintptr_t)p & M);
-    return ok;
+int pairs_of(const GsArgs& A, std::initializer_list<const void*> more) {
+    uintptr_t all = (uintptr_t)A.D * sizeof(T) | (uintptr_t)A.x_ts * sizeof(T) | (uintptr_t)A.a_ts * sizeof(T) | (uintptr_t)A.x | (uintptr_t)A.a | (uintptr_t)A.g;
+    if (A.g) all |= (uintptr_t)A.g_ts * sizeof(T);
+    for (const void* p : more) all |= (uintptr_t)p;
+    return all % (2 * sizeof(T)) ? 0 : all % 128 ? 1 : 2;
 }
 
 mb_status launch_setup(const GsArgs& A, const Chain& fwd, int64_t tiles, const Chain& back, int64_t tiles_back, hipStream_t s) {
@@ -1000,19 +1004,22 @@ template <typename T, bool OUT>
 mb_status run_forward(const GsArgs& A, hipStream_t s) {
     constexpr int K = kPer;
     const dim3 grid((unsigned)(A.tiles * A.cols)), block(kTile / K * 32);
-    if (pairs_ok<T>(A, {A.y})) hipLaunchKernelGGL((k_gs_forward<T, true, K, OUT>), grid, block, 0, s, A);
-    else hipLaunchKernelGGL((k_gs_forward<T, false, K, OUT>), grid, block, 0, s, A);
+    switch (pairs_of<T>(A, {A.y})) {
+        case 0: hipLaunchKernelGGL((k_gs_forward<T, 0, K, OUT>), grid, block, 0, s, A); break;
+        case 1: hipLaunchKernelGGL((k_gs_forward<T, 1, K, OUT>), grid, block, 0, s, A); break;
+        default: hipLaunchKernelGGL((k_gs_forward<T, 2, K, OUT>), grid, block, 0, s, A);
+    }
     return check_launch();
 }
 
 template <typename T>
 mb_status run_step(const GsArgs& A, int64_t n, hipStream_t s) {
     const int64_t blocks = (A.D + 511) / 512, most = max_workgroups(256) / blocks;       // rows of a launch
-    const bool pairs = pairs_ok<T>(A, {A.y});
+    const int pairs = pairs_of<T>(A, {A.y});
     for (int64_t at = 0; at < n; at += most) {
         const dim3 grid((unsigned)(std::min(most, n - at) * blocks));
-        if (pairs) hipLaunchKernelGGL((k_gs_step<T, true>), grid, dim3(256), 0, s, A, at, (int)blocks);
-        else hipLaunchKernelGGL((k_gs_step<T, false>), grid, dim3(256), 0, s, A, at, (int)blocks);
+        if (pairs) hipLaunchKernelGGL((k_gs_step<T, 1>), grid, dim3(256), 0, s, A, at, (int)blocks);
+        else hipLaunchKernelGGL((k_gs_step<T, 0>), grid, dim3(256), 0, s, A, at, (int)blocks);
         const mb_status st = check_launch();
         if (st != MB_OK) return st;
     }
@@ -1023,8 +1030,11 @@ template <typename T>
 mb_status run_backward(const GsArgs& A, hipStream_t s) {
     constexpr int K = kPerBack;
     const dim3 grid((unsigned)(A.tiles * A.cols)), block(kTileBack / K * 32);
-    if (pairs_ok<T>(A, {A.dy, A.dx, A.da, A.dg})) hipLaunchKernelGGL((k_gs_backward<T, true, K>), grid, block, 0, s, A);
-    else hipLaunchKernelGGL((k_gs_backward<T, false, K>), grid, block, 0, s, A);
+    switch (pairs_of<T>(A, {A.dy, A.dx, A.da, A.dg})) {
+        case 0: hipLaunchKernelGGL((k_gs_backward<T, 0, K>), grid, block, 0, s, A); break;
+        case 1: hipLaunchKernelGGL((k_gs_backward<T, 1, K>), grid, block, 0, s, A); break;
+        default: hipLaunchKernelGGL((k_gs_backward<T, 2, K>), grid, block, 0, s, A);
+    }
     return check_launch();
 }
 
