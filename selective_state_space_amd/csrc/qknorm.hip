@@ -89,7 +89,9 @@ struct Columns {
         }
         return d < D ? d : -1;
     }
-    __device__ __forceinline__ bool turns(int i) const { return 2 * (pair + i) < R; }
+    // VEC: all four or none
+    template <bool VEC>
+    __device__ __forceinline__ bool turns(int i) const { return 2 * (pair + (VEC ? 0 : i)) < R; }
 };
 
 __device__ __forceinline__ Columns columns(const QkArgs& A, int lane) {
@@ -170,11 +172,11 @@ template <typename T> struct Part<T, false> {
     }
 };
 
-// 1 / sqrt(mean x^2 + eps) of a row of the sum of squares ss.  Squares that leave fp32's range, above or, with an eps that does not
-// cover it, below (2^-100: those below the range are off by up to 2^-150 each), are summed once more of the values times a power of two
-// that brings the larger of them and of sqrt(eps) to between 1 and 4: `up`, which the result belongs to; 1 otherwise.
+// 1 / sqrt(mean x^2 + eps) of a row of the sum of squares ss.  Where squares leave fp32's range, above or, with an eps that does not
+// cover it, below (2^-100: those below the range are off by up to 2^-150 each), the row is multiplied by `up`, a power of two that brings
+// the larger of its values and of sqrt(eps) to between 1 and 4, and summed once more; `up` is 1 otherwise.
 template <int LPR>
-__device__ __forceinline__ float inverse_rms(float ss, const float (&u)[4], const float (&v)[4], int D, float eps, float& up) {
+__device__ __forceinline__ float inverse_rms(float ss, float (&u)[4], float (&v)[4], float inv_d, float eps, float& up) {
     up = 1.0f;
     if (__builtin_expect(ss > 3.0e38f || ss + eps < 0x1p-100f, false)) {
         float top = sqrtf(eps);
@@ -185,11 +187,16 @@ __device__ __forceinline__ float inverse_rms(float ss, const float (&u)[4], cons
             up = __uint_as_float((uint32_t)max(254 - (int)(bits >> 23), 1) << 23);
             ss = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) ss = fmaf(u[i] * up, u[i] * up, fmaf(v[i] * up, v[i] * up, ss));
+            for (int i = 0; i < 4; ++i) {
+                u[i] *= up;
+                v[i] *= up;
+                ss = fmaf(u[i], u[i], fmaf(v[i], v[i], ss));
+            }
             ss = row_all<LPR>(ss);
+            eps = eps * up * up;          // in this order: a square of up leaves fp32
         }
     }
-    return 1.0f / sqrtf(ss / (float)D + eps * up * up);
+    return __builtin_amdgcn_rsqf(fmaf(ss, inv_d, eps));
 }
 
 // Sines and cosines of `n` tokens from t0 on, LPR * 4 pairs each; pairs that do not turn are left out.  The angle in turns
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(256) k_qk_forward(QkArgs A) {
     const int64_t t0 = A.first + (int64_t)blockIdx.x * A.tokens;
     const int all = A.H[0] + A.H[1], h0 = blockIdx.y * A.heads, nh = min(A.heads, all - h0);
     const int rows = (int)min((int64_t)A.tokens, A.T - t0) * nh;
-    const float inv_nh = 1.0f / (float)nh;
+    const float inv_nh = 1.0f / (float)nh, inv_d = 1.0f / (float)A.D;
     const auto place = [&](int r, int& t, int& k, int& h) {
         t = (int)(((float)r + 0.5f) * inv_nh);       // at most 16 tokens and 8192 heads: off by less than 0.5 / nh
         h = h0 + r - t * nh;
@@ -261,12 +268,12 @@ __global__ void __launch_bounds__(256) k_qk_forward(QkArgs A) {
             x[b].get(u, v, c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) ss = fmaf(u[i], u[i], fmaf(v[i], v[i], ss));
-            const float rs = inverse_rms<LPR>(row_all<LPR>(ss), u, v, A.D, A.eps, up);
+            const float rs = inverse_rms<LPR>(row_all<LPR>(ss), u, v, inv_d, A.eps, up);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                u[i] = u[i] * up * rs * (k ? wu[1][i] : wu[0][i]);
-                v[i] = v[i] * up * rs * (k ? wv[1][i] : wv[0][i]);
-                if (c.turns(i)) {
+                u[i] *= rs * (k ? wu[1][i] : wu[0][i]);
+                v[i] *= rs * (k ? wv[1][i] : wv[0][i]);
+                if (c.turns<VEC>(i)) {
                     const f2 q = cs[t * LPR * 4 + c.pair + i];
                     turn(u[i], v[i], q[0], q[1]);
                 }
@@ -321,16 +328,16 @@ __global__ void __launch_bounds__(256) k_qk_backward(QkArgs A) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     ss = fmaf(u[i], u[i], fmaf(v[i], v[i], ss));
-                    if (c.turns(i)) {
+                    if (c.turns<VEC>(i)) {
                         const f2 q = cs[t[b] * LPR * 4 + c.pair + i];
                         turn(eu[i], ev[i], q[0], -q[1]);
                     }
                 }
-                const float rs = inverse_rms<LPR>(row_all<LPR>(ss), u, v, A.D, A.eps, scale_up);
+                const float rs = inverse_rms<LPR>(row_all<LPR>(ss), u, v, inv_d, A.eps, scale_up);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    u[i] = u[i] * scale_up * rs;
-                    v[i] = v[i] * scale_up * rs;
+                    u[i] *= rs;
+                    v[i] *= rs;
                     du[k][i] = live ? fmaf(eu[i], u[i], du[k][i]) : du[k][i];
                     dv[k][i] = live ? fmaf(ev[i], v[i], dv[k][i]) : dv[k][i];
                     eu[i] *= wu[k][i];
