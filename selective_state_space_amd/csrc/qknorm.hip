@@ -447,12 +447,14 @@ int lanes_of(int64_t D) {
     return l;
 }
 
-// Tokens that a workgroup takes at a time: eight rows for every place that it has, no more than leaves two workgroups a
-// compute unit.
+// Tokens that a workgroup takes at a time: eight rows or more for every place that it has, no more than leaves two workgroups a
+// compute unit.  A power of two: heads mostly come in numbers that then fill the batches (16384 tokens of 16 and 4 heads of 128, bf16, with
+// 7 tokens 47.2 us, 8 43.5, 10 and 16 45.0; the backward 57.0, 54.5, 58.4 and 57.1).
 int tokens_of(int64_t T, int64_t heads, int64_t D) {
     const int64_t places = 256 / lanes_of(D), want = 2 * (int64_t)device_cu_count();
-    int64_t n = std::min<int64_t>(std::max<int64_t>((8 * places + heads - 1) / heads, 1), kTokens);
-    while (n > 1 && (T + n - 1) / n < want) n = (n + 1) / 2;
+    int64_t n = 1;
+    while (n < kTokens && n * heads < 8 * places) n *= 2;
+    while (n > 1 && (T + n - 1) / n < want) n /= 2;
     return (int)n;
 }
 
