@@ -13,16 +13,15 @@
 // Handing on.  Workgroups take their tile from a counter, so that every tile in front of a taken one has been taken by a workgroup that
 // runs; a wait for a tile in front therefore ends.  A tile publishes (S, U) for each channel in one 64-bit store, which
 // readers poll until it is no longer the pattern that the first launch left there.  16 tiles make a group, whose last
-// tile also publishes the state behind it.  The state that enters a tile is composed of the state behind the group
-// before and the (S, U) of the group's tiles in front, always in this order: results do not depend on who came first.
+// tile also publishes the state behind it (and with few columns the group's (S, U)).  The state that enters a tile is composed of the state
+// behind the group before and the (S, U) of the group's tiles in front, always in this order: results do not depend on who came first.
 // Tiles in front of the one in which the first token's sequence starts are not looked at.
 //
 // What bounds it: bytes (12 of x and gates and 4 of y a token and channel in fp32, half of it in bf16, once each), and beside them the
 // gates' transcendentals and the waits for states, which four workgroups a compute unit hide in part.  16384 packed tokens of 1536 bf16
-// channels: 57 us for 201 MB, 3.5 TB/s (the loads and stores alone 39, the gates 5 to 8, counters 3, waits for tiles in front 6 to 10; a
-// pass for end states and one for outputs read 151 MB twice).  65536 tokens of 768: 101 us, 403 MB.  The backward of 16384 by 1536: 108 us for
-// 352 MB, 3.3 TB/s.  Few channels and one long sequence are bound by the chain of groups, 1.4 us each: 2^20 tokens of 64 channels
-// 680 us for 537 MB.
+// channels: 58 us for 201 MB, 3.5 TB/s (the loads and stores alone 39, the gates 5 to 8, counters 3, waits for tiles in front 6 to 10; a
+// pass for end states and one for outputs read 151 MB twice).  65536 tokens of 768: 102 us, 403 MB.  The backward of 16384 by 1536: 108 us for
+// 352 MB, 3.3 TB/s.  Few channels leave most of the card idle: 131072 tokens of 64 channels 41 us for 67 MB, their backward 76 for 117.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -40,7 +39,9 @@ constexpr int kEvery = 64;                  // tokens between the rows of states
 constexpr int kCols = 64;                   // channels of a tile
 constexpr int kTile = 128, kTileBack = 64;  // its tokens, forward and backward
 constexpr int kPer = 16, kPerBack = 8;      // tokens of a thread
-constexpr int kGroup = 16;                  // tiles of a group
+constexpr int kGroup = 16;                  // tiles of a group, groups of a group of groups
+constexpr int kDeep = 6;                    // columns up to which a group's last tile looks further (DEEP)
+template <bool DEEP> constexpr int kLook = DEEP ? 2 * kGroup : kGroup;       // words that a tile looks at
 constexpr int kCounter = 32;                // words between the counters of two columns
 constexpr uint64_t kNone = ~0ull;           // not published yet
 // Polls of one wait before it is given up (the result is NaN then): some seconds, which only a workspace
@@ -50,6 +51,7 @@ constexpr int kPolls = 1 << 22;
 // What the tiles of one direction hand on to each other, in the workspace.
 struct Chain {
     uint64_t* agg;       // (tiles, columns): (S, U) of a tile
+    uint64_t* gagg;      // (groups, columns): (S, U) of a group
     uint32_t* incl;      // (groups, columns): the state behind a group
     int* first;          // (tiles + 1): the last offset of cu at or before the tile's first token
     uint32_t* ticket;
@@ -351,30 +353,51 @@ __device__ __forceinline__ uint32_t peek(const uint32_t* p) { return __hip_atomi
 // One NaN for all: none looks like kNone.
 __device__ __forceinline__ uint32_t plain_bits(float v) { return v == v ? __float_as_uint(v) : 0x7fc00000u; }
 
-__device__ __forceinline__ void publish(const GsArgs& A, int j, int c, float S, float U) {
-    const uint64_t w = (uint64_t)plain_bits(S) | (uint64_t)plain_bits(U) << 32;
-    __hip_atomic_store(A.ch.agg + (int64_t)j * A.cols * kCols + c, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ uint64_t word_of(float S, float U) { return (uint64_t)plain_bits(S) | (uint64_t)plain_bits(U) << 32; }
+
+// Row `i` of a table of words, at channel c.
+__device__ __forceinline__ void publish(const GsArgs& A, uint64_t* table, int i, int c, uint64_t w) {
+    __hip_atomic_store(table + (int64_t)i * A.cols * kCols + c, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-__device__ __forceinline__ void publish_state(const GsArgs& A, int group, int c, float h) {
-    __hip_atomic_store(A.ch.incl + (int64_t)group * A.cols * kCols + c, plain_bits(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void publish_state(const GsArgs& A, int i, int c, float h) {
+    __hip_atomic_store(A.ch.incl + (int64_t)i * A.cols * kCols + c, plain_bits(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// What enters tile j of the chain (tiles counted in walking order): all waves fetch what the tiles of its group in front of it, from `src`
-// on, and the group before published, `look`; behind a barrier compose() puts it together, a channel a lane.
-template <int NW>
-__device__ __forceinline__ void fetch_look(const GsArgs& A, int j, int src, int col, uint64_t (*look)[kCols]) {
-    const int group = j / kGroup, lo = max(src, group * kGroup), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+// The words that tile j of the chain (tiles counted in walking order, its sequence from tile `src` on) looks at.  Rows 0 to 14: the tiles
+// of its group in front of it, from `tile` on.  Row 15: the state behind the group before.  States are so handed on from group to group, one
+// after the other, 1.4 us each, which with few columns takes longer than memory.  DEEP: a group's last tile (`last`) does not wait for that
+// state.  Its rows 16 to 30 are the groups of its group of groups in front of its own, from `group` on, row 31 the state behind the group of
+// groups before.  A sequence of 131072 tokens, bf16, group by group and DEEP: 64 channels 127 and 41 us, 256 130 and 82, 384 139 and
+// 110, 512 165 and 158, 640 167 and 169; backward 247 and 76, 270 and 186, 288 and 263, 345 and 357, 383 and 416.
+template <bool DEEP>
+struct Look {
+    int j, src, tile, group;
+    bool last, far;              // far: the sequence comes from another group
+    __device__ __forceinline__ Look(int j_, int src_) : j(j_), src(src_) {
+        tile = max(src, j / kGroup * kGroup);
+        group = max(src / kGroup, j / (kGroup * kGroup) * kGroup);
+        last = DEEP && j % kGroup == kGroup - 1;
+        far = src < j / kGroup * kGroup;
+    }
+    __device__ __forceinline__ bool state() const { return src < j / (kGroup * kGroup) * (kGroup * kGroup); }
+};
+
+// All waves fetch the rows of tiles (HIGH: of groups), and wait for those that are not published yet.
+template <int NW, bool HIGH, bool DEEP>
+__device__ __forceinline__ void fetch_look(const GsArgs& A, const Look<DEEP>& q, int col, uint64_t (*look)[kCols]) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t row = (int64_t)A.cols * kCols;
-    const uint64_t* agg = A.ch.agg + lo * row + col * kCols;
-    const uint32_t* incl = A.ch.incl + (group - 1) * row + col * kCols;
+    const uint64_t* words = (HIGH ? A.ch.gagg + q.group * row : A.ch.agg + q.tile * row) + col * kCols;
+    const int n_words = HIGH ? q.j / kGroup - q.group : q.j - q.tile, before = HIGH ? q.j / (kGroup * kGroup) * kGroup : q.j / kGroup;
+    const uint32_t* incl = A.ch.incl + (before - 1) * row + col * kCols;
+    const bool state = HIGH ? q.state() : q.far && !q.last;
+    if (HIGH) look += kGroup;
     int polls = 0;
     const auto read = [&](int i) -> uint64_t {
-        if (i == kGroup - 1) {
-            const uint32_t v = src < lo ? peek(incl + lane) : 0;
-            return v == (uint32_t)kNone ? kNone : v;
-        }
-        return lo + i < j ? peek(agg + i * row + lane) : 0;
+        if (i < kGroup - 1) return i < n_words ? peek(words + i * row + lane) : 0;
+        const uint32_t v = state ? peek(incl + lane) : 0;
+        return v == (uint32_t)kNone ? kNone : v;
     };
     // All reads are under way at a time; what came too early is read again, one word after the other.
     constexpr int N = kGroup / NW;
@@ -395,17 +418,64 @@ __device__ __forceinline__ void fetch_look(const GsArgs& A, int j, int src, int 
     }
 }
 
-__device__ __forceinline__ float compose(int j, int src, const uint64_t (*look)[kCols]) {
-    const int group = j / kGroup, lo = max(src, group * kGroup), lane = threadIdx.x & 63;
-    float h = src < lo ? __uint_as_float((uint32_t)look[kGroup - 1][lane]) : 0.0f;
+__device__ __forceinline__ float low(uint64_t w) { return __uint_as_float((uint32_t)w); }
+__device__ __forceinline__ float high(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32)); }
+
+// (S, U) of the group that ends with tile j, whose own is `own`: from the first tile of the sequence that goes on behind it; `cut`: which
+// begins in tile j.
+template <bool DEEP>
+__device__ __forceinline__ uint64_t compose_group(const Look<DEEP>& q, uint64_t own, bool cut, const uint64_t (*look)[kCols]) {
+    const int lane = threadIdx.x & 63;
+    float S = 0.0f, U = 0.0f;
 #pragma unroll 4
-    for (int i = 0; lo + i < j; ++i) {
+    for (int i = 0; q.tile + i < q.j; ++i) {
         const uint64_t w = look[i][lane];
-        const float U = __uint_as_float((uint32_t)(w >> 32));
-        h = src == lo + i ? U : fmaf(exp2_fast(__uint_as_float((uint32_t)w)), h, U);
+        S += low(w);
+        U = q.src == q.tile + i ? high(w) : fmaf(exp2_fast(low(w)), U, high(w));
+    }
+    return cut || q.src == q.j ? own : word_of(S + low(own), fmaf(exp2_fast(low(own)), U, high(own)));
+}
+
+// The state that enters tile j.
+template <bool DEEP>
+__device__ __forceinline__ float compose(const Look<DEEP>& q, const uint64_t (*look)[kCols]) {
+    const int lane = threadIdx.x & 63;
+    float h = 0.0f;
+    if (q.far && !q.last) h = low(look[kGroup - 1][lane]);
+    if constexpr (DEEP) {
+        if (q.far && q.last) {
+            if (q.state()) h = low(look[kLook<DEEP> - 1][lane]);
+#pragma unroll 4
+            for (int i = 0; q.group + i < q.j / kGroup; ++i) {
+                const uint64_t w = look[kGroup + i][lane];
+                h = q.src / kGroup == q.group + i ? high(w) : fmaf(exp2_fast(low(w)), h, high(w));
+            }
+        }
+    }
+#pragma unroll 4
+    for (int i = 0; q.tile + i < q.j; ++i) {
+        const uint64_t w = look[i][lane];
+        h = q.src == q.tile + i ? high(w) : fmaf(exp2_fast(low(w)), h, high(w));
     }
     return h;
 }
+
+// Fetches what tile j looks at; all threads together.  A group's last tile hands the group's (S, U) on before it waits for other groups'; its
+// own, `own`, is with the first 64 threads.
+template <int NW, bool DEEP>
+__device__ __forceinline__ void look_back(const GsArgs& A, const Look<DEEP>& q, int col, uint64_t own, bool cut, uint64_t (*look)[kCols]) {
+    if (q.src < q.j) fetch_look<NW, false>(A, q, col, look);
+    if constexpr (DEEP) {
+        if (q.last) {
+            lds_barrier();
+            if (threadIdx.x < kCols) publish(A, A.ch.gagg, q.j / kGroup, col * kCols + threadIdx.x, compose_group(q, own, cut, look));
+            if (q.far) fetch_look<NW, true>(A, q, col, look);
+        }
+    }
+    lds_barrier();
+}
+
+__host__ __device__ __forceinline__ int64_t groups_of(int64_t tiles) { return (tiles + kGroup - 1) / kGroup; }
 
 // Clears what the chains hand on and finds every tile's place among the offsets.  A launch of its own, 5 us behind another kernel's large
 // writes (2.5 behind small ones): nothing of a chain may be taken before all of it is clear.
@@ -421,9 +491,12 @@ __global__ void __launch_bounds__(256) k_gs_setup(Setup S) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         if (S.tiles[k] < 2) continue;
-        const int64_t words = (int64_t)S.tiles[k] * S.columns, states = (int64_t)((S.tiles[k] + kGroup - 1) / kGroup) * S.columns;
+        const int64_t words = (int64_t)S.tiles[k] * S.columns, groups = groups_of(S.tiles[k]) * S.columns;
         for (int64_t i = i0; i < words; i += step) S.ch[k].agg[i] = kNone;
-        for (int64_t i = i0; i < states; i += step) S.ch[k].incl[i] = (uint32_t)kNone;
+        for (int64_t i = i0; i < groups; i += step) {
+            S.ch[k].gagg[i] = kNone;
+            S.ch[k].incl[i] = (uint32_t)kNone;
+        }
         for (int64_t i = i0; i < S.columns / kCols; i += step) S.ch[k].ticket[i * kCounter] = 0;
         if (S.cu && S.n_seq < 64) {
             // one look at all offsets, a lane each
@@ -502,12 +575,12 @@ struct Source {
 // OUT: outputs and end states are written; otherwise the states for the backward alone.
 // Four workgroups a compute unit; three where fp32 channels come in pairs, whose registers would not hold it all otherwise (16384 tokens of
 // 2048 channels 113 us with four and 24 bytes of scratch, 106 with three; 8192 of 1536 47.5 and 43.2).
-template <typename T, int PAIR, int K, bool OUT>
+template <typename T, int PAIR, int K, bool OUT, bool DEEP>
 __global__ void __launch_bounds__(kTile / K * 32, sizeof(T) == 4 && PAIR ? 3 : 4) k_gs_forward(GsArgs A) {
     constexpr int NG = kTile / K, NX = kNext<PAIR>;
     __shared__ f2 comp[NG][kCols];
     __shared__ float entry[NG][kCols];
-    __shared__ uint64_t look[kGroup][kCols];
+    __shared__ uint64_t look[kLook<DEEP>][kCols];
     __shared__ Events<kTile, NG> ev;
     __shared__ int taken;
     const int c2 = first_channel<PAIR>(), grp = threadIdx.x >> 5;
@@ -595,23 +668,27 @@ __global__ void __launch_bounds__(kTile / K * 32, sizeof(T) == 4 && PAIR ? 3 : 4
 #pragma unroll
         for (int i = 0; i < 2; ++i) comp[grp][c2 + i * NX] = f2{S[i], U[i]};
         lds_barrier();
+        const Look<DEEP> q(j, p.src);
         if (A.tiles > 1) {
+            uint64_t own = 0;
+            bool cut = false;
             if (threadIdx.x < kCols) {
                 float St = 0.0f, Ut = 0.0f;
 #pragma unroll 4
                 for (int i = 0; i < NG; ++i) {
                     const f2 v = comp[i][threadIdx.x];
                     const bool off = v[0] > 0.0f;
+                    cut = cut || off;
                     St += off ? 0.0f : v[0];
                     Ut = off ? v[1] : fmaf(exp2_fast(v[0]), Ut, v[1]);
                 }
-                publish(A, j, col * kCols + threadIdx.x, St, Ut);
+                own = word_of(St, Ut);
+                publish(A, A.ch.agg, j, col * kCols + threadIdx.x, own);
             }
-            if (p.src < j) fetch_look<NG / 2>(A, j, p.src, col, look);
-            lds_barrier();
+            look_back<NG / 2>(A, q, col, own, cut, look);
         }
         if (threadIdx.x < kCols) {
-            float h = p.src < j ? compose(j, p.src, look) : 0.0f;
+            float h = p.src < j ? compose(q, look) : 0.0f;
 #pragma unroll 4
             for (int i = 0; i < NG; ++i) {
                 const f2 v = comp[i][threadIdx.x];
@@ -672,12 +749,12 @@ __global__ void __launch_bounds__(kTile / K * 32, sizeof(T) == 4 && PAIR ? 3 : 4
 // registers: forward and back for what the tile hands on, forward for h_{t-1}, back for G and the gradients.  64 tokens, eight a thread: what
 // is held of every token (two outputs' factors, a, s, the inputs) makes 160 registers, three workgroups a compute unit; four
 // tokens a thread (92 registers, 512 threads) took 122 us where this takes 108 (16384 by 1536, bf16).
-template <typename T, int PAIR, int K>
+template <typename T, int PAIR, int K, bool DEEP>
 __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A) {
     constexpr int NG = kTileBack / K, NT = NG * 32, NX = kNext<PAIR>;
     __shared__ f4 comp[NG][kCols];          // of every group: (S, U) forward, (S, V) backward
     __shared__ f2 entry[NG][kCols];         // the state in front of it, the gradient from behind it
-    __shared__ uint64_t look[kGroup][kCols];
+    __shared__ uint64_t look[kLook<DEEP>][kCols];
     __shared__ Events<kTileBack, NG> ev;
     __shared__ int taken;
     static_assert(kTileBack == kEvery, "a tile starts from a kept state");
@@ -767,23 +844,27 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
     for (int i = 0; i < 2; ++i) comp[grp][c2 + i * NX] = f4{cut ? 1.0f : S[i], U[i], cut_back ? 1.0f : S[i], V[i]};
     lds_barrier();
     const int src = A.tiles - 1 - p.src;
+    const Look<DEEP> look_at(jr, src);
     if (A.tiles > 1) {
+        uint64_t own = 0;
+        bool cut_any = false;
         if (threadIdx.x < kCols) {
             float St = 0.0f, Vt = 0.0f;
 #pragma unroll 4
             for (int i = NG - 1; i >= 0; --i) {
                 const f4 q = comp[i][threadIdx.x];
                 const bool off = q[2] > 0.0f;
+                cut_any = cut_any || off;
                 St += off ? 0.0f : q[2];
                 Vt = off ? q[3] : fmaf(exp2_fast(q[2]), Vt, q[3]);
             }
-            publish(A, jr, col * kCols + threadIdx.x, St, Vt);
+            own = word_of(St, Vt);
+            publish(A, A.ch.agg, jr, col * kCols + threadIdx.x, own);
         }
-        if (src < jr) fetch_look<NG / 2>(A, jr, src, col, look);
-        lds_barrier();
+        look_back<NG / 2>(A, look_at, col, own, cut_any, look);
     }
     if (threadIdx.x < kCols) {
-        float g = src < jr ? compose(jr, src, look) : 0.0f;
+        float g = src < jr ? compose(look_at, look) : 0.0f;
 #pragma unroll 4
         for (int i = NG - 1; i >= 0; --i) {
             const f4 q = comp[i][threadIdx.x];
@@ -954,15 +1035,16 @@ int64_t columns_of(int64_t D) { return (D + kCols - 1) / kCols * kCols; }
 // Where a chain's parts lie in the workspace from `at` on; returns the bytes it takes (none for one tile).
 size_t lay_out(Chain* ch, char* at, int64_t tiles, int64_t columns) {
     if (tiles < 2) return 0;
-    const size_t agg = up256((size_t)tiles * columns * 8), incl = up256((size_t)((tiles + kGroup - 1) / kGroup) * columns * 4);
-    const size_t first = up256((size_t)(tiles + 1) * 4);
+    const size_t agg = up256((size_t)tiles * columns * 8), gagg = up256((size_t)groups_of(tiles) * columns * 8);
+    const size_t incl = up256((size_t)groups_of(tiles) * columns * 4), first = up256((size_t)(tiles + 1) * 4);
     if (ch) {
         ch->agg = (uint64_t*)at;
-        ch->incl = (uint32_t*)(at + agg);
-        ch->first = (int*)(at + agg + incl);
-        ch->ticket = (uint32_t*)(at + agg + incl + first);
+        ch->gagg = (uint64_t*)(at + agg);
+        ch->incl = (uint32_t*)(at + agg + gagg);
+        ch->first = (int*)(at + agg + gagg + incl);
+        ch->ticket = (uint32_t*)(at + agg + gagg + incl + first);
     }
-    return agg + incl + first + up256((size_t)(columns / kCols) * kCounter * 4);
+    return agg + gagg + incl + first + up256((size_t)(columns / kCols) * kCounter * 4);
 }
 
 // The backward's workspace: both chains, the tiles' shares of the sums, the states where they are made again.
@@ -1011,16 +1093,21 @@ mb_status launch_setup(const GsArgs& A, const Chain& fwd, int64_t tiles, const C
     return check_launch();
 }
 
-template <typename T, bool OUT>
-mb_status run_forward(const GsArgs& A, hipStream_t s) {
+template <typename T, bool OUT, bool DEEP>
+mb_status run_forward_as(const GsArgs& A, hipStream_t s) {
     constexpr int K = kPer;
     const dim3 grid((unsigned)(A.tiles * A.cols)), block(kTile / K * 32);
     switch (pairs_of<T>(A, {A.y})) {
-        case 0: hipLaunchKernelGGL((k_gs_forward<T, 0, K, OUT>), grid, block, 0, s, A); break;
-        case 1: hipLaunchKernelGGL((k_gs_forward<T, 1, K, OUT>), grid, block, 0, s, A); break;
-        default: hipLaunchKernelGGL((k_gs_forward<T, 2, K, OUT>), grid, block, 0, s, A);
+        case 0: hipLaunchKernelGGL((k_gs_forward<T, 0, K, OUT, DEEP>), grid, block, 0, s, A); break;
+        case 1: hipLaunchKernelGGL((k_gs_forward<T, 1, K, OUT, DEEP>), grid, block, 0, s, A); break;
+        default: hipLaunchKernelGGL((k_gs_forward<T, 2, K, OUT, DEEP>), grid, block, 0, s, A);
     }
     return check_launch();
+}
+
+template <typename T, bool OUT>
+mb_status run_forward(const GsArgs& A, hipStream_t s) {
+    return A.cols <= kDeep ? run_forward_as<T, OUT, true>(A, s) : run_forward_as<T, OUT, false>(A, s);
 }
 
 template <typename T>
@@ -1037,16 +1124,21 @@ mb_status run_step(const GsArgs& A, int64_t n, hipStream_t s) {
     return MB_OK;
 }
 
-template <typename T>
-mb_status run_backward(const GsArgs& A, hipStream_t s) {
+template <typename T, bool DEEP>
+mb_status run_backward_as(const GsArgs& A, hipStream_t s) {
     constexpr int K = kPerBack;
     const dim3 grid((unsigned)(A.tiles * A.cols)), block(kTileBack / K * 32);
     switch (pairs_of<T>(A, {A.dy, A.dx, A.da, A.dg})) {
-        case 0: hipLaunchKernelGGL((k_gs_backward<T, 0, K>), grid, block, 0, s, A); break;
-        case 1: hipLaunchKernelGGL((k_gs_backward<T, 1, K>), grid, block, 0, s, A); break;
-        default: hipLaunchKernelGGL((k_gs_backward<T, 2, K>), grid, block, 0, s, A);
+        case 0: hipLaunchKernelGGL((k_gs_backward<T, 0, K, DEEP>), grid, block, 0, s, A); break;
+        case 1: hipLaunchKernelGGL((k_gs_backward<T, 1, K, DEEP>), grid, block, 0, s, A); break;
+        default: hipLaunchKernelGGL((k_gs_backward<T, 2, K, DEEP>), grid, block, 0, s, A);
     }
     return check_launch();
+}
+
+template <typename T>
+mb_status run_backward(const GsArgs& A, hipStream_t s) {
+    return A.cols <= kDeep ? run_backward_as<T, true>(A, s) : run_backward_as<T, false>(A, s);
 }
 
 // What every entry point takes: sizes, pointers and alignment of the inputs.

@@ -494,3 +494,32 @@ def test_tokens_of_no_sequence(head, tail, D, dtype):
     out = mb.mb_gated_scan_bwd(*ins, dy, g, dh_out=d["dh"].cuda(), **kw)
     for got in out[:3]:
         assert bool((got[:head] == 0).all()) and bool((got[head + T:] == 0).all())
+
+
+# tiles hold 128 tokens forward and 64 back, groups 16 tiles, groups of groups 256: sequences that begin, and end, in a group's
+# last tile, on its border, right behind it, and go on over many
+LONG = [[70001], [1925, 30000, 1000, 3000, 33000], [2048, 32768 - 2048, 1, 2047, 16384], [2047, 1, 14331, 16389, 20], [1900, 200, 62, 30600, 70, 34000]]
+
+
+@pytest.mark.parametrize("copies", [1, 131], ids=["few", "many"])
+@pytest.mark.parametrize("lens", LONG, ids=lambda v: "-".join(map(str, v)))
+def test_many_tiles(lens, copies):
+    """Three channels, once and many times over (few and many columns of tiles hand on in different ways)."""
+    D, T, n = 3, sum(lens), len(lens)
+    d = make(111, T, D, "f32", n, decay="slow")
+    c = {k: v.cuda().repeat(*[1] * (v.dim() - 1), copies) for k, v in d.items()}
+
+    def one(t, name):
+        t = t.reshape(*t.shape[:-1], copies, D)
+        assert torch.equal(t, t[..., :1, :].expand_as(t)), name
+        return t[..., 0, :]
+
+    kw = dict(a_bias=c["a_bias"], x_bias=c["x_bias"], cu_seqlens=offsets(lens).cuda(), h0=c["h0"])
+    y, h, kept = mb.mb_gated_scan(c["x"], c["a_gate"], c["decay"], c["x_gate"], states=True, **kw)
+    ry, rh, _, ty, th, _ = gf.scan(*wide(d), lens, d["h0"].double())
+    close(one(y, "y"), ry, tol(ty, ry, "f32"), "y")
+    close(one(h, "h"), rh, tol(th, rh, "f32"), "h")
+    ref, bound = gf.scan_bwd(*wide(d), lens, d["dy"].double(), d["h0"].double(), d["dh"].double())
+    out = mb.mb_gated_scan_bwd(c["x"], c["a_gate"], c["decay"], c["dy"], c["x_gate"], dh_out=c["dh"], states=kept, **kw)
+    for name, got in zip(("dx", "da_gate", "dx_gate", "ddecay", "da_bias", "dx_bias", "dh0"), out):
+        close(one(got, name), ref[name], tol(bound[name], ref[name], "f32"), name)
