@@ -748,7 +748,7 @@ mb_status mb_grad_norm_clip(const void* const* grads, void* const* outs, const i
  * reach the outputs and states of their channel from their token on, never earlier tokens, other
  * channels or other sequences (an infinity may become NaN).  Deterministic.
  * Supported: 1 <= D < 2^22, T < 2^31, n_seq <= 2^20, ceil(T / 64) ceil(D / 64) < 2^23.  Any alignment of the
- * element type's; even D and strides with pointers aligned to two elements read and write in pairs. 
+ * element type's; even D and strides with pointers aligned to two elements read and write in pairs.
  * ws: at least mb_workspace_size(MB_OP_GATED_SCAN, n_seq, T, D, 1, 1, 1, 1, 0) bytes, 256-byte
  * aligned (may be 0).  Two calls that run at the same time need a workspace each.
  */
