@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
         for (int i = 0; i < 2; ++i) v[i] = q && i < live ? q[(int64_t)row * A.D + c + i * NX] : 0.0f;
     };
 
-    // of every token: a, b, beta i, a^2 b / (1 - a^2) and then dla / G, s, la (1 - s), b (1 - i)
+    // of every token: a, beta i, a^2 b / (1 - a^2) and then dla / G, the smaller of s and 1 - s (1 - s negated), b (1 - i)
     float a[K][2], bi[K][2], r[K][2], sm[K][2], bn[K][2];
     float S[2] = {0.0f, 0.0f}, U[2] = {0.0f, 0.0f}, V[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -914,7 +914,9 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
             g[i] = a[k][i] * G;
             dx[i] = G * bi[k][i];
             dg[i] = G * bn[k][i];
-            const float m = sm[k][i], s = m < 0.0f ? 1.0f + m : m, not_s = m < 0.0f ? -m : 1.0f - m;
+            const float m = sm[k][i];
+            const bool open = (int)__float_as_uint(m) < 0;       // the sign, not the value: -0 is a gate so far open that 1 - s is zero
+            const float s = open ? 1.0f + m : m, not_s = open ? -m : 1.0f - m;
             da[i] = dla * (par.nd[i] * 0.69314718056f * s * not_s);
             sum[0][i] = fmaf(-dla, s, sum[0][i]);
             sum[1][i] += da[i];
