@@ -734,7 +734,8 @@ mb_status mb_grad_norm_clip(const void* const* grads, void* const* outs, const i
  *                 NULL: no input gate (its factor is 1; x_bias is then NULL too)
  *   x_stride, a_stride, g_stride : elements between the tokens of x, a_gate, x_gate, at least D and
  *                 below 2^22: they may be columns of one projection's output.  y is contiguous.
- *   decay       : (D) fp32, >= 0 (a negative one gives NaN; infinity: no memory)
+ *   decay       : (D) fp32, >= 0 (a negative one gives NaN; infinity: no memory, and NaN where a_gate +
+ *                 a_bias is below -87, whose s counts as zero)
  *   a_bias, x_bias : (D) fp32 or NULL (zeros)
  *   cu_seqlens, has_h0, slots, n_seq, n_slots : as mb_linear_attn (rows of y outside all sequences are
  *                 left as they were; offsets outside [0, T] are taken as the nearest bound; decreasing ones
@@ -782,7 +783,7 @@ mb_status mb_gated_scan_step(const void* x, const void* a_gate, const void* x_ga
  *     dla = G_t (a_t h_{t-1} - a_t^2 b / beta^2);   da_gate = dla la (1 - s);   ddecay = -sum dla s
  *     G = dh for the token before;  dh0 = G at the end;  da_bias = sum da_gate,  dx_bias = sum dx_gate
  * A step whose beta^2 is below 2^-120 (no decay at all) passes nothing through beta to ddecay and da_gate, where
- * the root has no derivative.
+ * the root has no derivative.  With infinite decay ddecay, da_gate and da_bias are zero.
  *   dy, dx, da_gate, dx_gate : (T, D) dtype, contiguous; dx_gate NULL exactly where x_gate is
  *   ddecay, da_bias, dx_bias : (D) fp32; NULL = not wanted
  *   h0, dh_out, dh0 : (n_seq, D) fp32; h0, dh_out NULL = zeros; dh0 NULL = not wanted

@@ -885,8 +885,10 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
     }
     lds_barrier();
     float h[2], g[2], sum[3][2];
+    float la_open[2];        // -decay; held finite: with infinite decay dla is zero, and so is what comes to the gate
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        la_open[i] = __builtin_elementwise_maximum(par.nd[i], -0x1.fffffep127f) * 0.69314718056f;
         h[i] = entry[grp][c2 + i * NX][0];
         g[i] = entry[grp][c2 + i * NX][1];
         sum[0][i] = sum[1][i] = sum[2][i] = 0.0f;
@@ -917,7 +919,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
             const float m = sm[k][i];
             const bool open = (int)__float_as_uint(m) < 0;       // the sign, not the value: -0 is a gate so far open that 1 - s is zero
             const float s = open ? 1.0f + m : m, not_s = open ? -m : 1.0f - m;
-            da[i] = dla * (par.nd[i] * 0.69314718056f * s * not_s);
+            da[i] = dla * (la_open[i] * s * not_s);
             sum[0][i] = fmaf(-dla, s, sum[0][i]);
             sum[1][i] += da[i];
             sum[2][i] += dg[i];

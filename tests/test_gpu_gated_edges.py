@@ -71,3 +71,23 @@ def test_gates_that_their_bias_opens(dtype):
     for name in ("y", "h") + NAMES:
         wide_type = name in ("h", "ddecay", "da_bias", "dx_bias", "dh0")
         close(got[name], ref[name], tol(bound[name], ref[name], "f32" if wide_type else dtype) + FAR, name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_of_channels_without_memory(dtype):
+    """Infinite decay: the outputs do not depend on the decay gate, so that nothing comes to it, its bias and the decay; the rest, and every
+    other channel, is as defined."""
+    lens, D, none = [70, 0, 200], 18, [0, 7, 17]
+    T = sum(lens)
+    d = make(75, T, D, dtype, len(lens))
+    d["decay"][none] = INF
+    d["a_gate"][100:120, 7] = 200.0
+    d["a_gate"][30, 17] = INF
+    got = both(d, lens)[0]
+    d["decay"][none] = 1e30                               # by definition the same values, and bounds that are numbers
+    ref, bound = both(d, lens)[1:]
+    for name in ("y", "h") + NAMES:
+        wide_type = name in ("h", "ddecay", "da_bias", "dx_bias", "dh0")
+        close(got[name], ref[name], tol(bound[name], ref[name], "f32" if wide_type else dtype), name)
+    for name in ("da_gate", "ddecay", "da_bias"):
+        assert bool((got[name][..., none] == 0).all()), name
