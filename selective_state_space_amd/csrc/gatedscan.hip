@@ -298,13 +298,17 @@ struct Events {
 
 // Fills them in, all threads together, a sequence each, and settles the sequences of no tokens: their `from` rows, or zeros, go to `to`, four
 // rows of the column's 64 channels at a time in a wave (offsets padded to a thousand sequences and more are all in one tile).  BACK: rows
-// are the sequences' numbers.
+// are the sequences' numbers, and behind the last sequence one of no row begins, which keeps that one's state from the tokens there.
 template <int TT, int NG, bool BACK>
 __device__ __forceinline__ void find_events(const GsArgs& A, const Place& p, Events<TT, NG>& ev, int col, const float* from, float* to) {
     constexpr int K = TT / NG;
     const int lane = threadIdx.x & 63;
     if (threadIdx.x < NG) ev.begins[threadIdx.x] = ev.ends[threadIdx.x] = 0;
     lds_barrier();
+    if (BACK && threadIdx.x == 0 && p.hi > 0 && p.hi < TT) {
+        ev.begin[p.hi] = -1;
+        atomicOr(&ev.begins[p.hi / K], 1u << p.hi % K);
+    }
     for (int s0 = p.sa; s0 <= p.sb; s0 += NG * 32) {
         const int s = s0 + (int)threadIdx.x;
         int row = -1;
@@ -786,8 +790,8 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
         find_events<kTileBack, NG, true>(A, p, ev, col, A.dh_out, A.dh0);
         begins = ev.begins[grp];
         ends = ev.ends[grp];
-        // Tokens of no sequence count as zeros, whatever they hold; no gradient comes to them (the walks back are cut where a
-        // sequence begins) and no state that is not finite, so that they add nothing to the sums.
+        // Tokens of no sequence count as zeros, whatever they hold; no gradient comes to them and no state that is not finite (the
+        // walks are cut where a sequence begins, and behind the last one), so that they add nothing to the sums.
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const bool in = grp * K + k >= p.lo && grp * K + k < p.hi;
@@ -801,7 +805,7 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
     const auto set = [&](float (&v)[2], const float* q, int row) {
         asm volatile("" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < 2; ++i) v[i] = q && i < live ? q[(int64_t)row * A.D + c + i * NX] : 0.0f;
+        for (int i = 0; i < 2; ++i) v[i] = q && row >= 0 && i < live ? q[(int64_t)row * A.D + c + i * NX] : 0.0f;
     };
 
     // of every token: a, beta i, a^2 b / (1 - a^2) and then dla / G, the smaller of s and 1 - s (1 - s negated), b (1 - i)
@@ -928,10 +932,11 @@ __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A)
         store2<T, PAIR>(bda, od, k * sd, da[0], da[1]);
         store2<T, PAIR>(bdg, od, k * sd, dg[0], dg[1]);
         if (!p.plain && (begins >> k & 1)) {
-            const int64_t at = (int64_t)ev.begin[grp * K + k] * A.D + c;
+            const int row = ev.begin[grp * K + k];
+            const int64_t at = (int64_t)row * A.D + c;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (A.dh0 && i < live) A.dh0[at + i * NX] = g[i];
+                if (A.dh0 && row >= 0 && i < live) A.dh0[at + i * NX] = g[i];
                 g[i] = 0.0f;            // for tokens of no sequence in front of it
             }
         }

@@ -91,3 +91,23 @@ def test_gradients_of_channels_without_memory(dtype):
         close(got[name], ref[name], tol(bound[name], ref[name], "f32" if wide_type else dtype), name)
     for name in ("da_gate", "ddecay", "da_bias"):
         assert bool((got[name][..., none] == 0).all()), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("tail", [0, 1, 9, 60, 150])
+def test_sums_behind_an_infinite_state(tail, dtype):
+    """An infinite last token makes the sums infinite, with the sign that its own share has: the tokens of no sequence behind it, whatever
+    they hold, add nothing (not 0 x infinity)."""
+    lens, D, c = [60, 40], 34, 5
+    T = sum(lens)
+    d = make(77, T + tail, D, dtype, len(lens))
+    for k in ("x", "a_gate", "x_gate", "dy"):
+        d[k][T:] = float("nan")
+    d["x"][T - 1, c] = INF
+    d["dy"][T - 1, c], d["dh"][1, c] = 1.0, 1.0
+    got, _, _ = both(d, lens)
+    # of the last token: G = 2, dla = -G a^2 b / beta^2 = -inf; ddecay -dla s, da_gate dla la (1 - s), dx_gate G b (1 - i)
+    for name in ("ddecay", "da_bias", "dx_bias"):
+        assert float(got[name][c]) == INF, name
+    for name in ("dx", "da_gate", "dx_gate"):
+        assert bool((got[name][T:] == 0).all()), name
