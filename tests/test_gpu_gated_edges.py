@@ -111,3 +111,24 @@ def test_sums_behind_an_infinite_state(tail, dtype):
         assert float(got[name][c]) == INF, name
     for name in ("dx", "da_gate", "dx_gate"):
         assert bool((got[name][T:] == 0).all()), name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sums_of_a_channel_with_an_infinity(dtype):
+    """An infinite input in the middle of a sequence: no sum of its channel comes out finite, every other one and the other
+    sequences' rows are as without it."""
+    lens, D, t, c = [200, 300, 150], 70, 333, 5
+    d = make(79, sum(lens), D, dtype, len(lens))
+    e = {k: v.clone() for k, v in d.items()}
+    e["x"][t, c] = INF
+    got, want = both(e, lens)[0], both(d, lens)[0]
+    for name in NAMES:
+        g, w = got[name].cpu().clone(), want[name].cpu()
+        if name in ("ddecay", "da_bias", "dx_bias"):
+            assert not bool(torch.isfinite(g[c])), name
+            g[c] = w[c]
+        elif name == "dh0":
+            g[1, c] = w[1, c]
+        else:
+            g[200:500, c] = w[200:500, c]
+        assert torch.equal(g, w), name
