@@ -726,8 +726,8 @@ mb_status mb_grad_norm_clip(const void* const* grads, void* const* outs, const i
 
 /*
  * Gated linear recurrence: every channel of every token has a decay of its own from a gate, and an
- * input that a second gate opens and that is scaled so that the state keeps its variance.  Per
- * sequence and channel c, with sigma(v) = 1 / (1 + e^-v):
+ * input that a second gate opens and that is scaled so that the state keeps its variance, the first
+ * token's of a sequence like any other's.  Per sequence and channel c, with sigma(v) = 1 / (1 + e^-v):
  *     s_t = sigma(a_gate_t + a_bias),  la_t = -decay s_t,  a_t = e^{la_t}
  *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigma(x_gate_t + x_bias) x_t,   y_t = h_t
  *   x, a_gate, x_gate, y : (T, D)  dtype   the tokens of all sequences, one after another; x_gate
@@ -748,6 +748,10 @@ mb_status mb_grad_norm_clip(const void* const* grads, void* const* outs, const i
  * Arithmetic and states are fp32; 1 - a^2 keeps its digits where a is next to 1.  NaN and infinities
  * reach the outputs and states of their channel from their token on, never earlier tokens, other
  * channels or other sequences (an infinity may become NaN).  Deterministic.
+ * Workgroups wait for states from those of earlier tokens (and in the backward for gradients from those
+ * of later ones).  A wait ends after some seconds at the latest.  Only a call whose workspace something else
+ * writes to, or whose workgroups are held up for that long, comes to this; what it waited for is then NaN
+ * in its outputs and end states, those in a pool too, and the status is MB_OK all the same.
  * Supported: 1 <= D < 2^22, T < 2^31, n_seq <= 2^20, ceil(T / 64) ceil(D / 64) < 2^23.  Any alignment of the
  * element type's; even D and strides with pointers aligned to two elements read and write in pairs.
  * ws: at least mb_workspace_size(MB_OP_GATED_SCAN, n_seq, T, D, 1, 1, 1, 1, 0) bytes, 256-byte
