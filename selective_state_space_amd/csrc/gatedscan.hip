@@ -18,10 +18,12 @@
 // Tiles in front of the one in which the first token's sequence starts are not looked at.
 //
 // What bounds it: bytes (12 of x and gates and 4 of y a token and channel in fp32, half of it in bf16, once each), and beside them the
-// gates' transcendentals and the waits for states, which four workgroups a compute unit hide in part.  16384 packed tokens of 1536 bf16
-// channels: 58 us for 201 MB, 3.5 TB/s (the loads and stores alone 39, the gates 5 to 8, counters 3, waits for tiles in front 6 to 10; a
-// pass for end states and one for outputs read 151 MB twice).  65536 tokens of 768: 102 us, 403 MB.  The backward of 16384 by 1536: 108 us for
-// 352 MB, 3.3 TB/s.  Few channels leave most of the card idle: 131072 tokens of 64 channels 41 us for 67 MB, their backward 76 for 117.
+// gates' transcendentals and the waits for states, which four workgroups a compute unit hide in part.  Here and below: times of the kernel
+// alone.  16384 packed tokens of 1536 bf16 channels, columns of one projection: 58 to 59 us for 201 MB, 3.4 TB/s (when it took 57, the
+// loads and stores alone took 39, the gates 5 to 8, counters 3, waits for tiles in front 6 to 10; a pass for end states and one for
+// outputs read 151 MB twice); one sequence of contiguous tensors 53.  65536 tokens of 768: 101 to 104 us, 403 MB.  The backward of 8 x 2048 by
+// 1536: 109 us for 352 MB, 3.2 TB/s.  Few channels leave most of the card idle: 131072 tokens of 64 channels 37 us for 67 MB, their
+// backward 64 for 117.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -44,8 +46,9 @@ constexpr int kDeep = 6;                    // columns up to which a group's las
 template <bool DEEP> constexpr int kLook = DEEP ? 2 * kGroup : kGroup;       // words that a tile looks at
 constexpr int kCounter = 32;                // words between the counters of two columns
 constexpr uint64_t kNone = ~0ull;           // not published yet
-// Polls of one wait before it is given up (the result is NaN then): some seconds, which only a workspace
-// that something else writes to at the same time can bring about.
+// Polls of one wait before it is given up: some seconds.  What was waited for counts as NaN then, in outputs and end states, and the
+// call has returned MB_OK long before.  A workspace that something else writes to at the same time brings it about, and so would a
+// workgroup of an earlier tile that is held up for as long (by a debugger, or where several processes share the card).
 constexpr int kPolls = 1 << 22;
 
 // What the tiles of one direction hand on to each other, in the workspace.
@@ -119,11 +122,12 @@ __device__ __forceinline__ void sigma2(float v, float nb, float& s, float& not_s
 // --------------------------------------------------------------- memory ----
 // A thread's two channels: beside each other where both can be read at a time (PAIR: they start on a border of two elements everywhere),
 // otherwise half a tile apart, so that a row's threads read neighbouring elements with each of two reads.  16384 tokens of 1001 bf16
-// channels, forward and backward: channels beside each other 55.7 and 107 us read one by one, 64 and 114 read in pairs from odd
-// addresses, half a tile apart 51.6 and 103.
+// channels, forward and backward: channels beside each other, read one by one, 63 and 129 us, half a tile apart 49 and 121 (pairs from odd
+// addresses 64 forward, where half a tile apart then took 52).
 // PAIR: 0 half a tile apart, 1 pairs, 2 pairs whose tiles' rows are whole lines of memory, 128 bytes.  Those are read past the caches; lines
-// that two tiles share are not.  16384 tokens of 1536 bf16 channels (whole lines): forward 57.7 us past the caches and 58.9 through
-// them, backward 106 and 114; of 1000 (shared): 48.7 and 45.0, 90 and 84; 8192 of 1530 fp32 channels (shared): 49.8 and 51.9, 87 and 81.
+// that two tiles share are not.  16384 tokens of 1536 bf16 channels (whole lines): forward 53 us past the caches and 55.5 through
+// them, backward 107 and 112; of 1000 (shared): 48.5 and 46.5, backward 87 both ways; 8192 of 1530 fp32 channels (shared): 50.5 and 52.5,
+// 86 and 91, the one kind that reading past the caches would serve better.
 template <int PAIR> constexpr int kNext = PAIR ? 1 : kCols / 2;
 template <int PAIR> __device__ __forceinline__ int first_channel() { return (threadIdx.x & 31) * (PAIR ? 2 : 1); }
 template <int PAIR> __device__ __forceinline__ int channels_of(int D, int c) { return (c < D) + (c + kNext<PAIR> < D); }
@@ -372,8 +376,13 @@ __device__ __forceinline__ void publish_state(const GsArgs& A, int i, int c, flo
 // of its group in front of it, from `tile` on.  Row 15: the state behind the group before.  States are so handed on from group to group, one
 // after the other, 1.4 us each, which with few columns takes longer than memory.  DEEP: a group's last tile (`last`) does not wait for that
 // state.  Its rows 16 to 30 are the groups of its group of groups in front of its own, from `group` on, row 31 the state behind the group of
-// groups before.  A sequence of 131072 tokens, bf16, group by group and DEEP: 64 channels 127 and 41 us, 256 130 and 82, 384 139 and
-// 110, 512 165 and 158, 640 167 and 169; backward 247 and 76, 270 and 186, 288 and 263, 345 and 357, 383 and 416.
+// groups before.  One sequence, bf16, group by group and DEEP, us:
+//     131072 tokens of    64 channels 122 and 37, 128 118 and 48, 256 126 and 79, 384 134 and 107, 512 170 and 160, 640 161 and 168
+//     backward                        222 and 64,     225 and 98,     247 and 173,    264 and 249,    320 and 345,    355 and 399
+//     16384 tokens of     64 channels 21.5 and 13.9, 384 27.5 and 22.2, 512 28.8 and 24.9;  backward 37 and 19, 48 and 45, 47 and 50
+//     2048 tokens of      64 channels 10.5 and 11.4, 384 10.6 and 11.4;                     backward 12.8 and 14.6, 14 and 15
+// 32 sequences of 2048 tokens of 64 channels 20 and 21, of 384 57 and 58, backward 39 and 41, 122 and 131.  One border (kDeep) serves both
+// directions and every length: the forward would gain up to 512 channels, and short sequences lose a little by it.
 template <bool DEEP>
 struct Look {
     int j, src, tile, group;
@@ -528,8 +537,9 @@ __global__ void __launch_bounds__(256) k_gs_setup(Setup S) {
 // then always in work.  One counter for all columns is slower: their adds come one after the other at one address, 12 us of the 73
 // that 16384 tokens of 1536 bf16 channels took with it; with a counter each, 128 bytes apart, 3 to 5.
 // Workgroups go to the eight dies in turn: a die, or two or four together where eight does not divide the columns, has columns that lie
-// beside each other, whose rows share lines where they are not aligned and pages of memory everywhere.  Against column b % cols, 16384 tokens of
-// 1536 bf16 channels: forward 60.1 and 57.3 us, backward 114 and 108; 16380 tokens of 1001 fp32 channels 36.8 and 34.2.
+// beside each other, whose rows share lines where they are not aligned and pages of memory everywhere.  Against column b % cols, 16384
+// tokens of 1536 bf16 channels in 8 sequences: forward 52.6 and 51.1 us, backward 107 and 104; 16380 tokens of 1001 fp32 channels 71.1
+// and 70.0, backward 139 and 128.
 __device__ __forceinline__ int column_of(const GsArgs& A) {
     const uint32_t b = blockIdx.x, cols = A.cols, shift = cols & 1 ? 0 : cols & 2 ? 1 : cols & 4 ? 2 : 3, per = cols >> shift;
     return (int)((b & ((1u << shift) - 1)) * per + (b >> shift) % per);
@@ -578,7 +588,7 @@ struct Source {
 // A thread holds K tokens of two channels; 32 threads side by side make a group's rows of 64 channels, NG groups the tile.
 // OUT: outputs and end states are written; otherwise the states for the backward alone.
 // Four workgroups a compute unit; three where fp32 channels come in pairs, whose registers would not hold it all otherwise (16384 tokens of
-// 2048 channels 113 us with four and 24 bytes of scratch, 106 with three; 8192 of 1536 47.5 and 43.2).
+// 2048 channels 113 us with four and 24 bytes of scratch, 106 with three; 8192 of 1536 48.8 and 44.7).
 template <typename T, int PAIR, int K, bool OUT, bool DEEP>
 __global__ void __launch_bounds__(kTile / K * 32, sizeof(T) == 4 && PAIR ? 3 : 4) k_gs_forward(GsArgs A) {
     constexpr int NG = kTile / K, NX = kNext<PAIR>;
@@ -752,7 +762,7 @@ __global__ void __launch_bounds__(kTile / K * 32, sizeof(T) == 4 && PAIR ? 3 : 4
 // the gradient that comes back out of the tiles behind, handed on like the states forward.  The tokens are walked three times in
 // registers: forward and back for what the tile hands on, forward for h_{t-1}, back for G and the gradients.  64 tokens, eight a thread: what
 // is held of every token (two outputs' factors, a, s, the inputs) makes 160 registers, three workgroups a compute unit; four
-// tokens a thread (92 registers, 512 threads) took 122 us where this takes 108 (16384 by 1536, bf16).
+// tokens a thread (92 registers, 512 threads) take 121 us where this takes 102 to 110 (8 x 2048 by 1536, bf16).
 template <typename T, int PAIR, int K, bool DEEP>
 __global__ void __launch_bounds__(kTileBack / K * 32, 3) k_gs_backward(GsArgs A) {
     constexpr int NG = kTileBack / K, NT = NG * 32, NX = kNext<PAIR>;
@@ -992,8 +1002,8 @@ __global__ void __launch_bounds__(1024) k_gs_sums(const float* __restrict__ part
 }
 
 // ----------------------------------------------------------------- step ----
-// Two channels of one sequence a thread, nothing shared.  One row of 1536 channels 2.8 us, the latency of the launch and two loads; 256
-// rows in a pool 4.2 us for 6.3 MB, most of it in the caches.
+// Two channels of one sequence a thread, nothing shared.  One row of 1536 channels 3.0 us, the latency of the launch and two loads; 256
+// rows in a pool 4.3 us for 6.3 MB, most of it in the caches.
 template <typename T, int PAIR>
 __global__ void __launch_bounds__(256) k_gs_step(GsArgs A, int64_t n0, int blocks) {
     const int64_t n = n0 + blockIdx.x / blocks;

@@ -8,10 +8,11 @@
 // Bound by HBM: a head's row is read once, kept in registers between the sum of squares and the turn, and written once.
 // LPR lanes (the power of two that holds D / 8) share a row, eight columns each as four pairs: the pairs' members lie in
 // one lane whichever way they are paired, two pieces of four neighbouring columns.  A workgroup takes some tokens with all
-// their heads, and makes the tokens' sines and cosines once, in LDS, for all of them.  16384 tokens of 16 and 16 heads of 128, bf16:
-// 52 us for 268 MB, 5.1 TB/s, the rate of a large copy (288 with the angles, reduced in fp64, made for every row); the
-// backward with 16 and 4 heads 52 us for 252 MB, 4.8 TB/s, and 4.7 for the sum over workgroups.  One token 3.4 us, 4095
-// tokens of 6 and 2 heads of 80 in fp32 10 us for 21 MB: the latency of load, angle, sum and store one behind the other.
+// their heads, and makes the tokens' sines and cosines once, in LDS, for all of them.  Times of the kernel alone: 16384 tokens of 16 and
+// 16 heads of 128, bf16, 52 to 58 us for 268 MB, 4.6 to 5.2 TB/s, about the rate of a large copy (288 with the angles, reduced in fp64,
+// made for every row); the backward with 16 and 4 heads 49 to 52 us for 252 MB, 4.8 to 5.1 TB/s, and 4.3 to 5.0 for the sum over
+// workgroups.  One token 3.4 us.  4095 tokens of 6 and 2 heads of 80 in fp32, 32 columns turned, 9.8 us for 21 MB: 512 of them take
+// 5.6, load, angle, sum and store one behind the other; the angles are 1.2 of the 9.8; the rest grows with the bytes (8190 tokens 14.4).
 #include <algorithm>
 #include <type_traits>
 
@@ -449,7 +450,7 @@ int lanes_of(int64_t D) {
 
 // Tokens that a workgroup takes at a time: eight rows or more for every place that it has, no more than leaves two workgroups a
 // compute unit.  A power of two: heads mostly come in numbers that then fill the batches (16384 tokens of 16 and 4 heads of 128, bf16, with
-// 7 tokens 47.2 us, 8 43.5, 10 and 16 45.0; the backward 57.0, 54.5, 58.4 and 57.1).
+// 7 tokens 45.6 us, 8 39.6, 10 44.4 and 16 42.0; the backward 54.0, 51.0, 54.4 and 52.0).
 int tokens_of(int64_t T, int64_t heads, int64_t D) {
     const int64_t places = 256 / lanes_of(D), want = 2 * (int64_t)device_cu_count();
     int64_t n = 1;
